@@ -328,6 +328,111 @@ int layer_output_error(const void* X, int x_dtype, int64_t rows, int64_t ldx,
                        const float* s, int group_size, double* out2,
                        void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Serving a layer whose weights are int8 codes with one scale per output
+ * channel: what the quantizers above give with group_size = in (and any
+ * bits; perm and g_idx do not matter with a single group).
+ *
+ * Quantization rule of every operator below: a set of values with largest
+ * magnitude a gets the fp32 scale S = a / 127 and the codes rint(x / S), half
+ * to even, in [-127, 127] (computed as x * (1 / S)). S below FLT_MIN becomes
+ * 0, with codes 0. A NaN or an infinity in the set makes S NaN, so everything
+ * stored with it reads as NaN.
+ *
+ * quantize_tokens_int8: one set per token (row). X [rows, in] bf16 or fp32;
+ * s fp32[in] (may be NULL) divides the columns first (AWQ's channel scales:
+ * codes of W diag(s) take X diag(s)^-1). codes int8 with row stride ldc
+ * (>= in, a multiple of 8), scales fp32[rows].
+ *
+ * matmul_int8: Y[t][o] = (sum_j A[t][j] codes[o][j]) * a_scales[t] * scales[o]
+ * + bias[o], the sums exact in int32, one rounding to Y's type (y_dtype).
+ * codes int8[out, in], scales fp32[out], bias fp32[out] or NULL; Y bf16 or
+ * fp32 [rows, out] with row stride ldy >= out.
+ *
+ * linear_int8: both in one call, Y = quantized(X diag(s)^-1) codes^T + bias.
+ *
+ * in: a multiple of 8 in [8, 131064]. Rows of int8 operands may have any row
+ * stride that is a multiple of 8. Asynchronous.
+ * Errors: EINVAL, EWORKSPACE, EHIP.
+ * ---------------------------------------------------------------------- */
+int quantize_tokens_int8(const void* X, int x_dtype, int64_t rows, int64_t in, int64_t ldx, const float* s,
+                         int8_t* codes, int64_t ldc, float* scales, void* stream);
+size_t matmul_int8_workspace_bytes(int64_t rows, int64_t out, int64_t in);
+int matmul_int8(const int8_t* A, int64_t lda, const float* a_scales, int64_t rows, const int8_t* codes, int64_t ldb,
+                const float* scales, int64_t out, int64_t in, const float* bias, int y_dtype, void* Y, int64_t ldy,
+                void* workspace, size_t workspace_bytes, void* stream);
+size_t linear_int8_workspace_bytes(int64_t rows, int64_t out, int64_t in);
+int linear_int8(const void* X, int x_dtype, int64_t rows, int64_t ldx, const float* s, const int8_t* codes,
+                int64_t ldb, const float* scales, int64_t out, int64_t in, const float* bias, int y_dtype, void* Y,
+                int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Int8 key/value cache: a pool of num_blocks blocks of block_size tokens,
+ *   k_codes int8[num_blocks][kv_heads][block_size][head_dim]
+ *   v_codes int8[num_blocks][kv_heads][head_dim][block_size]
+ *   k_scales, v_scales fp32[num_blocks][kv_heads]
+ * (value = code * scale of its block and head). Position p of sequence b is
+ * slot p % block_size of block block_table[b][p / block_size]; block_table is
+ * int32[batch, table_width], dense. block_size in {16, 32, 64, 128}, head_dim
+ * in {64, 128, 256}.
+ *
+ * A call takes the rows of several sequences one after another: sequence b
+ * has rows offsets[b] .. offsets[b + 1] (int32[batch + 1], from 0 to rows) of
+ * K and V ([rows, kv_heads, head_dim], bf16 or fp32, row strides ldk and ldv),
+ * at positions starts[b], starts[b] + 1, ... (int32[batch]). All of these are
+ * device arrays that the host never reads; what they say is checked on the
+ * device: rows outside [0, rows) are never touched, a position without a
+ * block (past table_width, a negative start, an id outside [0, num_blocks))
+ * is not written and reads as NaN. Rows of no sequence are left as they are.
+ *
+ * kv_cache_write_int8: quantizes the rows into their blocks. Per block and
+ * head, S = max(S_old, max |new values| / 127), with S_old the block's scale
+ * if it holds positions of the sequence below starts[b] and 0 otherwise; when
+ * S grows, the codes of those positions become rint(code * (S_old / S)).
+ * Slots past the written ones keep their bytes. A block written by a call
+ * must belong to one sequence only (a shared prefix ends at a block boundary).
+ *
+ * kv_cache_read_int8: K and V receive code * scale, rounded once to dtype.
+ *
+ * Asynchronous. Errors: EINVAL, EHIP.
+ * ---------------------------------------------------------------------- */
+int kv_cache_write_int8(int8_t* k_codes, int8_t* v_codes, float* k_scales, float* v_scales, int64_t num_blocks,
+                        int kv_heads, int head_dim, int block_size, const void* K, int64_t ldk, const void* V,
+                        int64_t ldv, int dtype, int64_t rows, const int32_t* offsets, const int32_t* starts,
+                        int64_t batch, const int32_t* block_table, int64_t table_width, void* stream);
+int kv_cache_read_int8(const int8_t* k_codes, const int8_t* v_codes, const float* k_scales, const float* v_scales,
+                       int64_t num_blocks, int kv_heads, int head_dim, int block_size, void* K, int64_t ldk, void* V,
+                       int64_t ldv, int dtype, int64_t rows, const int32_t* offsets, const int32_t* starts,
+                       int64_t batch, const int32_t* block_table, int64_t table_width, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Attention over the int8 cache. Q, O [rows, heads, head_dim] bf16 or fp32
+ * (row strides ldq, ldo), ragged as above; heads is a multiple of kv_heads,
+ * query head i reads kv head i / (heads / kv_heads). seq_lens int32[batch]:
+ * the keys of each sequence, the call's own tokens included; with n rows,
+ * query i of sequence b is at position p = seq_lens[b] - n + i. It attends to
+ * keys [max(0, p - window + 1), p] with causal = 1 (window 0: no lower
+ * limit), to all seq_lens[b] keys with causal = 0 (window must be 0).
+ *   O = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * q.k_j)
+ *   lse[rows, heads] (fp32, may be NULL) = ln sum_j w_j
+ * A query that attends to nothing gives O = 0, lse = -inf. A sequence longer
+ * than its row of block_table, and a key in a block without a valid id, give
+ * NaN to the queries concerned (all of the sequence's, those that attend).
+ *
+ * The codes enter the products exactly; sums, maxima and the output
+ * accumulate in fp32. Probabilities are held in 11 significant bits for bf16
+ * queries, 22 for fp32 queries. Asynchronous.
+ * Errors: EINVAL, EWORKSPACE, EHIP.
+ * ---------------------------------------------------------------------- */
+size_t attention_int8_cache_workspace_bytes(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim,
+                                            int block_size, int64_t table_width);
+int attention_int8_cache(const void* Q, int64_t ldq, void* O, int64_t ldo, float* lse, int dtype, int64_t rows,
+                         int heads, const int32_t* offsets, const int32_t* seq_lens, int64_t batch,
+                         const int32_t* block_table, int64_t table_width, const int8_t* k_codes, const int8_t* v_codes,
+                         const float* k_scales, const float* v_scales, int64_t num_blocks, int kv_heads, int head_dim,
+                         int block_size, float scale, int causal, int64_t window, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

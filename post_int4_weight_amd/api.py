@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -78,6 +79,18 @@ def _load() -> ctypes.CDLL:
         "ptq_test_gemm_f32_split3_workspace_bytes": (sz, [i64, i64, i64]),
         "ptq_test_gemm_f32_split3": (i32, [i64, i64, i64, vp, i64, i32, vp, i64, i32, vp, i64, ctypes.c_float, i32,
                                            i32, i32, vp, sz, vp]),
+        "quantize_tokens_int8": (i32, [vp, i32, i64, i64, i64, vp, vp, i64, vp, vp]),
+        "matmul_int8_workspace_bytes": (sz, [i64, i64, i64]),
+        "matmul_int8": (i32, [vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, i32, vp, i64, vp, sz, vp]),
+        "linear_int8_workspace_bytes": (sz, [i64, i64, i64]),
+        "linear_int8": (i32, [vp, i32, i64, i64, vp, vp, i64, vp, i64, i64, vp, i32, vp, i64, vp, sz, vp]),
+        "kv_cache_write_int8": (i32, [vp, vp, vp, vp, i64, i32, i32, i32, vp, i64, vp, i64, i32, i64, vp, vp, i64,
+                                      vp, i64, vp]),
+        "kv_cache_read_int8": (i32, [vp, vp, vp, vp, i64, i32, i32, i32, vp, i64, vp, i64, i32, i64, vp, vp, i64,
+                                     vp, i64, vp]),
+        "attention_int8_cache_workspace_bytes": (sz, [i64, i64, i32, i32, i32, i32, i64]),
+        "attention_int8_cache": (i32, [vp, i64, vp, i64, vp, i32, i64, i32, vp, vp, i64, vp, i64, vp, vp, vp, vp,
+                                       i64, i32, i32, i32, ctypes.c_float, i32, i64, vp, sz, vp]),
         "layer_output_error": (i32, [vp, i32, i64, i64, vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, i32, dp, vp, sz,
                                      vp]),
     }
@@ -371,6 +384,186 @@ def layer_output_error(X, W, codes, scales, g_idx=None, zeros=None, s=None, grou
                                    _ptr(scales), _ptr(g_idx), _ptr(zeros), _ptr(s), group_size, res, _ptr(ws), wsb,
                                    _stream()))
     return res[0], res[1]
+
+
+# ---------------------------------------------------------- int8 serving ---
+
+def _vector(t, n: int, dtype, name: str):
+    """t as n dense values of dtype (any shape with that many), or None."""
+    if t is not None and (t.dtype != dtype or t.numel() != n or not t.is_contiguous()):
+        raise ValueError(f"{name} must be {n} contiguous {dtype} values")
+    return _ptr(t)
+
+
+def _codes(t: torch.Tensor, name: str):
+    if t.dtype != torch.int8:
+        raise TypeError(f"{name} must be int8, not {t.dtype}")
+    return _rowmajor(t, name)
+
+
+def quantize_tokens_int8(X: torch.Tensor, s=None, codes=None, scales=None):
+    """quantize_tokens_int8 (include/ptq.h): X [rows, in] -> (codes int8 [rows, in], scales fp32 [rows]); s divides
+    the columns first."""
+    rows, n = X.shape
+    ldx = _rowmajor(X, "X")
+    if codes is None:
+        codes = torch.empty(rows, n, dtype=torch.int8, device=X.device)
+    if scales is None:
+        scales = torch.empty(rows, dtype=torch.float32, device=X.device)
+    if tuple(codes.shape) != (rows, n):
+        raise ValueError("codes must be [rows, in]")
+    _check(_lib.quantize_tokens_int8(_ptr(X), _dtype_code(X), rows, n, ldx, _vector(s, n, torch.float32, "s"),
+                                     _ptr(codes), _codes(codes, "codes"),
+                                     _vector(scales, rows, torch.float32, "scales"), _stream()))
+    return codes, scales
+
+
+def matmul_int8_workspace_bytes(rows: int, out: int, n: int) -> int:
+    return int(_lib.matmul_int8_workspace_bytes(rows, out, n))
+
+
+def _product_output(Y, rows, out, dtype, device):
+    if Y is None:
+        Y = torch.empty(rows, out, dtype=dtype, device=device)
+    elif tuple(Y.shape) != (rows, out):
+        raise ValueError("Y must be [rows, out]")
+    return Y, _rowmajor(Y, "Y") if rows > 1 else max(out, 1)
+
+
+def matmul_int8(A, a_scales, codes, scales, bias=None, out_dtype=torch.bfloat16, Y=None, workspace=None):
+    """matmul_int8 (include/ptq.h): Y[t][o] = (A codes^T)[t][o] * a_scales[t] * scales[o] + bias[o]."""
+    rows, n = A.shape
+    out = codes.shape[0]
+    if codes.shape[1] != n:
+        raise ValueError(f"codes has {codes.shape[1]} columns, A has {n}")
+    Y, ldy = _product_output(Y, rows, out, out_dtype, A.device)
+    ws, wsb = _workspace(matmul_int8_workspace_bytes(rows, out, n), A.device, workspace)
+    _check(_lib.matmul_int8(_ptr(A), _codes(A, "A"), _vector(a_scales, rows, torch.float32, "a_scales"), rows,
+                            _ptr(codes), _codes(codes, "codes"), _vector(scales, out, torch.float32, "scales"), out, n,
+                            _vector(bias, out, torch.float32, "bias"), _dtype_code(Y), _ptr(Y), ldy, _ptr(ws), wsb,
+                            _stream()))
+    return Y
+
+
+def linear_int8_workspace_bytes(rows: int, out: int, n: int) -> int:
+    return int(_lib.linear_int8_workspace_bytes(rows, out, n))
+
+
+def linear_int8(X, codes, scales, bias=None, s=None, out_dtype=None, Y=None, workspace=None):
+    """linear_int8 (include/ptq.h): X [rows, in] through int8 codes [out, in] with one scale per output channel
+    (group_size = in of the quantizers); the activations are quantized token by token. Y has X's dtype unless
+    out_dtype says otherwise."""
+    rows, n = X.shape
+    out = codes.shape[0]
+    if codes.shape[1] != n:
+        raise ValueError(f"codes has {codes.shape[1]} columns, X has {n}")
+    Y, ldy = _product_output(Y, rows, out, out_dtype or X.dtype, X.device)
+    ws, wsb = _workspace(linear_int8_workspace_bytes(rows, out, n), X.device, workspace)
+    _check(_lib.linear_int8(_ptr(X), _dtype_code(X), rows, _rowmajor(X, "X"), _vector(s, n, torch.float32, "s"),
+                            _ptr(codes), _codes(codes, "codes"), _vector(scales, out, torch.float32, "scales"), out, n,
+                            _vector(bias, out, torch.float32, "bias"), _dtype_code(Y), _ptr(Y), ldy, _ptr(ws), wsb,
+                            _stream()))
+    return Y
+
+
+class KVCacheInt8(NamedTuple):
+    """The four tensors of an int8 key/value cache (layout in include/ptq.h)."""
+    k: torch.Tensor           # int8 [num_blocks, kv_heads, block_size, head_dim]
+    v: torch.Tensor           # int8 [num_blocks, kv_heads, head_dim, block_size]
+    k_scales: torch.Tensor    # fp32 [num_blocks, kv_heads]
+    v_scales: torch.Tensor    # fp32 [num_blocks, kv_heads]
+
+    @classmethod
+    def empty(cls, num_blocks: int, kv_heads: int, head_dim: int, block_size: int = 64, device="cuda"):
+        codes = lambda *shape: torch.zeros(num_blocks, kv_heads, *shape, dtype=torch.int8, device=device)
+        scales = lambda: torch.zeros(num_blocks, kv_heads, dtype=torch.float32, device=device)
+        return cls(codes(block_size, head_dim), codes(head_dim, block_size), scales(), scales())
+
+    def _sizes(self):
+        nb, h, bs, d = self.k.shape
+        for t, shape, dtype in ((self.k, (nb, h, bs, d), torch.int8), (self.v, (nb, h, d, bs), torch.int8),
+                                (self.k_scales, (nb, h), torch.float32), (self.v_scales, (nb, h), torch.float32)):
+            if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+                raise ValueError(f"cache tensor must be contiguous {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+        return nb, h, d, bs
+
+
+def _heads3(t, rows, heads, dim, name):
+    """Row stride of a [rows, heads, dim] tensor whose heads follow each other."""
+    if tuple(t.shape) != (rows, heads, dim):
+        raise ValueError(f"{name} must be {(rows, heads, dim)}, got {tuple(t.shape)}")
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{name}: the heads of a row must follow each other")
+    return t.stride(0) if rows > 1 else heads * dim
+
+
+def _ragged(offsets, starts, block_table, name):
+    batch = starts.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError(f"block_table must be [{batch}, width]")
+    return (_vector(offsets, batch + 1, torch.int32, "offsets"), _vector(starts, batch, torch.int32, name), batch,
+            _vector(block_table, block_table.numel(), torch.int32, "block_table"), block_table.shape[1])
+
+
+def kv_cache_write_int8(cache: KVCacheInt8, K, V, offsets, starts, block_table):
+    """kv_cache_write_int8 (include/ptq.h): quantize K, V [rows, kv_heads, head_dim] into the cache, rows
+    offsets[b] .. offsets[b + 1] at positions starts[b], ... of sequence b."""
+    nb, h, d, bs = cache._sizes()
+    rows = K.shape[0]
+    ldk, ldv = _heads3(K, rows, h, d, "K"), _heads3(V, rows, h, d, "V")
+    if V.dtype != K.dtype:
+        raise TypeError("K and V must have one dtype")
+    _check(_lib.kv_cache_write_int8(_ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scales), _ptr(cache.v_scales), nb, h, d,
+                                    bs, _ptr(K), ldk, _ptr(V), ldv, _dtype_code(K), rows,
+                                    *_ragged(offsets, starts, block_table, "starts"), _stream()))
+
+
+def kv_cache_read_int8(cache: KVCacheInt8, offsets, starts, block_table, rows: int, out_dtype=torch.bfloat16, K=None,
+                       V=None):
+    """kv_cache_read_int8 (include/ptq.h): (K, V) [rows, kv_heads, head_dim] of the same ragged rows."""
+    nb, h, d, bs = cache._sizes()
+    if K is None:
+        K = torch.empty(rows, h, d, dtype=out_dtype, device=cache.k.device)
+    if V is None:
+        V = torch.empty(rows, h, d, dtype=K.dtype, device=cache.k.device)
+    ldk, ldv = _heads3(K, rows, h, d, "K"), _heads3(V, rows, h, d, "V")
+    if V.dtype != K.dtype:
+        raise TypeError("K and V must have one dtype")
+    _check(_lib.kv_cache_read_int8(_ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scales), _ptr(cache.v_scales), nb, h, d,
+                                   bs, _ptr(K), ldk, _ptr(V), ldv, _dtype_code(K), rows,
+                                   *_ragged(offsets, starts, block_table, "starts"), _stream()))
+    return K, V
+
+
+def attention_int8_cache_workspace_bytes(rows: int, batch: int, heads: int, kv_heads: int, head_dim: int,
+                                         block_size: int, table_width: int) -> int:
+    return int(_lib.attention_int8_cache_workspace_bytes(rows, batch, heads, kv_heads, head_dim, block_size,
+                                                         table_width))
+
+
+def attention_int8_cache(Q, cache: KVCacheInt8, offsets, seq_lens, block_table, scale=None, causal=True, window=0,
+                         O=None, lse=None, return_lse=False, workspace=None):
+    """attention_int8_cache (include/ptq.h): attention of Q [rows, heads, head_dim] over the cache; seq_lens counts
+    each sequence's keys, the call's own tokens included. Returns O, or (O, lse) with return_lse or a given lse."""
+    nb, h, d, bs = cache._sizes()
+    rows, heads = Q.shape[0], Q.shape[1]
+    if scale is None:
+        scale = d ** -0.5
+    if O is None:
+        O = torch.empty(rows, heads, d, dtype=Q.dtype, device=Q.device)
+    if lse is None and return_lse:
+        lse = torch.empty(rows, heads, dtype=torch.float32, device=Q.device)
+    ldq, ldo = _heads3(Q, rows, heads, d, "Q"), _heads3(O, rows, heads, d, "O")
+    if O.dtype != Q.dtype:
+        raise TypeError("O must have Q's dtype")
+    off, lens, batch, table, width = _ragged(offsets, seq_lens, block_table, "seq_lens")
+    ws, wsb = _workspace(attention_int8_cache_workspace_bytes(rows, batch, heads, h, d, bs, width), Q.device,
+                         workspace)
+    _check(_lib.attention_int8_cache(_ptr(Q), ldq, _ptr(O), ldo, _vector(lse, rows * heads, torch.float32, "lse"),
+                                     _dtype_code(Q), rows, heads, off, lens, batch, table, width, _ptr(cache.k),
+                                     _ptr(cache.v), _ptr(cache.k_scales), _ptr(cache.v_scales), nb, h, d, bs,
+                                     float(scale), int(bool(causal)), window, _ptr(ws), wsb, _stream()))
+    return O if lse is None else (O, lse)
 
 
 # ------------------------------------------------------------- test hook ---

@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libptq.so")
 
 SOURCES = ["api.cpp", "gemm_f32.hip", "gemm_bf16.hip", "chol.hip", "gptq.hip", "awq.hip", "pack.hip", "awq_gptq.hip",
-           "noalloc.hip"]
+           "noalloc.hip", "api_int8.cpp", "linear_int8.hip", "kv_cache.hip", "attention_int8.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # Packed-fp32 VALU ops are disabled for all device code (the compiler warns

@@ -1,0 +1,450 @@
+// Softmax attention of a ragged batch of queries over the int8 block cache
+// (layout in kv_cache.hip):
+//
+//   o = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q.k_j - m)
+//   k_j = S_k[block(j)] c_j,  v_j = S_v[block(j)] c'_j
+//
+// Arithmetic. Codes are exact in fp16, so both products run on the fp16
+// matrix cores: q is scaled by a power of two that brings its largest element
+// to [8, 16) (a bf16 q is then exact; an fp32 q is split into two fp16 terms),
+// S_k and the softmax scale multiply the fp32 sums, and S_v multiplies the
+// probabilities: w_j = p_j S_v[block(j)] / R in fp16 (two terms for fp32
+// queries), R a running maximum of S_v over what the wave has read, so w_j <=
+// p_j whatever the scales are. Sums, maxima and the output accumulate in fp32.
+#include "int8.hpp"
+
+#include <algorithm>
+#include <cmath>
+
+namespace ptq {
+namespace {
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int TR = 16;       // query rows (tokens x grouped heads) of a tile
+constexpr int TK = 64;       // tokens per step of a wave
+constexpr int NW = 4;        // waves of a workgroup, on different steps
+constexpr float PSHIFT = 8.f;   // p in [0, 2^8]: fp16 keeps 11 bits down to 2^-22 of the largest
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// 8 codes -> fp16: bytes offset to unsigned go under the exponent of 1024,
+// and 1024 + 128 comes off again (exact)
+__device__ __forceinline__ f16x8 half8(uint32_t a, uint32_t b) {
+    const uint32_t u = a ^ 0x80808080u, v = b ^ 0x80808080u, e = 0x64646464u;
+    union { uint32_t w[4]; f16x2 h[4]; f16x8 x; } r;
+    r.w[0] = __builtin_amdgcn_perm(e, u, 0x04010400u);
+    r.w[1] = __builtin_amdgcn_perm(e, u, 0x04030402u);
+    r.w[2] = __builtin_amdgcn_perm(e, v, 0x04010400u);
+    r.w[3] = __builtin_amdgcn_perm(e, v, 0x04030402u);
+    const f16x2 off = {(_Float16)1152.f, (_Float16)1152.f};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r.h[k] -= off;
+    return r.x;
+}
+
+struct AttnArgs {
+    Ragged g;
+    const int32_t* lens; const int32_t* table; int64_t width;
+    int heads, kv_heads, group, dim, bs, bs_log2;
+    int64_t num_blocks;
+    const int8_t* k; const int8_t* v; const float* ks; const float* vs;
+    const void* Q; int64_t ldq;
+    void* O; int64_t ldo;
+    float* lse;                    // [rows, heads] or null
+    float scale2;                  // softmax scale * log2(e)
+    int causal; int64_t window;
+    int nsplit;
+    float* part; float* part_lse;  // [nsplit][rows * heads][dim], [nsplit][rows * heads]
+};
+
+// One tile of query rows: flat rows f0 .. f0 + TR of sequence b, flat row =
+// token * group + head within the group.
+struct Tile {
+    int b;
+    int64_t off;           // first row (token) of the sequence
+    int rows;              // flat rows of the sequence
+    int f0;
+    int64_t len;           // keys of the sequence
+    int64_t pos0;          // position of the sequence's first query token
+    int it0, it1;          // steps of TK tokens with a key that some row of the tile attends to
+    int64_t lo_max, hi_min;   // steps within [lo_max, hi_min) need no mask
+    int64_t hi;            // end of the keys any row attends to
+    bool over;             // longer than its row of the table can hold: NaN
+};
+
+__device__ __forceinline__ int64_t row_lo(const AttnArgs& a, int64_t pos) {
+    return a.window > 0 ? std::max<int64_t>(0, pos - a.window + 1) : 0;
+}
+__device__ __forceinline__ int64_t row_hi(const AttnArgs& a, int64_t pos, int64_t len) {
+    return a.causal ? std::min<int64_t>(std::max<int64_t>(pos + 1, 0), len) : len;
+}
+
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t unit, int tr, Tile& t) {
+    int64_t local;
+    t.b = ragged_find(a.g, unit, a.group, tr, 1, &local);
+    t.off = ragged_offset(a.g, t.b);
+    const int64_t n = ragged_offset(a.g, t.b + 1) - t.off;
+    const int64_t rows = n * a.group, f0 = local * tr;
+    if (n <= 0 || f0 >= rows) return false;
+    t.rows = (int)rows;
+    t.f0 = (int)f0;
+    t.len = std::max<int64_t>(a.lens[t.b], 0);
+    t.pos0 = t.len - n;
+    t.over = t.len > a.width * a.bs;
+    t.len = std::min<int64_t>(t.len, a.width * a.bs);
+    const int64_t first = t.pos0 + f0 / a.group;
+    const int64_t last = t.pos0 + std::min<int64_t>(f0 + tr - 1, rows - 1) / a.group;
+    t.lo_max = row_lo(a, last);
+    t.hi_min = row_hi(a, first, t.len);
+    t.hi = row_hi(a, last, t.len);
+    const int64_t lo = row_lo(a, first);
+    t.it0 = (int)(lo / TK);
+    t.it1 = t.hi > lo ? (int)((t.hi + TK - 1) / TK) : t.it0;
+    return true;
+}
+
+// Steps of split s of a tile: an even share, at least one step a wave.
+__device__ __forceinline__ int split_steps(const Tile& t, int nsplit) {
+    const int n = t.it1 - t.it0;
+    return std::max(NW, (n + nsplit - 1) / nsplit);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_row4(T* p, float a, float b, float c, float d);
+template <>
+__device__ __forceinline__ void store_row4<float>(float* p, float a, float b, float c, float d) {
+    *(float4*)p = make_float4(a, b, c, d);
+}
+template <>
+__device__ __forceinline__ void store_row4<uint16_t>(uint16_t* p, float a, float b, float c, float d) {
+    *(uint2*)p = make_uint2(bf16_pair(a, b), bf16_pair(c, d));
+}
+
+// Few query rows, long caches: the scores are computed transposed,
+// S^T = K Q^T (tokens x rows), so a lane ends up with 16 scores of one query
+// row, and the probabilities are already the operand of O^T = V^T P^T: nothing
+// goes through LDS but the join of the waves. The tokens of a step are dealt
+// to operand rows so that lane group lg holds tokens 16 lg .. 16 lg + 15 (row r
+// of score block t is token 16 (r / 4) + 4 t + r % 4): V comes as one
+// 16-byte load per channel, and a lane's tokens lie in one block of the cache
+// (its size is a multiple of 16), so a lane needs one S_k and one S_v a step.
+template <typename T, int D>
+__global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
+    constexpr int NT = sizeof(T) == 4 ? 2 : 1;    // fp16 terms of q and of the probabilities
+    constexpr int NC = D / 32;                    // 32-deep steps of q.k
+    const int split = (int)(blockIdx.x % (unsigned)a.nsplit);
+    const int64_t tile = blockIdx.x / (unsigned)a.nsplit;
+    const int h = (int)(tile % a.kv_heads);
+    Tile tl;
+    if (!find_tile(a, tile / a.kv_heads, TR, tl)) return;
+    const int per = split_steps(tl, a.nsplit);
+    const int s0 = tl.it0 + split * per, s1 = std::min(s0 + per, tl.it1);
+    if (split > 0 && s0 >= s1) return;
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int li = lane & 15, lg = lane >> 4;
+    const int f = std::min(tl.f0 + li, tl.rows - 1);
+    const int64_t token = tl.off + f / a.group;
+    const int qh = h * a.group + f % a.group;
+    const int64_t pos = tl.pos0 + f / a.group;
+    const int64_t my_lo = row_lo(a, pos), my_hi = row_hi(a, pos, tl.len);
+
+    // q: operand column li, channels 64 (c / 2) + 16 lg + 8 (c % 2) + 0..7 of step c
+    f16x8 q[NT][NC];
+    float qs;
+    {
+        const T* p = (const T*)a.Q + token * a.ldq + (int64_t)qh * D;
+        float x[NC][8];
+        float m = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            load8(p + 64 * (c / 2) + 16 * lg + 8 * (c % 2), x[c]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(x[c][k]));
+        }
+        m = fmaxf(m, __shfl_xor(m, 16, 64));
+        m = fmaxf(m, __shfl_xor(m, 32, 64));
+        const int ex = (int)(__float_as_uint(m) >> 23);
+        const int field = std::min(257 - ex, 253);
+        const float up = __uint_as_float((uint32_t)field << 23);
+        qs = a.scale2 * __uint_as_float((uint32_t)(254 - field) << 23);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float y = x[c][k] * up;
+                q[0][c][k] = (_Float16)y;
+                if constexpr (NT == 2) q[1][c][k] = (_Float16)(y - (float)q[0][c][k]);
+            }
+    }
+
+    f32x4 acc[D / 16];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, l = tl.over ? __builtin_nanf("") : 0.f, R = 0.f;
+
+    const int32_t* table = a.table + (int64_t)tl.b * a.width;
+    const int64_t pool = (int64_t)a.bs * D;       // codes of one (block, head)
+    auto block_of = [&](int64_t pos) -> int {
+        if (pos >= tl.hi) return -1;
+        const int id = table[pos >> a.bs_log2];
+        return (id >= 0 && id < a.num_blocks) ? id : -1;
+    };
+    for (int it = s0 + wave; it < s1; it += NW) {
+        const int64_t base = (int64_t)it * TK;
+        const int64_t tk = base + 16 * (li >> 2), tv = base + 16 * lg;   // this lane's tokens: rows of K, columns of V
+        const int bk = block_of(tk), bv = block_of(tv);
+        uint4 kc[4][D / 64], vc[D / 16];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) kc[t][c] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) vc[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (bk >= 0) {
+            const int8_t* p = a.k + ((int64_t)bk * a.kv_heads + h) * pool + ((tk & (a.bs - 1)) + (li & 3)) * D + 16 * lg;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) kc[t][c] = *(const uint4*)(p + 4 * t * D + 64 * c);
+        }
+        float sk = tv < tl.hi ? __builtin_nanf("") : 0.f, sv = sk;
+        if (bv >= 0) {
+            const int64_t at = (int64_t)bv * a.kv_heads + h;
+            const int8_t* p = a.v + at * pool + li * a.bs + (tv & (a.bs - 1));
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) vc[i] = *(const uint4*)(p + 16 * i * a.bs);
+            sk = a.ks[at];
+            sv = a.vs[at];
+        }
+        // scores
+        f32x4 s[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                const f16x8 k0 = half8(kc[t][c].x, kc[t][c].y), k1 = half8(kc[t][c].z, kc[t][c].w);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, q[n][2 * c], s[t], 0, 0, 0);
+                    s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, q[n][2 * c + 1], s[t], 0, 0, 0);
+                }
+            }
+        }
+        const float ck = sk * qs;
+        const bool whole = base >= tl.lo_max && base + TK <= tl.hi_min;   // no row masks anything here
+        float top = -INFINITY;
+        const int r_lo = (int)(std::max<int64_t>(my_lo - tv, 0)), r_hi = (int)(std::min<int64_t>(my_hi - tv, 16));
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float x = s[t][i] * ck;
+                if (!whole && (4 * t + i < r_lo || 4 * t + i >= r_hi)) x = -INFINITY;
+                s[t][i] = x;
+                top = fmaxf(top, x);
+            }
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const float m_new = fmaxf(m, top);
+        const float m_sub = (m_new == -INFINITY ? 0.f : m_new) - PSHIFT;
+        float fall = m_new == m ? 1.f : exp2_fast(m - m_new);
+        l *= fall;
+        m = m_new;
+        // R: largest finite S_v so far, the same for every lane
+        float big = sv < INFINITY ? sv : 0.f;
+        big = fmaxf(big, __shfl_xor(big, 16, 64));
+        big = fmaxf(big, __shfl_xor(big, 32, 64));
+        if (big > R) {
+            fall *= __fdiv_rn(R, big);
+            R = big;
+        }
+        const float rv = R < FLT_MIN ? (sv == 0.f || sv < FLT_MIN ? 0.f : sv) : __fdiv_rn(sv, R);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][r] *= fall;
+        f16x8 w[NT][2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float p = exp2_fast(s[t][i] - m_sub);
+                l += p;
+                float y = p * rv;
+                if (!whole && (4 * t + i < r_lo || 4 * t + i >= r_hi)) y = 0.f;   // S_v of a block that is not this row's may be NaN
+                w[0][t >> 1][4 * (t & 1) + i] = (_Float16)y;
+                if constexpr (NT == 2)
+                    w[1][t >> 1][4 * (t & 1) + i] = (_Float16)(y - (float)w[0][t >> 1][4 * (t & 1) + i]);
+            }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            const f16x8 v0 = half8(vc[i].x, vc[i].y), v1 = half8(vc[i].z, vc[i].w);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, w[n][0], acc[i], 0, 0, 0);
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, w[n][1], acc[i], 0, 0, 0);
+            }
+        }
+    }
+
+    // join the waves: factors to the common maximum, then sums through LDS
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    __shared__ float sm[NW][TR], sl[NW][TR];
+    constexpr int DP = D < 128 ? D : 128;         // channels that go through LDS at a time
+    __shared__ __attribute__((aligned(16))) float so[NW][TR][DP + 4];
+    if (lg == 0) {
+        sm[wave][li] = m;
+        sl[wave][li] = l;
+    }
+    __syncthreads();
+    float M = sm[0][li];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) M = fmaxf(M, sm[w][li]);
+    const float M0 = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) L += sl[w][li] * exp2_fast(sm[w][li] - M0);
+    const float mine = (R > 0.f ? R : 1.f) * exp2_fast(m - M0) / (L == 0.f ? 1.f : L);
+    const bool split_out = a.nsplit > 1;
+    const int64_t nflat = a.g.rows * a.heads;
+#pragma unroll
+    for (int d0 = 0; d0 < D; d0 += DP) {
+        if (d0) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i) {
+            const f32x4 x = acc[d0 / 16 + i];
+            *(f32x4*)&so[wave][li][16 * i + 4 * lg] = f32x4{x[0] * mine, x[1] * mine, x[2] * mine, x[3] * mine};
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < TR * (DP / 4); c += 64 * NW) {
+            const int r = c / (DP / 4), d = 4 * (c % (DP / 4)), fr = tl.f0 + r;
+            if (fr >= tl.rows) continue;
+            f32x4 o = *(const f32x4*)&so[0][r][d];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) o += *(const f32x4*)&so[w][r][d];
+            const int64_t row = tl.off + fr / a.group;
+            const int head = h * a.group + fr % a.group;
+            if (split_out)
+                *(f32x4*)(a.part + (split * nflat + row * a.heads + head) * D + d0 + d) = o;
+            else
+                store_row4((T*)a.O + row * a.ldo + (int64_t)head * D + d0 + d, o[0], o[1], o[2], o[3]);
+        }
+    }
+    if (wave == 0 && lg == 0 && tl.f0 + li < tl.rows && (split_out || a.lse)) {
+        // L carries 2^PSHIFT
+        const float lse2 = L == 0.f ? -INFINITY : M0 - PSHIFT + __log2f(L);
+        const int64_t at = token * a.heads + qh;
+        if (split_out)
+            a.part_lse[split * nflat + at] = lse2;
+        else
+            a.lse[at] = lse2 * 0.6931471805599453f;
+    }
+}
+
+// Join of the splits: one workgroup per (tile, kv head), 16 threads a row.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
+    const int64_t tile = blockIdx.x;
+    const int h = (int)(tile % a.kv_heads);
+    Tile tl;
+    if (!find_tile(a, tile / a.kv_heads, TR, tl)) return;
+    const int per = split_steps(tl, a.nsplit);
+    const int n = std::max(1, (tl.it1 - tl.it0 + per - 1) / per);    // split 0 is always written
+    const int r = threadIdx.x / 16, c = threadIdx.x % 16, f = tl.f0 + r;
+    if (f >= tl.rows) return;
+    const int64_t row = tl.off + f / a.group, nflat = a.g.rows * a.heads;
+    const int head = h * a.group + f % a.group;
+    const int64_t at = row * a.heads + head;
+    float M = -INFINITY;
+    for (int s = 0; s < n; ++s) M = fmaxf(M, a.part_lse[s * nflat + at]);
+    const float M0 = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    f32x4 o[D / 64];
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < n; ++s) {
+        const float w = exp2_fast(a.part_lse[s * nflat + at] - M0);
+        L += w;
+        const float* p = a.part + (s * nflat + at) * D;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) o[i] += w * *(const f32x4*)(p + 64 * i + 4 * c);
+    }
+    const float inv = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i)
+        store_row4((T*)a.O + row * a.ldo + (int64_t)head * D + 64 * i + 4 * c, o[i][0] * inv, o[i][1] * inv,
+                   o[i][2] * inv, o[i][3] * inv);
+    if (a.lse && c == 0) a.lse[at] = L == 0.f ? -INFINITY : (M0 + __log2f(L)) * 0.6931471805599453f;
+}
+
+int64_t tile_units(int64_t rows, int64_t batch, int group) { return rows * group / TR + batch; }
+
+// Splits of the keys of a tile: enough workgroups for 256 CUs, a step per wave
+// at least at the longest length the table can hold.
+int splits(int64_t rows, int64_t batch, int heads, int kv_heads, int block, int64_t width) {
+    const int64_t units = tile_units(rows, batch, heads / kv_heads) * kv_heads;
+    const int64_t most = cdiv(width * block, TK * NW);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(cdiv(2048, units), most), 64));
+}
+
+template <typename T, int D>
+int launch(const AttnArgs& a, hipStream_t st) {
+    const int64_t units = tile_units(a.g.rows, a.g.batch, a.group) * a.kv_heads;
+    hipLaunchKernelGGL((attention_rows_kernel<T, D>), dim3((unsigned)(units * a.nsplit)), dim3(64 * NW), 0, st, a);
+    PTQ_LAUNCH_CHECK();
+    if (a.nsplit > 1) {
+        hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3((unsigned)units), dim3(256), 0, st, a);
+        PTQ_LAUNCH_CHECK();
+    }
+    return PTQ_OK;
+}
+
+template <typename T>
+int launch_dim(const AttnArgs& a, hipStream_t st) {
+    switch (a.dim) {
+        case 64: return launch<T, 64>(a, st);
+        case 128: return launch<T, 128>(a, st);
+        default: return launch<T, 256>(a, st);
+    }
+}
+
+}  // namespace
+
+size_t attention_int8_ws_bytes(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int block,
+                               int64_t width) {
+    const int n = splits(rows, batch, heads, kv_heads, block, width);
+    if (n == 1) return 0;
+    Sizer z;
+    z.take<float>((size_t)n * rows * heads * dim);
+    z.take<float>((size_t)n * rows * heads);
+    return z.bytes();
+}
+
+int run_attention_int8(const KVCacheInt8& c, const RaggedRows& r, int dtype, const void* Q, int64_t ldq, int heads,
+                       float scale, int causal, int64_t window, void* O, int64_t ldo, float* lse, void* ws,
+                       size_t ws_bytes, hipStream_t st) {
+    if (r.rows == 0 || r.batch == 0) return PTQ_OK;
+    AttnArgs a{};
+    a.g.offsets = r.offsets; a.g.batch = (int)r.batch; a.g.rows = r.rows;
+    a.lens = r.starts; a.table = r.table; a.width = r.width;
+    a.heads = heads; a.kv_heads = c.heads; a.group = heads / c.heads;
+    a.dim = c.dim; a.bs = c.block; a.bs_log2 = __builtin_ctz((unsigned)c.block); a.num_blocks = c.num_blocks;
+    a.k = c.k; a.v = c.v; a.ks = c.k_scales; a.vs = c.v_scales;
+    a.Q = Q; a.ldq = ldq; a.O = O; a.ldo = ldo; a.lse = lse;
+    a.scale2 = (float)(scale * 1.4426950408889634);
+    a.causal = causal; a.window = window;
+    a.nsplit = splits(r.rows, r.batch, heads, c.heads, c.block, r.width);
+    if (a.nsplit > 1) {
+        Arena ar(ws, ws_bytes);
+        a.part = ar.take<float>((size_t)a.nsplit * r.rows * heads * c.dim);
+        a.part_lse = ar.take<float>((size_t)a.nsplit * r.rows * heads);
+    }
+    return dtype == PTQ_F32 ? launch_dim<float>(a, st) : launch_dim<uint16_t>(a, st);
+}
+
+}  // namespace ptq

@@ -208,4 +208,39 @@ int run_awq(const void* W, int w_dtype, int64_t out, int64_t n, int64_t ldw, con
             int g, float* alpha_best, double* err_per_alpha, float* s, int8_t* codes,
             float* scales, void* ws, size_t ws_bytes, hipStream_t st);
 
+// Int8 linear layers (linear_int8.hip)
+int launch_quantize_tokens_int8(const void* X, int x_dtype, int64_t rows, int64_t in, int64_t ldx, const float* s,
+                                int8_t* codes, int64_t ldc, int64_t pad, float* scales, hipStream_t st);
+size_t matmul_int8_ws_bytes(int64_t rows, int64_t out, int64_t in);
+int run_matmul_int8(const int8_t* A, int64_t lda, const float* a_scales, int64_t rows, const int8_t* B, int64_t ldb,
+                    const float* b_scales, int64_t out, int64_t in, const float* bias, int y_dtype, void* Y,
+                    int64_t ldy, void* ws, size_t ws_bytes, hipStream_t st);
+size_t linear_int8_ws_bytes(int64_t rows, int64_t out, int64_t in);
+int run_linear_int8(const void* X, int x_dtype, int64_t rows, int64_t ldx, const float* s, const int8_t* codes,
+                    int64_t ldb, const float* scales, int64_t out, int64_t in, const float* bias, int y_dtype, void* Y,
+                    int64_t ldy, void* ws, size_t ws_bytes, hipStream_t st);
+
+// Int8 key/value cache (kv_cache.hip) and attention over it (attention_int8.hip)
+struct KVCacheInt8 {
+    int8_t* k; int8_t* v; float* k_scales; float* v_scales;
+    int64_t num_blocks;
+    int heads, dim, block;
+};
+// Rows of a ragged batch and where they are in their sequences: starts[b] is
+// the position of the first row (write, read) or the number of keys (attention).
+struct RaggedRows {
+    int64_t rows, batch;
+    const int32_t* offsets; const int32_t* starts;
+    const int32_t* table; int64_t width;
+};
+int launch_kv_write(const KVCacheInt8& c, const RaggedRows& r, int dtype, const void* K, int64_t ldk, const void* V,
+                    int64_t ldv, hipStream_t st);
+int launch_kv_read(const KVCacheInt8& c, const RaggedRows& r, int dtype, void* K, int64_t ldk, void* V, int64_t ldv,
+                   hipStream_t st);
+size_t attention_int8_ws_bytes(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int block,
+                               int64_t width);
+int run_attention_int8(const KVCacheInt8& c, const RaggedRows& r, int dtype, const void* Q, int64_t ldq, int heads,
+                       float scale, int causal, int64_t window, void* O, int64_t ldo, float* lse, void* ws,
+                       size_t ws_bytes, hipStream_t st);
+
 }  // namespace ptq

@@ -1,0 +1,99 @@
+// Shared device code of the int8 serving operators (linear_int8.hip,
+// kv_cache.hip, attention_int8.hip): the quantization rule, and ragged
+// batches.
+#pragma once
+
+#include "common.hpp"
+
+#include <float.h>
+
+namespace ptq {
+
+// ------------------------------------------------------ quantization rule --
+// One scale S for a set of values with largest magnitude a: S = a / 127, code
+// = rint(x / S) in [-127, 127]. S below FLT_MIN is stored as 0 (all codes 0):
+// 1 / S is then always finite. A NaN or an infinity among the values makes S
+// NaN, so what was stored with it reads as NaN instead of as a finite wrong
+// value. The division by S is a product with 1 / S (one division per set, not
+// one per value): it differs from the quotient by two roundings, 5e-6 of a
+// code step at code 40.
+// `amax` carries a NaN through (amax_acc).
+__device__ __forceinline__ float int8_scale(float amax) {
+    const float s = __fdiv_rn(amax, 127.0f);
+    if (!(s <= FLT_MAX)) return __builtin_nanf("");
+    return s < FLT_MIN ? 0.0f : s;
+}
+__device__ __forceinline__ float int8_inverse(float s) { return s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f; }
+// in [-127, 127] for every x (the code of a value whose set has S = NaN means nothing)
+__device__ __forceinline__ int int8_code(float x, float inv) {
+    return (int)rintf(fminf(fmaxf(x * inv, -127.0f), 127.0f));
+}
+// max(|x|, a) that keeps a NaN of either
+__device__ __forceinline__ float amax_acc(float a, float x) {
+    const float m = fabsf(x);
+    return (m > a || m != m) ? m : a;
+}
+
+// 8 consecutive elements of a row as floats
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+    const float4 a = *(const float4*)p, b = *(const float4*)(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
+    const uint4 a = *(const uint4*)p;
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        v[2 * k] = __uint_as_float(w[k] << 16);
+        v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+}
+
+// float -> output element; bf16 rounds to nearest even and keeps NaN a NaN
+__device__ __forceinline__ uint32_t bf16_of(float f) {
+    return f != f ? 0x7fc0u : (uint32_t)float_to_bf16_bits(f);
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) { return bf16_of(lo) | (bf16_of(hi) << 16); }
+
+// ----------------------------------------------------------- ragged batch --
+// Sequence b of a ragged batch owns rows offsets[b] .. offsets[b + 1]. A grid
+// that cannot know the offsets on the host numbers its work units so that
+// sequence b has first(b) = floor(offsets[b] mul / div) + extra b .. first(b + 1):
+// at least as many units as it needs, the spare ones exit. The wave that
+// looks unit w up reads 64 values of first() at a time.
+// Offsets are clamped to [0, rows], so a wrong one cannot lead outside the
+// caller's tensors.
+struct Ragged {
+    const int32_t* offsets;
+    int batch;
+    int64_t rows;
+};
+
+__device__ __forceinline__ int64_t ragged_offset(const Ragged& g, int b) {
+    const int64_t o = g.offsets[b];
+    return o < 0 ? 0 : (o > g.rows ? g.rows : o);
+}
+
+__device__ __forceinline__ int64_t ragged_first(const Ragged& g, int b, int mul, int div, int extra) {
+    return ragged_offset(g, b) * mul / div + (int64_t)extra * b;
+}
+
+// The sequence of unit w (the last b with first(b) <= w), and w - first(b) in *local.
+__device__ __forceinline__ int ragged_find(const Ragged& g, int64_t w, int mul, int div, int extra, int64_t* local) {
+    const int lane = threadIdx.x & 63;
+    int b = 0;
+    for (int b0 = 0; b0 < g.batch; b0 += 64) {
+        const int i = b0 + lane;
+        const bool le = i < g.batch && ragged_first(g, i, mul, div, extra) <= w;
+        const uint64_t vote = __ballot(le);
+        if (!vote) break;
+        b = b0 + 63 - __builtin_clzll(vote);
+        if (b != b0 + 63) break;
+    }
+    b = __builtin_amdgcn_readfirstlane(b);
+    *local = w - ragged_first(g, b, mul, div, extra);
+    return b;
+}
+
+}  // namespace ptq
