@@ -352,7 +352,7 @@ int layer_output_error(const void* X, int x_dtype, int64_t rows, int64_t ldx,
  * linear_int8: both in one call, Y = quantized(X diag(s)^-1) codes^T + bias.
  *
  * in: a multiple of 8 in [8, 131064]. Rows of int8 operands may have any row
- * stride that is a multiple of 8. Asynchronous.
+ * stride that is a multiple of 8 up to 2^22. Asynchronous.
  * Errors: EINVAL, EWORKSPACE, EHIP.
  * ---------------------------------------------------------------------- */
 int quantize_tokens_int8(const void* X, int x_dtype, int64_t rows, int64_t in, int64_t ldx, const float* s,

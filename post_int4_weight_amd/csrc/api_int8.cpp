@@ -20,6 +20,7 @@ int64_t elems16(int dtype) { return dtype == PTQ_BF16 ? 8 : 4; }
 
 // int32 sums of `in` products of int8 (at most 2^14 each)
 constexpr int64_t MAX_IN = ((int64_t)1 << 17) - 8;
+constexpr int64_t MAX_LD = (int64_t)1 << 22;      // 256 rows of codes within 32-bit offsets
 constexpr int64_t MAX_ROWS = ((int64_t)1 << 31) - 1;
 
 int check_sizes(const char* fn, int64_t rows, int64_t in) {
@@ -43,7 +44,9 @@ int check_float_rows(const char* fn, const char* name, const void* X, int dtype,
 int check_codes(const char* fn, const char* name, const void* p, int64_t in, int64_t ld) {
     if (!p) REFUSE("%s: %s is NULL", fn, name);
     if (!aligned16(p)) REFUSE("%s: %s is not 16-byte aligned", fn, name);
-    if (ld < in || ld % 8) REFUSE("%s: row stride %lld of %s: a multiple of 8, at least %lld", fn, (long long)ld, name, (long long)in);
+    if (ld < in || ld % 8 || ld > MAX_LD)
+        REFUSE("%s: row stride %lld of %s: a multiple of 8 in [%lld, %lld]", fn, (long long)ld, name, (long long)in,
+               (long long)MAX_LD);
     return PTQ_OK;
 }
 

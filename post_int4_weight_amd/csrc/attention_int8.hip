@@ -122,6 +122,37 @@ __device__ __forceinline__ void store_row4<uint16_t>(uint16_t* p, float a, float
     *(uint2*)p = make_uint2(bf16_pair(a, b), bf16_pair(c, d));
 }
 
+// One query row in fp16 terms: scaled by the power of two that brings its
+// largest element to [8, 16), negated for a negative softmax scale (scores
+// then grow with what the sums give). `at(c)`: first channel of fragment c.
+// The row is shared by the lanes that differ in the bits from GROUP up.
+// Returns the factor of the scores, in units of log2.
+template <typename T, int NC, int GROUP, int NT, typename F>
+__device__ __forceinline__ float load_query(const T* p, float scale2, f16x8 (&q)[NT][NC], F&& at) {
+    float x[NC][8];
+    float m = 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        load8(p + at(c), x[c]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(x[c][k]));
+    }
+#pragma unroll
+    for (int o = GROUP; o < 64; o *= 2) m = fmaxf(m, __shfl_xor(m, o, 64));
+    const int field = std::min(257 - (int)(__float_as_uint(m) >> 23), 253);
+    const float up = __uint_as_float((uint32_t)field << 23);
+    const float sign = scale2 < 0.f ? -up : up;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float y = x[c][k] * sign;
+            q[0][c][k] = (_Float16)y;
+            if constexpr (NT == 2) q[1][c][k] = (_Float16)(y - (float)q[0][c][k]);
+        }
+    return fabsf(scale2) * __uint_as_float((uint32_t)(254 - field) << 23);
+}
+
 // Few query rows, long caches: the scores are computed transposed,
 // S^T = K Q^T (tokens x rows), so a lane ends up with 16 scores of one query
 // row, and the probabilities are already the operand of O^T = V^T P^T: nothing
@@ -153,32 +184,8 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
 
     // q: operand column li, channels 64 (c / 2) + 16 lg + 8 (c % 2) + 0..7 of step c
     f16x8 q[NT][NC];
-    float qs;
-    {
-        const T* p = (const T*)a.Q + token * a.ldq + (int64_t)qh * D;
-        float x[NC][8];
-        float m = 0.f;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            load8(p + 64 * (c / 2) + 16 * lg + 8 * (c % 2), x[c]);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(x[c][k]));
-        }
-        m = fmaxf(m, __shfl_xor(m, 16, 64));
-        m = fmaxf(m, __shfl_xor(m, 32, 64));
-        const int ex = (int)(__float_as_uint(m) >> 23);
-        const int field = std::min(257 - ex, 253);
-        const float up = __uint_as_float((uint32_t)field << 23);
-        qs = a.scale2 * __uint_as_float((uint32_t)(254 - field) << 23);
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float y = x[c][k] * up;
-                q[0][c][k] = (_Float16)y;
-                if constexpr (NT == 2) q[1][c][k] = (_Float16)(y - (float)q[0][c][k]);
-            }
-    }
+    const float qs = load_query<T, NC, 16>((const T*)a.Q + token * a.ldq + (int64_t)qh * D, a.scale2, q,
+                                           [&](int c) { return 64 * (c / 2) + 16 * lg + 8 * (c % 2); });
 
     f32x4 acc[D / 16];
 #pragma unroll
@@ -346,16 +353,290 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
     }
 }
 
-// Join of the splits: one workgroup per (tile, kv head), 16 threads a row.
-template <typename T, int D>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
-    const int64_t tile = blockIdx.x;
+// Many query rows: 32 rows a wave, WAVES waves on the same keys. K and V go
+// through LDS once per workgroup, converted to fp16 on the way (a wave that
+// converted its own operands would spend more on that than on the products),
+// two buffers of TK tokens. S^T = K Q^T and O^T = V^T P^T as above, on 32x32x16
+// products: operand row r of a 32-token block is token 16 (r / 4 % 2) +
+// 4 (r / 8) + r % 4, so lane half hf holds tokens 16 hf .. 16 hf + 15, again in
+// one block of the cache: one S_k and one S_v per lane and score block, which
+// go into the exponent, w = 2^(s ck - m + log2 rv), and the sum of p takes
+// 1 / rv once per 16 values.
+// m follows the row maximum only when that exceeds it by 2^LAZY (fp16 has the
+// room): most steps then leave the output accumulators alone.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+constexpr float LAZY = 6.f;
+constexpr int LOG2_RV_MIN = -60;   // below it the block adds nothing to the output (w underflows), only to the sum
+
+template <int D>
+struct TileLds {
+    static constexpr int KROW = 2 * D, VROW = 2 * TK;       // bytes of a token of K, of a channel of V
+    static constexpr int K_BYTES = TK * KROW, V_BYTES = D * VROW, BUF = K_BYTES + V_BYTES;
+    static constexpr int BYTES = 2 * BUF;
+    // 16-byte slots, placed so that the 16 rows read together touch every bank
+    __device__ static __forceinline__ int k_at(int token, int chunk) {
+        const int f = D == 64 ? ((token >> 1) & 3) | ((token >> 2) & 4) : (token & 7) | ((token >> 1) & 8);
+        return token * KROW + 16 * (chunk ^ f);
+    }
+    __device__ static __forceinline__ int v_at(int d, int chunk) { return K_BYTES + d * VROW + 16 * (chunk ^ ((d >> 1) & 7)); }
+};
+
+template <typename T, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) {
+    constexpr int NT = sizeof(T) == 4 ? 2 : 1;
+    constexpr int NTH = 64 * WAVES, NC = D / 16, ND = D / 32;
+    constexpr int NCH = TK * D / 16;               // 16-byte chunks of K, and of V, in a step
+    constexpr int NL = 2 * NCH / NTH;              // loads per thread
+    static_assert(NL * NTH == 2 * NCH && NCH % 64 == 0, "staging loads");
+    using L = TileLds<D>;
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    __shared__ __attribute__((aligned(16))) float ssk[2][4], ssv[2][4];
+
+    const int split = (int)(blockIdx.x % (unsigned)a.nsplit);
+    const int64_t tile = blockIdx.x / (unsigned)a.nsplit;
     const int h = (int)(tile % a.kv_heads);
     Tile tl;
-    if (!find_tile(a, tile / a.kv_heads, TR, tl)) return;
+    // later tiles of a sequence have more keys: they go first
+    if (!find_tile(a, gridDim.x / (unsigned)a.nsplit / a.kv_heads - 1 - tile / a.kv_heads, 32 * WAVES, tl)) return;
+    const int per = split_steps(tl, a.nsplit);
+    const int s0 = tl.it0 + split * per, s1 = std::min(s0 + per, tl.it1);
+    if (split > 0 && s0 >= s1) return;
+
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int li = lane & 31, hf = lane >> 5;
+    const bool idle = tl.f0 + 32 * wave >= tl.rows;     // no row of this wave: it only helps staging
+    const int f = std::min(tl.f0 + 32 * wave + li, tl.rows - 1);
+    const int64_t token = tl.off + f / a.group;
+    const int qh = h * a.group + f % a.group;
+    const int64_t pos = tl.pos0 + f / a.group;
+    const int64_t my_lo = row_lo(a, pos), my_hi = row_hi(a, pos, tl.len);
+    // keys of the wave's rows: steps within [w_lo, w_hi) need no mask, those outside [w_min, w_max) nothing at all
+    const int fa = std::min(tl.f0 + 32 * wave, tl.rows - 1), fb = std::min(tl.f0 + 32 * wave + 31, tl.rows - 1);
+    const int64_t pa = tl.pos0 + fa / a.group, pb = tl.pos0 + fb / a.group;
+    const int64_t w_min = row_lo(a, pa), w_lo = row_lo(a, pb), w_hi = row_hi(a, pa, tl.len), w_max = row_hi(a, pb, tl.len);
+
+    f16x8 q[NT][NC];
+    const float qs = load_query<T, NC, 32>((const T*)a.Q + token * a.ldq + (int64_t)qh * D, a.scale2, q,
+                                           [&](int c) { return 16 * c + 8 * hf; });
+
+    f32x16 acc[ND];
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
+    float m = -INFINITY, l = tl.over ? __builtin_nanf("") : 0.f, R = 0.f, rcp_R = 0.f;
+
+    // staging: thread t moves chunks t + NTH i, first those of K (token, 16 channels), then those of V (channel, 16 tokens)
+    const int32_t* table = a.table + (int64_t)tl.b * a.width;
+    const int64_t pool = (int64_t)a.bs * D;
+    uint4 raw[NL];
+    float sk_r = 0.f, sv_r = 0.f;
+    auto block_of = [&](int64_t p) -> int {
+        if (p >= tl.hi) return -1;
+        const int id = table[p >> a.bs_log2];
+        return (id >= 0 && id < a.num_blocks) ? id : -1;
+    };
+    auto fetch = [&](int it) {
+        const int64_t base = (int64_t)it * TK;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int c = t + NTH * i, cv = c - NCH;
+            const bool isk = c < NCH;              // the same for a whole wave
+            const int tk = c / (D / 16);
+            const int64_t p = base + (isk ? tk & ~15 : 16 * (cv % 4));
+            const int b = block_of(p), slot = (int)(p & (a.bs - 1));
+            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (b >= 0) {
+                const int64_t at = ((int64_t)b * a.kv_heads + h) * pool;
+                raw[i] = *(const uint4*)(isk ? a.k + at + (slot + (tk & 15)) * D + 16 * (c % (D / 16))
+                                             : a.v + at + (cv / 4) * a.bs + slot);
+            }
+        }
+        if (t < 4) {
+            const int64_t p = base + 16 * t;
+            const int b = block_of(p);
+            sk_r = sv_r = p < tl.hi ? __builtin_nanf("") : 0.f;
+            if (b >= 0) {
+                sk_r = a.ks[(int64_t)b * a.kv_heads + h];
+                sv_r = a.vs[(int64_t)b * a.kv_heads + h];
+            }
+        }
+    };
+    auto stage = [&](int buf) {
+        unsigned char* S = smem + buf * L::BUF;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int c = t + NTH * i, cv = c - NCH;
+            const bool isk = c < NCH;
+            const int row = isk ? c / (D / 16) : cv / 4, at = 2 * (isk ? c % (D / 16) : cv % 4);
+            *(f16x8*)(S + (isk ? L::k_at(row, at) : L::v_at(row, at))) = half8(raw[i].x, raw[i].y);
+            *(f16x8*)(S + (isk ? L::k_at(row, at + 1) : L::v_at(row, at + 1))) = half8(raw[i].z, raw[i].w);
+        }
+        if (t < 4) {
+            ssk[buf][t] = sk_r;
+            ssv[buf][t] = sv_r;
+        }
+    };
+
+    const int krow = 16 * ((li >> 2) & 1) + 4 * (li >> 3) + (li & 3);   // token of operand row li
+    auto step = [&](int it, int buf) {
+        const int64_t base = (int64_t)it * TK;
+        if (base >= w_max || base + TK <= w_min) return;
+        const unsigned char* S = smem + buf * L::BUF;
+        const bool whole = base >= w_lo && base + TK <= w_hi;
+        f32x16 s[2];
+        float ck[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[u][r] = 0.f;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const f16x8 k = *(const f16x8*)(S + L::k_at(32 * u + krow, 2 * c + hf));
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[n][c], s[u], 0, 0, 0);
+            }
+            ck[u] = ssk[buf][2 * u + hf] * qs;
+        }
+        if (!whole) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int64_t g = base + 32 * u + 16 * hf;
+                const int lo = (int)std::max<int64_t>(my_lo - g, 0), hi = (int)std::min<int64_t>(my_hi - g, 16);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[u][r] = (r >= lo && r < hi) ? s[u][r] * ck[u] : -INFINITY;
+                ck[u] = 1.f;
+            }
+        }
+        float top[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            top[u] = s[u][0];
+#pragma unroll
+            for (int r = 1; r < 16; ++r) top[u] = fmaxf(top[u], s[u][r]);
+            top[u] *= ck[u];
+        }
+        float mx = fmaxf(top[0], top[1]);
+        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+        if (__any(mx > m + LAZY)) {
+            const float m_new = fmaxf(m, mx);
+            const float fall = m_new == m ? 1.f : exp2_fast(m - m_new);
+            m = m_new;
+            l *= fall;
+#pragma unroll
+            for (int i = 0; i < ND; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][r] *= fall;
+        }
+        const float m_sub = (m == -INFINITY ? 0.f : m) - PSHIFT;
+        float big = 0.f;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) big = fmaxf(big, ssv[buf][g] < INFINITY ? ssv[buf][g] : 0.f);
+        if (big > R) {     // the same for every lane
+            const float fall = big < FLT_MIN ? 0.f : R * __fdiv_rn(1.f, big);
+            R = big;
+            rcp_R = big < FLT_MIN ? 0.f : __fdiv_rn(1.f, big);
+#pragma unroll
+            for (int i = 0; i < ND; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][r] *= fall;
+        }
+        f16x8 w[NT][2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float rv = ssv[buf][2 * u + hf] * rcp_R;
+            const float lr = rv != rv ? rv : fmaxf(__builtin_amdgcn_logf(rv), (float)LOG2_RV_MIN);   // v_log_f32: base 2
+            const float off = m_sub - lr;
+            float sum = 0.f;
+            const int64_t g = base + 32 * u + 16 * hf;
+            const int lo = (int)std::max<int64_t>(my_lo - g, 0), hi = (int)std::min<int64_t>(my_hi - g, 16);
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) {
+                f32x2 e;
+                e[0] = exp2_fast(fmaf(s[u][r], ck[u], -off));
+                e[1] = exp2_fast(fmaf(s[u][r + 1], ck[u], -off));
+                if (!whole) {     // S_v of a block that is not this row's may be NaN
+                    if (r < lo || r >= hi) e[0] = 0.f;
+                    if (r + 1 < lo || r + 1 >= hi) e[1] = 0.f;
+                }
+                sum += e[0];
+                sum += e[1];
+                const f16x2 x = __builtin_convertvector(e, f16x2);
+                w[0][u][r >> 3][r & 7] = x[0];
+                w[0][u][r >> 3][(r & 7) + 1] = x[1];
+                if constexpr (NT == 2) {
+                    const f32x2 rest = {e[0] - (float)x[0], e[1] - (float)x[1]};
+                    const f16x2 y = __builtin_convertvector(rest, f16x2);
+                    w[1][u][r >> 3][r & 7] = y[0];
+                    w[1][u][r >> 3][(r & 7) + 1] = y[1];
+                }
+            }
+            l += whole || hi > lo ? sum * exp2_fast(-lr) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const f16x8 v = *(const f16x8*)(S + L::v_at(32 * i + li, 4 * u + 2 * hf + k));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[n][u][k], acc[i], 0, 0, 0);
+                }
+    };
+
+    if (s0 < s1) {
+        fetch(s0);
+        stage(0);
+        __syncthreads();
+        for (int it = s0; it < s1; ++it) {
+            const int buf = (it - s0) & 1;
+            if (it + 1 < s1) fetch(it + 1);
+            if (!idle) step(it, buf);
+            if (it + 1 < s1) stage(buf ^ 1);
+            __syncthreads();
+        }
+    }
+    if (idle) return;
+
+    l += __shfl_xor(l, 32, 64);
+    if (tl.f0 + 32 * wave + li >= tl.rows) return;
+    const float mine = (R > 0.f ? R : 1.f) / (l == 0.f ? 1.f : l);
+    const bool split_out = a.nsplit > 1;
+    const int64_t nflat = a.g.rows * a.heads, at = token * a.heads + qh;
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int d = 32 * i + 8 * b + 4 * hf;
+            const f32x4 o = {acc[i][4 * b] * mine, acc[i][4 * b + 1] * mine, acc[i][4 * b + 2] * mine,
+                             acc[i][4 * b + 3] * mine};
+            if (split_out)
+                *(f32x4*)(a.part + (split * nflat + at) * D + d) = o;
+            else
+                store_row4((T*)a.O + token * a.ldo + (int64_t)qh * D + d, o[0], o[1], o[2], o[3]);
+        }
+    if (hf == 0 && (split_out || a.lse)) {
+        const float lse2 = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) - PSHIFT + __log2f(l);
+        if (split_out)
+            a.part_lse[split * nflat + at] = lse2;
+        else
+            a.lse[at] = lse2 * 0.6931471805599453f;
+    }
+}
+
+// Join of the splits: 16 rows a workgroup, 16 threads a row; tr: rows of the
+// tiles that were split.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int tr) {
+    const int64_t part = blockIdx.x % (unsigned)(tr / TR), tile = blockIdx.x / (unsigned)(tr / TR);
+    const int h = (int)(tile % a.kv_heads);
+    Tile tl;
+    if (!find_tile(a, tile / a.kv_heads, tr, tl)) return;
     const int per = split_steps(tl, a.nsplit);
     const int n = std::max(1, (tl.it1 - tl.it0 + per - 1) / per);    // split 0 is always written
-    const int r = threadIdx.x / 16, c = threadIdx.x % 16, f = tl.f0 + r;
+    const int r = threadIdx.x / 16, c = threadIdx.x % 16, f = tl.f0 + (int)part * TR + r;
     if (f >= tl.rows) return;
     const int64_t row = tl.off + f / a.group, nflat = a.g.rows * a.heads;
     const int head = h * a.group + f % a.group;
@@ -382,34 +663,58 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     if (a.lse && c == 0) a.lse[at] = L == 0.f ? -INFINITY : (M0 + __log2f(L)) * 0.6931471805599453f;
 }
 
-int64_t tile_units(int64_t rows, int64_t batch, int group) { return rows * group / TR + batch; }
+int64_t tile_units(int64_t rows, int64_t batch, int group, int tr) { return rows * group / tr + batch; }
 
-// Splits of the keys of a tile: enough workgroups for 256 CUs, a step per wave
-// at least at the longest length the table can hold.
-int splits(int64_t rows, int64_t batch, int heads, int kv_heads, int block, int64_t width) {
-    const int64_t units = tile_units(rows, batch, heads / kv_heads) * kv_heads;
+// Waves of a tile: two per SIMD, or one at 256 channels (whose output and query
+// fragments take more than the 256 registers a second wave would leave).
+constexpr int tile_waves(int dim) { return dim == 256 ? 4 : 8; }
+
+// Which kernel, and how many splits of the keys.
+struct Plan {
+    int tr;        // rows of a tile: TR, or 32 tile_waves
+    int nsplit;
+};
+Plan plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int block, int64_t width) {
+    Plan p;
+    const int group = heads / kv_heads;
+    p.tr = rows * group >= 64 * batch ? 32 * tile_waves(dim) : TR;
+    const int64_t units = tile_units(rows, batch, group, p.tr) * kv_heads;
     const int64_t most = cdiv(width * block, TK * NW);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(cdiv(2048, units), most), 64));
+    const int64_t want = p.tr == TR ? 2048 : 256;
+    p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(cdiv(want, units), most), 64));
+    return p;
 }
 
 template <typename T, int D>
-int launch(const AttnArgs& a, hipStream_t st) {
-    const int64_t units = tile_units(a.g.rows, a.g.batch, a.group) * a.kv_heads;
-    hipLaunchKernelGGL((attention_rows_kernel<T, D>), dim3((unsigned)(units * a.nsplit)), dim3(64 * NW), 0, st, a);
+int launch(const AttnArgs& a, int tr, hipStream_t st) {
+    const int64_t units = tile_units(a.g.rows, a.g.batch, a.group, tr) * a.kv_heads;
+    if (tr == TR) {
+        hipLaunchKernelGGL((attention_rows_kernel<T, D>), dim3((unsigned)(units * a.nsplit)), dim3(64 * NW), 0, st, a);
+    } else {
+        constexpr int TILE_WAVES = tile_waves(D);
+        static bool ready = false;    // more than 64 KB of LDS
+        if (!ready) {
+            PTQ_HIP(hipFuncSetAttribute((const void*)attention_tile_kernel<T, D, TILE_WAVES>,
+                                        hipFuncAttributeMaxDynamicSharedMemorySize, TileLds<D>::BYTES));
+            ready = true;
+        }
+        hipLaunchKernelGGL((attention_tile_kernel<T, D, TILE_WAVES>), dim3((unsigned)(units * a.nsplit)),
+                           dim3(64 * TILE_WAVES), TileLds<D>::BYTES, st, a);
+    }
     PTQ_LAUNCH_CHECK();
     if (a.nsplit > 1) {
-        hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3((unsigned)units), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3((unsigned)(units * (tr / TR))), dim3(256), 0, st, a, tr);
         PTQ_LAUNCH_CHECK();
     }
     return PTQ_OK;
 }
 
 template <typename T>
-int launch_dim(const AttnArgs& a, hipStream_t st) {
+int launch_dim(const AttnArgs& a, int tr, hipStream_t st) {
     switch (a.dim) {
-        case 64: return launch<T, 64>(a, st);
-        case 128: return launch<T, 128>(a, st);
-        default: return launch<T, 256>(a, st);
+        case 64: return launch<T, 64>(a, tr, st);
+        case 128: return launch<T, 128>(a, tr, st);
+        default: return launch<T, 256>(a, tr, st);
     }
 }
 
@@ -417,7 +722,7 @@ int launch_dim(const AttnArgs& a, hipStream_t st) {
 
 size_t attention_int8_ws_bytes(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int block,
                                int64_t width) {
-    const int n = splits(rows, batch, heads, kv_heads, block, width);
+    const int n = plan(rows, batch, heads, kv_heads, dim, block, width).nsplit;
     if (n == 1) return 0;
     Sizer z;
     z.take<float>((size_t)n * rows * heads * dim);
@@ -438,13 +743,14 @@ int run_attention_int8(const KVCacheInt8& c, const RaggedRows& r, int dtype, con
     a.Q = Q; a.ldq = ldq; a.O = O; a.ldo = ldo; a.lse = lse;
     a.scale2 = (float)(scale * 1.4426950408889634);
     a.causal = causal; a.window = window;
-    a.nsplit = splits(r.rows, r.batch, heads, c.heads, c.block, r.width);
+    const Plan p = plan(r.rows, r.batch, heads, c.heads, c.dim, c.block, r.width);
+    a.nsplit = p.nsplit;
     if (a.nsplit > 1) {
         Arena ar(ws, ws_bytes);
         a.part = ar.take<float>((size_t)a.nsplit * r.rows * heads * c.dim);
         a.part_lse = ar.take<float>((size_t)a.nsplit * r.rows * heads);
     }
-    return dtype == PTQ_F32 ? launch_dim<float>(a, st) : launch_dim<uint16_t>(a, st);
+    return dtype == PTQ_F32 ? launch_dim<float>(a, p.tr, st) : launch_dim<uint16_t>(a, p.tr, st);
 }
 
 }  // namespace ptq

@@ -9,6 +9,7 @@
 #include "int8.hpp"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace ptq {
 namespace {
@@ -125,14 +126,6 @@ __device__ __forceinline__ void store4(const Int8GemmArgs& g, int64_t o, int64_t
     }
 }
 
-// Tile of TB x TB (outputs x tokens), 4 waves of 2 x 2, KT codes per stage,
-// staged through registers with every access checked: any sizes, strides of
-// any multiple of 8. 16-byte chunks of a staged row are XOR-swizzled by
-// (row >> 1) & 7 (128-byte rows: 16 rows at one chunk then touch every bank).
-constexpr int TB = 128, KT = 128, CH = KT / 16;
-
-__device__ __forceinline__ int swz(int r, int c) { return r * KT + 16 * (c ^ ((r >> 1) & 7)); }
-
 // 16 codes at k of a row; 0 past `in` (a multiple of 8) and for rows that are not there
 __device__ __forceinline__ uint4 load_codes(const int8_t* P, int64_t ld, int64_t r, int64_t rows, int64_t k, int in) {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -150,60 +143,278 @@ __device__ __forceinline__ uint4 load_codes(const int8_t* P, int64_t ld, int64_t
     return v;
 }
 
-__global__ __launch_bounds__(256) void matmul_int8_kernel(Int8GemmArgs g) {
-    __shared__ __attribute__((aligned(16))) unsigned char smem[2 * TB * KT];
-    unsigned char* const sw = smem;
-    unsigned char* const sc = smem + TB * KT;
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int64_t tiles = cdiv(g.out, TB);
-    const int64_t o0 = (blockIdx.x % tiles) * TB, r0 = (blockIdx.x / tiles) * TB;
-    const int wo = (wave >> 1) * (TB / 2), wr = (wave & 1) * (TB / 2);
+// 16 codes at an address that is a multiple of 8 (one 16-byte load)
+struct __attribute__((aligned(8))) Codes16 {
+    uint32_t w[4];
+};
+__device__ __forceinline__ i32x4 load_codes16(const int8_t* p) {
+    const Codes16 c = *(const Codes16*)p;
+    return i32x4{(int)c.w[0], (int)c.w[1], (int)c.w[2], (int)c.w[3]};
+}
+
+constexpr int KT = 128;        // codes per row and stage
+constexpr int NXCD = 8;
+
+// ---- few tokens: the weights are read once, straight into operand registers.
+// A workgroup owns 16 NA outputs; its waves share the depth in runs of KT, one
+// after another, so that together they read whole stretches of each row. Up
+// to 16 TM tokens: each wave reads their codes (which stay in L2) next to the
+// weights. The int32 partial sums meet in LDS.
+template <int NA, int TM, int WAVES, int UN>
+__global__ __launch_bounds__(64 * WAVES) void matmul_int8_few_kernel(Int8GemmArgs g) {
+    __shared__ __attribute__((aligned(16))) i32x4 part[WAVES][NA * TM][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int li = lane & 15, lg = lane >> 4;
-    i32x4 acc[4][4];
+    const int64_t o0 = (int64_t)blockIdx.x * (16 * NA);
+    const int8_t* w[NA];
+    const int8_t* c[TM];
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int a = 0; a < NA; ++a) w[a] = g.W + std::min<int64_t>(o0 + 16 * a + li, g.out - 1) * g.ldw + 16 * lg;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) acc[a][b] = i32x4{0, 0, 0, 0};
-    constexpr int PER = TB * CH / 256;
-    uint4 vw[PER], vc[PER];
-    auto load = [&](int k0) {
+    for (int b = 0; b < TM; ++b) c[b] = g.C + std::min<int64_t>(16 * b + li, g.rows - 1) * g.ldc + 16 * lg;
+    i32x4 acc[NA][TM];
 #pragma unroll
-        for (int q = 0; q < PER; ++q) {
-            const int idx = t + 256 * q, r = idx / CH, c = idx % CH;
-            vw[q] = load_codes(g.W, g.ldw, o0 + r, g.out, k0 + 16 * c, g.in);
-            vc[q] = load_codes(g.C, g.ldc, r0 + r, g.rows, k0 + 16 * c, g.in);
+    for (int a = 0; a < NA; ++a)
+#pragma unroll
+        for (int b = 0; b < TM; ++b) acc[a][b] = i32x4{0, 0, 0, 0};
+    const int full = g.in / KT;               // whole runs
+    int s = wave;
+    for (; s + (UN - 1) * WAVES < full; s += UN * WAVES) {
+        i32x4 fw[UN][NA][2], fc[UN][TM][2];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const int64_t k = (int64_t)(s + u * WAVES) * KT;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int a = 0; a < NA; ++a) fw[u][a][e] = load_codes16(w[a] + k + 64 * e);
+#pragma unroll
+                for (int b = 0; b < TM; ++b) fc[u][b][e] = load_codes16(c[b] + k + 64 * e);
+            }
         }
-    };
-    load(0);
-    for (int k0 = 0; k0 < g.in; k0 += KT) {
-        __syncthreads();
 #pragma unroll
-        for (int q = 0; q < PER; ++q) {
-            const int idx = t + 256 * q, r = idx / CH, c = idx % CH;
-            *(uint4*)(sw + swz(r, c)) = vw[q];
-            *(uint4*)(sc + swz(r, c)) = vc[q];
-        }
-        __syncthreads();
-        if (k0 + KT < g.in) load(k0 + KT);
+        for (int u = 0; u < UN; ++u)
 #pragma unroll
-        for (int kk = 0; kk < KT / 64; ++kk) {
-            i32x4 fw[4], fc[4];
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                fw[a] = *(const i32x4*)(sw + swz(wo + 16 * a + li, 4 * kk + lg));
-                fc[a] = *(const i32x4*)(sc + swz(wr + 16 * a + li, 4 * kk + lg));
+                for (int a = 0; a < NA; ++a)
+#pragma unroll
+                    for (int b = 0; b < TM; ++b)
+                        acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][a][e], fc[u][b][e], acc[a][b], 0, 0, 0);
+    }
+    for (; s * KT < g.in; s += WAVES) {       // the last runs, the ragged one among them
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int64_t k = (int64_t)s * KT + 64 * e;
+            i32x4 fw[NA], fc[TM];
+#pragma unroll
+            for (int a = 0; a < NA; ++a) {
+                const uint4 x = load_codes(w[a] - 16 * lg, 0, 0, 1, k + 16 * lg, g.in);
+                fw[a] = i32x4{(int)x.x, (int)x.y, (int)x.z, (int)x.w};
             }
 #pragma unroll
-            for (int a = 0; a < 4; ++a)
+            for (int b = 0; b < TM; ++b) {
+                const uint4 x = load_codes(c[b] - 16 * lg, 0, 0, 1, k + 16 * lg, g.in);
+                fc[b] = i32x4{(int)x.x, (int)x.y, (int)x.z, (int)x.w};
+            }
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
+            for (int a = 0; a < NA; ++a)
+#pragma unroll
+                for (int b = 0; b < TM; ++b)
                     acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[a], fc[b], acc[a][b], 0, 0, 0);
         }
     }
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int a = 0; a < NA; ++a)
 #pragma unroll
-        for (int b = 0; b < 4; ++b) store4(g, o0 + wo + 16 * a + 4 * lg, r0 + wr + 16 * b + li, acc[a][b]);
+        for (int b = 0; b < TM; ++b) part[wave][a * TM + b][lane] = acc[a][b];
+    __syncthreads();
+    for (int q = wave; q < NA * TM; q += WAVES) {
+        const int a = q / TM, b = q % TM;
+        i32x4 sum = part[0][q][lane];
+#pragma unroll
+        for (int v = 1; v < WAVES; ++v) sum += part[v][q][lane];
+        store4(g, o0 + 16 * a + 4 * lg, 16 * b + li, sum);
+    }
+}
+
+// ---- many tokens: tiles of TO outputs x TT tokens, WO x WT waves, stages of
+// KT codes copied straight into LDS (16 bytes a lane, no registers), two
+// stages in flight. Staged rows are 128 bytes; the 16-byte chunk c of row r
+// sits in slot c ^ ((r >> 1) & 7), so the 16 rows that an operand fetch reads
+// at one chunk touch every bank; the copy puts it there by choosing which
+// chunk each lane fetches. Rows past the end repeat the last one (their
+// outputs are dropped). The ragged end of `in` goes through registers, checked.
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+__device__ __forceinline__ int slot(int r, int c) { return r * KT + 16 * (c ^ ((r >> 1) & 7)); }
+
+// f(integral_constant<int, I>) for I = B .. E - 1, in order
+template <int B, int E, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+    if constexpr (B < E) {
+        f(std::integral_constant<int, B>{});
+        static_for<B + 1, E>(f);
+    }
+}
+
+// 16 bytes a lane from resource r at voff + soff into LDS at base + 16 lane
+__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t r, unsigned char* base, unsigned voff, unsigned soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)base, 16, voff, soff, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_copies() {   // vmcnt <= N, lgkmcnt = 0
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+}
+
+// Tiles in the order they are taken: strips of 8 tiles of outputs, column by
+// column, and a contiguous share of that for each XCD (workgroup b runs on
+// XCD b % 8), whose L2 then serves about 8 x 4 tiles' operands at a time.
+__device__ __forceinline__ bool tile_of(unsigned b, int to, int tt, int& o, int& r) {
+    const int n = to * tt, per = (n + NXCD - 1) / NXCD;
+    const int i = (int)(b % NXCD) * per + (int)(b / NXCD);
+    if ((int)(b / NXCD) >= per || i >= n) return false;
+    const int strip = i / (8 * tt), left = std::min(8, to - 8 * strip), j = i - strip * 8 * tt;
+    o = 8 * strip + j % left;
+    r = j / left;
+    return true;
+}
+
+template <int TO, int TT, int WO, int WT>
+__global__ __launch_bounds__(64 * WO * WT, 1) void matmul_int8_tile_kernel(Int8GemmArgs g, int tiles_o, int tiles_t) {
+    constexpr int NW = WO * WT, WA = TO / WO / 16, WB = TT / WT / 16;
+    constexpr int PW = TO / 8 / NW, PC = TT / 8 / NW;      // copies of 8 rows per wave and stage
+    constexpr int STAGE = (TO + TT) * KT;
+    constexpr int NM = WA * WB, NR = WA + WB, NL = PW + PC;
+    static_assert(PW * 8 * NW == TO && PC * 8 * NW == TT && NM >= NR && NL <= NM, "tile shape");
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    int to, tt;
+    if (!tile_of(blockIdx.x, tiles_o, tiles_t, to, tt)) return;
+    const int64_t o0 = (int64_t)to * TO, r0 = (int64_t)tt * TT;
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int wo = (wave / WT) * (TO / WO), wt = (wave % WT) * (TT / WT);
+    const int li = lane & 15, lg = lane >> 4;
+
+    // byte offsets of this lane's copies from the tile's first row
+    __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc((void*)(g.W + o0 * g.ldw), (short)0, 0x7fffffff, 0x00020000);
+    __amdgpu_buffer_rsrc_t rc = __builtin_amdgcn_make_buffer_rsrc((void*)(g.C + r0 * g.ldc), (short)0, 0x7fffffff, 0x00020000);
+    unsigned vw[PW], vc[PC];
+#pragma unroll
+    for (int q = 0; q < PW; ++q) {
+        const int r = 8 * (wave * PW + q) + (lane >> 3);
+        vw[q] = (unsigned)(std::min<int64_t>(r, g.out - 1 - o0) * g.ldw + 16 * ((lane & 7) ^ ((r >> 1) & 7)));
+    }
+#pragma unroll
+    for (int q = 0; q < PC; ++q) {
+        const int r = 8 * (wave * PC + q) + (lane >> 3);
+        vc[q] = (unsigned)(std::min<int64_t>(r, g.rows - 1 - r0) * g.ldc + 16 * ((lane & 7) ^ ((r >> 1) & 7)));
+    }
+    auto copy_one = [&](int s, int buf, auto qc) {
+        constexpr int q = decltype(qc)::value;
+        unsigned char* base = smem + buf * STAGE;
+        if constexpr (q < PW) copy16(rw, base + (wave * PW + q) * 1024, vw[q], (unsigned)(s * KT));
+        else copy16(rc, base + TO * KT + (wave * PC + q - PW) * 1024, vc[q - PW], (unsigned)(s * KT));
+    };
+
+    i32x4 acc[WA][WB];
+#pragma unroll
+    for (int a = 0; a < WA; ++a)
+#pragma unroll
+        for (int b = 0; b < WB; ++b) acc[a][b] = i32x4{0, 0, 0, 0};
+    // Pipeline over the two 64-deep halves of a stage: the fragments of the
+    // next half are read while this half's products run. The barrier sits
+    // before a stage's second half, whose fragments are in registers by then:
+    // past it the next stage has landed for every wave, and this stage's
+    // buffer takes the copies of the stage after that.
+    i32x4 fw[2][WA], fc[2][WB];
+    auto read_one = [&](int buf, int half, int set, int q) {
+        const unsigned char* S = smem + buf * STAGE;
+        if (q == 0) fw[set][0] = *(const i32x4*)(S + slot(wo + li, 4 * half + lg));
+        else if (q <= WB) fc[set][q - 1] = *(const i32x4*)(S + TO * KT + slot(wt + 16 * (q - 1) + li, 4 * half + lg));
+        else fw[set][q - WB] = *(const i32x4*)(S + slot(wo + 16 * (q - WB) + li, 4 * half + lg));
+    };
+    auto mfma_one = [&](int set, int i) {
+        acc[i / WB][i % WB] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[set][i / WB], fc[set][i % WB], acc[i / WB][i % WB], 0, 0, 0);
+    };
+    const int full = g.in / KT;
+    if (full > 0) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) static_for<0, NL>([&](auto q) { copy_one(std::min(s, full - 1), s, q); });
+        wait_copies<NL>();
+        __builtin_amdgcn_s_barrier();
+#pragma unroll
+        for (int q = 0; q < NR; ++q) read_one(0, 0, 0, q);
+        for (int s = 0; s < full; ++s) {
+            const int buf = s & 1;
+#pragma unroll
+            for (int q = 0; q < NR; ++q) read_one(buf, 1, 1, q);
+#pragma unroll
+            for (int i = 0; i < NM; ++i) mfma_one(0, i);
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            if constexpr (NM > NR) __builtin_amdgcn_sched_group_barrier(0x008, NM - NR, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            wait_copies<0>();
+            __builtin_amdgcn_s_barrier();
+            // past the last stage the copies repeat it into the free buffer
+            const int next = std::min(s + 2, full - 1);
+            static_for<0, NM>([&](auto ic) {
+                constexpr int i = decltype(ic)::value;
+                mfma_one(1, i);
+                if constexpr (i < NR) read_one(buf ^ 1, 0, 0, i);
+                static_for<i * NL / NM, (i + 1) * NL / NM>([&](auto q) { copy_one(next, buf, q); });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        }
+        wait_copies<0>();
+    }
+    if (full * KT < g.in) {
+        __syncthreads();
+        for (int c = t; c < (TO + TT) * 8; c += 64 * NW) {
+            const int r = c / 8, k = c % 8;
+            const uint4 v = r < TO ? load_codes(g.W, g.ldw, o0 + r, g.out, full * KT + 16 * k, g.in)
+                                   : load_codes(g.C, g.ldc, r0 + r - TO, g.rows, full * KT + 16 * k, g.in);
+            *(uint4*)(smem + slot(r, k)) = v;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int q = 0; q < NR; ++q) read_one(0, half, 0, q);
+#pragma unroll
+            for (int i = 0; i < NM; ++i) mfma_one(0, i);
+        }
+    }
+#pragma unroll
+    for (int a = 0; a < WA; ++a)
+#pragma unroll
+        for (int b = 0; b < WB; ++b) store4(g, o0 + wo + 16 * a + 4 * lg, r0 + wt + 16 * b + li, acc[a][b]);
+}
+
+template <int NA, int TM, int WAVES, int UN>
+void launch_few(const Int8GemmArgs& g, hipStream_t st) {
+    hipLaunchKernelGGL((matmul_int8_few_kernel<NA, TM, WAVES, UN>), dim3((unsigned)cdiv(g.out, 16 * NA)),
+                       dim3(64 * WAVES), 0, st, g);
+}
+
+template <int TO, int TT, int WO, int WT>
+int launch_tile(const Int8GemmArgs& g, hipStream_t st) {
+    constexpr int lds = 2 * (TO + TT) * KT;
+    static bool ready = false;
+    if (!ready) {
+        PTQ_HIP(hipFuncSetAttribute((const void*)matmul_int8_tile_kernel<TO, TT, WO, WT>,
+                                    hipFuncAttributeMaxDynamicSharedMemorySize, lds));
+        ready = true;
+    }
+    const int64_t to = cdiv(g.out, TO), tt = cdiv(g.rows, TT);
+    hipLaunchKernelGGL((matmul_int8_tile_kernel<TO, TT, WO, WT>), dim3((unsigned)(cdiv(to * tt, NXCD) * NXCD)),
+                       dim3(64 * WO * WT), lds, st, g, (int)to, (int)tt);
+    return PTQ_OK;
 }
 
 template <typename T>
@@ -247,8 +458,12 @@ int run_matmul_int8(const int8_t* A, int64_t lda, const float* a_scales, int64_t
     g.in = (int)in;
     g.sw = b_scales; g.sx = a_scales; g.bias = bias;
     g.Y = Y; g.ldy = ldy; g.y_dtype = y_dtype;
-    hipLaunchKernelGGL(matmul_int8_kernel, dim3((unsigned)(cdiv(out, TB) * cdiv(rows, TB))), dim3(256), 0, st,
-                       g);
+    if (rows <= 16) launch_few<1, 1, 16, 2>(g, st);
+    else if (rows <= 32) launch_few<1, 2, 16, 2>(g, st);
+    else if (rows <= 48) launch_few<2, 3, 8, 2>(g, st);
+    else if (rows <= 64) launch_few<2, 4, 8, 2>(g, st);
+    else if (cdiv(rows, 256) * cdiv(out, 256) >= 200) PTQ_TRY((launch_tile<256, 256, 4, 2>(g, st)));
+    else PTQ_TRY((launch_tile<128, 128, 2, 2>(g, st)));
     PTQ_LAUNCH_CHECK();
     return PTQ_OK;
 }
