@@ -115,7 +115,7 @@ int quantize_tokens_int8(const void* X, int x_dtype, int64_t rows, int64_t in, i
     if (s && !aligned16(s)) REFUSE("%s: s is not 16-byte aligned", fn);
     PTQ_TRY(check_codes(fn, "codes", codes, in, ldc));
     if (!scales) REFUSE("%s: scales is NULL", fn);
-    return launch_quantize_tokens_int8(X, x_dtype, rows, in, ldx, s, codes, ldc, in, scales, (hipStream_t)stream);
+    return launch_quantize_tokens_int8(X, x_dtype, rows, in, ldx, s, codes, ldc, scales, (hipStream_t)stream);
 }
 
 size_t matmul_int8_workspace_bytes(int64_t rows, int64_t out, int64_t in) {

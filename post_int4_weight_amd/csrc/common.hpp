@@ -210,7 +210,7 @@ int run_awq(const void* W, int w_dtype, int64_t out, int64_t n, int64_t ldw, con
 
 // Int8 linear layers (linear_int8.hip)
 int launch_quantize_tokens_int8(const void* X, int x_dtype, int64_t rows, int64_t in, int64_t ldx, const float* s,
-                                int8_t* codes, int64_t ldc, int64_t pad, float* scales, hipStream_t st);
+                                int8_t* codes, int64_t ldc, float* scales, hipStream_t st);
 size_t matmul_int8_ws_bytes(int64_t rows, int64_t out, int64_t in);
 int run_matmul_int8(const int8_t* A, int64_t lda, const float* a_scales, int64_t rows, const int8_t* B, int64_t ldb,
                     const float* b_scales, int64_t out, int64_t in, const float* bias, int y_dtype, void* Y,

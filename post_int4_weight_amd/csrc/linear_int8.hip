@@ -16,6 +16,9 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
+constexpr int KT = 128;        // codes per row and stage of the product
+constexpr int NXCD = 8;
+
 // ------------------------------------------------------------------ tokens --
 // One workgroup per token. The row is read once: a thread keeps up to 4 chunks
 // of 8 values in registers between the maximum and the codes (rows of up to
@@ -23,7 +26,7 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 constexpr int QKEEP = 4;
 
 template <typename T, bool SMOOTH>
-__global__ __launch_bounds__(1024) void quantize_tokens_kernel(const T* __restrict__ X, int64_t ldx, int in, int pad,
+__global__ __launch_bounds__(1024) void quantize_tokens_kernel(const T* __restrict__ X, int64_t ldx, int in, int shift,
                                                                const float* __restrict__ s, int8_t* __restrict__ codes,
                                                                int64_t ldc, float* __restrict__ scales) {
     const int64_t row = blockIdx.x;
@@ -65,11 +68,12 @@ __global__ __launch_bounds__(1024) void quantize_tokens_kernel(const T* __restri
     const float S = int8_scale(a), inv = int8_inverse(S);
     if (t == 0) scales[row] = S;
     int8_t* out = codes + row * ldc;
+    const int whole = in / KT * (KT / 8);     // the last stage's codes move up by shift, zeros go before them
     auto store = [&](int c, const float (&v)[8]) {
         uint32_t w[2] = {0u, 0u};
 #pragma unroll
         for (int k = 0; k < 8; ++k) w[k >> 2] |= (uint32_t)(uint8_t)int8_code(v[k], inv) << (8 * (k & 3));
-        *(uint2*)(out + 8 * c) = make_uint2(w[0], w[1]);
+        *(uint2*)(out + 8 * c + (c >= whole ? shift : 0)) = make_uint2(w[0], w[1]);
     };
 #pragma unroll
     for (int i = 0; i < QKEEP; ++i) {
@@ -81,7 +85,7 @@ __global__ __launch_bounds__(1024) void quantize_tokens_kernel(const T* __restri
         chunk(c, v);
         store(c, v);
     }
-    for (int c = nch + t; c < pad / 8; c += nt) *(uint2*)(out + 8 * c) = make_uint2(0u, 0u);
+    if (t < shift / 8) *(uint2*)(out + 8 * (whole + t)) = make_uint2(0u, 0u);
 }
 
 // ----------------------------------------------------------------- product --
@@ -91,6 +95,7 @@ struct Int8GemmArgs {
     int in;
     const float* sw; const float* sx; const float* bias;
     void* Y; int64_t ldy; int y_dtype;
+    int nsplit; int* part;     // shares of the depth, their int32 sums [split][tile][value / 4][thread][4]
 };
 
 // Accumulators of v_mfma_i32_16x16x64_i8: lane l supplies row l % 16 of each
@@ -152,90 +157,145 @@ __device__ __forceinline__ i32x4 load_codes16(const int8_t* p) {
     return i32x4{(int)c.w[0], (int)c.w[1], (int)c.w[2], (int)c.w[3]};
 }
 
-constexpr int KT = 128;        // codes per row and stage
-constexpr int NXCD = 8;
-
 // ---- few tokens: the weights are read once, straight into operand registers.
-// A workgroup owns 16 NA outputs; its waves share the depth in runs of KT, one
-// after another, so that together they read whole stretches of each row. Up
-// to 16 TM tokens: each wave reads their codes (which stay in L2) next to the
-// weights. The int32 partial sums meet in LDS.
-template <int NA, int TM, int WAVES, int UN>
-__global__ __launch_bounds__(64 * WAVES) void matmul_int8_few_kernel(Int8GemmArgs g) {
-    __shared__ __attribute__((aligned(16))) i32x4 part[WAVES][NA * TM][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int li = lane & 15, lg = lane >> 4;
-    const int64_t o0 = (int64_t)blockIdx.x * (16 * NA);
-    const int8_t* w[NA];
-    const int8_t* c[TM];
+// A workgroup owns 16 outputs; its 16 waves share the depth in runs of KT, one
+// after another, so that together they read whole stretches of each row. Each
+// wave reads the tokens' codes (which stay in L2, or LDS) next to the weights.
+// The int32 partial sums meet in LDS.
+constexpr int FW = 16, FUN = 2;      // waves; runs of a wave in flight
+
+// the weights of runs s, s + FW, ... of this lane
+__device__ __forceinline__ void load_runs(const int8_t* w, int s, i32x4 (&fw)[FUN][2]) {
 #pragma unroll
-    for (int a = 0; a < NA; ++a) w[a] = g.W + std::min<int64_t>(o0 + 16 * a + li, g.out - 1) * g.ldw + 16 * lg;
+    for (int u = 0; u < FUN; ++u)
 #pragma unroll
-    for (int b = 0; b < TM; ++b) c[b] = g.C + std::min<int64_t>(16 * b + li, g.rows - 1) * g.ldc + 16 * lg;
-    i32x4 acc[NA][TM];
-#pragma unroll
-    for (int a = 0; a < NA; ++a)
-#pragma unroll
-        for (int b = 0; b < TM; ++b) acc[a][b] = i32x4{0, 0, 0, 0};
-    const int full = g.in / KT;               // whole runs
+        for (int e = 0; e < 2; ++e) fw[u][e] = load_codes16(w + (int64_t)(s + u * FW) * KT + 64 * e);
+}
+
+// fw holds the first runs if there are FUN whole ones; codes(k): the lane's 16 codes at k, with k + 16 <= the
+// codes' own end for whole runs, and tail(k) the same anywhere
+template <typename F, typename G>
+__device__ __forceinline__ i32x4 sum_runs(const int8_t* w, int in, int wave, int lg, i32x4 (&fw)[FUN][2], F&& codes, G&& tail) {
+    i32x4 acc = i32x4{0, 0, 0, 0};
+    const int full = in / KT;
     int s = wave;
-    for (; s + (UN - 1) * WAVES < full; s += UN * WAVES) {
-        i32x4 fw[UN][NA][2], fc[UN][TM][2];
+    while (s + (FUN - 1) * FW < full) {
+        i32x4 fc[FUN][2];
 #pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            const int64_t k = (int64_t)(s + u * WAVES) * KT;
+        for (int u = 0; u < FUN; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < 2; ++e) fc[u][e] = codes((s + u * FW) * KT + 64 * e);
 #pragma unroll
-                for (int a = 0; a < NA; ++a) fw[u][a][e] = load_codes16(w[a] + k + 64 * e);
+        for (int u = 0; u < FUN; ++u)
 #pragma unroll
-                for (int b = 0; b < TM; ++b) fc[u][b][e] = load_codes16(c[b] + k + 64 * e);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < UN; ++u)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int a = 0; a < NA; ++a)
-#pragma unroll
-                    for (int b = 0; b < TM; ++b)
-                        acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][a][e], fc[u][b][e], acc[a][b], 0, 0, 0);
+            for (int e = 0; e < 2; ++e) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][e], fc[u][e], acc, 0, 0, 0);
+        s += FUN * FW;
+        if (s + (FUN - 1) * FW < full) load_runs(w, s, fw);
     }
-    for (; s * KT < g.in; s += WAVES) {       // the last runs, the ragged one among them
+    for (; s * KT < in; s += FW) {       // the last runs, the ragged one among them
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int64_t k = (int64_t)s * KT + 64 * e;
-            i32x4 fw[NA], fc[TM];
+            const int k = s * KT + 64 * e;
+            const uint4 x = load_codes(w - 16 * lg, 0, 0, 1, k + 16 * lg, in);
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(i32x4{(int)x.x, (int)x.y, (int)x.z, (int)x.w}, tail(k), acc, 0, 0, 0);
+        }
+    }
+    return acc;
+}
+
+__global__ __launch_bounds__(64 * FW) void matmul_int8_few_kernel(Int8GemmArgs g, unsigned strips) {
+    __shared__ __attribute__((aligned(16))) i32x4 part[FW][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int li = lane & 15, lg = lane >> 4;
+    const int64_t o0 = (int64_t)(blockIdx.x % strips) * 16, r0 = (int64_t)(blockIdx.x / strips) * 16;
+    const int8_t* w = g.W + std::min<int64_t>(o0 + li, g.out - 1) * g.ldw + 16 * lg;
+    const int8_t* c = g.C + std::min<int64_t>(r0 + li, g.rows - 1) * g.ldc + 16 * lg;
+    i32x4 fw[FUN][2];
+    if (wave + (FUN - 1) * FW < g.in / KT) load_runs(w, wave, fw);
+    part[wave][lane] = sum_runs(w, g.in, wave, lg, fw, [&](int k) { return load_codes16(c + k); },
+                                [&](int k) {
+                                    const uint4 x = load_codes(c - 16 * lg, 0, 0, 1, k + 16 * lg, g.in);
+                                    return i32x4{(int)x.x, (int)x.y, (int)x.z, (int)x.w};
+                                });
+    __syncthreads();
+    if (wave) return;
+    i32x4 sum = part[0][lane];
 #pragma unroll
-            for (int a = 0; a < NA; ++a) {
-                const uint4 x = load_codes(w[a] - 16 * lg, 0, 0, 1, k + 16 * lg, g.in);
-                fw[a] = i32x4{(int)x.x, (int)x.y, (int)x.z, (int)x.w};
+    for (int v = 1; v < FW; ++v) sum += part[v][lane];
+    store4(g, o0 + 4 * lg, r0 + li, sum);
+}
+
+// The same with the tokens quantized in every workgroup, while its first
+// weights are on their way: one launch instead of two, for up to 16 tokens of
+// up to FUSED_MOST values together (their codes stay in LDS). 2^RL >= rows: the waves that share a row are FW / 2^RL.
+constexpr int FUSED_MOST = 65536, FKEEP = FUSED_MOST / 8 / (64 * FW);
+__host__ __device__ inline int fused_pitch(int in) { return (in + KT - 1) / KT * KT + 16; }   // rows start on different banks
+
+template <typename T, bool SMOOTH>
+__global__ __launch_bounds__(64 * FW) void linear_int8_few_kernel(Int8GemmArgs g, const T* __restrict__ X, int64_t ldx,
+                                                                  const float* __restrict__ s, int rl) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char codes[];
+    __shared__ __attribute__((aligned(16))) i32x4 part[FW][64];
+    __shared__ float red[FW], sx[FW];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int li = lane & 15, lg = lane >> 4;
+    const int64_t o0 = (int64_t)blockIdx.x * 16;
+    const int8_t* w = g.W + std::min<int64_t>(o0 + li, g.out - 1) * g.ldw + 16 * lg;
+    i32x4 fw[FUN][2];
+    if (wave + (FUN - 1) * FW < g.in / KT) load_runs(w, wave, fw);
+
+    const int wpr = FW >> rl, row = wave / wpr, nch = g.in / 8, pitch = fused_pitch(g.in);
+    const bool have = row < g.rows;
+    float keep[FKEEP][8];
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < FKEEP; ++i) {
+        const int c = (wave % wpr + i * wpr) * 64 + lane;
+        if (have && c < nch) {
+            load8(X + row * ldx + 8 * c, keep[i]);
+            if (SMOOTH) {
+                float d[8];
+                load8(s + 8 * c, d);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) keep[i][k] = __fdiv_rn(keep[i][k], d[k]);
             }
 #pragma unroll
-            for (int b = 0; b < TM; ++b) {
-                const uint4 x = load_codes(c[b] - 16 * lg, 0, 0, 1, k + 16 * lg, g.in);
-                fc[b] = i32x4{(int)x.x, (int)x.y, (int)x.z, (int)x.w};
-            }
-#pragma unroll
-            for (int a = 0; a < NA; ++a)
-#pragma unroll
-                for (int b = 0; b < TM; ++b)
-                    acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[a], fc[b], acc[a][b], 0, 0, 0);
+            for (int k = 0; k < 8; ++k) a = amax_acc(a, keep[i][k]);
         }
     }
 #pragma unroll
-    for (int a = 0; a < NA; ++a)
-#pragma unroll
-        for (int b = 0; b < TM; ++b) part[wave][a * TM + b][lane] = acc[a][b];
+    for (int off = 32; off > 0; off >>= 1) a = amax_acc(a, __shfl_xor(a, off, 64));
+    if (lane == 0) red[wave] = a;
     __syncthreads();
-    for (int q = wave; q < NA * TM; q += WAVES) {
-        const int a = q / TM, b = q % TM;
-        i32x4 sum = part[0][q][lane];
+    a = 0.f;
+    for (int v = 0; v < wpr; ++v) a = amax_acc(a, red[row * wpr + v]);
+    const float S = int8_scale(a), inv = int8_inverse(S);
+    if (lane == 0 && wave % wpr == 0) sx[row] = S;
+    if (have) {
+        unsigned char* out = codes + row * pitch;
 #pragma unroll
-        for (int v = 1; v < WAVES; ++v) sum += part[v][q][lane];
-        store4(g, o0 + 16 * a + 4 * lg, 16 * b + li, sum);
+        for (int i = 0; i < FKEEP; ++i) {
+            const int c = (wave % wpr + i * wpr) * 64 + lane;
+            if (c < nch) {
+                uint32_t x[2] = {0u, 0u};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k >> 2] |= (uint32_t)(uint8_t)int8_code(keep[i][k], inv) << (8 * (k & 3));
+                *(uint2*)(out + 8 * c) = make_uint2(x[0], x[1]);
+            }
+        }
+        if (wave % wpr == 0 && nch + lane < (pitch - 16) / 8) *(uint2*)(out + 8 * (nch + lane)) = make_uint2(0u, 0u);
     }
+    __syncthreads();
+    const unsigned char* c = codes + std::min(li, (int)g.rows - 1) * pitch + 16 * lg;
+    auto at = [&](int k) { return *(const i32x4*)(c + k); };
+    part[wave][lane] = sum_runs(w, g.in, wave, lg, fw, at, at);
+    __syncthreads();
+    if (wave) return;
+    i32x4 sum = part[0][lane];
+#pragma unroll
+    for (int v = 1; v < FW; ++v) sum += part[v][lane];
+    g.sx = sx;
+    store4(g, o0 + 4 * lg, li, sum);
 }
 
 // ---- many tokens: tiles of TO outputs x TT tokens, WO x WT waves, stages of
@@ -282,13 +342,73 @@ __device__ __forceinline__ bool tile_of(unsigned b, int to, int tt, int& o, int&
     return true;
 }
 
-template <int TO, int TT, int WO, int WT>
+// Outputs of 16 tokens x 16 WA outputs of a wave, from accumulators to rows of
+// Y through the wave's own piece of LDS: a row is then written in whole
+// stretches (the accumulators hold 4 outputs of one token a lane: 8 bytes in
+// bf16), by single elements where Y's rows are not aligned.
+template <int WA>
+constexpr int rows_bytes() { return 16 * (16 * WA + 4) * 4; }
+
+template <int WA, typename F>
+__device__ __forceinline__ void store_rows(const Int8GemmArgs& g, int64_t o0, int64_t r0, unsigned char* lds, F&& acc) {
+    constexpr int OW = 16 * WA, PITCH = OW + 4;
+    const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+    int* S = (int*)lds;
+#pragma unroll
+    for (int a = 0; a < WA; ++a) *(i32x4*)(S + li * PITCH + 16 * a + 4 * lg) = acc(a);
+    __builtin_amdgcn_wave_barrier();
+    const int rows = (int)std::min<int64_t>(16, g.rows - r0);
+    const int e = g.y_dtype == PTQ_F32 ? 4 : 2;
+    if (((uintptr_t)g.Y | (uint64_t)g.ldy * e) % (4 * e) == 0 && o0 + OW <= g.out) {
+        constexpr int PR = OW / 4, RI = 64 / PR;      // lanes per row, rows at a time
+        const int o = 4 * (lane % PR);
+        float sw[4], bias[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            sw[k] = g.sw[o0 + o + k];
+            bias[k] = g.bias ? g.bias[o0 + o + k] : 0.f;
+        }
+#pragma unroll
+        for (int r = lane / PR; r < 16; r += RI) {
+            if (r >= rows) break;
+            const i32x4 x = *(const i32x4*)(S + r * PITCH + o);
+            const float sx = g.sx[r0 + r];
+            float y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = (float)x[k] * (sx * sw[k]) + bias[k];
+            const int64_t at = (r0 + r) * g.ldy + o0 + o;
+            if (e == 4) *(float4*)((float*)g.Y + at) = make_float4(y[0], y[1], y[2], y[3]);
+            else *(uint2*)((uint16_t*)g.Y + at) = make_uint2(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]));
+        }
+    } else {
+        constexpr int PR = OW < 64 ? OW : 64, RI = 64 / PR;
+        for (int o = lane % PR; o < OW; o += PR) {
+            if (o0 + o >= g.out) break;
+            const float sw = g.sw[o0 + o], bias = g.bias ? g.bias[o0 + o] : 0.f;
+#pragma unroll 4
+            for (int r = lane / PR; r < rows; r += RI) {
+                const float y = (float)S[r * PITCH + o] * (g.sx[r0 + r] * sw) + bias;
+                const int64_t at = (r0 + r) * g.ldy + o0 + o;
+                if (e == 4) ((float*)g.Y)[at] = y;
+                else ((uint16_t*)g.Y)[at] = (uint16_t)bf16_of(y);
+            }
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+}
+
+// The tokens' codes come in stages of their own (see tile_ldc): whole stages
+// of KT, then, where `in` leaves a rest, one with the last KT codes of the row
+// of which those that an earlier stage had are zero. The weights' last stage
+// then simply starts at in - KT: no access needs a check. in >= KT.
+template <int TO, int TT, int WO, int WT, int NST>
 __global__ __launch_bounds__(64 * WO * WT, 1) void matmul_int8_tile_kernel(Int8GemmArgs g, int tiles_o, int tiles_t) {
     constexpr int NW = WO * WT, WA = TO / WO / 16, WB = TT / WT / 16;
     constexpr int PW = TO / 8 / NW, PC = TT / 8 / NW;      // copies of 8 rows per wave and stage
     constexpr int STAGE = (TO + TT) * KT;
     constexpr int NM = WA * WB, NR = WA + WB, NL = PW + PC;
-    static_assert(PW * 8 * NW == TO && PC * 8 * NW == TT && NM >= NR && NL <= NM, "tile shape");
+    static_assert(PW * 8 * NW == TO && PC * 8 * NW == TT && NST >= 2, "tile shape");
+    static_assert(NW * rows_bytes<WA>() <= NST * STAGE, "epilogue fits the stages");
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     int to, tt;
     if (!tile_of(blockIdx.x, tiles_o, tiles_t, to, tt)) return;
@@ -311,10 +431,11 @@ __global__ __launch_bounds__(64 * WO * WT, 1) void matmul_int8_tile_kernel(Int8G
         const int r = 8 * (wave * PC + q) + (lane >> 3);
         vc[q] = (unsigned)(std::min<int64_t>(r, g.rows - 1 - r0) * g.ldc + 16 * ((lane & 7) ^ ((r >> 1) & 7)));
     }
+    const int stages = (g.in + KT - 1) / KT;
     auto copy_one = [&](int s, int buf, auto qc) {
         constexpr int q = decltype(qc)::value;
         unsigned char* base = smem + buf * STAGE;
-        if constexpr (q < PW) copy16(rw, base + (wave * PW + q) * 1024, vw[q], (unsigned)(s * KT));
+        if constexpr (q < PW) copy16(rw, base + (wave * PW + q) * 1024, vw[q], (unsigned)std::min(s * KT, g.in - KT));
         else copy16(rc, base + TO * KT + (wave * PC + q - PW) * 1024, vc[q - PW], (unsigned)(s * KT));
     };
 
@@ -327,7 +448,7 @@ __global__ __launch_bounds__(64 * WO * WT, 1) void matmul_int8_tile_kernel(Int8G
     // next half are read while this half's products run. The barrier sits
     // before a stage's second half, whose fragments are in registers by then:
     // past it the next stage has landed for every wave, and this stage's
-    // buffer takes the copies of the stage after that.
+    // buffer takes the copies of the stage NST later.
     i32x4 fw[2][WA], fc[2][WB];
     auto read_one = [&](int buf, int half, int set, int q) {
         const unsigned char* S = smem + buf * STAGE;
@@ -338,159 +459,310 @@ __global__ __launch_bounds__(64 * WO * WT, 1) void matmul_int8_tile_kernel(Int8G
     auto mfma_one = [&](int set, int i) {
         acc[i / WB][i % WB] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[set][i / WB], fc[set][i % WB], acc[i / WB][i % WB], 0, 0, 0);
     };
-    const int full = g.in / KT;
-    if (full > 0) {
+    // this split's stages: an even share
+    const int first = (int)((int64_t)stages * blockIdx.y / g.nsplit), last = (int)((int64_t)stages * (blockIdx.y + 1) / g.nsplit);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) static_for<0, NL>([&](auto q) { copy_one(std::min(s, full - 1), s, q); });
-        wait_copies<NL>();
+    for (int s = 0; s < NST; ++s) static_for<0, NL>([&](auto q) { copy_one(std::min(first + s, last - 1), s, q); });
+    wait_copies<(NST - 1) * NL>();
+    __builtin_amdgcn_s_barrier();
+#pragma unroll
+    for (int q = 0; q < NR; ++q) read_one(0, 0, 0, q);
+    int buf = 0;
+    for (int s = first; s < last; ++s) {
+        const int after = buf + 1 == NST ? 0 : buf + 1;
+#pragma unroll
+        for (int q = 0; q < NR; ++q) read_one(buf, 1, 1, q);
+#pragma unroll
+        for (int i = 0; i < NM; ++i) mfma_one(0, i);
+#pragma unroll
+        for (int i = 0; i < NR && i < NM; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        if constexpr (NM > NR) __builtin_amdgcn_sched_group_barrier(0x008, NM - NR, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        wait_copies<(NST - 2) * NL>();
         __builtin_amdgcn_s_barrier();
-#pragma unroll
-        for (int q = 0; q < NR; ++q) read_one(0, 0, 0, q);
-        for (int s = 0; s < full; ++s) {
-            const int buf = s & 1;
-#pragma unroll
-            for (int q = 0; q < NR; ++q) read_one(buf, 1, 1, q);
-#pragma unroll
-            for (int i = 0; i < NM; ++i) mfma_one(0, i);
-#pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            }
-            if constexpr (NM > NR) __builtin_amdgcn_sched_group_barrier(0x008, NM - NR, 0);
+        // past the last stage the copies repeat it into the free buffer
+        const int next = std::min(s + NST, last - 1);
+        static_for<0, NM>([&](auto ic) {
+            constexpr int i = decltype(ic)::value;
+            mfma_one(1, i);
+            if constexpr (i < NR) read_one(after, 0, 0, i);
+            static_for<i * NL / NM, (i + 1) * NL / NM>([&](auto q) { copy_one(next, buf, q); });
             __builtin_amdgcn_sched_barrier(0);
-            wait_copies<0>();
-            __builtin_amdgcn_s_barrier();
-            // past the last stage the copies repeat it into the free buffer
-            const int next = std::min(s + 2, full - 1);
-            static_for<0, NM>([&](auto ic) {
-                constexpr int i = decltype(ic)::value;
-                mfma_one(1, i);
-                if constexpr (i < NR) read_one(buf ^ 1, 0, 0, i);
-                static_for<i * NL / NM, (i + 1) * NL / NM>([&](auto q) { copy_one(next, buf, q); });
-                __builtin_amdgcn_sched_barrier(0);
-            });
-        }
-        wait_copies<0>();
+        });
+        static_for<NM, NR>([&](auto q) { read_one(after, 0, 0, decltype(q)::value); });
+        buf = after;
     }
-    if (full * KT < g.in) {
-        __syncthreads();
-        for (int c = t; c < (TO + TT) * 8; c += 64 * NW) {
-            const int r = c / 8, k = c % 8;
-            const uint4 v = r < TO ? load_codes(g.W, g.ldw, o0 + r, g.out, full * KT + 16 * k, g.in)
-                                   : load_codes(g.C, g.ldc, r0 + r - TO, g.rows, full * KT + 16 * k, g.in);
-            *(uint4*)(smem + slot(r, k)) = v;
-        }
-        __syncthreads();
+    wait_copies<0>();
+    if (g.nsplit > 1) {
+        i32x4* p = (i32x4*)g.part + ((int64_t)blockIdx.y * tiles_o * tiles_t + (int64_t)tt * tiles_o + to) * (TO * TT / 4) + t;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int b = 0; b < WB; ++b)
 #pragma unroll
-            for (int q = 0; q < NR; ++q) read_one(0, half, 0, q);
-#pragma unroll
-            for (int i = 0; i < NM; ++i) mfma_one(0, i);
-        }
+            for (int a = 0; a < WA; ++a) p[(b * WA + a) * (64 * NW)] = acc[a][b];
+        return;
     }
+    __syncthreads();
+    unsigned char* mine = smem + wave * rows_bytes<WA>();
 #pragma unroll
-    for (int a = 0; a < WA; ++a)
-#pragma unroll
-        for (int b = 0; b < WB; ++b) store4(g, o0 + wo + 16 * a + 4 * lg, r0 + wt + 16 * b + li, acc[a][b]);
+    for (int b = 0; b < WB; ++b)
+        if (r0 + wt + 16 * b < g.rows) store_rows<WA>(g, o0 + wo, r0 + wt + 16 * b, mine, [&](int a) { return acc[a][b]; });
 }
 
-template <int NA, int TM, int WAVES, int UN>
-void launch_few(const Int8GemmArgs& g, hipStream_t st) {
-    hipLaunchKernelGGL((matmul_int8_few_kernel<NA, TM, WAVES, UN>), dim3((unsigned)cdiv(g.out, 16 * NA)),
-                       dim3(64 * WAVES), 0, st, g);
-}
-
+// Sum of the splits of a tile, 16 tokens of each wave at a time.
 template <int TO, int TT, int WO, int WT>
-int launch_tile(const Int8GemmArgs& g, hipStream_t st) {
-    constexpr int lds = 2 * (TO + TT) * KT;
+__global__ __launch_bounds__(64 * WO * WT) void matmul_int8_join_kernel(Int8GemmArgs g, int tiles_o, int tiles_t) {
+    constexpr int NW = WO * WT, WA = TO / WO / 16, WB = TT / WT / 16;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[NW * rows_bytes<WA>()];
+    const int b = blockIdx.x % WB, tile = blockIdx.x / WB, t = threadIdx.x, wave = t >> 6;
+    const int64_t o0 = (int64_t)(tile % tiles_o) * TO + (wave / WT) * (TO / WO);
+    const int64_t r0 = (int64_t)(tile / tiles_o) * TT + (wave % WT) * (TT / WT) + 16 * b;
+    if (r0 >= g.rows) return;
+    const int64_t step = (int64_t)tiles_o * tiles_t * (TO * TT / 4);
+    const i32x4* p = (const i32x4*)g.part + (int64_t)tile * (TO * TT / 4) + b * WA * (64 * NW) + t;
+    i32x4 sum[WA];
+#pragma unroll
+    for (int a = 0; a < WA; ++a) sum[a] = p[a * (64 * NW)];
+    for (int s = 1; s < g.nsplit; ++s)
+#pragma unroll
+        for (int a = 0; a < WA; ++a) sum[a] += p[s * step + a * (64 * NW)];
+    store_rows<WA>(g, o0, r0, lds + wave * rows_bytes<WA>(), [&](int a) { return sum[a]; });
+}
+
+void launch_few(const Int8GemmArgs& g, hipStream_t st) {
+    const int64_t strips = cdiv(g.out, 16);
+    hipLaunchKernelGGL(matmul_int8_few_kernel, dim3((unsigned)(strips * cdiv(g.rows, 16))), dim3(64 * FW), 0, st, g,
+                       (unsigned)strips);
+}
+
+// ceil(log2(rows)) if the fused kernel takes them, else -1
+int fused_rows_log2(int64_t rows, int64_t in) {
+    if (rows > 16) return -1;
+    const int rl = rows <= 1 ? 0 : rows <= 2 ? 1 : rows <= 4 ? 2 : rows <= 8 ? 3 : 4;
+    return (in << rl) <= FUSED_MOST ? rl : -1;
+}
+
+template <typename T, bool SMOOTH>
+int launch_fused(const Int8GemmArgs& g, const T* X, int64_t ldx, const float* s, int rl, hipStream_t st) {
     static bool ready = false;
     if (!ready) {
-        PTQ_HIP(hipFuncSetAttribute((const void*)matmul_int8_tile_kernel<TO, TT, WO, WT>,
+        PTQ_HIP(hipFuncSetAttribute((const void*)linear_int8_few_kernel<T, SMOOTH>,
+                                    hipFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024));
+        ready = true;
+    }
+    hipLaunchKernelGGL((linear_int8_few_kernel<T, SMOOTH>), dim3((unsigned)cdiv(g.out, 16)), dim3(64 * FW),
+                       (unsigned)(g.rows * fused_pitch(g.in)), st, g, X, ldx, s, rl);
+    return PTQ_OK;
+}
+
+template <int TO, int TT, int WO, int WT, int NST>
+int launch_tile(const Int8GemmArgs& g, hipStream_t st) {
+    constexpr int lds = NST * (TO + TT) * KT;
+    static bool ready = false;
+    if (!ready) {
+        PTQ_HIP(hipFuncSetAttribute((const void*)matmul_int8_tile_kernel<TO, TT, WO, WT, NST>,
                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds));
         ready = true;
     }
     const int64_t to = cdiv(g.out, TO), tt = cdiv(g.rows, TT);
-    hipLaunchKernelGGL((matmul_int8_tile_kernel<TO, TT, WO, WT>), dim3((unsigned)(cdiv(to * tt, NXCD) * NXCD)),
-                       dim3(64 * WO * WT), lds, st, g, (int)to, (int)tt);
+    hipLaunchKernelGGL((matmul_int8_tile_kernel<TO, TT, WO, WT, NST>),
+                       dim3((unsigned)(cdiv(to * tt, NXCD) * NXCD), g.nsplit), dim3(64 * WO * WT), lds, st, g, (int)to, (int)tt);
+    if (g.nsplit > 1)
+        hipLaunchKernelGGL((matmul_int8_join_kernel<TO, TT, WO, WT>), dim3((unsigned)(to * tt * (TT / WT / 16))),
+                           dim3(64 * WO * WT), 0, st, g, (int)to, (int)tt);
     return PTQ_OK;
 }
 
+// Codes of a caller with a ragged `in`, put into stages (tile_ldc).
+__global__ __launch_bounds__(256) void stage_codes_kernel(const int8_t* __restrict__ A, int64_t lda, int64_t rows, int in,
+                                                          int8_t* __restrict__ C, int64_t ldc) {
+    const int whole = in / KT * KT, shift = (int)ldc - in, nch = (int)(ldc / 8);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * nch; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / nch;
+        const int at = 8 * (int)(i % nch), k = at < whole ? at : at - shift;
+        uint2 v = make_uint2(0u, 0u);
+        if (at < whole || k >= whole) v = *(const uint2*)(A + r * lda + k);
+        *(uint2*)(C + r * ldc + at) = v;
+    }
+}
+
 template <typename T>
-void launch_tokens(const T* X, int64_t rows, int in, int64_t ldx, const float* s, int8_t* codes, int64_t ldc, int pad,
+void launch_tokens(const T* X, int64_t rows, int in, int64_t ldx, const float* s, int8_t* codes, int64_t ldc, int shift,
                    float* scales, hipStream_t st) {
     const int nt = in <= 8192 ? 256 : in <= 16384 ? 512 : 1024;
     if (s)
-        hipLaunchKernelGGL((quantize_tokens_kernel<T, true>), dim3((unsigned)rows), dim3(nt), 0, st, X, ldx, in, pad, s,
+        hipLaunchKernelGGL((quantize_tokens_kernel<T, true>), dim3((unsigned)rows), dim3(nt), 0, st, X, ldx, in, shift, s,
                            codes, ldc, scales);
     else
-        hipLaunchKernelGGL((quantize_tokens_kernel<T, false>), dim3((unsigned)rows), dim3(nt), 0, st, X, ldx, in, pad,
+        hipLaunchKernelGGL((quantize_tokens_kernel<T, false>), dim3((unsigned)rows), dim3(nt), 0, st, X, ldx, in, shift,
                            s, codes, ldc, scales);
+}
+
+int launch_quantize(const void* X, int x_dtype, int64_t rows, int64_t in, int64_t ldx, const float* s, int8_t* codes,
+                    int64_t ldc, int shift, float* scales, hipStream_t st) {
+    if (rows == 0) return PTQ_OK;
+    if (x_dtype == PTQ_F32)
+        launch_tokens((const float*)X, rows, (int)in, ldx, s, codes, ldc, shift, scales, st);
+    else
+        launch_tokens((const uint16_t*)X, rows, (int)in, ldx, s, codes, ldc, shift, scales, st);
+    PTQ_LAUNCH_CHECK();
+    return PTQ_OK;
+}
+
+// How a product runs: few = the streaming kernel, else tiles of shape `shape`
+// with the depth in nsplit shares.
+struct Plan {
+    bool few;
+    int shape, nsplit;
+};
+// Tile shapes; us: time of a stage of one workgroup per CU. Rings are as deep
+// as LDS allows without losing a second workgroup to it (small tiles wait for
+// their copies, so 5 stages against 3 at 64 x 64: 4096 x 4096 weights, 200
+// tokens 10.8 against 14.4 us; 8 against 2 at 32 x 32).
+struct Shape {
+    int to, tt;
+    float us;
+};
+constexpr Shape SHAPES[] = {{256, 256, 2.55f}, {128, 256, 1.47f}, {128, 128, 1.38f},
+                            {64, 64, 0.449f},  {64, 32, 0.336f},  {32, 32, 0.193f}};
+
+// The streaming kernel serves up to 16 tokens on weights of up to 2^25 codes
+// (4096 x 4096, 1 token: 6.2 us against 6.9 for 32 x 32 tiles; 8192 x 8192, 8
+// tokens: 16.0 against 14.6) and depths below one stage. Otherwise the shape
+// and the split with the least estimate: workgroups per CU times the stages of
+// one, at least the weights at 3.88 TB/s, and for splits 5 us and the partial
+// sums written and read at 2.04 TB/s. The constants are fitted to 4107 timings
+// of 170 products, 1 to 4096 tokens, 255 x 2056 to 28672 x 8192 weights; the
+// choice is 0.8% slower than the best of each in the mean, 14% at worst (512
+// tokens, 5003 x 4104: 34.4 against 30.3 us).
+Plan plan(int64_t rows, int64_t out, int64_t in) {
+    Plan p{in < KT || (rows <= 16 && out * in <= ((int64_t)1 << 25)), 0, 1};
+    if (p.few) return p;
+    const int64_t stages = cdiv(in, KT);
+    double least = 1e300;
+    for (int k = 0; k < (int)(sizeof(SHAPES) / sizeof(SHAPES[0])); ++k) {
+        const Shape& h = SHAPES[k];
+        const int64_t tiles = cdiv(out, h.to) * cdiv(rows, h.tt);
+        for (int ns : {1, 2, 3, 4, 6, 8, 12, 16}) {
+            if (ns > 1 && (stages < 4 * ns || tiles * ns > 2048)) break;
+            double us = std::max((double)cdiv(tiles * ns, 256) * cdiv(stages, ns) * h.us, out * in / 3.88e6);
+            if (ns > 1) us += 5.0 + (double)tiles * ns * h.to * h.tt * 8 / 2.04e6;
+            if (us < least) {
+                least = us;
+                p.shape = k;
+                p.nsplit = ns;
+            }
+        }
+    }
+    return p;
+}
+
+// Row stride of the tokens' codes in stages.
+int64_t tile_ldc(int64_t in) { return cdiv(in, KT) * KT; }
+
+size_t part_elems(const Plan& p, int64_t rows, int64_t out) {
+    if (p.few || p.nsplit == 1) return 0;
+    const Shape s = SHAPES[p.shape];
+    return (size_t)p.nsplit * cdiv(out, s.to) * cdiv(rows, s.tt) * s.to * s.tt;
+}
+
+// C: the tokens' codes as the plan wants them (in stages for tiles)
+int run_product(const Plan& p, const int8_t* C, int64_t ldc, const float* sx, int64_t rows, const int8_t* B, int64_t ldb,
+                const float* sw, int64_t out, int64_t in, const float* bias, int y_dtype, void* Y, int64_t ldy, int* part,
+                hipStream_t st) {
+    Int8GemmArgs g{};
+    g.W = B; g.ldw = ldb; g.out = out;
+    g.C = C; g.ldc = ldc; g.rows = rows;
+    g.in = (int)in;
+    g.sw = sw; g.sx = sx; g.bias = bias;
+    g.Y = Y; g.ldy = ldy; g.y_dtype = y_dtype;
+    g.nsplit = p.nsplit; g.part = part;
+    if (p.few) {
+        launch_few(g, st);
+    } else {
+        switch (p.shape) {
+            case 0: PTQ_TRY((launch_tile<256, 256, 4, 2, 2>(g, st))); break;
+            case 1: PTQ_TRY((launch_tile<128, 256, 2, 4, 3>(g, st))); break;
+            case 2: PTQ_TRY((launch_tile<128, 128, 2, 2, 4>(g, st))); break;
+            case 3: PTQ_TRY((launch_tile<64, 64, 2, 2, 5>(g, st))); break;
+            case 4: PTQ_TRY((launch_tile<64, 32, 2, 2, 5>(g, st))); break;
+            default: PTQ_TRY((launch_tile<32, 32, 2, 2, 8>(g, st)));
+        }
+    }
+    PTQ_LAUNCH_CHECK();
+    return PTQ_OK;
 }
 
 }  // namespace
 
 int launch_quantize_tokens_int8(const void* X, int x_dtype, int64_t rows, int64_t in, int64_t ldx, const float* s,
-                                int8_t* codes, int64_t ldc, int64_t pad, float* scales, hipStream_t st) {
-    if (rows == 0) return PTQ_OK;
-    if (x_dtype == PTQ_F32)
-        launch_tokens((const float*)X, rows, (int)in, ldx, s, codes, ldc, (int)pad, scales, st);
-    else
-        launch_tokens((const uint16_t*)X, rows, (int)in, ldx, s, codes, ldc, (int)pad, scales, st);
-    PTQ_LAUNCH_CHECK();
-    return PTQ_OK;
+                                int8_t* codes, int64_t ldc, float* scales, hipStream_t st) {
+    return launch_quantize(X, x_dtype, rows, in, ldx, s, codes, ldc, 0, scales, st);
 }
 
 size_t matmul_int8_ws_bytes(int64_t rows, int64_t out, int64_t in) {
-    (void)rows; (void)out; (void)in;
-    return 0;
+    const Plan p = plan(rows, out, in);
+    Sizer z;
+    z.take<int>(part_elems(p, rows, out));
+    if (!p.few && in % KT) z.take<int8_t>((size_t)(rows * tile_ldc(in)));
+    return z.bytes();
 }
 
 int run_matmul_int8(const int8_t* A, int64_t lda, const float* a_scales, int64_t rows, const int8_t* B, int64_t ldb,
                     const float* b_scales, int64_t out, int64_t in, const float* bias, int y_dtype, void* Y,
                     int64_t ldy, void* ws, size_t ws_bytes, hipStream_t st) {
-    (void)ws; (void)ws_bytes;
-    if (rows == 0 || out == 0) return PTQ_OK;
-    Int8GemmArgs g{};
-    g.W = B; g.ldw = ldb; g.out = out;
-    g.C = A; g.ldc = lda; g.rows = rows;
-    g.in = (int)in;
-    g.sw = b_scales; g.sx = a_scales; g.bias = bias;
-    g.Y = Y; g.ldy = ldy; g.y_dtype = y_dtype;
-    if (rows <= 16) launch_few<1, 1, 16, 2>(g, st);
-    else if (rows <= 32) launch_few<1, 2, 16, 2>(g, st);
-    else if (rows <= 48) launch_few<2, 3, 8, 2>(g, st);
-    else if (rows <= 64) launch_few<2, 4, 8, 2>(g, st);
-    else if (cdiv(rows, 256) * cdiv(out, 256) >= 200) PTQ_TRY((launch_tile<256, 256, 4, 2>(g, st)));
-    else PTQ_TRY((launch_tile<128, 128, 2, 2>(g, st)));
-    PTQ_LAUNCH_CHECK();
-    return PTQ_OK;
+    const Plan p = plan(rows, out, in);
+    Arena a(ws, ws_bytes);
+    int* part = a.take<int>(part_elems(p, rows, out));
+    if (!p.few && in % KT) {
+        const int64_t ldc = tile_ldc(in);
+        int8_t* c = a.take<int8_t>((size_t)(rows * ldc));
+        hipLaunchKernelGGL(stage_codes_kernel, dim3((unsigned)std::min<int64_t>(cdiv(rows * ldc, 2048), 8192)), dim3(256), 0,
+                           st, A, lda, rows, (int)in, c, ldc);
+        PTQ_LAUNCH_CHECK();
+        A = c;
+        lda = ldc;
+    }
+    return run_product(p, A, lda, a_scales, rows, B, ldb, b_scales, out, in, bias, y_dtype, Y, ldy, part, st);
 }
-
-// The tokens' codes are padded with zeros to whole stages of the product.
-int64_t linear_int8_ldc(int64_t in) { return cdiv(in, KT) * KT; }
 
 size_t linear_int8_ws_bytes(int64_t rows, int64_t out, int64_t in) {
     Sizer z;
-    z.take<int8_t>((size_t)(rows * linear_int8_ldc(in)));
+    z.take<int8_t>((size_t)(rows * tile_ldc(in)));
     z.take<float>((size_t)rows);
-    z.take<char>(matmul_int8_ws_bytes(rows, out, in));
+    z.take<int>(part_elems(plan(rows, out, in), rows, out));
     return z.bytes();
 }
 
 int run_linear_int8(const void* X, int x_dtype, int64_t rows, int64_t ldx, const float* s, const int8_t* codes,
                     int64_t ldb, const float* scales, int64_t out, int64_t in, const float* bias, int y_dtype, void* Y,
                     int64_t ldy, void* ws, size_t ws_bytes, hipStream_t st) {
-    if (rows == 0 || out == 0) return PTQ_OK;
+    const Plan p = plan(rows, out, in);
     Arena a(ws, ws_bytes);
-    const int64_t ldc = linear_int8_ldc(in);
+    const int64_t ldc = tile_ldc(in);
     int8_t* c = a.take<int8_t>((size_t)(rows * ldc));
     float* sx = a.take<float>((size_t)rows);
-    const size_t mb = matmul_int8_ws_bytes(rows, out, in);
-    char* mw = a.take<char>(mb);
-    PTQ_TRY(launch_quantize_tokens_int8(X, x_dtype, rows, in, ldx, s, c, ldc, ldc, sx, st));
-    return run_matmul_int8(c, ldc, sx, rows, codes, ldb, scales, out, in, bias, y_dtype, Y, ldy, mw, mb, st);
+    int* part = a.take<int>(part_elems(p, rows, out));
+    const int rl = p.few ? fused_rows_log2(rows, in) : -1;
+    if (rl >= 0) {
+        Int8GemmArgs g{};
+        g.W = codes; g.ldw = ldb; g.out = out;
+        g.rows = rows; g.in = (int)in;
+        g.sw = scales; g.bias = bias;
+        g.Y = Y; g.ldy = ldy; g.y_dtype = y_dtype;
+        if (x_dtype == PTQ_F32)
+            PTQ_TRY(s ? (launch_fused<float, true>(g, (const float*)X, ldx, s, rl, st))
+                      : (launch_fused<float, false>(g, (const float*)X, ldx, s, rl, st)));
+        else
+            PTQ_TRY(s ? (launch_fused<uint16_t, true>(g, (const uint16_t*)X, ldx, s, rl, st))
+                      : (launch_fused<uint16_t, false>(g, (const uint16_t*)X, ldx, s, rl, st)));
+        PTQ_LAUNCH_CHECK();
+        return PTQ_OK;
+    }
+    PTQ_TRY(launch_quantize(X, x_dtype, rows, in, ldx, s, c, ldc, p.few ? 0 : (int)(ldc - in), sx, st));
+    return run_product(p, c, ldc, sx, rows, codes, ldb, scales, out, in, bias, y_dtype, Y, ldy, part, st);
 }
 
 }  // namespace ptq
