@@ -229,6 +229,7 @@ int attention_int8_cache(const void* Q, int64_t ldq, void* O, int64_t ldo, float
     if (window > 0 && !causal) REFUSE("%s: a window needs causal = 1", fn);
     if (rows == 0 || batch == 0) return PTQ_OK;
     PTQ_TRY(check_cache_pointers(fn, c));
+    if (num_blocks < 1) REFUSE("%s: num_blocks = 0", fn);
     const int64_t n = (int64_t)heads * head_dim;
     PTQ_TRY(check_float_rows(fn, "Q", Q, dtype, n, ldq));
     PTQ_TRY(check_float_rows(fn, "O", O, dtype, n, ldo));

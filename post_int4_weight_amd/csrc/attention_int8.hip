@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 namespace ptq {
 namespace {
@@ -197,7 +198,7 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
     auto block_of = [&](int64_t pos) -> int {
         if (pos >= tl.hi) return -1;
         const int id = table[pos >> a.bs_log2];
-        return (id >= 0 && id < a.num_blocks) ? id : -1;
+        return (unsigned)id < (unsigned)a.num_blocks ? id : -1;
     };
     for (int it = s0 + wave; it < s1; it += NW) {
         const int64_t base = (int64_t)it * TK;
@@ -355,42 +356,60 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
 
 // Many query rows: 32 rows a wave, WAVES waves on the same keys. K and V go
 // through LDS once per workgroup, converted to fp16 on the way (a wave that
-// converted its own operands would spend more on that than on the products),
-// two buffers of TK tokens. S^T = K Q^T and O^T = V^T P^T as above, on 32x32x16
-// products: operand row r of a 32-token block is token 16 (r / 4 % 2) +
-// 4 (r / 8) + r % 4, so lane half hf holds tokens 16 hf .. 16 hf + 15, again in
-// one block of the cache: one S_k and one S_v per lane and score block, which
-// go into the exponent, w = 2^(s ck - m + log2 rv), and the sum of p takes
-// 1 / rv once per 16 values.
+// converted its own operands would spend more on that than on the products).
+// S^T = K Q^T and O^T = V^T P^T as above, on 32x32x16 products: operand row r
+// of a 32-token block is token 16 (r / 4 % 2) + 4 (r / 8) + r % 4, so lane
+// half hf holds tokens 16 hf .. 16 hf + 15, again in one block of the cache:
+// one S_k and one S_v per lane and score block, which go into the exponent,
+// w = 2^(s ck - m + log2 rv), and the sum of p takes 1 / rv once per 16 values.
 // m follows the row maximum only when that exceeds it by 2^LAZY (fp16 has the
 // room): most steps then leave the output accumulators alone.
+//
+// A step takes 512 + 512 matrix cycles a wave (D = 128) and as much again in
+// vector instructions, so the two are interleaved by hand: while the matrix
+// cores compute the scores of step it + 1, the exponentials of step it run
+// between them; the maximum of the new scores runs between the products with
+// V. Two waves share a SIMD. LDS holds K one step ahead of V.
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 constexpr float LAZY = 6.f;
+
+// x is computed here: without this the compiler moves the sums and maxima of a
+// step behind its products, and every probability stays in a register till then
+__device__ __forceinline__ void pin(float& x) { asm volatile("" : "+v"(x)); }
 constexpr int LOG2_RV_MIN = -60;   // below it the block adds nothing to the output (w underflows), only to the sum
+
+// f(integral_constant<int, I>) for I = B .. E - 1, in order
+template <int B, int E, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+    if constexpr (B < E) {
+        f(std::integral_constant<int, B>{});
+        static_for<B + 1, E>(f);
+    }
+}
 
 template <int D>
 struct TileLds {
     static constexpr int KROW = 2 * D, VROW = 2 * TK;       // bytes of a token of K, of a channel of V
-    static constexpr int K_BYTES = TK * KROW, V_BYTES = D * VROW, BUF = K_BYTES + V_BYTES;
-    static constexpr int BYTES = 2 * BUF;
+    static constexpr int K_BYTES = TK * KROW, V_BYTES = D * VROW;
+    static constexpr int BYTES = 2 * (K_BYTES + V_BYTES);
     // 16-byte slots, placed so that the 16 rows read together touch every bank
-    __device__ static __forceinline__ int k_at(int token, int chunk) {
-        const int f = D == 64 ? ((token >> 1) & 3) | ((token >> 2) & 4) : (token & 7) | ((token >> 1) & 8);
-        return token * KROW + 16 * (chunk ^ f);
+    __host__ __device__ static constexpr int k_swz(int token) {
+        return D == 64 ? ((token >> 1) & 3) | ((token >> 2) & 4) : (token & 7) | ((token >> 1) & 8);
     }
-    __device__ static __forceinline__ int v_at(int d, int chunk) { return K_BYTES + d * VROW + 16 * (chunk ^ ((d >> 1) & 7)); }
+    __device__ static __forceinline__ int k_at(int token, int chunk) { return token * KROW + 16 * (chunk ^ k_swz(token)); }
+    __device__ static __forceinline__ int v_at(int d, int chunk) { return d * VROW + 16 * (chunk ^ ((d >> 1) & 7)); }
 };
 
 template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) {
     constexpr int NT = sizeof(T) == 4 ? 2 : 1;
+    constexpr bool PIPE = NT == 1;                 // scores one step ahead (their second set takes 32 registers)
     constexpr int NTH = 64 * WAVES, NC = D / 16, ND = D / 32;
     constexpr int NCH = TK * D / 16;               // 16-byte chunks of K, and of V, in a step
-    constexpr int NL = 2 * NCH / NTH;              // loads per thread
-    static_assert(NL * NTH == 2 * NCH && NCH % 64 == 0, "staging loads");
+    static_assert(NCH % 64 == 0 && NCH <= NTH, "one chunk of each a thread");
     using L = TileLds<D>;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    __shared__ __attribute__((aligned(16))) float ssk[2][4], ssv[2][4];
+    __shared__ __attribute__((aligned(16))) float ssk[4][4], ssv[2][4];   // scales of steps it % 4, it % 2
 
     const int split = (int)(blockIdx.x % (unsigned)a.nsplit);
     const int64_t tile = blockIdx.x / (unsigned)a.nsplit;
@@ -399,21 +418,21 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
     // later tiles of a sequence have more keys: they go first
     if (!find_tile(a, gridDim.x / (unsigned)a.nsplit / a.kv_heads - 1 - tile / a.kv_heads, 32 * WAVES, tl)) return;
     const int per = split_steps(tl, a.nsplit);
-    const int s0 = tl.it0 + split * per, s1 = std::min(s0 + per, tl.it1);
+    const int s0 = __builtin_amdgcn_readfirstlane(tl.it0 + split * per);
+    const int s1 = __builtin_amdgcn_readfirstlane(std::min(s0 + per, tl.it1));
     if (split > 0 && s0 >= s1) return;
 
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int li = lane & 31, hf = lane >> 5;
     const bool idle = tl.f0 + 32 * wave >= tl.rows;     // no row of this wave: it only helps staging
     const int f = std::min(tl.f0 + 32 * wave + li, tl.rows - 1);
     const int64_t token = tl.off + f / a.group;
     const int qh = h * a.group + f % a.group;
     const int64_t pos = tl.pos0 + f / a.group;
-    const int64_t my_lo = row_lo(a, pos), my_hi = row_hi(a, pos, tl.len);
-    // keys of the wave's rows: steps within [w_lo, w_hi) need no mask, those outside [w_min, w_max) nothing at all
-    const int fa = std::min(tl.f0 + 32 * wave, tl.rows - 1), fb = std::min(tl.f0 + 32 * wave + 31, tl.rows - 1);
-    const int64_t pa = tl.pos0 + fa / a.group, pb = tl.pos0 + fb / a.group;
-    const int64_t w_min = row_lo(a, pa), w_lo = row_lo(a, pb), w_hi = row_hi(a, pa, tl.len), w_max = row_hi(a, pb, tl.len);
+    // keys of this lane's row; the wave's rows have none from w_max on
+    const int my_lo = (int)row_lo(a, pos), my_hi = (int)row_hi(a, pos, tl.len);
+    const int fb = std::min(tl.f0 + 32 * wave + 31, tl.rows - 1);
+    const int w_max = idle ? 0 : __builtin_amdgcn_readfirstlane((int)row_hi(a, tl.pos0 + fb / a.group, tl.len));
 
     f16x8 q[NT][NC];
     const float qs = load_query<T, NC, 32>((const T*)a.Q + token * a.ldq + (int64_t)qh * D, a.scale2, q,
@@ -426,177 +445,275 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
         for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
     float m = -INFINITY, l = tl.over ? __builtin_nanf("") : 0.f, R = 0.f, rcp_R = 0.f;
 
-    // staging: thread t moves chunks t + NTH i, first those of K (token, 16 channels), then those of V (channel, 16 tokens)
+    // Staging: one 16-byte chunk of K (16 channels of a token) and one of V (16 tokens of a channel) per thread and
+    // step. A wave's chunks lie in one block of the cache, of K because its tokens are neighbours, of V by the way the
+    // chunks are dealt: gpr = chunks of a channel that are neighbours in a block. So block ids and addresses are
+    // scalar. An id is read a step before the codes it leads to, and looked at only then: a wait for it in between
+    // would wait for the codes requested before it, too.
     const int32_t* table = a.table + (int64_t)tl.b * a.width;
-    const int64_t pool = (int64_t)a.bs * D;
-    uint4 raw[NL];
+    const int64_t pool = (int64_t)a.bs * D, stride = (int64_t)a.kv_heads * pool;
+    const int8_t* kp = a.k + (int64_t)h * pool;
+    const int8_t* vp = a.v + (int64_t)h * pool;
+    const int end = __builtin_amdgcn_readfirstlane((int)tl.hi), bmask = a.bs - 1;
+    const bool stages = NCH >= NTH || wave < NCH / 64;       // waves past the chunks have none
+    const int ktok = t / (D / 16), gpr = std::min(a.bs, TK) / 16, nblk = 4 / gpr;
+    const int vblk = wave % nblk, vd = (wave / nblk) * (64 / gpr) + lane / gpr, vgrp = vblk * gpr + lane % gpr;
+    const unsigned koff = (unsigned)((ktok & bmask) * D + 16 * (t % (D / 16)));
+    const unsigned voff = (unsigned)(vd * a.bs + ((16 * vgrp) & bmask));
+    // block of position p: one without a valid id, and positions past the keys, stand for some other block of the
+    // pool, whose codes are as good as any (the scale says NaN, or the mask leaves them out)
+    auto entry = [&](int p) { return table[std::min(p, end - 1) >> a.bs_log2]; };
+    auto ok = [&](int id) { return (unsigned)id < (unsigned)a.num_blocks; };
+    auto base = [&](const int8_t* from, int id) { return from + (int64_t)__builtin_amdgcn_readfirstlane(ok(id) ? id : 0) * stride; };
+    const int kfirst = 16 * (wave * 64 / (D / 16) / 16), vfirst = vblk * gpr * 16;      // first token of the wave's chunks' block
+    int idk = 0, idv = 0;
+    // lanes 0 .. 3 of wave 0 bring the scales of the step's four groups of 16 tokens
+    int ids_now = 0, ids_next = 0;
+    auto scale_of = [&](const float* scales, int it, int id) {
+        return it * TK + 16 * t >= end ? 0.f : ok(id) ? scales[(int64_t)id * a.kv_heads + h] : __builtin_nanf("");
+    };
+    uint4 rk, rv_;
     float sk_r = 0.f, sv_r = 0.f;
-    auto block_of = [&](int64_t p) -> int {
-        if (p >= tl.hi) return -1;
-        const int id = table[p >> a.bs_log2];
-        return (id >= 0 && id < a.num_blocks) ? id : -1;
+    auto fetch_k = [&](int it) {            // K of step it, whose id is in idk; then the next id
+        if (stages) rk = *(const uint4*)(base(kp, idk) + ((it * TK) & bmask) * D + koff);
+        idk = entry((it + 1) * TK + kfirst);
     };
-    auto fetch = [&](int it) {
-        const int64_t base = (int64_t)it * TK;
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int c = t + NTH * i, cv = c - NCH;
-            const bool isk = c < NCH;              // the same for a whole wave
-            const int tk = c / (D / 16);
-            const int64_t p = base + (isk ? tk & ~15 : 16 * (cv % 4));
-            const int b = block_of(p), slot = (int)(p & (a.bs - 1));
-            raw[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (b >= 0) {
-                const int64_t at = ((int64_t)b * a.kv_heads + h) * pool;
-                raw[i] = *(const uint4*)(isk ? a.k + at + (slot + (tk & 15)) * D + 16 * (c % (D / 16))
-                                             : a.v + at + (cv / 4) * a.bs + slot);
-            }
-        }
-        if (t < 4) {
-            const int64_t p = base + 16 * t;
-            const int b = block_of(p);
-            sk_r = sv_r = p < tl.hi ? __builtin_nanf("") : 0.f;
-            if (b >= 0) {
-                sk_r = a.ks[(int64_t)b * a.kv_heads + h];
-                sv_r = a.vs[(int64_t)b * a.kv_heads + h];
-            }
-        }
+    auto fetch_v = [&](int it) {
+        if (stages) rv_ = *(const uint4*)(base(vp, idv) + ((it * TK) & bmask) + voff);
+        idv = entry((it + 1) * TK + vfirst);
     };
-    auto stage = [&](int buf) {
-        unsigned char* S = smem + buf * L::BUF;
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int c = t + NTH * i, cv = c - NCH;
-            const bool isk = c < NCH;
-            const int row = isk ? c / (D / 16) : cv / 4, at = 2 * (isk ? c % (D / 16) : cv % 4);
-            *(f16x8*)(S + (isk ? L::k_at(row, at) : L::v_at(row, at))) = half8(raw[i].x, raw[i].y);
-            *(f16x8*)(S + (isk ? L::k_at(row, at + 1) : L::v_at(row, at + 1))) = half8(raw[i].z, raw[i].w);
+    const int ka = L::k_at(ktok, 2 * (t % (D / 16))), kb = L::k_at(ktok, 2 * (t % (D / 16)) + 1);
+    const int va = 2 * L::K_BYTES + L::v_at(vd, 2 * vgrp), vb = 2 * L::K_BYTES + L::v_at(vd, 2 * vgrp + 1);
+    auto stage_k = [&](int buf, int n) {      // n: which step of the split this is
+        if (stages) {
+            *(f16x8*)(smem + buf * L::K_BYTES + ka) = half8(rk.x, rk.y);
+            *(f16x8*)(smem + buf * L::K_BYTES + kb) = half8(rk.z, rk.w);
         }
-        if (t < 4) {
-            ssk[buf][t] = sk_r;
-            ssv[buf][t] = sv_r;
+        if (t < 4) ssk[n & 3][t] = sk_r;
+    };
+    auto stage_v = [&](int buf) {
+        if (stages) {
+            *(f16x8*)(smem + buf * L::V_BYTES + va) = half8(rv_.x, rv_.y);
+            *(f16x8*)(smem + buf * L::V_BYTES + vb) = half8(rv_.z, rv_.w);
         }
+        if (t < 4) ssv[buf][t] = sv_r;
     };
 
+    // operand fragments of this lane: the swizzle XORs their chunk, everything else is a constant offset
     const int krow = 16 * ((li >> 2) & 1) + 4 * (li >> 3) + (li & 3);   // token of operand row li
-    auto step = [&](int it, int buf) {
-        const int64_t base = (int64_t)it * TK;
-        if (base >= w_max || base + TK <= w_min) return;
-        const unsigned char* S = smem + buf * L::BUF;
-        const bool whole = base >= w_lo && base + TK <= w_hi;
-        f32x16 s[2];
+    int kat[NC], vat[4];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) kat[c] = L::k_at(krow, (2 * c) ^ hf);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) vat[k] = 2 * L::K_BYTES + L::v_at(li, (4 * (k >> 1) + (k & 1)) ^ (2 * hf));
+    auto k_frag = [&](int buf, int u, int c) {      // scores u (tokens 32 u ..), channels 16 c ..
+        return *(const f16x8*)(smem + kat[c] + buf * L::K_BYTES + 32 * u * L::KROW);
+    };
+    auto v_frag = [&](int buf, int i, int k) {      // channels 32 i .., tokens 32 (k / 2) + 16 hf + 8 (k % 2) ..
+        return *(const f16x8*)(smem + vat[k] + buf * L::V_BYTES + 32 * i * L::VROW);
+    };
+
+    float top[2];            // largest raw score of each block of 32 tokens
+    auto top_of = [&](f32x16 (&s)[2], int u, int r) {
+        top[u] = r ? fmaxf(fmaxf(top[u], s[u][r]), s[u][r + 1]) : fmaxf(s[u][0], s[u][1]);
+        pin(top[u]);
+    };
+    auto zero = [&](f32x16 (&s)[2]) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[u][r] = 0.f;
+    };
+    auto scores = [&](int buf, f32x16 (&s)[2]) {
+        zero(s);
+        static_for<0, 2 * NC>([&](auto jc) {
+            constexpr int j = decltype(jc)::value, u = j / NC, c = j % NC;
+            const f16x8 k = k_frag(buf, u, c);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[n][c], s[u], 0, 0, 0);
+        });
+#pragma unroll
+        for (int r = 0; r < 16; r += 2) {
+            top_of(s, 0, r);
+            top_of(s, 1, r);
+        }
+    };
+    auto scale_acc = [&](float x) {
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][r] *= x;
+    };
+
+    // step it with the scores s; sn receives those of step it + 1 (of whatever LDS holds after the last one).
+    // buf: the buffers of this step's K and V; the next step's K is in the other one
+    auto body = [&](auto masked_c, int buf, int it, f32x16 (&s)[2], f32x16 (&sn)[2]) {
+        constexpr bool MASKED = decltype(masked_c)::value;
+        constexpr bool AHEAD = PIPE && !MASKED;           // scores of the next step while this one runs; s and sn differ
+        const int g0 = it * TK + 16 * hf;           // this lane's tokens: g0 + 32 u + r
         float ck[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
+            ck[u] = ssk[(it - s0) & 3][2 * u + hf] * qs;
+            if constexpr (MASKED) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[u][r] = 0.f;
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const f16x8 k = *(const f16x8*)(S + L::k_at(32 * u + krow, 2 * c + hf));
-#pragma unroll
-                for (int n = 0; n < NT; ++n) s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[n][c], s[u], 0, 0, 0);
-            }
-            ck[u] = ssk[buf][2 * u + hf] * qs;
-        }
-        if (!whole) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int64_t g = base + 32 * u + 16 * hf;
-                const int lo = (int)std::max<int64_t>(my_lo - g, 0), hi = (int)std::min<int64_t>(my_hi - g, 16);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[u][r] = (r >= lo && r < hi) ? s[u][r] * ck[u] : -INFINITY;
+                for (int r = 0; r < 16; ++r) {
+                    const int g = g0 + 32 * u + r;
+                    s[u][r] = (g >= my_lo && g < my_hi) ? s[u][r] * ck[u] : -INFINITY;
+                    top[u] = r ? fmaxf(top[u], s[u][r]) : s[u][r];
+                }
                 ck[u] = 1.f;
             }
         }
-        float top[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            top[u] = s[u][0];
-#pragma unroll
-            for (int r = 1; r < 16; ++r) top[u] = fmaxf(top[u], s[u][r]);
-            top[u] *= ck[u];
-        }
-        float mx = fmaxf(top[0], top[1]);
+        float mx = fmaxf(top[0] * ck[0], top[1] * ck[1]);
         mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
         if (__any(mx > m + LAZY)) {
             const float m_new = fmaxf(m, mx);
             const float fall = m_new == m ? 1.f : exp2_fast(m - m_new);
             m = m_new;
             l *= fall;
-#pragma unroll
-            for (int i = 0; i < ND; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[i][r] *= fall;
+            scale_acc(fall);
         }
         const float m_sub = (m == -INFINITY ? 0.f : m) - PSHIFT;
+        const f32x4 sv4 = *(const f32x4*)ssv[buf];
         float big = 0.f;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) big = fmaxf(big, ssv[buf][g] < INFINITY ? ssv[buf][g] : 0.f);
-        if (big > R) {     // the same for every lane
-            const float fall = big < FLT_MIN ? 0.f : R * __fdiv_rn(1.f, big);
-            R = big;
+        for (int g = 0; g < 4; ++g) big = fmaxf(big, sv4[g] < INFINITY ? sv4[g] : 0.f);
+        if (__any(big > R)) {     // the same for every lane
             rcp_R = big < FLT_MIN ? 0.f : __fdiv_rn(1.f, big);
-#pragma unroll
-            for (int i = 0; i < ND; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[i][r] *= fall;
+            scale_acc(R * rcp_R);
+            R = big;
         }
-        f16x8 w[NT][2][2];
+        float lr[2], off[2], sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const float rv = ssv[buf][2 * u + hf] * rcp_R;
-            const float lr = rv != rv ? rv : fmaxf(__builtin_amdgcn_logf(rv), (float)LOG2_RV_MIN);   // v_log_f32: base 2
-            const float off = m_sub - lr;
-            float sum = 0.f;
-            const int64_t g = base + 32 * u + 16 * hf;
-            const int lo = (int)std::max<int64_t>(my_lo - g, 0), hi = (int)std::min<int64_t>(my_hi - g, 16);
-#pragma unroll
-            for (int r = 0; r < 16; r += 2) {
-                f32x2 e;
-                e[0] = exp2_fast(fmaf(s[u][r], ck[u], -off));
-                e[1] = exp2_fast(fmaf(s[u][r + 1], ck[u], -off));
-                if (!whole) {     // S_v of a block that is not this row's may be NaN
-                    if (r < lo || r >= hi) e[0] = 0.f;
-                    if (r + 1 < lo || r + 1 >= hi) e[1] = 0.f;
-                }
-                sum += e[0];
-                sum += e[1];
-                const f16x2 x = __builtin_convertvector(e, f16x2);
-                w[0][u][r >> 3][r & 7] = x[0];
-                w[0][u][r >> 3][(r & 7) + 1] = x[1];
-                if constexpr (NT == 2) {
-                    const f32x2 rest = {e[0] - (float)x[0], e[1] - (float)x[1]};
-                    const f16x2 y = __builtin_convertvector(rest, f16x2);
-                    w[1][u][r >> 3][r & 7] = y[0];
-                    w[1][u][r >> 3][(r & 7) + 1] = y[1];
-                }
-            }
-            l += whole || hi > lo ? sum * exp2_fast(-lr) : 0.f;
+            const float rv = (hf ? sv4[2 * u + 1] : sv4[2 * u]) * rcp_R;
+            lr[u] = rv != rv ? rv : fmaxf(__builtin_amdgcn_logf(rv), (float)LOG2_RV_MIN);   // v_log_f32: base 2
+            off[u] = m_sub - lr[u];
         }
+        f16x8 w[NT][2][2];
+        auto pair = [&](int u, int r) {      // two probabilities
+            f32x2 e;
+            e[0] = exp2_fast(fmaf(s[u][r], ck[u], -off[u]));
+            e[1] = exp2_fast(fmaf(s[u][r + 1], ck[u], -off[u]));
+            if constexpr (MASKED) {     // S_v of a block that is not this row's may be NaN
+                const int g = g0 + 32 * u + r;
+                if (g < my_lo || g >= my_hi) e[0] = 0.f;
+                if (g + 1 < my_lo || g + 1 >= my_hi) e[1] = 0.f;
+            }
+            sum[u] += e[0];
+            sum[u] += e[1];
+            pin(sum[u]);
+            const f16x2 x = __builtin_convertvector(e, f16x2);
+            w[0][u][r >> 3][r & 7] = x[0];
+            w[0][u][r >> 3][(r & 7) + 1] = x[1];
+            if constexpr (NT == 2) {
+                const f32x2 rest = {e[0] - (float)x[0], e[1] - (float)x[1]};
+                const f16x2 y = __builtin_convertvector(rest, f16x2);
+                w[1][u][r >> 3][r & 7] = y[0];
+                w[1][u][r >> 3][(r & 7) + 1] = y[1];
+            }
+        };
+        if constexpr (AHEAD) {
+            // block u of the new scores next to block u of the probabilities: three of the four are live at a time
+            f16x8 kf[2 * NC];
+            kf[0] = k_frag(buf ^ 1, 0, 0);
+            kf[1] = k_frag(buf ^ 1, 0, 1);
+            static_for<0, 2 * NC>([&](auto jc) {
+                constexpr int j = decltype(jc)::value, u = j / NC, c = j % NC;
+                if constexpr (j + 2 < 2 * NC) kf[j + 2] = k_frag(buf ^ 1, (j + 2) / NC, (j + 2) % NC);
+                if constexpr (c == 0) {
 #pragma unroll
-        for (int i = 0; i < ND; ++i)
+                    for (int r = 0; r < 16; ++r) sn[u][r] = 0.f;
+                }
+                sn[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[j], q[0][c], sn[u], 0, 0, 0);
+                static_for<8 * c / NC, 8 * (c + 1) / NC>([&](auto pc) { pair(u, 2 * decltype(pc)::value); });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        } else {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const f16x8 v = *(const f16x8*)(S + L::v_at(32 * i + li, 4 * u + 2 * hf + k));
+                for (int r = 0; r < 16; r += 2) pair(u, r);
+        }
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[n][u][k], acc[i], 0, 0, 0);
-                }
+        for (int u = 0; u < 2; ++u) {
+            const float add = sum[u] * exp2_fast(-lr[u]);
+            // 0 (1 / rv) of a foreign block may be NaN
+            if (!MASKED || (g0 + 32 * u + 16 > my_lo && g0 + 32 * u < my_hi)) l += add;
+        }
+        f16x8 vf[4 * ND];
+        vf[0] = v_frag(buf, 0, 0);
+        vf[1] = v_frag(buf, 1, 0);
+        static_for<0, 4 * ND>([&](auto jc) {
+            constexpr int j = decltype(jc)::value, i = j % ND, uk = j / ND;
+            if constexpr (j + 2 < 4 * ND) vf[j + 2] = v_frag(buf, (j + 2) % ND, (j + 2) / ND);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[j], w[n][uk >> 1][uk & 1], acc[i], 0, 0, 0);
+            if constexpr (AHEAD)
+                static_for<16 * j / (4 * ND), 16 * (j + 1) / (4 * ND)>([&](auto pc) {
+                    constexpr int pr = decltype(pc)::value;
+                    top_of(sn, pr >> 3, 2 * (pr & 7));
+                });
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        if constexpr (!AHEAD) scores(buf ^ 1, sn);
     };
 
     if (s0 < s1) {
-        fetch(s0);
-        stage(0);
-        __syncthreads();
-        for (int it = s0; it < s1; ++it) {
-            const int buf = (it - s0) & 1;
-            if (it + 1 < s1) fetch(it + 1);
-            if (!idle) step(it, buf);
-            if (it + 1 < s1) stage(buf ^ 1);
-            __syncthreads();
+        idk = entry(s0 * TK + kfirst);
+        idv = entry(s0 * TK + vfirst);
+        fetch_k(s0);
+        fetch_v(s0);
+        if (t < 4) {
+            ids_now = entry(s0 * TK + 16 * t);
+            ids_next = entry((s0 + 1) * TK + 16 * t);
+            sk_r = scale_of(a.ks, s0, ids_now);
+            sv_r = scale_of(a.vs, s0, ids_now);
         }
+        stage_k(0, 0);
+        stage_v(0);
+        fetch_k(s0 + 1);
+        if (t < 4) {
+            sk_r = scale_of(a.ks, s0 + 1, ids_next);
+            ids_now = ids_next;
+            ids_next = entry((s0 + 2) * TK + 16 * t);
+        }
+        stage_k(1, 1);
+        __syncthreads();
+        f32x16 sa[2];
+        scores(0, sa);
+        __syncthreads();      // the first step's staging reuses this buffer of K
+        auto step = [&](auto masked_c, int buf, int it, f32x16 (&s)[2], f32x16 (&sn)[2]) {
+            fetch_k(it + 2);      // past the last step: some block, into a buffer that nobody reads
+            fetch_v(it + 1);
+            if (t < 4) {
+                sk_r = scale_of(a.ks, it + 2, ids_next);
+                sv_r = scale_of(a.vs, it + 1, ids_now);
+                ids_now = ids_next;
+                ids_next = entry((it + 3) * TK + 16 * t);
+            }
+            if (!decltype(masked_c)::value || it * TK < w_max) body(masked_c, buf, it, s, sn);
+            stage_k(buf, it + 2 - s0);      // waves behind may still want this step's scales: not its slot
+            stage_v(buf ^ 1);
+            __syncthreads();
+        };
+        // steps that some row of the tile masks (the start of windows, the diagonal) go through loops of their own, with
+        // what makes the count of the others between them even on either side
+        int it = s0;
+        const int whole = std::min((int)((tl.lo_max + TK - 1) / TK), s1), last = std::min((int)(tl.hi_min / TK), s1);
+        for (; it < whole || ((it - s0) & 1 && it < s1); ++it) step(std::true_type{}, (it - s0) & 1, it, sa, sa);
+        if constexpr (PIPE) {
+            f32x16 sb[2];
+            for (; it + 1 < last; it += 2) {
+                step(std::false_type{}, 0, it, sa, sb);
+                step(std::false_type{}, 1, it + 1, sb, sa);
+            }
+        } else {
+            for (; it < last; ++it) step(std::false_type{}, (it - s0) & 1, it, sa, sa);
+        }
+        for (; it < s1; ++it) step(std::true_type{}, (it - s0) & 1, it, sa, sa);
     }
     if (idle) return;
 
@@ -665,19 +782,20 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int tr)
 
 int64_t tile_units(int64_t rows, int64_t batch, int group, int tr) { return rows * group / tr + batch; }
 
-// Waves of a tile: two per SIMD, or one at 256 channels (whose output and query
-// fragments take more than the 256 registers a second wave would leave).
-constexpr int tile_waves(int dim) { return dim == 256 ? 4 : 8; }
+// Waves of a tile: two per SIMD. At 256 channels the output and query
+// fragments of 32 rows leave no registers for the rest: those go through
+// attention_rows_kernel whatever the number of rows.
+constexpr int TILE_WAVES = 8;
 
 // Which kernel, and how many splits of the keys.
 struct Plan {
-    int tr;        // rows of a tile: TR, or 32 tile_waves
+    int tr;        // rows of a tile: TR, or 32 TILE_WAVES
     int nsplit;
 };
 Plan plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int block, int64_t width) {
     Plan p;
     const int group = heads / kv_heads;
-    p.tr = rows * group >= 64 * batch ? 32 * tile_waves(dim) : TR;
+    p.tr = dim <= 128 && rows * group >= 64 * batch ? 32 * TILE_WAVES : TR;
     const int64_t units = tile_units(rows, batch, group, p.tr) * kv_heads;
     const int64_t most = cdiv(width * block, TK * NW);
     const int64_t want = p.tr == TR ? 2048 : 256;
@@ -690,8 +808,7 @@ int launch(const AttnArgs& a, int tr, hipStream_t st) {
     const int64_t units = tile_units(a.g.rows, a.g.batch, a.group, tr) * a.kv_heads;
     if (tr == TR) {
         hipLaunchKernelGGL((attention_rows_kernel<T, D>), dim3((unsigned)(units * a.nsplit)), dim3(64 * NW), 0, st, a);
-    } else {
-        constexpr int TILE_WAVES = tile_waves(D);
+    } else if constexpr (D <= 128) {
         static bool ready = false;    // more than 64 KB of LDS
         if (!ready) {
             PTQ_HIP(hipFuncSetAttribute((const void*)attention_tile_kernel<T, D, TILE_WAVES>,

@@ -123,6 +123,7 @@ def test_attention(lib):
     _refused(lib, call(causal=0, window=3), "window")
     _refused(lib, call(lens=None), "seq_lens")
     _refused(lib, call(k=None), "cache pointer")
+    _refused(lib, call(nb=0), "num_blocks")
     _refused(lib, call(Q=ODD), "Q is not")
     _refused(lib, call(ldo=250), "row stride")
     _refused(lib, call(dt=9), "dtype")
