@@ -112,17 +112,6 @@ __device__ __forceinline__ int split_steps(const Tile& t, int nsplit) {
     return std::max(NW, (n + nsplit - 1) / nsplit);
 }
 
-template <typename T>
-__device__ __forceinline__ void store_row4(T* p, float a, float b, float c, float d);
-template <>
-__device__ __forceinline__ void store_row4<float>(float* p, float a, float b, float c, float d) {
-    *(float4*)p = make_float4(a, b, c, d);
-}
-template <>
-__device__ __forceinline__ void store_row4<uint16_t>(uint16_t* p, float a, float b, float c, float d) {
-    *(uint2*)p = make_uint2(bf16_pair(a, b), bf16_pair(c, d));
-}
-
 // One query row in fp16 terms: scaled by the power of two that brings its
 // largest element to [8, 16), negated for a negative softmax scale (scores
 // then grow with what the sums give). `at(c)`: first channel of fragment c.
@@ -340,7 +329,7 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
             if (split_out)
                 *(f32x4*)(a.part + (split * nflat + row * a.heads + head) * D + d0 + d) = o;
             else
-                store_row4((T*)a.O + row * a.ldo + (int64_t)head * D + d0 + d, o[0], o[1], o[2], o[3]);
+                store4((T*)a.O + row * a.ldo + (int64_t)head * D + d0 + d, o[0], o[1], o[2], o[3]);
         }
     }
     if (wave == 0 && lg == 0 && tl.f0 + li < tl.rows && (split_out || a.lse)) {
@@ -370,7 +359,6 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
 // cores compute the scores of step it + 1, the exponentials of step it run
 // between them; the maximum of the new scores runs between the products with
 // V. Two waves share a SIMD. LDS holds K one step ahead of V.
-typedef float f32x2 __attribute__((ext_vector_type(2)));
 constexpr float LAZY = 6.f;
 
 // x is computed here: without this the compiler moves the sums and maxima of a
@@ -732,7 +720,7 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
             if (split_out)
                 *(f32x4*)(a.part + (split * nflat + at) * D + d) = o;
             else
-                store_row4((T*)a.O + token * a.ldo + (int64_t)qh * D + d, o[0], o[1], o[2], o[3]);
+                store4((T*)a.O + token * a.ldo + (int64_t)qh * D + d, o[0], o[1], o[2], o[3]);
         }
     if (hf == 0 && (split_out || a.lse)) {
         const float lse2 = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) - PSHIFT + __log2f(l);
@@ -775,7 +763,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int tr)
     const float inv = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
 #pragma unroll
     for (int i = 0; i < D / 64; ++i)
-        store_row4((T*)a.O + row * a.ldo + (int64_t)head * D + 64 * i + 4 * c, o[i][0] * inv, o[i][1] * inv,
+        store4((T*)a.O + row * a.ldo + (int64_t)head * D + 64 * i + 4 * c, o[i][0] * inv, o[i][1] * inv,
                    o[i][2] * inv, o[i][3] * inv);
     if (a.lse && c == 0) a.lse[at] = L == 0.f ? -INFINITY : (M0 + __log2f(L)) * 0.6931471805599453f;
 }

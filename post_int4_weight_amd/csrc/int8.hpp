@@ -24,9 +24,19 @@ __device__ __forceinline__ float int8_scale(float amax) {
     return s < FLT_MIN ? 0.0f : s;
 }
 __device__ __forceinline__ float int8_inverse(float s) { return s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f; }
-// in [-127, 127] for every x (the code of a value whose set has S = NaN means nothing)
-__device__ __forceinline__ int int8_code(float x, float inv) {
-    return (int)rintf(fminf(fmaxf(x * inv, -127.0f), 127.0f));
+// The codes of 4 values, low byte first. Adding 3 * 2^22 to a product of at most
+// 2^22 rounds it to a whole number, half to even, and leaves that number's low
+// byte in the sum's. |x inv| <= 127 (1 + 2^-22) for every x of the set, so
+// nothing needs clamping; the product has its own rounding (no fma).
+__device__ __forceinline__ uint32_t int8_code4(float x0, float x1, float x2, float x3, float inv) {
+#pragma clang fp contract(off)
+    const float magic = 12582912.0f;
+    const uint32_t a = __float_as_uint(x0 * inv + magic), b = __float_as_uint(x1 * inv + magic);
+    const uint32_t c = __float_as_uint(x2 * inv + magic), d = __float_as_uint(x3 * inv + magic);
+    return __builtin_amdgcn_perm(b, a, 0x0c0c0400u) | __builtin_amdgcn_perm(d, c, 0x04000c0cu);
+}
+__device__ __forceinline__ uint2 int8_code8(const float (&v)[8], float inv) {
+    return make_uint2(int8_code4(v[0], v[1], v[2], v[3], inv), int8_code4(v[4], v[5], v[6], v[7], inv));
 }
 // max(|x|, a) that keeps a NaN of either
 __device__ __forceinline__ float amax_acc(float a, float x) {
@@ -50,11 +60,30 @@ __device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
     }
 }
 
-// float -> output element; bf16 rounds to nearest even and keeps NaN a NaN
-__device__ __forceinline__ uint32_t bf16_of(float f) {
-    return f != f ? 0x7fc0u : (uint32_t)float_to_bf16_bits(f);
+// 4 consecutive elements
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
+    const float4 a = *(const float4*)p;
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
 }
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) { return bf16_of(lo) | (bf16_of(hi) << 16); }
+__device__ __forceinline__ void load4(const uint16_t* p, float (&v)[4]) {
+    const uint2 a = *(const uint2*)p;
+    v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);
+    v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xffff0000u);
+}
+
+// float -> bf16, to nearest even, a NaN stays one (v_cvt_pk_bf16_f32)
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    union { bf16x2 h; uint32_t w; } u;
+    u.h = __builtin_convertvector(f32x2{lo, hi}, bf16x2);
+    return u.w;
+}
+__device__ __forceinline__ uint32_t bf16_of(float f) { return bf16_pair(f, 0.f) & 0xffffu; }
+__device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) { *(float4*)p = make_float4(a, b, c, d); }
+__device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, float d) {
+    *(uint2*)p = make_uint2(bf16_pair(a, b), bf16_pair(c, d));
+}
 
 // ----------------------------------------------------------- ragged batch --
 // Sequence b of a ragged batch owns rows offsets[b] .. offsets[b + 1]. A grid

@@ -56,15 +56,6 @@ struct CacheArgs {
     float* scales[2];
 };
 
-constexpr int KEEP = 4;      // chunks of 8 values a thread holds
-
-// codes of 8 values, low bytes first
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int k = 0; k < 8; ++k) w[k >> 2] |= (uint32_t)(uint8_t)int8_code(v[k], inv) << (8 * (k & 3));
-    return make_uint2(w[0], w[1]);
-}
 __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
     uint32_t r = 0;
 #pragma unroll
@@ -72,53 +63,82 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
     return r;
 }
 
-// grid (units, heads, 2): z = 0 keys, 1 values. blockDim.x * KEEP chunks cover a block.
+// Both kernels give a thread 64 codes of one (block, head): of K 8 chunks of 8
+// channels of a token, per = bs dim / 64 chunks apart; of V 4 channels of 16
+// tokens, so that a row of the input (or output) and 16 slots of the block are
+// both whole accesses and the codes change order in registers.
+// Threads of a workgroup: `per` for each head, as many heads as make 256.
+constexpr int CODES = 64;
+struct HeadThreads {
+    int h, q;            // head, thread within the head
+    int quad, seg;       // V: channels 4 quad .., slots 16 seg ..
+};
+__device__ __forceinline__ HeadThreads head_threads(const CacheArgs& a, int per) {
+    HeadThreads x;
+    const int t = threadIdx.x;
+    x.h = blockIdx.y * (blockDim.x / per) + t / per;
+    x.q = t % per;
+    x.quad = x.q % (a.dim / 4);
+    x.seg = x.q / (a.dim / 4);
+    return x;
+}
+
+// grid (units, groups of heads, 2): z = 0 keys, 1 values
 template <typename T>
-__global__ __launch_bounds__(1024) void kv_write_kernel(CacheArgs a, const T* __restrict__ K, int64_t ldk,
-                                                        const T* __restrict__ V, int64_t ldv) {
-    extern __shared__ __attribute__((aligned(16))) unsigned char image[];   // values: [dim][bs + 16]
-    __shared__ float red[16];
+__global__ __launch_bounds__(512) void kv_write_kernel(CacheArgs a, int per, const T* __restrict__ K, int64_t ldk,
+                                                       const T* __restrict__ V, int64_t ldv) {
+    __shared__ float red[8];
     BlockSpan s;
     if (!find_block(a.g, a.starts, a.table, a.width, a.num_blocks, a.bs, blockIdx.x, s) || s.id < 0) return;
     const bool val = blockIdx.z == 1;
-    const int h = blockIdx.y, t = threadIdx.x, nt = blockDim.x;
-    const T* X = val ? V : K;
+    const HeadThreads x = head_threads(a, per);
+    const bool live = x.h < a.heads;
     const int64_t ld = val ? ldv : ldk;
-    const int cpr = a.dim / 8, nch = a.bs * cpr;
-    float keep[KEEP][8];
-    float m = 0.f;
+    const T* X = (val ? V : K) + s.row0 * ld + (int64_t)std::min(x.h, a.heads - 1) * a.dim;
+    const int cpr = a.dim / 8;
+    // all loads at once: a slot that is not the call's reads the nearest one that is (the maximum is the same)
+    float v[CODES];      // K: [chunk][channel], V: [slot][channel]
+    if (!val) {
 #pragma unroll
-    for (int i = 0; i < KEEP; ++i) {
-        const int c = t + i * nt, slot = c / cpr;
-        if (c < nch && slot >= s.lo && slot < s.hi) {
-            load8(X + (s.row0 + slot) * ld + (int64_t)h * a.dim + 8 * (c % cpr), keep[i]);
+        for (int i = 0; i < 8; ++i) {
+            const int c = x.q + i * per, slot = std::min(std::max(c / cpr, s.lo), s.hi - 1);
+            load8(X + slot * ld + 8 * (c % cpr), *(float (*)[8])&v[8 * i]);
+        }
+    } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) m = amax_acc(m, keep[i][k]);
+        for (int i = 0; i < 16; ++i) {
+            const int slot = std::min(std::max(16 * x.seg + i, s.lo), s.hi - 1);
+            load4(X + slot * ld + 4 * x.quad, *(float (*)[4])&v[4 * i]);
         }
     }
+    float m = 0.f;
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) m = amax_acc(m, __shfl_xor(m, off, 64));
-    if ((t & 63) == 0) red[t >> 6] = m;
-    float* scale = a.scales[val] + (int64_t)s.id * a.heads + h;
-    const float S_old = s.lo > 0 ? *scale : 0.f;
-    __syncthreads();
-    m = 0.f;
-    for (int w = 0; w < nt / 64; ++w) m = amax_acc(m, red[w]);
+    for (int i = 0; i < CODES; ++i) m = amax_acc(m, v[i]);
+    float* scale = a.scales[val] + (int64_t)s.id * a.heads + x.h;
+    const float S_old = live && s.lo > 0 ? *scale : 0.f;
+    for (int off = (per < 64 ? per : 64) / 2; off > 0; off >>= 1) m = amax_acc(m, __shfl_xor(m, off, 64));
+    if (per > 64) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+        __syncthreads();
+        const int first = threadIdx.x / per * (per / 64);
+        m = 0.f;
+        for (int w = 0; w < per / 64; ++w) m = amax_acc(m, red[first + w]);
+    }
+    if (!live) return;
     float S = int8_scale(m);
     if (S_old >= S || S_old != S_old) S = S_old;
     const float inv = int8_inverse(S);
     const float ratio = S > S_old ? S_old * inv : 1.f;
     const bool recode = s.lo > 0 && ratio != 1.f;
-    if (t == 0) *scale = S;
-    int8_t* codes = a.codes[val] + ((int64_t)s.id * a.heads + h) * a.bs * a.dim;
+    if (x.q == 0) *scale = S;
+    int8_t* codes = a.codes[val] + ((int64_t)s.id * a.heads + x.h) * a.bs * a.dim;
     if (!val) {
 #pragma unroll
-        for (int i = 0; i < KEEP; ++i) {
-            const int c = t + i * nt, slot = c / cpr;
-            if (c >= nch) break;
+        for (int i = 0; i < 8; ++i) {
+            const int c = x.q + i * per, slot = c / cpr;
             uint2* p = (uint2*)(codes + 8 * c);
             if (slot >= s.lo && slot < s.hi) {
-                *p = codes8(keep[i], inv);
+                *p = int8_code8(*(float (*)[8])&v[8 * i], inv);
             } else if (slot < s.lo && recode) {
                 const uint2 w = *p;
                 *p = make_uint2(recode4(w.x, ratio), recode4(w.y, ratio));
@@ -126,90 +146,88 @@ __global__ __launch_bounds__(1024) void kv_write_kernel(CacheArgs a, const T* __
         }
         return;
     }
-    // values: the new codes go through LDS into channel-major order, then
-    // 16 slots of a channel at a time into the block
-    const int pitch = a.bs + 16;
+    const int s0 = 16 * x.seg;
+    const bool all = s.lo <= s0 && s.hi >= s0 + 16;
+    if (s.hi <= s0 || (s.lo >= s0 + 16 && !recode)) return;
 #pragma unroll
-    for (int i = 0; i < KEEP; ++i) {
-        const int c = t + i * nt, slot = c / cpr;
-        if (c < nch && slot >= s.lo && slot < s.hi) {
-            const uint2 w = codes8(keep[i], inv);
-            unsigned char* p = image + 8 * (c % cpr) * pitch + slot;
+    for (int k = 0; k < 4; ++k) {
+        uint4* p = (uint4*)(codes + (4 * x.quad + k) * a.bs + s0);
+        uint32_t n[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) p[k * pitch] = (unsigned char)((k < 4 ? w.x : w.y) >> (8 * (k & 3)));
-        }
-    }
-    __syncthreads();
-    const int seg = a.bs / 16;
-    for (int c = t; c < a.dim * seg; c += nt) {
-        const int d = c / seg, s0 = 16 * (c % seg);
-        uint4* p = (uint4*)(codes + d * a.bs + s0);
-        uint4 w = *(const uint4*)(image + d * pitch + s0);
-        if (s.lo > s0 || s.hi < s0 + 16) {       // not all of it is new
-            if (s.hi <= s0 || (s.lo >= s0 + 16 && !recode)) continue;
-            uint4 old = *p;
-            uint32_t* n = (uint32_t*)&w;
-            uint32_t* o = (uint32_t*)&old;
+        for (int q = 0; q < 4; ++q)
+            n[q] = int8_code4(v[16 * q + k], v[16 * q + 4 + k], v[16 * q + 8 + k], v[16 * q + 12 + k], inv);
+        if (!all) {      // slots before lo keep their codes, at the new scale; those from hi on their bytes
+            const uint4 w = *p;
+            const uint32_t old[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                uint32_t keepmask = 0, oldmask = 0;
+                uint32_t fresh = 0, held = 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int slot = s0 + 4 * q + k;
-                    if (slot >= s.lo && slot < s.hi) keepmask |= 0xffu << (8 * k);
-                    if (slot < s.lo) oldmask |= 0xffu << (8 * k);
+                for (int e = 0; e < 4; ++e) {
+                    const int slot = s0 + 4 * q + e;
+                    if (slot >= s.lo && slot < s.hi) fresh |= 0xffu << (8 * e);
+                    if (slot < s.lo) held |= 0xffu << (8 * e);
                 }
-                const uint32_t r = recode ? ((recode4(o[q], ratio) & oldmask) | (o[q] & ~oldmask)) : o[q];
-                n[q] = (n[q] & keepmask) | (r & ~keepmask);
+                const uint32_t o = recode ? (recode4(old[q], ratio) & held) | (old[q] & ~held) : old[q];
+                n[q] = (n[q] & fresh) | (o & ~fresh);
             }
         }
-        *p = w;
+        *p = make_uint4(n[0], n[1], n[2], n[3]);
     }
 }
 
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-    *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
-    *(float4*)(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
-    *(uint4*)p = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
-                            bf16_pair(v[6], v[7]));
-}
+// byte k of w as a number, times S
+__device__ __forceinline__ float value_of(uint32_t w, int k, float S) { return (float)(int8_t)(w >> (8 * k)) * S; }
 
 template <typename T>
-__global__ __launch_bounds__(256) void kv_read_kernel(CacheArgs a, T* __restrict__ K, int64_t ldk,
+__global__ __launch_bounds__(512) void kv_read_kernel(CacheArgs a, int per, T* __restrict__ K, int64_t ldk,
                                                       T* __restrict__ V, int64_t ldv) {
-    extern __shared__ __attribute__((aligned(16))) unsigned char image[];   // values: [dim][bs + 16]
     BlockSpan s;
     if (!find_block(a.g, a.starts, a.table, a.width, a.num_blocks, a.bs, blockIdx.x, s)) return;
-    const bool val = blockIdx.z == 1;
-    const int h = blockIdx.y, t = threadIdx.x, nt = blockDim.x;
-    T* X = val ? V : K;
-    const int64_t ld = val ? ldv : ldk;
-    const float S = s.id >= 0 ? a.scales[val][(int64_t)s.id * a.heads + h] : __builtin_nanf("");
-    const int8_t* codes = a.codes[val] + ((int64_t)std::max(s.id, 0) * a.heads + h) * a.bs * a.dim;
-    const bool have = s.id >= 0;
-    const int pitch = a.bs + 16, cpr = a.dim / 8;
-    if (val && have) {
-        const int seg = a.bs / 16;
-        for (int c = t; c < a.dim * seg; c += nt) {
-            const int d = c / seg, s0 = 16 * (c % seg);
-            *(uint4*)(image + d * pitch + s0) = *(const uint4*)(codes + d * a.bs + s0);
-        }
-        __syncthreads();
-    }
-    for (int c = t + s.lo * cpr; c < s.hi * cpr; c += nt) {
-        const int slot = c / cpr, d0 = 8 * (c % cpr);
-        uint2 w = make_uint2(0u, 0u);
-        if (have && !val) w = *(const uint2*)(codes + 8 * c);
-        float v[8];
+    const bool val = blockIdx.z == 1, have = s.id >= 0;
+    const HeadThreads x = head_threads(a, per);
+    if (x.h >= a.heads) return;
+    const int64_t ld = val ? ldv : ldk, at = (int64_t)(have ? s.id : 0) * a.heads + x.h;
+    T* X = (val ? V : K) + s.row0 * ld + (int64_t)x.h * a.dim;
+    const int8_t* codes = a.codes[val] + at * a.bs * a.dim;
+    const float S = have ? a.scales[val][at] : __builtin_nanf("");
+    if (!val) {
+        const int cpr = a.dim / 8;
+        uint2 w[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int8_t q = (have && val) ? (int8_t)image[(d0 + k) * pitch + slot]
-                                           : (int8_t)((k < 4 ? w.x : w.y) >> (8 * (k & 3)));
-            v[k] = (float)q * S;
+        for (int i = 0; i < 8; ++i) w[i] = have ? *(const uint2*)(codes + 8 * (x.q + i * per)) : make_uint2(0u, 0u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = x.q + i * per, slot = c / cpr;
+            if (slot < s.lo || slot >= s.hi) continue;
+            T* p = X + slot * ld + 8 * (c % cpr);
+            if constexpr (sizeof(T) == 2) {
+                *(uint4*)p = make_uint4(bf16_pair(value_of(w[i].x, 0, S), value_of(w[i].x, 1, S)),
+                                        bf16_pair(value_of(w[i].x, 2, S), value_of(w[i].x, 3, S)),
+                                        bf16_pair(value_of(w[i].y, 0, S), value_of(w[i].y, 1, S)),
+                                        bf16_pair(value_of(w[i].y, 2, S), value_of(w[i].y, 3, S)));
+            } else {
+                store4(p, value_of(w[i].x, 0, S), value_of(w[i].x, 1, S), value_of(w[i].x, 2, S), value_of(w[i].x, 3, S));
+                store4(p + 4, value_of(w[i].y, 0, S), value_of(w[i].y, 1, S), value_of(w[i].y, 2, S), value_of(w[i].y, 3, S));
+            }
         }
-        store8(X + (s.row0 + slot) * ld + (int64_t)h * a.dim + d0, v);
+        return;
+    }
+    uint4 w[4];          // 16 slots of each channel
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        w[k] = have ? *(const uint4*)(codes + (4 * x.quad + k) * a.bs + 16 * x.seg) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t c[4] = {((const uint32_t*)&w[0])[q], ((const uint32_t*)&w[1])[q], ((const uint32_t*)&w[2])[q],
+                               ((const uint32_t*)&w[3])[q]};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int slot = 16 * x.seg + 4 * q + e;
+            if (slot >= s.lo && slot < s.hi)
+                store4(X + slot * ld + 4 * x.quad, value_of(c[0], e, S), value_of(c[1], e, S), value_of(c[2], e, S),
+                       value_of(c[3], e, S));
+        }
     }
 }
 
@@ -223,9 +241,18 @@ CacheArgs cache_args(const KVCacheInt8& c, const RaggedRows& r) {
     return a;
 }
 
-// units of ragged_find(mul = 1, div = bs, extra = 2)
-dim3 block_grid(const KVCacheInt8& c, const RaggedRows& r) {
-    return dim3((unsigned)(r.rows / c.block + 2 * r.batch), (unsigned)c.heads, 2);
+// units of ragged_find(mul = 1, div = bs, extra = 2) x groups of heads x {K, V}, and the threads of a workgroup
+struct Launch {
+    dim3 grid, block;
+    int per;
+};
+Launch block_launch(const KVCacheInt8& c, const RaggedRows& r) {
+    Launch l;
+    l.per = c.block * c.dim / CODES;
+    const int nt = std::max(l.per, std::min(256, (int)cdiv((int64_t)l.per * c.heads, 64) * 64));
+    l.block = dim3((unsigned)nt);
+    l.grid = dim3((unsigned)(r.rows / c.block + 2 * r.batch), (unsigned)cdiv(c.heads, nt / l.per), 2);
+    return l;
 }
 
 }  // namespace
@@ -234,13 +261,12 @@ int launch_kv_write(const KVCacheInt8& c, const RaggedRows& r, int dtype, const 
                     int64_t ldv, hipStream_t st) {
     if (r.rows == 0 || r.batch == 0) return PTQ_OK;
     const CacheArgs a = cache_args(c, r);
-    const int nt = std::max(64, c.block * c.dim / (8 * KEEP));
-    const int lds = c.dim * (c.block + 16);
+    const Launch l = block_launch(c, r);
     if (dtype == PTQ_F32)
-        hipLaunchKernelGGL(kv_write_kernel<float>, block_grid(c, r), dim3(nt), lds, st, a, (const float*)K, ldk,
-                           (const float*)V, ldv);
+        hipLaunchKernelGGL(kv_write_kernel<float>, l.grid, l.block, 0, st, a, l.per, (const float*)K, ldk, (const float*)V,
+                           ldv);
     else
-        hipLaunchKernelGGL(kv_write_kernel<uint16_t>, block_grid(c, r), dim3(nt), lds, st, a, (const uint16_t*)K, ldk,
+        hipLaunchKernelGGL(kv_write_kernel<uint16_t>, l.grid, l.block, 0, st, a, l.per, (const uint16_t*)K, ldk,
                            (const uint16_t*)V, ldv);
     PTQ_LAUNCH_CHECK();
     return PTQ_OK;
@@ -250,13 +276,12 @@ int launch_kv_read(const KVCacheInt8& c, const RaggedRows& r, int dtype, void* K
                    hipStream_t st) {
     if (r.rows == 0 || r.batch == 0) return PTQ_OK;
     const CacheArgs a = cache_args(c, r);
-    const int lds = c.dim * (c.block + 16);
+    const Launch l = block_launch(c, r);
     if (dtype == PTQ_F32)
-        hipLaunchKernelGGL(kv_read_kernel<float>, block_grid(c, r), dim3(256), lds, st, a, (float*)K, ldk, (float*)V,
-                           ldv);
+        hipLaunchKernelGGL(kv_read_kernel<float>, l.grid, l.block, 0, st, a, l.per, (float*)K, ldk, (float*)V, ldv);
     else
-        hipLaunchKernelGGL(kv_read_kernel<uint16_t>, block_grid(c, r), dim3(256), lds, st, a, (uint16_t*)K, ldk,
-                           (uint16_t*)V, ldv);
+        hipLaunchKernelGGL(kv_read_kernel<uint16_t>, l.grid, l.block, 0, st, a, l.per, (uint16_t*)K, ldk, (uint16_t*)V,
+                           ldv);
     PTQ_LAUNCH_CHECK();
     return PTQ_OK;
 }

@@ -70,10 +70,7 @@ __global__ __launch_bounds__(1024) void quantize_tokens_kernel(const T* __restri
     int8_t* out = codes + row * ldc;
     const int whole = in / KT * (KT / 8);     // the last stage's codes move up by shift, zeros go before them
     auto store = [&](int c, const float (&v)[8]) {
-        uint32_t w[2] = {0u, 0u};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k >> 2] |= (uint32_t)(uint8_t)int8_code(v[k], inv) << (8 * (k & 3));
-        *(uint2*)(out + 8 * c + (c >= whole ? shift : 0)) = make_uint2(w[0], w[1]);
+        *(uint2*)(out + 8 * c + (c >= whole ? shift : 0)) = int8_code8(v, inv);
     };
 #pragma unroll
     for (int i = 0; i < QKEEP; ++i) {
@@ -102,7 +99,7 @@ struct Int8GemmArgs {
 // operand and the 16 consecutive codes at 16 (l / 16) of the 64-deep step;
 // register r of lane l holds W row 4 (l / 16) + r, token l % 16, so a lane
 // stores 4 consecutive outputs of one token.
-__device__ __forceinline__ void store4(const Int8GemmArgs& g, int64_t o, int64_t token, i32x4 acc) {
+__device__ __forceinline__ void store_out(const Int8GemmArgs& g, int64_t o, int64_t token, i32x4 acc) {
     if (token >= g.rows) return;
     const float sx = g.sx[token];
     float y[4];
@@ -222,7 +219,7 @@ __global__ __launch_bounds__(64 * FW) void matmul_int8_few_kernel(Int8GemmArgs g
     i32x4 sum = part[0][lane];
 #pragma unroll
     for (int v = 1; v < FW; ++v) sum += part[v][lane];
-    store4(g, o0 + 4 * lg, r0 + li, sum);
+    store_out(g, o0 + 4 * lg, r0 + li, sum);
 }
 
 // The same with the tokens quantized in every workgroup, while its first
@@ -276,12 +273,7 @@ __global__ __launch_bounds__(64 * FW) void linear_int8_few_kernel(Int8GemmArgs g
 #pragma unroll
         for (int i = 0; i < FKEEP; ++i) {
             const int c = (wave % wpr + i * wpr) * 64 + lane;
-            if (c < nch) {
-                uint32_t x[2] = {0u, 0u};
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[k >> 2] |= (uint32_t)(uint8_t)int8_code(keep[i][k], inv) << (8 * (k & 3));
-                *(uint2*)(out + 8 * c) = make_uint2(x[0], x[1]);
-            }
+            if (c < nch) *(uint2*)(out + 8 * c) = int8_code8(keep[i], inv);
         }
         if (wave % wpr == 0 && nch + lane < (pitch - 16) / 8) *(uint2*)(out + 8 * (nch + lane)) = make_uint2(0u, 0u);
     }
@@ -295,7 +287,7 @@ __global__ __launch_bounds__(64 * FW) void linear_int8_few_kernel(Int8GemmArgs g
 #pragma unroll
     for (int v = 1; v < FW; ++v) sum += part[v][lane];
     g.sx = sx;
-    store4(g, o0 + 4 * lg, li, sum);
+    store_out(g, o0 + 4 * lg, li, sum);
 }
 
 // ---- many tokens: tiles of TO outputs x TT tokens, WO x WT waves, stages of
