@@ -60,12 +60,12 @@ __device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
     }
 }
 
-// 4 consecutive elements
-__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
-    const float4 a = *(const float4*)p;
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+// 4 or 2 consecutive elements
+__device__ __forceinline__ void load_n(const float* p, float (&v)[2]) {
+    const float2 a = *(const float2*)p;
+    v[0] = a.x; v[1] = a.y;
 }
-__device__ __forceinline__ void load4(const uint16_t* p, float (&v)[4]) {
+__device__ __forceinline__ void load_n(const uint16_t* p, float (&v)[4]) {
     const uint2 a = *(const uint2*)p;
     v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);
     v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xffff0000u);

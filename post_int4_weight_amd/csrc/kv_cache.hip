@@ -63,44 +63,51 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
     return r;
 }
 
-// Both kernels give a thread 64 codes of one (block, head): of K 8 chunks of 8
-// channels of a token, per = bs dim / 64 chunks apart; of V 4 channels of 16
-// tokens, so that a row of the input (or output) and 16 slots of the block are
-// both whole accesses and the codes change order in registers.
+// Both kernels give a thread 16 NV codes of one (block, head): of K 2 NV chunks
+// of 8 channels of a token, per = bs dim / (16 NV) chunks apart; of V NV
+// channels of 16 tokens, so that a row of the input (or output) and 16 slots
+// of the block are both whole accesses and the codes change order in registers.
+// NV = 4, or 2 where fp32 values are held until the block's maximum is known
+// (64 of them took 115 registers a thread, and the write 29 us where NV = 2
+// takes 16.5: 61 prompts, 12 heads of 64).
 // Threads of a workgroup: `per` for each head, as many heads as make 256.
-constexpr int CODES = 64;
+template <typename T>
+constexpr int write_nv() { return sizeof(T) == 4 ? 2 : 4; }
+constexpr int READ_NV = 4;
 struct HeadThreads {
     int h, q;            // head, thread within the head
-    int quad, seg;       // V: channels 4 quad .., slots 16 seg ..
+    int quad, seg;       // V: channels NV quad .., slots 16 seg ..
 };
+template <int NV>
 __device__ __forceinline__ HeadThreads head_threads(const CacheArgs& a, int per) {
     HeadThreads x;
     const int t = threadIdx.x;
     x.h = blockIdx.y * (blockDim.x / per) + t / per;
     x.q = t % per;
-    x.quad = x.q % (a.dim / 4);
-    x.seg = x.q / (a.dim / 4);
+    x.quad = x.q % (a.dim / NV);
+    x.seg = x.q / (a.dim / NV);
     return x;
 }
 
 // grid (units, groups of heads, 2): z = 0 keys, 1 values
 template <typename T>
-__global__ __launch_bounds__(512) void kv_write_kernel(CacheArgs a, int per, const T* __restrict__ K, int64_t ldk,
+__global__ __launch_bounds__(sizeof(T) == 4 ? 1024 : 512) void kv_write_kernel(CacheArgs a, int per, const T* __restrict__ K, int64_t ldk,
                                                        const T* __restrict__ V, int64_t ldv) {
-    __shared__ float red[8];
+    constexpr int NV = write_nv<T>();
+    __shared__ float red[16];
     BlockSpan s;
     if (!find_block(a.g, a.starts, a.table, a.width, a.num_blocks, a.bs, blockIdx.x, s) || s.id < 0) return;
     const bool val = blockIdx.z == 1;
-    const HeadThreads x = head_threads(a, per);
+    const HeadThreads x = head_threads<NV>(a, per);
     const bool live = x.h < a.heads;
     const int64_t ld = val ? ldv : ldk;
     const T* X = (val ? V : K) + s.row0 * ld + (int64_t)std::min(x.h, a.heads - 1) * a.dim;
     const int cpr = a.dim / 8;
     // all loads at once: a slot that is not the call's reads the nearest one that is (the maximum is the same)
-    float v[CODES];      // K: [chunk][channel], V: [slot][channel]
+    float v[16 * NV];      // K: [chunk][channel], V: [slot][channel]
     if (!val) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 2 * NV; ++i) {
             const int c = x.q + i * per, slot = std::min(std::max(c / cpr, s.lo), s.hi - 1);
             load8(X + slot * ld + 8 * (c % cpr), *(float (*)[8])&v[8 * i]);
         }
@@ -108,12 +115,12 @@ __global__ __launch_bounds__(512) void kv_write_kernel(CacheArgs a, int per, con
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int slot = std::min(std::max(16 * x.seg + i, s.lo), s.hi - 1);
-            load4(X + slot * ld + 4 * x.quad, *(float (*)[4])&v[4 * i]);
+            load_n(X + slot * ld + NV * x.quad, *(float (*)[NV])&v[NV * i]);
         }
     }
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < CODES; ++i) m = amax_acc(m, v[i]);
+    for (int i = 0; i < 16 * NV; ++i) m = amax_acc(m, v[i]);
     float* scale = a.scales[val] + (int64_t)s.id * a.heads + x.h;
     const float S_old = live && s.lo > 0 ? *scale : 0.f;
     for (int off = (per < 64 ? per : 64) / 2; off > 0; off >>= 1) m = amax_acc(m, __shfl_xor(m, off, 64));
@@ -134,7 +141,7 @@ __global__ __launch_bounds__(512) void kv_write_kernel(CacheArgs a, int per, con
     int8_t* codes = a.codes[val] + ((int64_t)s.id * a.heads + x.h) * a.bs * a.dim;
     if (!val) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 2 * NV; ++i) {
             const int c = x.q + i * per, slot = c / cpr;
             uint2* p = (uint2*)(codes + 8 * c);
             if (slot >= s.lo && slot < s.hi) {
@@ -150,12 +157,12 @@ __global__ __launch_bounds__(512) void kv_write_kernel(CacheArgs a, int per, con
     const bool all = s.lo <= s0 && s.hi >= s0 + 16;
     if (s.hi <= s0 || (s.lo >= s0 + 16 && !recode)) return;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        uint4* p = (uint4*)(codes + (4 * x.quad + k) * a.bs + s0);
+    for (int k = 0; k < NV; ++k) {
+        uint4* p = (uint4*)(codes + (NV * x.quad + k) * a.bs + s0);
         uint32_t n[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            n[q] = int8_code4(v[16 * q + k], v[16 * q + 4 + k], v[16 * q + 8 + k], v[16 * q + 12 + k], inv);
+            n[q] = int8_code4(v[(4 * q) * NV + k], v[(4 * q + 1) * NV + k], v[(4 * q + 2) * NV + k], v[(4 * q + 3) * NV + k], inv);
         if (!all) {      // slots before lo keep their codes, at the new scale; those from hi on their bytes
             const uint4 w = *p;
             const uint32_t old[4] = {w.x, w.y, w.z, w.w};
@@ -185,7 +192,7 @@ __global__ __launch_bounds__(512) void kv_read_kernel(CacheArgs a, int per, T* _
     BlockSpan s;
     if (!find_block(a.g, a.starts, a.table, a.width, a.num_blocks, a.bs, blockIdx.x, s)) return;
     const bool val = blockIdx.z == 1, have = s.id >= 0;
-    const HeadThreads x = head_threads(a, per);
+    const HeadThreads x = head_threads<READ_NV>(a, per);
     if (x.h >= a.heads) return;
     const int64_t ld = val ? ldv : ldk, at = (int64_t)(have ? s.id : 0) * a.heads + x.h;
     T* X = (val ? V : K) + s.row0 * ld + (int64_t)x.h * a.dim;
@@ -246,9 +253,9 @@ struct Launch {
     dim3 grid, block;
     int per;
 };
-Launch block_launch(const KVCacheInt8& c, const RaggedRows& r) {
+Launch block_launch(const KVCacheInt8& c, const RaggedRows& r, int nv) {
     Launch l;
-    l.per = c.block * c.dim / CODES;
+    l.per = c.block * c.dim / (16 * nv);
     const int nt = std::max(l.per, std::min(256, (int)cdiv((int64_t)l.per * c.heads, 64) * 64));
     l.block = dim3((unsigned)nt);
     l.grid = dim3((unsigned)(r.rows / c.block + 2 * r.batch), (unsigned)cdiv(c.heads, nt / l.per), 2);
@@ -261,7 +268,7 @@ int launch_kv_write(const KVCacheInt8& c, const RaggedRows& r, int dtype, const 
                     int64_t ldv, hipStream_t st) {
     if (r.rows == 0 || r.batch == 0) return PTQ_OK;
     const CacheArgs a = cache_args(c, r);
-    const Launch l = block_launch(c, r);
+    const Launch l = block_launch(c, r, dtype == PTQ_F32 ? write_nv<float>() : write_nv<uint16_t>());
     if (dtype == PTQ_F32)
         hipLaunchKernelGGL(kv_write_kernel<float>, l.grid, l.block, 0, st, a, l.per, (const float*)K, ldk, (const float*)V,
                            ldv);
@@ -276,7 +283,7 @@ int launch_kv_read(const KVCacheInt8& c, const RaggedRows& r, int dtype, void* K
                    hipStream_t st) {
     if (r.rows == 0 || r.batch == 0) return PTQ_OK;
     const CacheArgs a = cache_args(c, r);
-    const Launch l = block_launch(c, r);
+    const Launch l = block_launch(c, r, READ_NV);
     if (dtype == PTQ_F32)
         hipLaunchKernelGGL(kv_read_kernel<float>, l.grid, l.block, 0, st, a, l.per, (float*)K, ldk, (float*)V, ldv);
     else
