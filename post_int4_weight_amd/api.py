@@ -391,9 +391,11 @@ def layer_output_error(X, W, codes, scales, g_idx=None, zeros=None, s=None, grou
 
 def _vector(t, n: int, dtype, name: str):
     """t as n dense values of dtype (any shape with that many), or None."""
-    if t is not None and (t.dtype != dtype or t.numel() != n or not t.is_contiguous()):
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be {n} contiguous {dtype} values")
-    return _ptr(t)
+    return t.data_ptr()
 
 
 def _codes(t: torch.Tensor, name: str):
@@ -481,21 +483,24 @@ class KVCacheInt8(NamedTuple):
         return cls(codes(block_size, head_dim), codes(head_dim, block_size), scales(), scales())
 
     def _sizes(self):
-        nb, h, bs, d = self.k.shape
-        for t, shape, dtype in ((self.k, (nb, h, bs, d), torch.int8), (self.v, (nb, h, d, bs), torch.int8),
-                                (self.k_scales, (nb, h), torch.float32), (self.v_scales, (nb, h), torch.float32)):
-            if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
-                raise ValueError(f"cache tensor must be contiguous {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+        k, v, ks, vs = self
+        nb, h, bs, d = k.shape
+        if (v.shape != (nb, h, d, bs) or ks.shape != (nb, h) or vs.shape != (nb, h) or k.dtype != torch.int8
+                or v.dtype != torch.int8 or ks.dtype != torch.float32 or vs.dtype != torch.float32
+                or not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous())):
+            raise ValueError("cache tensors must be contiguous: int8 k [blocks, heads, block_size, dim] and v "
+                             "[blocks, heads, dim, block_size], fp32 scales [blocks, heads]")
         return nb, h, d, bs
 
 
 def _heads3(t, rows, heads, dim, name):
     """Row stride of a [rows, heads, dim] tensor whose heads follow each other."""
-    if tuple(t.shape) != (rows, heads, dim):
+    if t.shape != (rows, heads, dim):
         raise ValueError(f"{name} must be {(rows, heads, dim)}, got {tuple(t.shape)}")
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != dim):
         raise ValueError(f"{name}: the heads of a row must follow each other")
-    return t.stride(0) if rows > 1 else heads * dim
+    return s0 if rows > 1 else heads * dim
 
 
 def _ragged(offsets, starts, block_table, name):

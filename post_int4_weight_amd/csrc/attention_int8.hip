@@ -25,8 +25,10 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int TR = 16;       // query rows (tokens x grouped heads) of a tile
 constexpr int TK = 64;       // tokens per step of a wave
-constexpr int NW = 4;        // waves of a workgroup, on different steps
-constexpr float PSHIFT = 8.f;   // p in [0, 2^8]: fp16 keeps 11 bits down to 2^-22 of the largest
+constexpr float PSHIFT = 8.f;   // p up to 2^8: fp16 keeps 11 bits down to 2^-22 of the largest
+// The reference m of a row follows its maximum only when that exceeds it by
+// 2^LAZY (fp16 has the room): most steps leave the output accumulators alone.
+constexpr float LAZY = 6.f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -47,7 +49,7 @@ __device__ __forceinline__ f16x8 half8(uint32_t a, uint32_t b) {
 
 struct AttnArgs {
     Ragged g;
-    const int32_t* lens; const int32_t* table; int64_t width;
+    const int32_t* table; int64_t width;      // g.starts: the lengths
     int heads, kv_heads, group, dim, bs, bs_log2;
     int64_t num_blocks;
     const int8_t* k; const int8_t* v; const float* ks; const float* vs;
@@ -83,15 +85,14 @@ __device__ __forceinline__ int64_t row_hi(const AttnArgs& a, int64_t pos, int64_
 }
 
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t unit, int tr, Tile& t) {
-    int64_t local;
-    t.b = ragged_find(a.g, unit, a.group, tr, 1, &local);
-    t.off = ragged_offset(a.g, t.b);
-    const int64_t n = ragged_offset(a.g, t.b + 1) - t.off;
-    const int64_t rows = n * a.group, f0 = local * tr;
+    const RaggedUnit u = ragged_find(a.g, unit, a.group, tr, 1);
+    t.b = u.b;
+    t.off = u.off;
+    const int64_t n = u.rows, rows = n * a.group, f0 = u.local * tr;
     if (n <= 0 || f0 >= rows) return false;
     t.rows = (int)rows;
     t.f0 = (int)f0;
-    t.len = std::max<int64_t>(a.lens[t.b], 0);
+    t.len = std::max(u.start, 0);
     t.pos0 = t.len - n;
     t.over = t.len > a.width * a.bs;
     t.len = std::min<int64_t>(t.len, a.width * a.bs);
@@ -106,10 +107,11 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t unit, int t
     return true;
 }
 
-// Steps of split s of a tile: an even share, at least one step a wave.
+// Steps of a split of a tile: an even share, at least MIN_STEPS.
+constexpr int MIN_STEPS = 4;
 __device__ __forceinline__ int split_steps(const Tile& t, int nsplit) {
     const int n = t.it1 - t.it0;
-    return std::max(NW, (n + nsplit - 1) / nsplit);
+    return std::max(MIN_STEPS, (n + nsplit - 1) / nsplit);
 }
 
 // One query row in fp16 terms: scaled by the power of two that brings its
@@ -151,7 +153,15 @@ __device__ __forceinline__ float load_query(const T* p, float scale2, f16x8 (&q)
 // of score block t is token 16 (r / 4) + 4 t + r % 4): V comes as one
 // 16-byte load per channel, and a lane's tokens lie in one block of the cache
 // (its size is a multiple of 16), so a lane needs one S_k and one S_v a step.
-template <typename T, int D>
+// The waves of a workgroup take every NW-th step; the codes of a wave's next
+// step are on their way while it works on one, the block ids one step earlier.
+template <int D>
+struct StepCodes {
+    uint4 k[4][D / 64], v[D / 16];
+    float sk, sv;
+};
+
+template <typename T, int D, int NW>
 __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
     constexpr int NT = sizeof(T) == 4 ? 2 : 1;    // fp16 terms of q and of the probabilities
     constexpr int NC = D / 32;                    // 32-deep steps of q.k
@@ -164,77 +174,75 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
     const int s0 = tl.it0 + split * per, s1 = std::min(s0 + per, tl.it1);
     if (split > 0 && s0 >= s1) return;
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int li = lane & 15, lg = lane >> 4;
     const int f = std::min(tl.f0 + li, tl.rows - 1);
     const int64_t token = tl.off + f / a.group;
     const int qh = h * a.group + f % a.group;
     const int64_t pos = tl.pos0 + f / a.group;
-    const int64_t my_lo = row_lo(a, pos), my_hi = row_hi(a, pos, tl.len);
-
-    // q: operand column li, channels 64 (c / 2) + 16 lg + 8 (c % 2) + 0..7 of step c
-    f16x8 q[NT][NC];
-    const float qs = load_query<T, NC, 16>((const T*)a.Q + token * a.ldq + (int64_t)qh * D, a.scale2, q,
-                                           [&](int c) { return 64 * (c / 2) + 16 * lg + 8 * (c % 2); });
-
-    f32x4 acc[D / 16];
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, l = tl.over ? __builtin_nanf("") : 0.f, R = 0.f;
+    const int my_lo = (int)row_lo(a, pos), my_hi = (int)row_hi(a, pos, tl.len);
 
     const int32_t* table = a.table + (int64_t)tl.b * a.width;
-    const int64_t pool = (int64_t)a.bs * D;       // codes of one (block, head)
-    auto block_of = [&](int64_t pos) -> int {
-        if (pos >= tl.hi) return -1;
-        const int id = table[pos >> a.bs_log2];
-        return (unsigned)id < (unsigned)a.num_blocks ? id : -1;
+    const int64_t pool = (int64_t)a.bs * D, stride = (int64_t)a.kv_heads * pool;      // codes of a (block, head), of a block
+    const int8_t* kp = a.k + (int64_t)h * pool;
+    const int8_t* vp = a.v + (int64_t)h * pool;
+    const int end = (int)tl.hi, bmask = a.bs - 1;
+    const int kgrp = 16 * (li >> 2), vgrp = 16 * lg;      // this lane's tokens of a step: rows of K, columns of V
+    // block of position p: one without a valid id, and positions past the keys, stand for some other block of the
+    // pool, whose codes are as good as any (the scale says NaN, or the mask leaves them out)
+    auto entry = [&](int p) { return table[std::min(p, end - 1) >> a.bs_log2]; };
+    auto ok = [&](int id) { return (unsigned)id < (unsigned)a.num_blocks; };
+    int idk = 0, idv = 0;                                 // of the step to load next
+    auto ids = [&](int it) {
+        idk = entry(it * TK + kgrp);
+        idv = entry(it * TK + vgrp);
     };
-    for (int it = s0 + wave; it < s1; it += NW) {
-        const int64_t base = (int64_t)it * TK;
-        const int64_t tk = base + 16 * (li >> 2), tv = base + 16 * lg;   // this lane's tokens: rows of K, columns of V
-        const int bk = block_of(tk), bv = block_of(tv);
-        uint4 kc[4][D / 64], vc[D / 16];
+    auto load = [&](int it, StepCodes<D>& c) {
+        const int tk = it * TK + kgrp, tv = it * TK + vgrp;
+        const int8_t* p = kp + (ok(idk) ? idk : 0) * stride + (((tk & bmask) + (li & 3)) * D + 16 * lg);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) kc[t][c] = make_uint4(0u, 0u, 0u, 0u);
+            for (int e = 0; e < D / 64; ++e) c.k[t][e] = *(const uint4*)(p + 4 * t * D + 64 * e);
+        const int bv = ok(idv) ? idv : 0;
+        const int8_t* q = vp + bv * stride + (li * a.bs + (tv & bmask));
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) vc[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (bk >= 0) {
-            const int8_t* p = a.k + ((int64_t)bk * a.kv_heads + h) * pool + ((tk & (a.bs - 1)) + (li & 3)) * D + 16 * lg;
+        for (int i = 0; i < D / 16; ++i) c.v[i] = *(const uint4*)(q + 16 * i * a.bs);
+        const int64_t at = (int64_t)bv * a.kv_heads + h;
+        c.sk = a.ks[at];
+        c.sv = a.vs[at];
+        if (!ok(idv)) c.sk = c.sv = __builtin_nanf("");
+        if (tv >= end) c.sk = c.sv = 0.f;
+    };
+
+    // q: operand column li, channels 64 (c / 2) + 16 lg + 8 (c % 2) + 0..7 of step c
+    f16x8 q[NT][NC];
+    f32x4 acc[D / 16];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c) kc[t][c] = *(const uint4*)(p + 4 * t * D + 64 * c);
-        }
-        float sk = tv < tl.hi ? __builtin_nanf("") : 0.f, sv = sk;
-        if (bv >= 0) {
-            const int64_t at = (int64_t)bv * a.kv_heads + h;
-            const int8_t* p = a.v + at * pool + li * a.bs + (tv & (a.bs - 1));
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) vc[i] = *(const uint4*)(p + 16 * i * a.bs);
-            sk = a.ks[at];
-            sv = a.vs[at];
-        }
+    for (int i = 0; i < D / 16; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float qs = 0.f, m = -INFINITY, l = tl.over ? __builtin_nanf("") : 0.f, R = 0.f, rcp_R = 0.f;
+
+    auto work = [&](int it, const StepCodes<D>& c) {
         // scores
         f32x4 s[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                const f16x8 k0 = half8(kc[t][c].x, kc[t][c].y), k1 = half8(kc[t][c].z, kc[t][c].w);
+            for (int e = 0; e < D / 64; ++e) {
+                const f16x8 k0 = half8(c.k[t][e].x, c.k[t][e].y), k1 = half8(c.k[t][e].z, c.k[t][e].w);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, q[n][2 * c], s[t], 0, 0, 0);
-                    s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, q[n][2 * c + 1], s[t], 0, 0, 0);
+                    s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, q[n][2 * e], s[t], 0, 0, 0);
+                    s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, q[n][2 * e + 1], s[t], 0, 0, 0);
                 }
             }
         }
-        const float ck = sk * qs;
-        const bool whole = base >= tl.lo_max && base + TK <= tl.hi_min;   // no row masks anything here
+        const float ck = c.sk * qs;
+        const int tv = it * TK + vgrp;
+        const bool whole = it * TK >= tl.lo_max && it * TK + TK <= tl.hi_min;   // no row masks anything here
+        const int r_lo = my_lo - tv, r_hi = my_hi - tv;
         float top = -INFINITY;
-        const int r_lo = (int)(std::max<int64_t>(my_lo - tv, 0)), r_hi = (int)(std::min<int64_t>(my_hi - tv, 16));
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -246,53 +254,76 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
             }
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float m_new = fmaxf(m, top);
-        const float m_sub = (m_new == -INFINITY ? 0.f : m_new) - PSHIFT;
-        float fall = m_new == m ? 1.f : exp2_fast(m - m_new);
-        l *= fall;
-        m = m_new;
         // R: largest finite S_v so far, the same for every lane
-        float big = sv < INFINITY ? sv : 0.f;
+        float big = c.sv < INFINITY ? c.sv : 0.f;
         big = fmaxf(big, __shfl_xor(big, 16, 64));
         big = fmaxf(big, __shfl_xor(big, 32, 64));
-        if (big > R) {
-            fall *= __fdiv_rn(R, big);
-            R = big;
+        if (__any(top > m + LAZY || big > R)) {
+            const float m_new = fmaxf(m, top);
+            float fall = m_new == m ? 1.f : exp2_fast(m - m_new);
+            m = m_new;
+            l *= fall;
+            if (big > R) {
+                rcp_R = big < FLT_MIN ? 0.f : __fdiv_rn(1.f, big);
+                fall *= R * rcp_R;
+                R = big;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[i][r] *= fall;
         }
-        const float rv = R < FLT_MIN ? (sv == 0.f || sv < FLT_MIN ? 0.f : sv) : __fdiv_rn(sv, R);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[i][r] *= fall;
+        const float m_sub = (m == -INFINITY ? 0.f : m) - PSHIFT, rv = c.sv * rcp_R;
         f16x8 w[NT][2];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float p = exp2_fast(s[t][i] - m_sub);
-                l += p;
-                float y = p * rv;
-                if (!whole && (4 * t + i < r_lo || 4 * t + i >= r_hi)) y = 0.f;   // S_v of a block that is not this row's may be NaN
-                w[0][t >> 1][4 * (t & 1) + i] = (_Float16)y;
-                if constexpr (NT == 2)
-                    w[1][t >> 1][4 * (t & 1) + i] = (_Float16)(y - (float)w[0][t >> 1][4 * (t & 1) + i]);
+            for (int i = 0; i < 4; i += 2) {
+                const float p0 = exp2_fast(s[t][i] - m_sub), p1 = exp2_fast(s[t][i + 1] - m_sub);
+                l += p0;
+                l += p1;
+                f32x2 y = {p0 * rv, p1 * rv};
+                if (!whole) {      // S_v of a block that is not this row's may be NaN
+                    if (4 * t + i < r_lo || 4 * t + i >= r_hi) y[0] = 0.f;
+                    if (4 * t + i + 1 < r_lo || 4 * t + i + 1 >= r_hi) y[1] = 0.f;
+                }
+                const f16x2 x = __builtin_convertvector(y, f16x2);
+                const int e = 4 * (t & 1) + i;
+                w[0][t >> 1][e] = x[0];
+                w[0][t >> 1][e + 1] = x[1];
+                if constexpr (NT == 2) {
+                    const f16x2 z = __builtin_convertvector((f32x2{y[0] - (float)x[0], y[1] - (float)x[1]}), f16x2);
+                    w[1][t >> 1][e] = z[0];
+                    w[1][t >> 1][e + 1] = z[1];
+                }
             }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-            const f16x8 v0 = half8(vc[i].x, vc[i].y), v1 = half8(vc[i].z, vc[i].w);
+            const f16x8 v0 = half8(c.v[i].x, c.v[i].y), v1 = half8(c.v[i].z, c.v[i].w);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, w[n][0], acc[i], 0, 0, 0);
                 acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, w[n][1], acc[i], 0, 0, 0);
             }
         }
+    };
+
+    int it = s0 + wave;
+    if (it < s1) ids(it);
+    qs = load_query<T, NC, 16>((const T*)a.Q + token * a.ldq + (int64_t)qh * D, a.scale2, q,
+                               [&](int c) { return 64 * (c / 2) + 16 * lg + 8 * (c % 2); });
+    for (; it < s1; it += NW) {
+        StepCodes<D> c;
+        load(it, c);
+        if (it + NW < s1) ids(it + NW);
+        work(it, c);
     }
 
     // join the waves: factors to the common maximum, then sums through LDS
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
     __shared__ float sm[NW][TR], sl[NW][TR];
-    constexpr int DP = D < 128 ? D : 128;         // channels that go through LDS at a time
+    constexpr int DP = D * NW <= 512 ? D : 512 / NW;      // channels that go through LDS at a time
     __shared__ __attribute__((aligned(16))) float so[NW][TR][DP + 4];
     if (lg == 0) {
         sm[wave][li] = m;
@@ -351,15 +382,11 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
 // half hf holds tokens 16 hf .. 16 hf + 15, again in one block of the cache:
 // one S_k and one S_v per lane and score block, which go into the exponent,
 // w = 2^(s ck - m + log2 rv), and the sum of p takes 1 / rv once per 16 values.
-// m follows the row maximum only when that exceeds it by 2^LAZY (fp16 has the
-// room): most steps then leave the output accumulators alone.
-//
 // A step takes 512 + 512 matrix cycles a wave (D = 128) and as much again in
 // vector instructions, so the two are interleaved by hand: while the matrix
 // cores compute the scores of step it + 1, the exponentials of step it run
 // between them; the maximum of the new scores runs between the products with
 // V. Two waves share a SIMD. LDS holds K one step ahead of V.
-constexpr float LAZY = 6.f;
 
 // x is computed here: without this the compiler moves the sums and maxima of a
 // step behind its products, and every probability stays in a register till then
@@ -774,10 +801,12 @@ int64_t tile_units(int64_t rows, int64_t batch, int group, int tr) { return rows
 // fragments of 32 rows leave no registers for the rest: those go through
 // attention_rows_kernel whatever the number of rows.
 constexpr int TILE_WAVES = 8;
+constexpr int64_t SHORT_KEYS = 2048;
 
 // Which kernel, and how many splits of the keys.
 struct Plan {
     int tr;        // rows of a tile: TR, or 32 TILE_WAVES
+    int nw;        // waves of attention_rows_kernel
     int nsplit;
 };
 Plan plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int block, int64_t width) {
@@ -785,26 +814,40 @@ Plan plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int blo
     const int group = heads / kv_heads;
     p.tr = dim <= 128 && rows * group >= 64 * batch ? 32 * TILE_WAVES : TR;
     const int64_t units = tile_units(rows, batch, group, p.tr) * kv_heads;
-    const int64_t most = cdiv(width * block, TK * NW);
+    const int64_t longest = width * block, most = cdiv(longest, TK * MIN_STEPS);
     const int64_t want = p.tr == TR ? 2048 : 256;
     p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(cdiv(want, units), most), 64));
+    // short sequences: eight waves and no second launch
+    p.nw = 4;
+    if (p.tr == TR && dim <= 128 && p.nsplit > 1 && longest <= SHORT_KEYS) {
+        p.nw = 8;
+        p.nsplit = 1;
+    }
     return p;
 }
 
 template <typename T, int D>
-int launch(const AttnArgs& a, int tr, hipStream_t st) {
+int launch(const AttnArgs& a, const Plan& p, hipStream_t st) {
+    const int tr = p.tr;
     const int64_t units = tile_units(a.g.rows, a.g.batch, a.group, tr) * a.kv_heads;
-    if (tr == TR) {
-        hipLaunchKernelGGL((attention_rows_kernel<T, D>), dim3((unsigned)(units * a.nsplit)), dim3(64 * NW), 0, st, a);
-    } else if constexpr (D <= 128) {
-        static bool ready = false;    // more than 64 KB of LDS
-        if (!ready) {
-            PTQ_HIP(hipFuncSetAttribute((const void*)attention_tile_kernel<T, D, TILE_WAVES>,
-                                        hipFuncAttributeMaxDynamicSharedMemorySize, TileLds<D>::BYTES));
-            ready = true;
+    const dim3 grid((unsigned)(units * a.nsplit));
+    if constexpr (D <= 128) {
+        if (tr != TR) {
+            static bool ready = false;    // more than 64 KB of LDS
+            if (!ready) {
+                PTQ_HIP(hipFuncSetAttribute((const void*)attention_tile_kernel<T, D, TILE_WAVES>,
+                                            hipFuncAttributeMaxDynamicSharedMemorySize, TileLds<D>::BYTES));
+                ready = true;
+            }
+            hipLaunchKernelGGL((attention_tile_kernel<T, D, TILE_WAVES>), grid, dim3(64 * TILE_WAVES), TileLds<D>::BYTES, st,
+                               a);
+        } else if (p.nw == 8) {
+            hipLaunchKernelGGL((attention_rows_kernel<T, D, 8>), grid, dim3(512), 0, st, a);
+        } else {
+            hipLaunchKernelGGL((attention_rows_kernel<T, D, 4>), grid, dim3(256), 0, st, a);
         }
-        hipLaunchKernelGGL((attention_tile_kernel<T, D, TILE_WAVES>), dim3((unsigned)(units * a.nsplit)),
-                           dim3(64 * TILE_WAVES), TileLds<D>::BYTES, st, a);
+    } else {
+        hipLaunchKernelGGL((attention_rows_kernel<T, D, 4>), grid, dim3(256), 0, st, a);
     }
     PTQ_LAUNCH_CHECK();
     if (a.nsplit > 1) {
@@ -815,11 +858,11 @@ int launch(const AttnArgs& a, int tr, hipStream_t st) {
 }
 
 template <typename T>
-int launch_dim(const AttnArgs& a, int tr, hipStream_t st) {
+int launch_dim(const AttnArgs& a, const Plan& p, hipStream_t st) {
     switch (a.dim) {
-        case 64: return launch<T, 64>(a, tr, st);
-        case 128: return launch<T, 128>(a, tr, st);
-        default: return launch<T, 256>(a, tr, st);
+        case 64: return launch<T, 64>(a, p, st);
+        case 128: return launch<T, 128>(a, p, st);
+        default: return launch<T, 256>(a, p, st);
     }
 }
 
@@ -840,8 +883,8 @@ int run_attention_int8(const KVCacheInt8& c, const RaggedRows& r, int dtype, con
                        size_t ws_bytes, hipStream_t st) {
     if (r.rows == 0 || r.batch == 0) return PTQ_OK;
     AttnArgs a{};
-    a.g.offsets = r.offsets; a.g.batch = (int)r.batch; a.g.rows = r.rows;
-    a.lens = r.starts; a.table = r.table; a.width = r.width;
+    a.g.offsets = r.offsets; a.g.starts = r.starts; a.g.batch = (int)r.batch; a.g.rows = r.rows;
+    a.table = r.table; a.width = r.width;
     a.heads = heads; a.kv_heads = c.heads; a.group = heads / c.heads;
     a.dim = c.dim; a.bs = c.block; a.bs_log2 = __builtin_ctz((unsigned)c.block); a.num_blocks = c.num_blocks;
     a.k = c.k; a.v = c.v; a.ks = c.k_scales; a.vs = c.v_scales;
@@ -855,7 +898,7 @@ int run_attention_int8(const KVCacheInt8& c, const RaggedRows& r, int dtype, con
         a.part = ar.take<float>((size_t)a.nsplit * r.rows * heads * c.dim);
         a.part_lse = ar.take<float>((size_t)a.nsplit * r.rows * heads);
     }
-    return dtype == PTQ_F32 ? launch_dim<float>(a, p.tr, st) : launch_dim<uint16_t>(a, p.tr, st);
+    return dtype == PTQ_F32 ? launch_dim<float>(a, p, st) : launch_dim<uint16_t>(a, p, st);
 }
 
 }  // namespace ptq

@@ -6,6 +6,7 @@
 #include "common.hpp"
 
 #include <float.h>
+#include <algorithm>
 
 namespace ptq {
 
@@ -86,43 +87,47 @@ __device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, f
 }
 
 // ----------------------------------------------------------- ragged batch --
-// Sequence b of a ragged batch owns rows offsets[b] .. offsets[b + 1]. A grid
-// that cannot know the offsets on the host numbers its work units so that
-// sequence b has first(b) = floor(offsets[b] mul / div) + extra b .. first(b + 1):
-// at least as many units as it needs, the spare ones exit. The wave that
-// looks unit w up reads 64 values of first() at a time.
+// Sequence b of a ragged batch owns rows offsets[b] .. offsets[b + 1], and has
+// a number starts[b] of its own. A grid that cannot know the offsets on the
+// host numbers its work units so that sequence b has units
+// first(b) = floor(offsets[b] mul / div) + extra b .. first(b + 1): at least as
+// many as it needs, the spare ones exit. The wave that looks a unit up reads
+// 64 sequences at once, everything it needs of them in one round of loads.
 // Offsets are clamped to [0, rows], so a wrong one cannot lead outside the
 // caller's tensors.
 struct Ragged {
     const int32_t* offsets;
+    const int32_t* starts;
     int batch;
     int64_t rows;
 };
 
-__device__ __forceinline__ int64_t ragged_offset(const Ragged& g, int b) {
-    const int64_t o = g.offsets[b];
-    return o < 0 ? 0 : (o > g.rows ? g.rows : o);
-}
+struct RaggedUnit {
+    int b;                 // the sequence: the last one with first(b) <= w
+    int64_t off, rows;     // its rows
+    int start;             // starts[b]
+    int64_t local;         // w - first(b)
+};
 
-__device__ __forceinline__ int64_t ragged_first(const Ragged& g, int b, int mul, int div, int extra) {
-    return ragged_offset(g, b) * mul / div + (int64_t)extra * b;
-}
-
-// The sequence of unit w (the last b with first(b) <= w), and w - first(b) in *local.
-__device__ __forceinline__ int ragged_find(const Ragged& g, int64_t w, int mul, int div, int extra, int64_t* local) {
+__device__ __forceinline__ RaggedUnit ragged_find(const Ragged& g, int64_t w, int mul, int div, int extra) {
     const int lane = threadIdx.x & 63;
-    int b = 0;
+    auto clamp = [&](int o) { return (int)(o < 0 ? 0 : (o > g.rows ? g.rows : o)); };
+    RaggedUnit u{};
     for (int b0 = 0; b0 < g.batch; b0 += 64) {
-        const int i = b0 + lane;
-        const bool le = i < g.batch && ragged_first(g, i, mul, div, extra) <= w;
-        const uint64_t vote = __ballot(le);
+        const int i = std::min(b0 + lane, g.batch - 1);
+        const int o = clamp(g.offsets[i]), n = clamp(g.offsets[i + 1]), st = g.starts[i];
+        const int64_t first = (int64_t)o * mul / div + (int64_t)extra * i;
+        const uint64_t vote = __ballot(b0 + lane < g.batch && first <= w);
         if (!vote) break;
-        b = b0 + 63 - __builtin_clzll(vote);
-        if (b != b0 + 63) break;
+        const int at = 63 - __builtin_clzll(vote);
+        u.b = b0 + at;
+        u.off = __builtin_amdgcn_readlane(o, at);
+        u.rows = std::max(__builtin_amdgcn_readlane(n, at) - (int)u.off, 0);
+        u.start = __builtin_amdgcn_readlane(st, at);
+        u.local = w - (u.off * mul / div + (int64_t)extra * u.b);
+        if (at != 63) break;
     }
-    b = __builtin_amdgcn_readfirstlane(b);
-    *local = w - ragged_first(g, b, mul, div, extra);
-    return b;
+    return u;
 }
 
 }  // namespace ptq

@@ -14,8 +14,6 @@
 // summed or raced over, and the same call twice leaves the same cache.
 #include "int8.hpp"
 
-#include <algorithm>
-
 namespace ptq {
 namespace {
 
@@ -29,27 +27,25 @@ struct BlockSpan {
 };
 
 // false: a spare unit
-__device__ __forceinline__ bool find_block(const Ragged& g, const int32_t* starts, const int32_t* table,
-                                           int64_t width, int64_t num_blocks, int bs, int64_t unit, BlockSpan& s) {
-    int64_t j;
-    s.b = ragged_find(g, unit, 1, bs, 2, &j);
-    const int64_t o = ragged_offset(g, s.b), n = ragged_offset(g, s.b + 1) - o;
-    if (n <= 0) return false;
-    const int64_t given = starts[s.b], start = given < 0 ? 0 : given;
-    const int64_t at = start / bs + j;
+__device__ __forceinline__ bool find_block(const Ragged& g, const int32_t* table, int64_t width, int64_t num_blocks,
+                                           int bs, int64_t unit, BlockSpan& s) {
+    const RaggedUnit u = ragged_find(g, unit, 1, bs, 2);
+    if (u.rows <= 0) return false;
+    const int64_t start = std::max(u.start, 0), at = start / bs + u.local;
+    s.b = u.b;
     s.p0 = at * bs;
-    if (s.p0 >= start + n) return false;
+    if (s.p0 >= start + u.rows) return false;
     s.lo = (int)std::max<int64_t>(start - s.p0, 0);
-    s.hi = (int)std::min<int64_t>(start + n - s.p0, bs);
-    s.row0 = o + s.p0 - start;
-    s.id = (at < width && given >= 0) ? table[s.b * width + at] : -1;
-    if (s.id < 0 || s.id >= num_blocks) s.id = -1;
+    s.hi = (int)std::min<int64_t>(start + u.rows - s.p0, bs);
+    s.row0 = u.off + s.p0 - start;
+    s.id = (at < width && u.start >= 0) ? table[s.b * width + at] : -1;
+    if (s.id >= num_blocks) s.id = -1;
     return true;
 }
 
 struct CacheArgs {
     Ragged g;
-    const int32_t* starts; const int32_t* table; int64_t width;
+    const int32_t* table; int64_t width;
     int heads, dim, bs;
     int64_t num_blocks;
     int8_t* codes[2];        // k, v
@@ -96,7 +92,7 @@ __global__ __launch_bounds__(sizeof(T) == 4 ? 1024 : 512) void kv_write_kernel(C
     constexpr int NV = write_nv<T>();
     __shared__ float red[16];
     BlockSpan s;
-    if (!find_block(a.g, a.starts, a.table, a.width, a.num_blocks, a.bs, blockIdx.x, s) || s.id < 0) return;
+    if (!find_block(a.g, a.table, a.width, a.num_blocks, a.bs, blockIdx.x, s) || s.id < 0) return;
     const bool val = blockIdx.z == 1;
     const HeadThreads x = head_threads<NV>(a, per);
     const bool live = x.h < a.heads;
@@ -190,7 +186,7 @@ template <typename T>
 __global__ __launch_bounds__(512) void kv_read_kernel(CacheArgs a, int per, T* __restrict__ K, int64_t ldk,
                                                       T* __restrict__ V, int64_t ldv) {
     BlockSpan s;
-    if (!find_block(a.g, a.starts, a.table, a.width, a.num_blocks, a.bs, blockIdx.x, s)) return;
+    if (!find_block(a.g, a.table, a.width, a.num_blocks, a.bs, blockIdx.x, s)) return;
     const bool val = blockIdx.z == 1, have = s.id >= 0;
     const HeadThreads x = head_threads<READ_NV>(a, per);
     if (x.h >= a.heads) return;
@@ -240,8 +236,8 @@ __global__ __launch_bounds__(512) void kv_read_kernel(CacheArgs a, int per, T* _
 
 CacheArgs cache_args(const KVCacheInt8& c, const RaggedRows& r) {
     CacheArgs a{};
-    a.g.offsets = r.offsets; a.g.batch = (int)r.batch; a.g.rows = r.rows;
-    a.starts = r.starts; a.table = r.table; a.width = r.width;
+    a.g.offsets = r.offsets; a.g.starts = r.starts; a.g.batch = (int)r.batch; a.g.rows = r.rows;
+    a.table = r.table; a.width = r.width;
     a.heads = c.heads; a.dim = c.dim; a.bs = c.block; a.num_blocks = c.num_blocks;
     a.codes[0] = c.k; a.codes[1] = c.v;
     a.scales[0] = c.k_scales; a.scales[1] = c.v_scales;
