@@ -378,53 +378,67 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
 // through LDS once per workgroup, converted to fp16 on the way (a wave that
 // converted its own operands would spend more on that than on the products).
 // S^T = K Q^T and O^T = V^T P^T as above, on 32x32x16 products: operand row r
-// of a 32-token block is token 16 (r / 4 % 2) + 4 (r / 8) + r % 4, so lane
+// of a block of 32 tokens is token 16 (r / 4 % 2) + 4 (r / 8) + r % 4, so lane
 // half hf holds tokens 16 hf .. 16 hf + 15, again in one block of the cache:
 // one S_k and one S_v per lane and score block, which go into the exponent,
 // w = 2^(s ck - m + log2 rv), and the sum of p takes 1 / rv once per 16 values.
-// A step takes 512 + 512 matrix cycles a wave (D = 128) and as much again in
-// vector instructions, so the two are interleaved by hand: while the matrix
-// cores compute the scores of step it + 1, the exponentials of step it run
-// between them; the maximum of the new scores runs between the products with
-// V. Two waves share a SIMD. LDS holds K one step ahead of V.
-
-// x is computed here: without this the compiler moves the sums and maxima of a
-// step behind its products, and every probability stays in a register till then
-__device__ __forceinline__ void pin(float& x) { asm volatile("" : "+v"(x)); }
-constexpr int LOG2_RV_MIN = -60;   // below it the block adds nothing to the output (w underflows), only to the sum
-
-// f(integral_constant<int, I>) for I = B .. E - 1, in order
+//
+// A block of 32 tokens takes 512 matrix cycles a wave (D = 128) and about as
+// many in vector instructions, so three blocks are in work at a time: the
+// products give the scores of block n + 1 and the output of block n - 1 while
+// the exponentials of block n run between them, and an operand fragment is
+// read from LDS AHEAD products before its own. LDS holds three steps of K and
+// of V, so that one barrier a step is enough.
 template <int B, int E, typename F>
-__device__ __forceinline__ void static_for(F&& f) {
+__device__ __forceinline__ void static_for(F&& f) {      // f(integral_constant<int, I>) for I = B .. E - 1, in order
     if constexpr (B < E) {
         f(std::integral_constant<int, B>{});
         static_for<B + 1, E>(f);
     }
 }
 
+// x is computed here: without this the compiler moves the sums and maxima of a
+// block behind its products, and every probability stays in a register till then
+__device__ __forceinline__ void pin(float& x) { asm volatile("" : "+v"(x)); }
+
+constexpr float LOG2_RV_MIN = -60;   // below it a block adds nothing to the output (w underflows), only to the sum
+
+// the larger of x in this lane and in lane ^ 32
+__device__ __forceinline__ float max_halves(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    float larger;      // fmaxf would make both canonical first
+    asm("v_max_f32 %0, %1, %2" : "=v"(larger) : "v"(r[0]), "v"(r[1]));
+    return larger;
+}
+
+// Rows of K are in the order of the operand's rows, and 16 bytes longer than
+// their values: 16 neighbours touch every bank, and an operand fragment is one
+// lane address and a constant.
 template <int D>
 struct TileLds {
-    static constexpr int KROW = 2 * D, VROW = 2 * TK;       // bytes of a token of K, of a channel of V
+    static constexpr int KROW = 2 * D + 16, VROW = 2 * TK + 16;       // bytes of a token of K, of a channel of V
     static constexpr int K_BYTES = TK * KROW, V_BYTES = D * VROW;
-    static constexpr int BYTES = 2 * (K_BYTES + V_BYTES);
-    // 16-byte slots, placed so that the 16 rows read together touch every bank
-    __host__ __device__ static constexpr int k_swz(int token) {
-        return D == 64 ? ((token >> 1) & 3) | ((token >> 2) & 4) : (token & 7) | ((token >> 1) & 8);
+    static constexpr int BYTES = 3 * (K_BYTES + V_BYTES);
+    // operand row of a token of a step
+    __host__ __device__ static constexpr int k_row(int token) {
+        return (token & ~31) | (token >> 2 & 3) << 3 | (token >> 4 & 1) << 2 | (token & 3);
     }
-    __device__ static __forceinline__ int k_at(int token, int chunk) { return token * KROW + 16 * (chunk ^ k_swz(token)); }
-    __device__ static __forceinline__ int v_at(int d, int chunk) { return d * VROW + 16 * (chunk ^ ((d >> 1) & 7)); }
 };
 
 template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) {
     constexpr int NT = sizeof(T) == 4 ? 2 : 1;
-    constexpr bool PIPE = NT == 1;                 // scores one step ahead (their second set takes 32 registers)
+    constexpr bool PIPE = NT == 1;                 // two terms of everything would not fit the registers
+    constexpr int AHEAD = 3;
+    constexpr int STAGE_EVERY = D / 64;
     constexpr int NTH = 64 * WAVES, NC = D / 16, ND = D / 32;
     constexpr int NCH = TK * D / 16;               // 16-byte chunks of K, and of V, in a step
     static_assert(NCH % 64 == 0 && NCH <= NTH, "one chunk of each a thread");
     using L = TileLds<D>;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    __shared__ __attribute__((aligned(16))) float ssk[4][4], ssv[2][4];   // scales of steps it % 4, it % 2
+    // of step it, at (it - s0) % 4: S_k of the lane half's group in either block, then log2 S_v of them (NaN: S_v is
+    // not finite); the largest finite S_v, negative if one is not finite
+    __shared__ __attribute__((aligned(16))) float ssc[4][2][4], sbig[4];
 
     const int split = (int)(blockIdx.x % (unsigned)a.nsplit);
     const int64_t tile = blockIdx.x / (unsigned)a.nsplit;
@@ -458,13 +472,15 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
     for (int i = 0; i < ND; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
-    float m = -INFINITY, l = tl.over ? __builtin_nanf("") : 0.f, R = 0.f, rcp_R = 0.f;
+    // ref, limit: what m comes down to for the exponents, the score from which it moves
+    float m = -INFINITY, ref = -PSHIFT, limit = -INFINITY, l = tl.over ? __builtin_nanf("") : 0.f;
+    float R = 0.f, log2_R = 0.f, poison = 0.f;
 
     // Staging: one 16-byte chunk of K (16 channels of a token) and one of V (16 tokens of a channel) per thread and
     // step. A wave's chunks lie in one block of the cache, of K because its tokens are neighbours, of V by the way the
-    // chunks are dealt: gpr = chunks of a channel that are neighbours in a block. So block ids and addresses are
-    // scalar. An id is read a step before the codes it leads to, and looked at only then: a wait for it in between
-    // would wait for the codes requested before it, too.
+    // chunks are dealt: gpr = chunks of a channel that are neighbours in a block. So ids and addresses of blocks are
+    // scalar. The ids of a step's four groups are requested a step before the codes they lead to, in lanes 0 .. 3 of
+    // every quad, and looked at only then: a wait in between would wait for the codes requested before them, too.
     const int32_t* table = a.table + (int64_t)tl.b * a.width;
     const int64_t pool = (int64_t)a.bs * D, stride = (int64_t)a.kv_heads * pool;
     const int8_t* kp = a.k + (int64_t)h * pool;
@@ -475,266 +491,319 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
     const int vblk = wave % nblk, vd = (wave / nblk) * (64 / gpr) + lane / gpr, vgrp = vblk * gpr + lane % gpr;
     const unsigned koff = (unsigned)((ktok & bmask) * D + 16 * (t % (D / 16)));
     const unsigned voff = (unsigned)(vd * a.bs + ((16 * vgrp) & bmask));
-    // block of position p: one without a valid id, and positions past the keys, stand for some other block of the
-    // pool, whose codes are as good as any (the scale says NaN, or the mask leaves them out)
-    auto entry = [&](int p) { return table[std::min(p, end - 1) >> a.bs_log2]; };
-    auto ok = [&](int id) { return (unsigned)id < (unsigned)a.num_blocks; };
-    auto base = [&](const int8_t* from, int id) { return from + (int64_t)__builtin_amdgcn_readfirstlane(ok(id) ? id : 0) * stride; };
-    const int kfirst = 16 * (wave * 64 / (D / 16) / 16), vfirst = vblk * gpr * 16;      // first token of the wave's chunks' block
-    int idk = 0, idv = 0;
-    // lanes 0 .. 3 of wave 0 bring the scales of the step's four groups of 16 tokens
-    int ids_now = 0, ids_next = 0;
-    auto scale_of = [&](const float* scales, int it, int id) {
-        return it * TK + 16 * t >= end ? 0.f : ok(id) ? scales[(int64_t)id * a.kv_heads + h] : __builtin_nanf("");
+    const int kgrp = wave * 64 / (D / 16) / 16 % 4, vfirst = vblk * gpr;      // a group of the wave's chunks' block
+    auto entries = [&](int it) {
+        const unsigned p = (unsigned)std::min(it * TK + 16 * (lane & 3), end - 1);
+        return *(const int32_t*)((const char*)table + (p >> a.bs_log2 << 2));
     };
+    // a block without a valid id, and positions past the keys, stand for some other block of the pool, whose codes
+    // are as good as any (the scale says NaN, or the mask leaves them out)
+    auto valid = [&](int id) { return (unsigned)id < (unsigned)a.num_blocks ? id : 0; };
+    auto base = [&](const int8_t* from, int ids, int group) {
+        return from + (int64_t)valid(__builtin_amdgcn_readlane(ids, group)) * stride;
+    };
+    int ids1 = 0, ids2 = 0;         // of the next step, of the one after it
     uint4 rk, rv_;
-    float sk_r = 0.f, sv_r = 0.f;
-    auto fetch_k = [&](int it) {            // K of step it, whose id is in idk; then the next id
-        if (stages) rk = *(const uint4*)(base(kp, idk) + ((it * TK) & bmask) * D + koff);
-        idk = entry((it + 1) * TK + kfirst);
+    float sk_r, sv_r;
+    auto fetch_k = [&](int it, int ids) {
+        if (stages) rk = *(const uint4*)(base(kp, ids, kgrp) + ((it * TK) & bmask) * D + koff);
     };
-    auto fetch_v = [&](int it) {
-        if (stages) rv_ = *(const uint4*)(base(vp, idv) + ((it * TK) & bmask) + voff);
-        idv = entry((it + 1) * TK + vfirst);
+    auto fetch_v = [&](int it, int ids) {
+        if (stages) rv_ = *(const uint4*)(base(vp, ids, vfirst) + ((it * TK) & bmask) + voff);
     };
-    const int ka = L::k_at(ktok, 2 * (t % (D / 16))), kb = L::k_at(ktok, 2 * (t % (D / 16)) + 1);
-    const int va = 2 * L::K_BYTES + L::v_at(vd, 2 * vgrp), vb = 2 * L::K_BYTES + L::v_at(vd, 2 * vgrp + 1);
-    auto stage_k = [&](int buf, int n) {      // n: which step of the split this is
-        if (stages) {
-            *(f16x8*)(smem + buf * L::K_BYTES + ka) = half8(rk.x, rk.y);
-            *(f16x8*)(smem + buf * L::K_BYTES + kb) = half8(rk.z, rk.w);
+    auto fetch_scales = [&](int ids) {
+        if (wave == 0) {
+            const int64_t at = (int64_t)valid(ids) * a.kv_heads + h;
+            sk_r = a.ks[at];
+            sv_r = a.vs[at];
         }
-        if (t < 4) ssk[n & 3][t] = sk_r;
     };
-    auto stage_v = [&](int buf) {
-        if (stages) {
-            *(f16x8*)(smem + buf * L::V_BYTES + va) = half8(rv_.x, rv_.y);
-            *(f16x8*)(smem + buf * L::V_BYTES + vb) = half8(rv_.z, rv_.w);
+    const int kto = L::k_row(ktok) * L::KROW + 32 * (t % (D / 16));
+    const int vto = 3 * L::K_BYTES + vd * L::VROW + 32 * vgrp;
+    auto stage_k = [&](int at, int half) {    // at: offset of the buffer
+        if (stages) *(f16x8*)(smem + at + kto + 16 * half) = half ? half8(rk.z, rk.w) : half8(rk.x, rk.y);
+    };
+    auto stage_v = [&](int at, int half) {
+        if (stages) *(f16x8*)(smem + at + vto + 16 * half) = half ? half8(rv_.z, rv_.w) : half8(rv_.x, rv_.y);
+    };
+    auto stage_scales = [&](int it, int ids) {
+        if (wave == 0 && lane < 4) {
+            const bool past = it * TK + 16 * lane >= end, known = (unsigned)ids < (unsigned)a.num_blocks;
+            const float sk = past ? 0.f : known ? sk_r : __builtin_nanf("");
+            const float sv = past || !known ? 0.f : sv_r;
+            const bool bad = !(sv < INFINITY);
+            float* to = ssc[(it - s0) & 3][lane & 1] + (lane >> 1);
+            to[0] = sk;
+            to[2] = bad ? __builtin_nanf("") : __builtin_amdgcn_logf(sv);     // v_log_f32: base 2
+            float big = bad ? 0.f : sv;
+            big = fmaxf(big, __shfl_xor(big, 1, 4));
+            big = fmaxf(big, __shfl_xor(big, 2, 4));
+            const bool any_bad = __ballot(bad) != 0;
+            if (lane == 0) sbig[(it - s0) & 3] = any_bad ? -big : big;
         }
-        if (t < 4) ssv[buf][t] = sv_r;
+    };
+    // buffers of K of this step and the next two, of V of the last step, this one and the next
+    int k0 = 0, k1 = L::K_BYTES, k2 = 2 * L::K_BYTES, vm = 2 * L::V_BYTES, v0 = 0, v1 = L::V_BYTES;
+
+    // operand fragments of this lane
+    const int kfrom = li * L::KROW + 16 * hf, vfrom = 3 * L::K_BYTES + li * L::VROW + 32 * hf;
+    auto k_frag = [&](int at, int u, int c) {       // tokens 32 u .., channels 16 c ..
+        return *(const f16x8*)(smem + at + kfrom + 32 * u * L::KROW + 32 * c);
+    };
+    auto v_frag = [&](int at, int u, int j) {       // product j of a block: channels 32 (j % ND) .., tokens 16 hf + 8 (j / ND) ..
+        return *(const f16x8*)(smem + at + vfrom + 32 * (j % ND) * L::VROW + 64 * u + 16 * (j / ND));
     };
 
-    // operand fragments of this lane: the swizzle XORs their chunk, everything else is a constant offset
-    const int krow = 16 * ((li >> 2) & 1) + 4 * (li >> 3) + (li & 3);   // token of operand row li
-    int kat[NC], vat[4];
+    auto clear = [&](f32x16& x) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) kat[c] = L::k_at(krow, (2 * c) ^ hf);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) vat[k] = 2 * L::K_BYTES + L::v_at(li, (4 * (k >> 1) + (k & 1)) ^ (2 * hf));
-    auto k_frag = [&](int buf, int u, int c) {      // scores u (tokens 32 u ..), channels 16 c ..
-        return *(const f16x8*)(smem + kat[c] + buf * L::K_BYTES + 32 * u * L::KROW);
+        for (int r = 0; r < 16; ++r) x[r] = 0.f;
     };
-    auto v_frag = [&](int buf, int i, int k) {      // channels 32 i .., tokens 32 (k / 2) + 16 hf + 8 (k % 2) ..
-        return *(const f16x8*)(smem + vat[k] + buf * L::V_BYTES + 32 * i * L::VROW);
+    auto top_of = [&](const f32x16& s, float& top, int r) {
+        top = r ? fmaxf(fmaxf(top, s[r]), s[r + 1]) : fmaxf(s[0], s[1]);
+        pin(top);
     };
-
-    float top[2];            // largest raw score of each block of 32 tokens
-    auto top_of = [&](f32x16 (&s)[2], int u, int r) {
-        top[u] = r ? fmaxf(fmaxf(top[u], s[u][r]), s[u][r + 1]) : fmaxf(s[u][0], s[u][1]);
-        pin(top[u]);
+    auto scores = [&](int at, int u, f32x16& s, float& top) __attribute__((always_inline)) {
+        clear(s);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const f16x8 k = k_frag(at, u, c);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[n][c], s, 0, 0, 0);
+        }
+#pragma unroll
+        for (int r = 0; r < 16; r += 2) top_of(s, top, r);
     };
-    auto zero = [&](f32x16 (&s)[2]) {
+    using Probs = f16x8[NT][2];
+    auto output = [&](int at, int u, const Probs& w) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int j = 0; j < 2 * ND; ++j) {
+            const f16x8 v = v_frag(at, u, j);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[u][r] = 0.f;
-    };
-    auto scores = [&](int buf, f32x16 (&s)[2]) {
-        zero(s);
-        static_for<0, 2 * NC>([&](auto jc) {
-            constexpr int j = decltype(jc)::value, u = j / NC, c = j % NC;
-            const f16x8 k = k_frag(buf, u, c);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[n][c], s[u], 0, 0, 0);
-        });
-#pragma unroll
-        for (int r = 0; r < 16; r += 2) {
-            top_of(s, 0, r);
-            top_of(s, 1, r);
+            for (int n = 0; n < NT; ++n) acc[j % ND] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[n][j / ND], acc[j % ND], 0, 0, 0);
         }
     };
-    auto scale_acc = [&](float x) {
+    auto forget = [&](Probs& w) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[n][k][e] = (_Float16)0.f;
+    };
+    // A row moves to another reference when its largest score mx exceeds limit, all rows when S_v exceeds R; big: of sbig,
+    // as bits, so that a negative one is large, too. What was pending at the old references is in acc already.
+    auto over_R = [&](unsigned big) { return big > __float_as_uint(R); };
+    auto move = [&](float mx, unsigned big_bits) __attribute__((always_inline)) {
+        const float m_new = fmaxf(m, mx), big = fabsf(__uint_as_float(big_bits));
+        float fall = m_new == m ? 1.f : exp2_fast(m - m_new);
+        m = m_new;
+        ref = (m == -INFINITY ? 0.f : m) - PSHIFT;
+        limit = m + LAZY;
+        l *= fall;
+        if (big > R) {     // the same for every lane
+            fall *= big < FLT_MIN ? 0.f : __fdiv_rn(R, big);
+            R = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(big)));
+            log2_R = big < FLT_MIN ? 0.f : __builtin_amdgcn_logf(big);
+        }
 #pragma unroll
         for (int i = 0; i < ND; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][r] *= x;
+            for (int r = 0; r < 16; ++r) acc[i][r] *= fall;
+    };
+    auto scales_of = [&](int it) { return *(const f32x4*)ssc[(it - s0) & 3][hf]; };
+    auto big_of = [&](int it) { return sbig[(it - s0) & 3]; };
+    auto bits = [](float big) { return (unsigned)__builtin_amdgcn_readfirstlane(__float_as_uint(big)); };
+    auto log2_rv = [&](float log2_sv) { return fmaxf(log2_sv - log2_R, LOG2_RV_MIN); };      // of NaN, too
+    // two probabilities of block (it, u), into w and sum; lo, hi: the row's keys within the lane's 16
+    auto pair = [&](auto masked, const f32x16& s, float ck, float off, int r, Probs& w, float& sum, int lo, int hi) {
+        f32x2 e;
+        e[0] = exp2_fast(fmaf(s[r], ck, -off));
+        e[1] = exp2_fast(fmaf(s[r + 1], ck, -off));
+        if constexpr (decltype(masked)::value) {     // S_v of a block that is not this row's may be NaN
+            if (r < lo || r >= hi) e[0] = 0.f;
+            if (r + 1 < lo || r + 1 >= hi) e[1] = 0.f;
+        }
+        sum += e[0];
+        sum += e[1];
+        pin(sum);
+        const f16x2 x = __builtin_convertvector(e, f16x2);
+        w[0][r >> 3][r & 7] = x[0];
+        w[0][r >> 3][(r & 7) + 1] = x[1];
+        if constexpr (NT == 2) {
+            const f32x2 rest = {e[0] - (float)x[0], e[1] - (float)x[1]};
+            const f16x2 y = __builtin_convertvector(rest, f16x2);
+            w[1][r >> 3][r & 7] = y[0];
+            w[1][r >> 3][(r & 7) + 1] = y[1];
+        }
     };
 
-    // step it with the scores s; sn receives those of step it + 1 (of whatever LDS holds after the last one).
-    // buf: the buffers of this step's K and V; the next step's K is in the other one
-    auto body = [&](auto masked_c, int buf, int it, f32x16 (&s)[2], f32x16 (&sn)[2]) {
-        constexpr bool MASKED = decltype(masked_c)::value;
-        constexpr bool AHEAD = PIPE && !MASKED;           // scores of the next step while this one runs; s and sn differ
-        const int g0 = it * TK + 16 * hf;           // this lane's tokens: g0 + 32 u + r
-        float ck[2];
+    // one block by itself: steps that some row of the tile masks, and fp32 queries
+    auto plain_block = [&](auto masked, int it, int u) __attribute__((always_inline)) {
+        f32x16 s;
+        float top;
+        scores(k0, u, s, top);
+        const f32x4 sc = scales_of(it);
+        float ck = sc[u] * qs;
+        const int g0 = it * TK + 32 * u + 16 * hf, lo = my_lo - g0, hi = my_hi - g0;
+        if constexpr (decltype(masked)::value) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            ck[u] = ssk[(it - s0) & 3][2 * u + hf] * qs;
-            if constexpr (MASKED) {
+            for (int r = 0; r < 16; ++r) s[r] = (r >= lo && r < hi) ? s[r] * ck : -INFINITY;
+            ck = 1.f;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int g = g0 + 32 * u + r;
-                    s[u][r] = (g >= my_lo && g < my_hi) ? s[u][r] * ck[u] : -INFINITY;
-                    top[u] = r ? fmaxf(top[u], s[u][r]) : s[u][r];
-                }
-                ck[u] = 1.f;
-            }
+            for (int r = 0; r < 16; r += 2) top_of(s, top, r);
         }
-        float mx = fmaxf(top[0] * ck[0], top[1] * ck[1]);
-        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-        if (__any(mx > m + LAZY)) {
-            const float m_new = fmaxf(m, mx);
-            const float fall = m_new == m ? 1.f : exp2_fast(m - m_new);
-            m = m_new;
-            l *= fall;
-            scale_acc(fall);
-        }
-        const float m_sub = (m == -INFINITY ? 0.f : m) - PSHIFT;
-        const f32x4 sv4 = *(const f32x4*)ssv[buf];
-        float big = 0.f;
+        const float mx = max_halves(top * ck);
+        const unsigned big = bits(big_of(it));
+        if (over_R(big) || __any(mx > limit)) move(mx, big);
+        const bool mine = !decltype(masked)::value || (lo < 16 && hi > 0);
+        if (mine && sc[2 + u] != sc[2 + u]) poison = sc[2 + u];
+        const float lr = log2_rv(sc[2 + u]), off = ref - lr;
+        Probs w;
+        float sum = 0.f;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) big = fmaxf(big, sv4[g] < INFINITY ? sv4[g] : 0.f);
-        if (__any(big > R)) {     // the same for every lane
-            rcp_R = big < FLT_MIN ? 0.f : __fdiv_rn(1.f, big);
-            scale_acc(R * rcp_R);
-            R = big;
-        }
-        float lr[2], off[2], sum[2] = {0.f, 0.f};
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const float rv = (hf ? sv4[2 * u + 1] : sv4[2 * u]) * rcp_R;
-            lr[u] = rv != rv ? rv : fmaxf(__builtin_amdgcn_logf(rv), (float)LOG2_RV_MIN);   // v_log_f32: base 2
-            off[u] = m_sub - lr[u];
-        }
-        f16x8 w[NT][2][2];
-        auto pair = [&](int u, int r) {      // two probabilities
-            f32x2 e;
-            e[0] = exp2_fast(fmaf(s[u][r], ck[u], -off[u]));
-            e[1] = exp2_fast(fmaf(s[u][r + 1], ck[u], -off[u]));
-            if constexpr (MASKED) {     // S_v of a block that is not this row's may be NaN
-                const int g = g0 + 32 * u + r;
-                if (g < my_lo || g >= my_hi) e[0] = 0.f;
-                if (g + 1 < my_lo || g + 1 >= my_hi) e[1] = 0.f;
-            }
-            sum[u] += e[0];
-            sum[u] += e[1];
-            pin(sum[u]);
-            const f16x2 x = __builtin_convertvector(e, f16x2);
-            w[0][u][r >> 3][r & 7] = x[0];
-            w[0][u][r >> 3][(r & 7) + 1] = x[1];
-            if constexpr (NT == 2) {
-                const f32x2 rest = {e[0] - (float)x[0], e[1] - (float)x[1]};
-                const f16x2 y = __builtin_convertvector(rest, f16x2);
-                w[1][u][r >> 3][r & 7] = y[0];
-                w[1][u][r >> 3][(r & 7) + 1] = y[1];
-            }
+        for (int r = 0; r < 16; r += 2) pair(masked, s, ck, off, r, w, sum, lo, hi);
+        l += sum * exp2_fast(-lr);
+        output(v0, u, w);
+    };
+    // block u of a step with scales sc, with scores s and their maximum, next to the scores of the block after it (K at nk, block nu; into
+    // sn, topn) and the output of the block before it (V at pv, block pu, probabilities wp); its own go to w
+    auto piped_block = [&](auto uc, const f32x4& sc, unsigned big, const f32x16& s, float top, int nk, int nu, f32x16& sn, float& topn, int pv, int pu,
+                           Probs& wp, Probs& w, auto stage) __attribute__((always_inline)) {
+        f16x8 fr[NC + 2 * ND];
+        auto frag = [&](auto jc) {
+            constexpr int j = decltype(jc)::value;
+            if constexpr (j < NC) fr[j] = k_frag(nk, nu, j);
+            else if constexpr (j < NC + 2 * ND) fr[j] = v_frag(pv, pu, j - NC);
         };
-        if constexpr (AHEAD) {
-            // block u of the new scores next to block u of the probabilities: three of the four are live at a time
-            f16x8 kf[2 * NC];
-            kf[0] = k_frag(buf ^ 1, 0, 0);
-            kf[1] = k_frag(buf ^ 1, 0, 1);
-            static_for<0, 2 * NC>([&](auto jc) {
-                constexpr int j = decltype(jc)::value, u = j / NC, c = j % NC;
-                if constexpr (j + 2 < 2 * NC) kf[j + 2] = k_frag(buf ^ 1, (j + 2) / NC, (j + 2) % NC);
-                if constexpr (c == 0) {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) sn[u][r] = 0.f;
-                }
-                sn[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[j], q[0][c], sn[u], 0, 0, 0);
-                static_for<8 * c / NC, 8 * (c + 1) / NC>([&](auto pc) { pair(u, 2 * decltype(pc)::value); });
-                __builtin_amdgcn_sched_barrier(0);
+        static_for<0, AHEAD>(frag);
+        constexpr int u = decltype(uc)::value;
+        const float ck = sc[u] * qs;
+        const float mx = max_halves(top * ck);
+        if ((u == 0 && over_R(big)) || __any(mx > limit)) {      // R is the step's
+            output(pv, pu, wp);
+            forget(wp);
+            move(mx, big);
+            if (u == 0 && sc[2] + sc[3] != sc[2] + sc[3]) poison = __builtin_nanf("");
+        }
+        const float lr = log2_rv(sc[2 + u]), off = ref - lr;
+        float sum = 0.f;
+        static_for<0, NC + 2 * ND>([&](auto jc) {
+            constexpr int j = decltype(jc)::value;
+            frag(std::integral_constant<int, j + AHEAD>{});
+            if constexpr (j == 0) clear(sn);
+            if constexpr (j < NC) {
+                sn = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[j], q[0][j], sn, 0, 0, 0);
+            } else {
+                constexpr int i = (j - NC) % ND, k = (j - NC) / ND;
+                acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[j], wp[0][k], acc[i], 0, 0, 0);
+            }
+            static_for<8 * j / (NC + 2 * ND), 8 * (j + 1) / (NC + 2 * ND)>([&](auto pc) {
+                pair(std::false_type{}, s, ck, off, 2 * decltype(pc)::value, w, sum, 0, 16);
             });
-        } else {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int r = 0; r < 16; r += 2) pair(u, r);
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const float add = sum[u] * exp2_fast(-lr[u]);
-            // 0 (1 / rv) of a foreign block may be NaN
-            if (!MASKED || (g0 + 32 * u + 16 > my_lo && g0 + 32 * u < my_hi)) l += add;
-        }
-        f16x8 vf[4 * ND];
-        vf[0] = v_frag(buf, 0, 0);
-        vf[1] = v_frag(buf, 1, 0);
-        static_for<0, 4 * ND>([&](auto jc) {
-            constexpr int j = decltype(jc)::value, i = j % ND, uk = j / ND;
-            if constexpr (j + 2 < 4 * ND) vf[j + 2] = v_frag(buf, (j + 2) % ND, (j + 2) / ND);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[j], w[n][uk >> 1][uk & 1], acc[i], 0, 0, 0);
-            if constexpr (AHEAD)
-                static_for<16 * j / (4 * ND), 16 * (j + 1) / (4 * ND)>([&](auto pc) {
-                    constexpr int pr = decltype(pc)::value;
-                    top_of(sn, pr >> 3, 2 * (pr & 7));
+            if constexpr (j % STAGE_EVERY == 0 && j / STAGE_EVERY < 4) stage(std::integral_constant<int, j / STAGE_EVERY>{});
+            // the new scores are complete a product after their last one
+            if constexpr (j > NC)
+                static_for<8 * (j - NC - 1) / (2 * ND - 1), 8 * (j - NC) / (2 * ND - 1)>([&](auto pc) {
+                    top_of(sn, topn, 2 * decltype(pc)::value);
                 });
             __builtin_amdgcn_sched_barrier(0);
         });
-        if constexpr (!AHEAD) scores(buf ^ 1, sn);
+        l += sum * exp2_fast(-lr);
     };
 
     if (s0 < s1) {
-        idk = entry(s0 * TK + kfirst);
-        idv = entry(s0 * TK + vfirst);
-        fetch_k(s0);
-        fetch_v(s0);
-        if (t < 4) {
-            ids_now = entry(s0 * TK + 16 * t);
-            ids_next = entry((s0 + 1) * TK + 16 * t);
-            sk_r = scale_of(a.ks, s0, ids_now);
-            sv_r = scale_of(a.vs, s0, ids_now);
+        ids1 = entries(s0);
+        ids2 = entries(s0 + 1);
+        fetch_k(s0, ids1);
+        fetch_v(s0, ids1);
+        fetch_scales(ids1);
+        for (int half : {0, 1}) {
+            stage_k(k0, half);
+            stage_v(v0, half);
         }
-        stage_k(0, 0);
-        stage_v(0);
-        fetch_k(s0 + 1);
-        if (t < 4) {
-            sk_r = scale_of(a.ks, s0 + 1, ids_next);
-            ids_now = ids_next;
-            ids_next = entry((s0 + 2) * TK + 16 * t);
-        }
-        stage_k(1, 1);
+        stage_scales(s0, ids1);
+        fetch_k(s0 + 1, ids2);
+        fetch_scales(ids2);
+        for (int half : {0, 1}) stage_k(k1, half);
+        stage_scales(s0 + 1, ids2);
+        ids1 = ids2;
+        ids2 = entries(s0 + 2);
         __syncthreads();
-        f32x16 sa[2];
-        scores(0, sa);
-        __syncthreads();      // the first step's staging reuses this buffer of K
-        auto step = [&](auto masked_c, int buf, int it, f32x16 (&s)[2], f32x16 (&sn)[2]) {
-            fetch_k(it + 2);      // past the last step: some block, into a buffer that nobody reads
-            fetch_v(it + 1);
-            if (t < 4) {
-                sk_r = scale_of(a.ks, it + 2, ids_next);
-                sv_r = scale_of(a.vs, it + 1, ids_now);
-                ids_now = ids_next;
-                ids_next = entry((it + 3) * TK + 16 * t);
-            }
-            if (!decltype(masked_c)::value || it * TK < w_max) body(masked_c, buf, it, s, sn);
-            stage_k(buf, it + 2 - s0);      // waves behind may still want this step's scales: not its slot
-            stage_v(buf ^ 1);
-            __syncthreads();
+        int ids3;
+        auto begin = [&](int it) {      // past the last step: some block, into a buffer that nobody reads
+            fetch_k(it + 2, ids2);
+            fetch_v(it + 1, ids1);
+            fetch_scales(ids2);
+            ids3 = entries(it + 3);
         };
-        // steps that some row of the tile masks (the start of windows, the diagonal) go through loops of their own, with
-        // what makes the count of the others between them even on either side
+        auto stage = [&](auto part) {
+            constexpr int i = decltype(part)::value;
+            if constexpr (i < 2) stage_k(k2, i);
+            else stage_v(v1, i - 2);
+        };
+        auto finish = [&] {
+            __syncthreads();
+            ids1 = ids2;
+            ids2 = ids3;
+            const int k = k0, v = vm;
+            k0 = k1;
+            k1 = k2;
+            k2 = k;
+            vm = v0;
+            v0 = v1;
+            v1 = v;
+        };
+        auto plain_step = [&](auto masked, int it) __attribute__((always_inline)) {
+            begin(it);
+            if (!decltype(masked)::value || it * TK < w_max) {
+                plain_block(masked, it, 0);
+                plain_block(masked, it, 1);
+            }
+            static_for<0, 4>(stage);
+            stage_scales(it + 2, ids2);
+            finish();
+        };
+        // steps that some row of the tile masks (the start of windows, the diagonal) go through loops of their own
         int it = s0;
-        const int whole = std::min((int)((tl.lo_max + TK - 1) / TK), s1), last = std::min((int)(tl.hi_min / TK), s1);
-        for (; it < whole || ((it - s0) & 1 && it < s1); ++it) step(std::true_type{}, (it - s0) & 1, it, sa, sa);
+        const int whole = std::min(__builtin_amdgcn_readfirstlane((int)((tl.lo_max + TK - 1) / TK)), s1);
+        const int last = std::min(__builtin_amdgcn_readfirstlane((int)(tl.hi_min / TK)), s1);
+        for (; it < whole; ++it) plain_step(std::true_type{}, it);
         if constexpr (PIPE) {
-            f32x16 sb[2];
-            for (; it + 1 < last; it += 2) {
-                step(std::false_type{}, 0, it, sa, sb);
-                step(std::false_type{}, 1, it + 1, sb, sa);
+            if (it < last) {
+                f32x16 sa, sb;
+                float ta, tb;
+                Probs wa, wb;
+                scores(k0, 0, sa, ta);
+                forget(wb);
+                int pv = v0;        // nothing before the first block: zero probabilities on any V that is there
+                f32x4 sc = scales_of(it), sc_next;
+                float big = big_of(it), big_next;
+                for (; it < last; ++it) {
+                    begin(it);
+                    piped_block(std::integral_constant<int, 0>{}, sc, bits(big), sa, ta, k0, 1, sb, tb, pv, 1, wb, wa,
+                                [](auto) {});
+                    stage_scales(it + 2, ids2);
+                    sc_next = scales_of(it + 1);
+                    big_next = big_of(it + 1);
+                    piped_block(std::integral_constant<int, 1>{}, sc, bits(big), sb, tb, k1, 0, sa, ta, v0, 0, wa, wb, stage);
+                    sc = sc_next;
+                    big = big_next;
+                    finish();
+                    pv = vm;
+                }
+                output(pv, 1, wb);
             }
         } else {
-            for (; it < last; ++it) step(std::false_type{}, (it - s0) & 1, it, sa, sa);
+            for (; it < last; ++it) plain_step(std::false_type{}, it);
         }
-        for (; it < s1; ++it) step(std::true_type{}, (it - s0) & 1, it, sa, sa);
+        for (; it < s1; ++it) plain_step(std::true_type{}, it);
     }
     if (idle) return;
 
     l += __shfl_xor(l, 32, 64);
     if (tl.f0 + 32 * wave + li >= tl.rows) return;
-    const float mine = (R > 0.f ? R : 1.f) / (l == 0.f ? 1.f : l);
+    poison += __shfl_xor(poison, 32, 64);
+    const float mine = (R > 0.f ? R : 1.f) / (l == 0.f ? 1.f : l) + poison;
     const bool split_out = a.nsplit > 1;
     const int64_t nflat = a.g.rows * a.heads, at = token * a.heads + qh;
 #pragma unroll

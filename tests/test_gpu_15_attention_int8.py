@@ -187,6 +187,30 @@ def test_non_finite_stays_with_its_rows(gpu, qn):
     assert torch.equal(got[keep], clean[keep])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("qn", [(1, 1), (300, 150)])
+def test_non_finite_values_keep_lse(gpu, qn, dim, dtype):
+    """S_v that is not finite makes the outputs NaN and leaves lse, which V has no part in, as it was."""
+    from post_int4_weight_amd import api
+    announce(f"attention, lse next to NaN values {qn} {dim} {dtype}")
+    lens = [700, 150]
+    cache, table, vals, Q, args = _simple(api, gpu, lens, qn, dtype, dim=dim)
+    clean, want = api.attention_int8_cache(Q, cache, *args, return_lse=True)
+    for at in (5, 42):                       # positions 80 .. 95, that all see; 672 .. 687
+        bad = int(table[0, at])
+        keep = cache.v_scales[bad, 1].clone()
+        cache.v_scales[bad, 1] = float("nan")
+        got, lse = api.attention_int8_cache(Q, cache, *args, return_lse=True)
+        torch.cuda.synchronize()
+        cache.v_scales[bad, 1] = keep
+        seen = torch.zeros(Q.shape[:2], dtype=torch.bool, device=gpu)
+        seen[:qn[0], 2:] = (torch.arange(lens[0] - qn[0], lens[0], device=gpu) >= 16 * at)[:, None]
+        assert torch.isnan(got[seen]).all()
+        assert torch.allclose(got[~seen].float(), clean[~seen].float(), rtol=2.0 ** -7, atol=1e-5)
+        assert torch.allclose(lse, want, rtol=1e-5, atol=1e-5)
+
+
 @pytest.mark.parametrize("qn", [(1, 1), (100, 60)])
 def test_bad_tables_and_lengths(gpu, qn):
     """Ids outside the pool give NaN; so does a length past the table, to its sequence only."""
