@@ -401,6 +401,11 @@ __device__ __forceinline__ void static_for(F&& f) {      // f(integral_constant<
 // block behind its products, and every probability stays in a register till then
 __device__ __forceinline__ void pin(float& x) { asm volatile("" : "+v"(x)); }
 
+template <int QUAD_PERM>
+__device__ __forceinline__ float swap_lanes(float x) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), QUAD_PERM, 0xf, 0xf, true));
+}
+
 constexpr float LOG2_RV_MIN = -60;   // below it a block adds nothing to the output (w underflows), only to the sum
 
 // the larger of x in this lane and in lane ^ 32
@@ -418,7 +423,7 @@ template <int D>
 struct TileLds {
     static constexpr int KROW = 2 * D + 16, VROW = 2 * TK + 16;       // bytes of a token of K, of a channel of V
     static constexpr int K_BYTES = TK * KROW, V_BYTES = D * VROW;
-    static constexpr int BYTES = 3 * (K_BYTES + V_BYTES);
+    static constexpr int V_AT = 2 * K_BYTES, BYTES = V_AT + 3 * V_BYTES;
     // operand row of a token of a step
     __host__ __device__ static constexpr int k_row(int token) {
         return (token & ~31) | (token >> 2 & 3) << 3 | (token >> 4 & 1) << 2 | (token & 3);
@@ -430,7 +435,6 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
     constexpr int NT = sizeof(T) == 4 ? 2 : 1;
     constexpr bool PIPE = NT == 1;                 // two terms of everything would not fit the registers
     constexpr int AHEAD = 3;
-    constexpr int STAGE_EVERY = D / 64;
     constexpr int NTH = 64 * WAVES, NC = D / 16, ND = D / 32;
     constexpr int NCH = TK * D / 16;               // 16-byte chunks of K, and of V, in a step
     static_assert(NCH % 64 == 0 && NCH <= NTH, "one chunk of each a thread");
@@ -502,7 +506,7 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
     auto base = [&](const int8_t* from, int ids, int group) {
         return from + (int64_t)valid(__builtin_amdgcn_readlane(ids, group)) * stride;
     };
-    int ids1 = 0, ids2 = 0;         // of the next step, of the one after it
+    int ids2 = 0, ids3 = 0;         // of steps it + 2, it + 3
     uint4 rk, rv_;
     float sk_r, sv_r;
     auto fetch_k = [&](int it, int ids) {
@@ -519,7 +523,7 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
         }
     };
     const int kto = L::k_row(ktok) * L::KROW + 32 * (t % (D / 16));
-    const int vto = 3 * L::K_BYTES + vd * L::VROW + 32 * vgrp;
+    const int vto = L::V_AT + vd * L::VROW + 32 * vgrp;
     auto stage_k = [&](int at, int half) {    // at: offset of the buffer
         if (stages) *(f16x8*)(smem + at + kto + 16 * half) = half ? half8(rk.z, rk.w) : half8(rk.x, rk.y);
     };
@@ -536,17 +540,17 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
             to[0] = sk;
             to[2] = bad ? __builtin_nanf("") : __builtin_amdgcn_logf(sv);     // v_log_f32: base 2
             float big = bad ? 0.f : sv;
-            big = fmaxf(big, __shfl_xor(big, 1, 4));
-            big = fmaxf(big, __shfl_xor(big, 2, 4));
+            big = fmaxf(big, swap_lanes<0xB1>(big));        // quad_perm [1, 0, 3, 2]
+            big = fmaxf(big, swap_lanes<0x4E>(big));        // quad_perm [2, 3, 0, 1]
             const bool any_bad = __ballot(bad) != 0;
             if (lane == 0) sbig[(it - s0) & 3] = any_bad ? -big : big;
         }
     };
-    // buffers of K of this step and the next two, of V of the last step, this one and the next
-    int k0 = 0, k1 = L::K_BYTES, k2 = 2 * L::K_BYTES, vm = 2 * L::V_BYTES, v0 = 0, v1 = L::V_BYTES;
+    // buffers of K of this step and the next, of V of the last step, this one and the next
+    int k0 = 0, k1 = L::K_BYTES, vm = 2 * L::V_BYTES, v0 = 0, v1 = L::V_BYTES;
 
     // operand fragments of this lane
-    const int kfrom = li * L::KROW + 16 * hf, vfrom = 3 * L::K_BYTES + li * L::VROW + 32 * hf;
+    const int kfrom = li * L::KROW + 16 * hf, vfrom = L::V_AT + li * L::VROW + 32 * hf;
     auto k_frag = [&](int at, int u, int c) {       // tokens 32 u .., channels 16 c ..
         return *(const f16x8*)(smem + at + kfrom + 32 * u * L::KROW + 32 * c);
     };
@@ -665,31 +669,60 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
         l += sum * exp2_fast(-lr);
         output(v0, u, w);
     };
-    // block u of a step with scales sc, with scores s and their maximum, next to the scores of the block after it (K at nk, block nu; into
-    // sn, topn) and the output of the block before it (V at pv, block pu, probabilities wp); its own go to w
-    auto piped_block = [&](auto uc, const f32x4& sc, unsigned big, const f32x16& s, float top, int nk, int nu, f32x16& sn, float& topn, int pv, int pu,
-                           Probs& wp, Probs& w, auto stage) __attribute__((always_inline)) {
-        f16x8 fr[NC + 2 * ND];
-        auto frag = [&](auto jc) {
-            constexpr int j = decltype(jc)::value;
-            if constexpr (j < NC) fr[j] = k_frag(nk, nu, j);
-            else if constexpr (j < NC + 2 * ND) fr[j] = v_frag(pv, pu, j - NC);
-        };
-        static_for<0, AHEAD>(frag);
-        constexpr int u = decltype(uc)::value;
-        const float ck = sc[u] * qs;
-        const float mx = max_halves(top * ck);
-        if ((u == 0 && over_R(big)) || __any(mx > limit)) {      // R is the step's
+    // What a block needs to know before its exponentials: S_k, the largest score of each row, whether a row has to move
+    struct Head {
+        float ck, mx, lr, off;
+        unsigned big;
+        bool moves;
+    };
+    auto head_of = [&](float sk, float lv, unsigned big, float top, bool first) {
+        Head h;
+        h.ck = sk * qs;
+        h.mx = max_halves(top * h.ck);
+        h.big = big;
+        h.moves = (first && over_R(big)) || __any(h.mx > limit);      // S_v's are the step's
+        h.lr = log2_rv(lv);
+        h.off = ref - h.lr;
+        return h;
+    };
+    // Block u of a step with scales sc, scores s and head h, next to the scores of the block after it (K at nk, block nu;
+    // into sn, topn) and the output of the block before it (V at pv, block pu, probabilities wp); its own go to w. pre:
+    // the first fragments, then those of the block after (K at nk2, block nu2). at_slot: what else goes between products
+    // head: of the next block, once its maxima are known
+    auto piped_block = [&](auto uc, const f32x4& sc, Head& h, const f32x16& s, f32x16& sn, f16x8 (&pre)[AHEAD], int nk, int nu,
+                           int pv, int pu, int nk2, int nu2, Probs& wp, Probs& w, auto at_slot,
+                           auto next_head) __attribute__((always_inline)) {
+        constexpr int u = decltype(uc)::value, N = NC + 2 * ND, PER = 16 / N;      // values a product
+        if (h.moves) {
             output(pv, pu, wp);
             forget(wp);
-            move(mx, big);
+            move(h.mx, h.big);
             if (u == 0 && sc[2] + sc[3] != sc[2] + sc[3]) poison = __builtin_nanf("");
+            h.lr = log2_rv(sc[2 + u]);
+            h.off = ref - h.lr;
         }
-        const float lr = log2_rv(sc[2 + u]), off = ref - lr;
-        float sum = 0.f;
-        static_for<0, NC + 2 * ND>([&](auto jc) {
-            constexpr int j = decltype(jc)::value;
-            frag(std::integral_constant<int, j + AHEAD>{});
+        f16x8 fr[N];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) fr[j] = pre[j];
+        float sum = 0.f, topn = 0.f, e[16];
+        auto add_up = [&](auto jc) {           // values PER j .. of the last slot
+            constexpr int r0 = PER * decltype(jc)::value;
+#pragma unroll
+            for (int r = r0; r < r0 + PER; ++r) {
+                sum = r ? sum + e[r] : e[r];
+                if (r & 1) {
+                    const f16x2 x = __builtin_convertvector((f32x2{e[r - 1], e[r]}), f16x2);
+                    w[0][r >> 3][(r & 7) - 1] = x[0];
+                    w[0][r >> 3][r & 7] = x[1];
+                }
+            }
+            pin(sum);
+        };
+        static_for<0, N>([&](auto jc) {
+            constexpr int j = decltype(jc)::value, J = j + AHEAD;
+            if constexpr (J < NC) fr[J] = k_frag(nk, nu, J);
+            else if constexpr (J < N) fr[J] = v_frag(pv, pu, J - NC);
+            else pre[J - N] = k_frag(nk2, nu2, J - N);
             if constexpr (j == 0) clear(sn);
             if constexpr (j < NC) {
                 sn = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[j], q[0][j], sn, 0, 0, 0);
@@ -697,71 +730,76 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
                 constexpr int i = (j - NC) % ND, k = (j - NC) / ND;
                 acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[j], wp[0][k], acc[i], 0, 0, 0);
             }
-            static_for<8 * j / (NC + 2 * ND), 8 * (j + 1) / (NC + 2 * ND)>([&](auto pc) {
-                pair(std::false_type{}, s, ck, off, 2 * decltype(pc)::value, w, sum, 0, 16);
-            });
-            if constexpr (j % STAGE_EVERY == 0 && j / STAGE_EVERY < 4) stage(std::integral_constant<int, j / STAGE_EVERY>{});
+#pragma unroll
+            for (int r = PER * j; r < PER * (j + 1); ++r) e[r] = exp2_fast(fmaf(s[r], h.ck, -h.off));
+            if constexpr (j > 0) add_up(std::integral_constant<int, j - 1>{});
+            at_slot(jc);
             // the new scores are complete a product after their last one
-            if constexpr (j > NC)
-                static_for<8 * (j - NC - 1) / (2 * ND - 1), 8 * (j - NC) / (2 * ND - 1)>([&](auto pc) {
+            constexpr int FROM = NC + 1, LAST = N - 2;
+            if constexpr (j >= FROM && j < LAST)
+                static_for<8 * (j - FROM) / (LAST - FROM), 8 * (j + 1 - FROM) / (LAST - FROM)>([&](auto pc) {
                     top_of(sn, topn, 2 * decltype(pc)::value);
                 });
+            if constexpr (j == N - 1) {
+                add_up(jc);
+                l += sum * exp2_fast(-h.lr);
+                h = next_head(topn);
+            }
             __builtin_amdgcn_sched_barrier(0);
         });
-        l += sum * exp2_fast(-lr);
     };
 
     if (s0 < s1) {
-        ids1 = entries(s0);
-        ids2 = entries(s0 + 1);
-        fetch_k(s0, ids1);
-        fetch_v(s0, ids1);
-        fetch_scales(ids1);
+        const int ids0 = entries(s0), ids1 = entries(s0 + 1);
+        fetch_k(s0, ids0);
+        fetch_v(s0, ids0);
+        fetch_scales(ids0);
         for (int half : {0, 1}) {
             stage_k(k0, half);
             stage_v(v0, half);
         }
-        stage_scales(s0, ids1);
-        fetch_k(s0 + 1, ids2);
-        fetch_scales(ids2);
+        stage_scales(s0, ids0);
+        fetch_k(s0 + 1, ids1);
+        fetch_scales(ids1);
         for (int half : {0, 1}) stage_k(k1, half);
-        stage_scales(s0 + 1, ids2);
-        ids1 = ids2;
+        stage_scales(s0 + 1, ids1);
+        // what a step finds: K of it and it + 1, V of it, scales of it and it + 1 in LDS; K of it + 2, V of it + 1 and
+        // scales of it + 2 on their way (past the last step: of some block, into a buffer that nobody reads)
         ids2 = entries(s0 + 2);
+        ids3 = entries(s0 + 3);
+        fetch_k(s0 + 2, ids2);
+        fetch_v(s0 + 1, ids1);
+        fetch_scales(ids2);
         __syncthreads();
-        int ids3;
-        auto begin = [&](int it) {      // past the last step: some block, into a buffer that nobody reads
-            fetch_k(it + 2, ids2);
-            fetch_v(it + 1, ids1);
-            fetch_scales(ids2);
-            ids3 = entries(it + 3);
+        auto next_scales = [&](int it) {
+            stage_scales(it + 2, ids2);
+            fetch_scales(ids3);
         };
-        auto stage = [&](auto part) {
-            constexpr int i = decltype(part)::value;
-            if constexpr (i < 2) stage_k(k2, i);
-            else stage_v(v1, i - 2);
-        };
-        auto finish = [&] {
-            __syncthreads();
-            ids1 = ids2;
+        auto next_ids = [&](int it) {
             ids2 = ids3;
+            ids3 = entries(it + 4);
+        };
+        auto rotate = [&] {
             const int k = k0, v = vm;
             k0 = k1;
-            k1 = k2;
-            k2 = k;
+            k1 = k;
             vm = v0;
             v0 = v1;
             v1 = v;
         };
         auto plain_step = [&](auto masked, int it) __attribute__((always_inline)) {
-            begin(it);
+            for (int half : {0, 1}) stage_v(v1, half);
+            fetch_v(it + 2, ids2);
             if (!decltype(masked)::value || it * TK < w_max) {
                 plain_block(masked, it, 0);
                 plain_block(masked, it, 1);
             }
-            static_for<0, 4>(stage);
-            stage_scales(it + 2, ids2);
-            finish();
+            __syncthreads();
+            for (int half : {0, 1}) stage_k(k0, half);
+            fetch_k(it + 3, ids3);
+            next_scales(it);
+            next_ids(it);
+            rotate();
         };
         // steps that some row of the tile masks (the start of windows, the diagonal) go through loops of their own
         int it = s0;
@@ -771,27 +809,50 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
         if constexpr (PIPE) {
             if (it < last) {
                 f32x16 sa, sb;
-                float ta, tb;
+                f16x8 pre[AHEAD];
                 Probs wa, wb;
-                scores(k0, 0, sa, ta);
+                float top;
+                scores(k0, 0, sa, top);
                 forget(wb);
                 int pv = v0;        // nothing before the first block: zero probabilities on any V that is there
                 f32x4 sc = scales_of(it), sc_next;
-                float big = big_of(it), big_next;
+                float big_next;
+                Head h = head_of(sc[0], sc[2], bits(big_of(it)), top, true);
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) pre[j] = k_frag(k0, 1, j);
                 for (; it < last; ++it) {
-                    begin(it);
-                    piped_block(std::integral_constant<int, 0>{}, sc, bits(big), sa, ta, k0, 1, sb, tb, pv, 1, wb, wa,
-                                [](auto) {});
-                    stage_scales(it + 2, ids2);
-                    sc_next = scales_of(it + 1);
-                    big_next = big_of(it + 1);
-                    piped_block(std::integral_constant<int, 1>{}, sc, bits(big), sb, tb, k1, 0, sa, ta, v0, 0, wa, wb, stage);
+                    // K of this step is not read after product NC - 1, what the last step staged is not before the last
+                    // AHEAD products: the barrier goes in between, where no access to LDS that it has to order is open
+                    piped_block(std::integral_constant<int, 0>{}, sc, h, sa, sb, pre, k0, 1, pv, 1, k1, 0, wb, wa,
+                        [&](auto slot) {
+                            if constexpr (decltype(slot)::value == NC) {
+                                asm volatile("" ::: "memory");
+                                __builtin_amdgcn_s_barrier();
+                                asm volatile("" ::: "memory");
+                            }
+                        },
+                        [&](float topn) { return head_of(sc[1], sc[3], 0, topn, false); });
+                    piped_block(std::integral_constant<int, 1>{}, sc, h, sb, sa, pre, k1, 0, v0, 0, k1, 1, wa, wb,
+                        [&](auto slot) {
+                            constexpr int j = decltype(slot)::value * 16 / (NC + 2 * ND);       // of 16, or every second
+                            if constexpr (j == 0) {
+                                sc_next = scales_of(it + 1);
+                                big_next = big_of(it + 1);
+                            }
+                            if constexpr (j == 2) stage_k(k0, 0);
+                            if constexpr (j == 4) stage_k(k0, 1), fetch_k(it + 3, ids3);
+                            if constexpr (j == 6) stage_v(v1, 0);
+                            if constexpr (j == 8) stage_v(v1, 1), fetch_v(it + 2, ids2);
+                            if constexpr (j == 10) next_scales(it);
+                            if constexpr (j == 12) next_ids(it);
+                        },
+                        [&](float topn) { return head_of(sc_next[0], sc_next[2], bits(big_next), topn, true); });
                     sc = sc_next;
-                    big = big_next;
-                    finish();
+                    rotate();
                     pv = vm;
                 }
                 output(pv, 1, wb);
+                __syncthreads();
             }
         } else {
             for (; it < last; ++it) plain_step(std::false_type{}, it);
