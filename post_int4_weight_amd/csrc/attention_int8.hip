@@ -107,11 +107,12 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t unit, int t
     return true;
 }
 
-// Steps of a split of a tile: an even share, at least MIN_STEPS.
-constexpr int MIN_STEPS = 4;
-__device__ __forceinline__ int split_steps(const Tile& t, int nsplit) {
+// Steps of a split of a tile of tr rows: an even share, but not so few that
+// the start of a workgroup and the join would outweigh them.
+constexpr int min_steps(int tr) { return tr == TR ? 8 : 4; }
+__device__ __forceinline__ int split_steps(const Tile& t, int nsplit, int tr) {
     const int n = t.it1 - t.it0;
-    return std::max(MIN_STEPS, (n + nsplit - 1) / nsplit);
+    return std::max(min_steps(tr), (n + nsplit - 1) / nsplit);
 }
 
 // One query row in fp16 terms: scaled by the power of two that brings its
@@ -170,7 +171,7 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
     const int h = (int)(tile % a.kv_heads);
     Tile tl;
     if (!find_tile(a, tile / a.kv_heads, TR, tl)) return;
-    const int per = split_steps(tl, a.nsplit);
+    const int per = split_steps(tl, a.nsplit, TR);
     const int s0 = tl.it0 + split * per, s1 = std::min(s0 + per, tl.it1);
     if (split > 0 && s0 >= s1) return;
 
@@ -383,12 +384,22 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
 // one S_k and one S_v per lane and score block, which go into the exponent,
 // w = 2^(s ck - m + log2 rv), and the sum of p takes 1 / rv once per 16 values.
 //
-// A block of 32 tokens takes 512 matrix cycles a wave (D = 128) and about as
-// many in vector instructions, so three blocks are in work at a time: the
+// What bounds it (D = 128): a product holds the SIMD's vector pipe for 24 of its
+// 32 cycles' worth, so products and the 8 vector instructions that go with each
+// of them (scale, exponential, sum, rounding of its share of probabilities,
+// maxima, conversion of the codes) come to about 40 cycles, and the fragment a
+// product reads takes LDS another 32. All three being near, a wave must never
+// wait with only one other on its SIMD: three blocks are in work at a time, the
 // products give the scores of block n + 1 and the output of block n - 1 while
-// the exponentials of block n run between them, and an operand fragment is
-// read from LDS AHEAD products before its own. LDS holds three steps of K and
-// of V, so that one barrier a step is enough.
+// the exponentials of block n run between them, and everything else of a step
+// (fetching and staging the next ones, its only barrier, the head of the next
+// block) lies between products, too. A fragment is read AHEAD products early.
+// Measured, 4 prompts of 2000 .. 4096 tokens over 5000 keys, 32 query heads on
+// 8: 652 us, 43% of the matrix cycles; phases one after the other were 785. 64
+// rows a wave halve the LDS reads, but then one wave a SIMD has to issue
+// everything, and a sixth more of it to move accumulators between register
+// files: 917 us against 773 on the same card. Fragments 6 products early, or
+// wave priorities, change it by 1%.
 template <int B, int E, typename F>
 __device__ __forceinline__ void static_for(F&& f) {      // f(integral_constant<int, I>) for I = B .. E - 1, in order
     if constexpr (B < E) {
@@ -450,7 +461,7 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
     Tile tl;
     // later tiles of a sequence have more keys: they go first
     if (!find_tile(a, gridDim.x / (unsigned)a.nsplit / a.kv_heads - 1 - tile / a.kv_heads, 32 * WAVES, tl)) return;
-    const int per = split_steps(tl, a.nsplit);
+    const int per = split_steps(tl, a.nsplit, 32 * WAVES);
     const int s0 = __builtin_amdgcn_readfirstlane(tl.it0 + split * per);
     const int s1 = __builtin_amdgcn_readfirstlane(std::min(s0 + per, tl.it1));
     if (split > 0 && s0 >= s1) return;
@@ -745,7 +756,6 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
                 l += sum * exp2_fast(-h.lr);
                 h = next_head(topn);
             }
-            __builtin_amdgcn_sched_barrier(0);
         });
     };
 
@@ -896,26 +906,44 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int tr)
     const int h = (int)(tile % a.kv_heads);
     Tile tl;
     if (!find_tile(a, tile / a.kv_heads, tr, tl)) return;
-    const int per = split_steps(tl, a.nsplit);
+    const int per = split_steps(tl, a.nsplit, tr);
     const int n = std::max(1, (tl.it1 - tl.it0 + per - 1) / per);    // split 0 is always written
     const int r = threadIdx.x / 16, c = threadIdx.x % 16, f = tl.f0 + (int)part * TR + r;
     if (f >= tl.rows) return;
     const int64_t row = tl.off + f / a.group, nflat = a.g.rows * a.heads;
     const int head = h * a.group + f % a.group;
     const int64_t at = row * a.heads + head;
-    float M = -INFINITY;
-    for (int s = 0; s < n; ++s) M = fmaxf(M, a.part_lse[s * nflat + at]);
-    const float M0 = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
+    // JB splits at a time, all their loads at once
+    constexpr int JB = 8;
+    float M = -INFINITY, M0 = 0.f, L = 0.f;
     f32x4 o[D / 64];
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < n; ++s) {
-        const float w = exp2_fast(a.part_lse[s * nflat + at] - M0);
-        L += w;
-        const float* p = a.part + (s * nflat + at) * D;
+    for (int s = 0; s < n; s += JB) {
+        float lse[JB];
+        f32x4 v[JB][D / 64];
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) o[i] += w * *(const f32x4*)(p + 64 * i + 4 * c);
+        for (int j = 0; j < JB; ++j) {
+            const int64_t from = std::min(s + j, n - 1) * nflat + at;
+            lse[j] = s + j < n ? a.part_lse[from] : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) v[j][i] = *(const f32x4*)(a.part + from * D + 64 * i + 4 * c);
+        }
+        const float before = M;
+#pragma unroll
+        for (int j = 0; j < JB; ++j) M = fmaxf(M, lse[j]);
+        M0 = M == -INFINITY ? 0.f : M;
+        const float fall = exp2_fast(before - M0);
+        L *= fall;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) o[i] *= fall;
+#pragma unroll
+        for (int j = 0; j < JB; ++j) {
+            const float w = exp2_fast(lse[j] - M0);
+            L += w;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) o[i] += (s + j < n ? w : 0.f) * v[j][i];
+        }
     }
     const float inv = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
 #pragma unroll
@@ -931,29 +959,59 @@ int64_t tile_units(int64_t rows, int64_t batch, int group, int tr) { return rows
 // fragments of 32 rows leave no registers for the rest: those go through
 // attention_rows_kernel whatever the number of rows.
 constexpr int TILE_WAVES = 8;
-constexpr int64_t SHORT_KEYS = 2048;
 
-// Which kernel, and how many splits of the keys.
+// Which kernel, and how many splits of the keys. Lengths are not known here:
+// keys is the most there may be, and every sequence but one is taken to end half
+// way through a tile.
 struct Plan {
     int tr;        // rows of a tile: TR, or 32 TILE_WAVES
     int nw;        // waves of attention_rows_kernel
     int nsplit;
 };
-Plan plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int block, int64_t width) {
+int64_t likely_tiles(int64_t rows, int64_t batch, int group, int tr) {
+    return std::max<int64_t>({1, batch, cdiv(rows * group, tr) + (batch - 1) / 2});
+}
+int64_t most_keys(int64_t rows, int64_t batch, int block, int64_t width, int64_t window) {
+    const int64_t keys = width * block;
+    return window > 0 ? std::min(keys, window + cdiv(rows, std::max<int64_t>(batch, 1))) : keys;
+}
+// Tiles, one workgroup on a CU at a time: splits as long as all run at once. 1
+// sequence of 512 queries on 8 kv heads over 4000 keys: 59 us with the 256
+// workgroups that 4 splits make, 78 with 2 splits, 77 with 8.
+// Few rows: splits of 32 steps up to 1536 workgroups (64 sequences of 100 ..
+// 16000 keys on 8 heads: 227 us with 3 splits, 243 with 2, 259 with 1), and
+// shorter ones only up to 512 (16 sequences of 100 .. 8000 keys: 34.8 us with 4
+// splits, 38.2 with 8, 51.5 with 16; 128 sequences of 100 .. 4000 keys: 124 with
+// 1, 136 with 2).
+// Up to 2048 keys eight waves share a tile instead, and there is no join: 1000
+// keys 14.3 us, split 19; 16 sequences of 2000 keys 20.9 and 25.3. At 4000 keys
+// of one sequence it is 29 against 19.
+Plan plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int64_t keys, bool tiles) {
     Plan p;
-    const int group = heads / kv_heads;
-    p.tr = dim <= 128 && rows * group >= 64 * batch ? 32 * TILE_WAVES : TR;
-    const int64_t units = tile_units(rows, batch, group, p.tr) * kv_heads;
-    const int64_t longest = width * block, most = cdiv(longest, TK * MIN_STEPS);
-    const int64_t want = p.tr == TR ? 2048 : 256;
-    p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(cdiv(want, units), most), 64));
-    // short sequences: eight waves and no second launch
+    p.tr = tiles ? 32 * TILE_WAVES : TR;
+    const int64_t units = likely_tiles(rows, batch, heads / kv_heads, p.tr) * kv_heads;
+    const int64_t want = tiles ? 256 / units : std::max(512 / units, std::min(1536 / units, cdiv(keys, 32 * TK)));
+    const int64_t most = std::min<int64_t>(cdiv(keys, 8 * TK), 64);
+    p.nsplit = (int)std::max<int64_t>(1, std::min(want, most));
     p.nw = 4;
-    if (p.tr == TR && dim <= 128 && p.nsplit > 1 && longest <= SHORT_KEYS) {
+    if (!tiles && dim <= 128 && p.nsplit > 1 && keys <= 2048) {
         p.nw = 8;
         p.nsplit = 1;
     }
     return p;
+}
+// Microseconds that either kernel takes, fitted to both kernels' times at 2 ..
+// 512 queries on 1000 .. 16000 keys, 64 and 128 channels: a start, and steps of
+// 64 keys, 4 at a time on a CU or one. At 8 sequences on 8 kv heads of 4 query
+// heads over 2000 keys: 16 queries 22.7 us with few rows at a time and 34.6 with
+// tiles, 32 queries 39.3 and 38.7, 64 queries 73.6 and 53.1.
+bool use_tiles(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int64_t keys) {
+    if (dim > 128) return false;
+    const int group = heads / kv_heads;
+    const double steps = (double)keys / TK * kv_heads * dim / 128;
+    const double few = 18 + 1.85 / 1024 * steps * likely_tiles(rows, batch, group, TR);
+    const double many = 38 + 2.1 / 256 * steps * likely_tiles(rows, batch, group, 32 * TILE_WAVES);
+    return many < few;
 }
 
 template <typename T, int D>
@@ -1000,7 +1058,11 @@ int launch_dim(const AttnArgs& a, const Plan& p, hipStream_t st) {
 
 size_t attention_int8_ws_bytes(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int block,
                                int64_t width) {
-    const int n = plan(rows, batch, heads, kv_heads, dim, block, width).nsplit;
+    // a window makes the splits fewer, and may choose few rows at a time where the whole length would choose tiles
+    const int64_t keys = most_keys(rows, batch, block, width, 0);
+    int n = plan(rows, batch, heads, kv_heads, dim, keys, false).nsplit;
+    if (use_tiles(rows, batch, heads, kv_heads, dim, keys))
+        n = std::max(n, plan(rows, batch, heads, kv_heads, dim, keys, true).nsplit);
     if (n == 1) return 0;
     Sizer z;
     z.take<float>((size_t)n * rows * heads * dim);
@@ -1021,7 +1083,9 @@ int run_attention_int8(const KVCacheInt8& c, const RaggedRows& r, int dtype, con
     a.Q = Q; a.ldq = ldq; a.O = O; a.ldo = ldo; a.lse = lse;
     a.scale2 = (float)(scale * 1.4426950408889634);
     a.causal = causal; a.window = window;
-    const Plan p = plan(r.rows, r.batch, heads, c.heads, c.dim, c.block, r.width);
+    const int64_t keys = most_keys(r.rows, r.batch, c.block, r.width, window);
+    const Plan p = plan(r.rows, r.batch, heads, c.heads, c.dim, keys,
+                        use_tiles(r.rows, r.batch, heads, c.heads, c.dim, keys));
     a.nsplit = p.nsplit;
     if (a.nsplit > 1) {
         Arena ar(ws, ws_bytes);
