@@ -154,8 +154,11 @@ __device__ __forceinline__ float load_query(const T* p, float scale2, f16x8 (&q)
 // of score block t is token 16 (r / 4) + 4 t + r % 4): V comes as one
 // 16-byte load per channel, and a lane's tokens lie in one block of the cache
 // (its size is a multiple of 16), so a lane needs one S_k and one S_v a step.
-// The waves of a workgroup take every NW-th step; the codes of a wave's next
-// step are on their way while it works on one, the block ids one step earlier.
+// The waves of a workgroup take every NW-th step; block ids come a step early.
+// What bounds it is memory: each step's 16 KB (D = 128) are requested at once,
+// and the other waves of the CU, four a SIMD, work meanwhile. A second buffer
+// for the next step's codes halves those waves: 280 us against 253. 64
+// sequences of 100 .. 16000 keys, 64 query heads on 8: 227 us, 4.7 TB/s.
 template <int D>
 struct StepCodes {
     uint4 k[4][D / 64], v[D / 16];
@@ -899,7 +902,9 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
 }
 
 // Join of the splits: 16 rows a workgroup, 16 threads a row; tr: rows of the
-// tiles that were split.
+// tiles that were split. A join that reads one split after the other waits for
+// memory each time: 1 query over 16000 keys, 63 splits, 47.8 us in all, 21.8
+// with JB splits at a time.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int tr) {
     const int64_t part = blockIdx.x % (unsigned)(tr / TR), tile = blockIdx.x / (unsigned)(tr / TR);

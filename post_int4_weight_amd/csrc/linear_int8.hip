@@ -6,6 +6,9 @@
 // channel: group_size = in) and c, sx the codes and scales of the activations,
 // quantized token by token (quantize_tokens_int8; "int8.hpp" has the rule).
 // The sums are exact: products of int8 in int32, in < 131072.
+// Measured: 1 token, 4096 x 4096: 6.8 us; 37 tokens, 8192 x 28672: 43 us, the
+// codes at 5.4 TB/s; 8192 tokens, 8192 x 8192: 413 .. 425 us, the product alone
+// 362 .. 385 us, 2.9 .. 3.0 POP/s.
 #include "int8.hpp"
 
 #include <algorithm>
