@@ -244,7 +244,7 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
         }
         const float ck = c.sk * qs;
         const int tv = it * TK + vgrp;
-        const bool whole = it * TK >= tl.lo_max && it * TK + TK <= tl.hi_min;   // no row masks anything here
+        const bool whole = it * TK >= tl.lo_max && (int64_t)it * TK + TK <= tl.hi_min;   // no row masks anything here
         const int r_lo = my_lo - tv, r_hi = my_hi - tv;
         float top = -INFINITY;
 #pragma unroll
@@ -511,7 +511,7 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
     const unsigned voff = (unsigned)(vd * a.bs + ((16 * vgrp) & bmask));
     const int kgrp = wave * 64 / (D / 16) / 16 % 4, vfirst = vblk * gpr;      // a group of the wave's chunks' block
     auto entries = [&](int it) {
-        const unsigned p = (unsigned)std::min(it * TK + 16 * (lane & 3), end - 1);
+        const unsigned p = std::min((unsigned)it * TK + 16 * (lane & 3), (unsigned)end - 1);     // it is past the end, too
         return *(const int32_t*)((const char*)table + (p >> a.bs_log2 << 2));
     };
     // a block without a valid id, and positions past the keys, stand for some other block of the pool, whose codes
@@ -546,7 +546,7 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
     };
     auto stage_scales = [&](int it, int ids) {
         if (wave == 0 && lane < 4) {
-            const bool past = it * TK + 16 * lane >= end, known = (unsigned)ids < (unsigned)a.num_blocks;
+            const bool past = (unsigned)it * TK + 16 * lane >= (unsigned)end, known = (unsigned)ids < (unsigned)a.num_blocks;
             const float sk = past ? 0.f : known ? sk_r : __builtin_nanf("");
             const float sv = past || !known ? 0.f : sv_r;
             const bool bad = !(sv < INFINITY);
