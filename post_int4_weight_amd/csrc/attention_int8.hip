@@ -1079,6 +1079,8 @@ int run_attention_int8(const KVCacheInt8& c, const RaggedRows& r, int dtype, con
                        float scale, int causal, int64_t window, void* O, int64_t ldo, float* lse, void* ws,
                        size_t ws_bytes, hipStream_t st) {
     if (r.rows == 0 || r.batch == 0) return PTQ_OK;
+    // as long as the longest sequence there can be: none (and positions less a window stay far from 2^63)
+    if (window >= r.width * c.block) window = 0;
     AttnArgs a{};
     a.g.offsets = r.offsets; a.g.starts = r.starts; a.g.batch = (int)r.batch; a.g.rows = r.rows;
     a.table = r.table; a.width = r.width;
