@@ -216,6 +216,7 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
         c.sk = a.ks[at];
         c.sv = a.vs[at];
         if (!ok(idv)) c.sk = c.sv = __builtin_nanf("");
+        if (!(c.sv < INFINITY)) c.sv = __builtin_nanf("");     // times codes of one sign it would stay infinite
         if (tv >= end) c.sk = c.sv = 0.f;
     };
 

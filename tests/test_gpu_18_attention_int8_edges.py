@@ -27,3 +27,26 @@ def test_window_without_end(gpu, window, kernel):
     torch.cuda.synchronize()
     assert torch.isfinite(want).all() and (want[10:50] != 0).any(-1).all()
     assert torch.equal(got, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_infinite_values(gpu, kernel, dim, dtype):
+    """An infinite S_v gives NaN, not infinities, to the rows that attend to it; lse, which V has no part in, stays."""
+    from post_int4_weight_amd import api
+    announce(f"attention, infinite S_v {kernel} {dim} {dtype}")
+    lens, qn = [177, 100], (1, 1) if kernel == "rows" else (60, 30)
+    cache, table, vals, Q, args = KERNELS[kernel](api, gpu, lens, qn, dtype, dim=dim)
+    clean, want = api.attention_int8_cache(Q, cache, *args, return_lse=True)
+    for at in (0, 11):                       # positions 0 .. 15; 176 alone
+        bad = int(table[0, at])
+        keep = cache.v_scales[bad, 1].clone()
+        cache.v_scales[bad, 1] = float("inf")
+        got, lse = api.attention_int8_cache(Q, cache, *args, return_lse=True)
+        torch.cuda.synchronize()
+        cache.v_scales[bad, 1] = keep
+        seen = torch.zeros(Q.shape[:2], dtype=torch.bool, device=gpu)
+        seen[:qn[0], 2:] = (torch.arange(lens[0] - qn[0], lens[0], device=gpu) >= 16 * at)[:, None]
+        assert torch.isnan(got[seen]).all() and torch.isfinite(got[~seen]).all()
+        assert torch.allclose(lse, want, rtol=1e-5, atol=1e-5)
