@@ -56,6 +56,34 @@ int ptq_test_gemm_f32_pair(int64_t M0, int64_t N0, int64_t K0, const float* A0, 
                            const float* B1, int64_t ldb1, float* C1, int64_t ldc1, float alpha1, int beta_one1,
                            int tri1, int upper_only1, void* stream);
 
+/* matmul_int8 with the kernel given instead of chosen: shape -1 is the
+ * streaming kernel (nsplit 1), 0 .. 5 are tiles of 256 x 256, 128 x 256,
+ * 128 x 128, 64 x 64, 64 x 32 and 32 x 32 outputs x tokens (in >= 128), with
+ * the depth in nsplit shares (at most 16, and ceil(in / 128)). _plan says what
+ * matmul_int8 chooses. Returns PTQ_OK, PTQ_EINVAL, PTQ_EWORKSPACE or PTQ_EHIP. */
+int ptq_test_matmul_int8_plan(int64_t rows, int64_t out, int64_t in, int* shape, int* nsplit);
+size_t ptq_test_matmul_int8_workspace_bytes(int shape, int nsplit, int64_t rows, int64_t out, int64_t in);
+int ptq_test_matmul_int8(int shape, int nsplit, const int8_t* A, int64_t lda, const float* a_scales, int64_t rows,
+                         const int8_t* codes, int64_t ldb, const float* scales, int64_t out, int64_t in,
+                         const float* bias, int y_dtype, void* Y, int64_t ldy, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* attention_int8_cache with the kernel given instead of chosen: tiles of 256
+ * rows (1; head_dim up to 128) or few rows at a time (0), the waves of the
+ * latter (4, or 8 with nsplit 1 and head_dim up to 128), and the splits of the
+ * keys (1 .. 64). _plan says what attention_int8_cache chooses. Returns PTQ_OK,
+ * PTQ_EINVAL, PTQ_EWORKSPACE or PTQ_EHIP. */
+int ptq_test_attention_int8_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim, int block_size,
+                                 int64_t table_width, int64_t window, int* tiles, int* waves, int* nsplit);
+size_t ptq_test_attention_int8_workspace_bytes(int nsplit, int64_t rows, int heads, int head_dim);
+int ptq_test_attention_int8_cache(int tiles, int waves, int nsplit, const void* Q, int64_t ldq, void* O, int64_t ldo,
+                                  float* lse, int dtype, int64_t rows, int heads, const int32_t* offsets,
+                                  const int32_t* seq_lens, int64_t batch, const int32_t* block_table,
+                                  int64_t table_width, const int8_t* k_codes, const int8_t* v_codes,
+                                  const float* k_scales, const float* v_scales, int64_t num_blocks, int kv_heads,
+                                  int head_dim, int block_size, float scale, int causal, int64_t window,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -91,6 +91,16 @@ def _load() -> ctypes.CDLL:
         "attention_int8_cache_workspace_bytes": (sz, [i64, i64, i32, i32, i32, i32, i64]),
         "attention_int8_cache": (i32, [vp, i64, vp, i64, vp, i32, i64, i32, vp, vp, i64, vp, i64, vp, vp, vp, vp,
                                        i64, i32, i32, i32, ctypes.c_float, i32, i64, vp, sz, vp]),
+        "ptq_test_matmul_int8_plan": (i32, [i64, i64, i64, ctypes.POINTER(i32), ctypes.POINTER(i32)]),
+        "ptq_test_matmul_int8_workspace_bytes": (sz, [i32, i32, i64, i64, i64]),
+        "ptq_test_matmul_int8": (i32, [i32, i32, vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, i32, vp, i64, vp, sz,
+                                       vp]),
+        "ptq_test_attention_int8_plan": (i32, [i64, i64, i32, i32, i32, i32, i64, i64, ctypes.POINTER(i32),
+                                               ctypes.POINTER(i32), ctypes.POINTER(i32)]),
+        "ptq_test_attention_int8_workspace_bytes": (sz, [i32, i64, i32, i32]),
+        "ptq_test_attention_int8_cache": (i32, [i32, i32, i32, vp, i64, vp, i64, vp, i32, i64, i32, vp, vp, i64, vp,
+                                                i64, vp, vp, vp, vp, i64, i32, i32, i32, ctypes.c_float, i32, i64,
+                                                vp, sz, vp]),
         "layer_output_error": (i32, [vp, i32, i64, i64, vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, i32, dp, vp, sz,
                                      vp]),
     }
@@ -599,3 +609,49 @@ def _test_gemm_f32_split3(A, B, C, M, N, K, layout_a, layout_b, alpha=1.0, beta_
                                          _ptr(C), C.stride(0), float(alpha), int(beta_one), int(tri),
                                          int(upper_only), _ptr(ws), wsb, _stream()))
     return C
+
+
+def _test_matmul_int8_plan(rows, out, n):
+    """ptq_test_matmul_int8_plan (include/ptq_testing.h): (shape, nsplit) that matmul_int8 chooses."""
+    shape, nsplit = ctypes.c_int(), ctypes.c_int()
+    _check(_lib.ptq_test_matmul_int8_plan(rows, out, n, ctypes.byref(shape), ctypes.byref(nsplit)))
+    return shape.value, nsplit.value
+
+
+def _test_matmul_int8(shape, nsplit, A, a_scales, codes, scales, bias=None, out_dtype=torch.bfloat16, Y=None):
+    """ptq_test_matmul_int8 (include/ptq_testing.h): matmul_int8 by the kernel that shape and nsplit name."""
+    rows, n = A.shape
+    out = codes.shape[0]
+    Y, ldy = _product_output(Y, rows, out, out_dtype, A.device)
+    ws, wsb = _workspace(int(_lib.ptq_test_matmul_int8_workspace_bytes(shape, nsplit, rows, out, n)), A.device, None)
+    _check(_lib.ptq_test_matmul_int8(shape, nsplit, _ptr(A), _codes(A, "A"),
+                                     _vector(a_scales, rows, torch.float32, "a_scales"), rows, _ptr(codes),
+                                     _codes(codes, "codes"), _vector(scales, out, torch.float32, "scales"), out, n,
+                                     _vector(bias, out, torch.float32, "bias"), _dtype_code(Y), _ptr(Y), ldy, _ptr(ws),
+                                     wsb, _stream()))
+    return Y
+
+
+def _test_attention_int8_plan(rows, batch, heads, kv_heads, head_dim, block_size, table_width, window=0):
+    """ptq_test_attention_int8_plan (include/ptq_testing.h): (tiles, waves, nsplit) that attention_int8_cache chooses."""
+    plan = [ctypes.c_int() for _ in range(3)]
+    _check(_lib.ptq_test_attention_int8_plan(rows, batch, heads, kv_heads, head_dim, block_size, table_width, window,
+                                             *map(ctypes.byref, plan)))
+    return tuple(x.value for x in plan)
+
+
+def _test_attention_int8_cache(tiles, waves, nsplit, Q, cache, offsets, seq_lens, block_table, scale=None, causal=True,
+                               window=0):
+    """ptq_test_attention_int8_cache (include/ptq_testing.h): (O, lse) by the kernel that the first three name."""
+    nb, h, d, bs = cache._sizes()
+    rows, heads = Q.shape[0], Q.shape[1]
+    O = torch.empty(rows, heads, d, dtype=Q.dtype, device=Q.device)
+    lse = torch.empty(rows, heads, dtype=torch.float32, device=Q.device)
+    off, lens, batch, table, width = _ragged(offsets, seq_lens, block_table, "seq_lens")
+    ws, wsb = _workspace(int(_lib.ptq_test_attention_int8_workspace_bytes(nsplit, rows, heads, d)), Q.device, None)
+    _check(_lib.ptq_test_attention_int8_cache(int(tiles), waves, nsplit, _ptr(Q), _heads3(Q, rows, heads, d, "Q"),
+                                              _ptr(O), heads * d, _ptr(lse), _dtype_code(Q), rows, heads, off, lens,
+                                              batch, table, width, _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scales),
+                                              _ptr(cache.v_scales), nb, h, d, bs, float(scale or d ** -0.5),
+                                              int(bool(causal)), window, _ptr(ws), wsb, _stream()))
+    return O, lse

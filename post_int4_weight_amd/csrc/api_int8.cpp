@@ -1,9 +1,11 @@
 // C ABI of the int8 serving operators (declared in include/ptq.h): argument
 // checks, before any HIP call, and the calls into linear_int8.hip,
 // kv_cache.hip and attention_int8.hip.
+#include <algorithm>
 #include <cmath>
 
 #include "common.hpp"
+#include "ptq_testing.h"
 
 namespace ptq {
 namespace {
@@ -99,6 +101,57 @@ int check_ragged(const char* fn, const RaggedRows& r, const char* starts, int he
     return PTQ_OK;
 }
 
+// matmul_int8 with the plan given, or chosen
+int matmul(const char* fn, const Int8Plan* given, const int8_t* A, int64_t lda, const float* a_scales, int64_t rows,
+           const int8_t* codes, int64_t ldb, const float* scales, int64_t out, int64_t in, const float* bias,
+           int y_dtype, void* Y, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+    PTQ_TRY(check_sizes(fn, rows, in));
+    PTQ_TRY(check_out(fn, rows, out));
+    if (rows == 0 || out == 0) return PTQ_OK;
+    PTQ_TRY(check_codes(fn, "A", A, in, lda));
+    if (!a_scales) REFUSE("%s: a_scales is NULL", fn);
+    PTQ_TRY(check_product(fn, codes, ldb, scales, out, in, y_dtype, Y, ldy));
+    const Int8Plan p = given ? *given : matmul_int8_plan(rows, out, in);
+    const size_t need = matmul_int8_ws_bytes(p, rows, out, in);
+    if (need && (!workspace || workspace_bytes < need)) {
+        set_error("%s: workspace %zu bytes, need %zu", fn, workspace ? workspace_bytes : (size_t)0, need);
+        return PTQ_EWORKSPACE;
+    }
+    return run_matmul_int8(p, A, lda, a_scales, rows, codes, ldb, scales, out, in, bias, y_dtype, Y, ldy, workspace,
+                           workspace_bytes, (hipStream_t)stream);
+}
+
+// attention_int8_cache with the plan given, or chosen
+int attention(const char* fn, const AttnPlan* given, const KVCacheInt8& c, const RaggedRows& r, int dtype,
+              const void* Q, int64_t ldq, int heads, float scale, int causal, int64_t window, void* O, int64_t ldo,
+              float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    PTQ_TRY(check_cache(fn, c));
+    if (heads < 1 || heads > 65535 || heads % c.heads)
+        REFUSE("%s: heads = %d must be a multiple of kv_heads = %d, at most 65535", fn, heads, c.heads);
+    PTQ_TRY(check_ragged(fn, r, "seq_lens", heads));
+    if (!std::isfinite(scale)) REFUSE("%s: scale is not finite", fn);
+    if (causal != 0 && causal != 1) REFUSE("%s: causal = %d is neither 0 nor 1", fn, causal);
+    if (window < 0) REFUSE("%s: window = %lld < 0", fn, (long long)window);
+    if (window > 0 && !causal) REFUSE("%s: a window needs causal = 1", fn);
+    if (r.rows == 0 || r.batch == 0) return PTQ_OK;
+    PTQ_TRY(check_cache_pointers(fn, c));
+    if (c.num_blocks < 1) REFUSE("%s: num_blocks = 0", fn);
+    const int64_t n = (int64_t)heads * c.dim;
+    PTQ_TRY(check_float_rows(fn, "Q", Q, dtype, n, ldq));
+    PTQ_TRY(check_float_rows(fn, "O", O, dtype, n, ldo));
+    const AttnPlan p =
+        given ? *given : attention_int8_plan(r.rows, r.batch, heads, c.heads, c.dim, c.block, r.width, window);
+    const size_t need = given ? attention_int8_part_bytes(p.nsplit, r.rows, heads, c.dim)
+                              : attention_int8_ws_bytes(r.rows, r.batch, heads, c.heads, c.dim, c.block, r.width);
+    if (need && (!workspace || workspace_bytes < need)) {
+        set_error("%s: workspace %zu bytes, need %zu", fn, workspace ? workspace_bytes : (size_t)0, need);
+        return PTQ_EWORKSPACE;
+    }
+    if (need && !aligned16(workspace)) REFUSE("%s: workspace is not 16-byte aligned", fn);
+    return run_attention_int8(p, c, r, dtype, Q, ldq, heads, scale, causal, window, O, ldo, lse, workspace,
+                              workspace_bytes, (hipStream_t)stream);
+}
+
 }  // namespace
 }  // namespace ptq
 
@@ -119,26 +172,43 @@ int quantize_tokens_int8(const void* X, int x_dtype, int64_t rows, int64_t in, i
 }
 
 size_t matmul_int8_workspace_bytes(int64_t rows, int64_t out, int64_t in) {
-    return rows > 0 && out > 0 && in > 0 ? matmul_int8_ws_bytes(rows, out, in) : 0;
+    return rows > 0 && out > 0 && in > 0 ? matmul_int8_ws_bytes(matmul_int8_plan(rows, out, in), rows, out, in) : 0;
 }
 
 int matmul_int8(const int8_t* A, int64_t lda, const float* a_scales, int64_t rows, const int8_t* codes, int64_t ldb,
                 const float* scales, int64_t out, int64_t in, const float* bias, int y_dtype, void* Y, int64_t ldy,
                 void* workspace, size_t workspace_bytes, void* stream) {
-    const char* fn = "matmul_int8";
-    PTQ_TRY(check_sizes(fn, rows, in));
-    PTQ_TRY(check_out(fn, rows, out));
-    if (rows == 0 || out == 0) return PTQ_OK;
-    PTQ_TRY(check_codes(fn, "A", A, in, lda));
-    if (!a_scales) REFUSE("%s: a_scales is NULL", fn);
-    PTQ_TRY(check_product(fn, codes, ldb, scales, out, in, y_dtype, Y, ldy));
-    const size_t need = matmul_int8_ws_bytes(rows, out, in);
-    if (need && (!workspace || workspace_bytes < need)) {
-        set_error("%s: workspace %zu bytes, need %zu", fn, workspace ? workspace_bytes : (size_t)0, need);
-        return PTQ_EWORKSPACE;
-    }
-    return run_matmul_int8(A, lda, a_scales, rows, codes, ldb, scales, out, in, bias, y_dtype, Y, ldy, workspace,
-                           workspace_bytes, (hipStream_t)stream);
+    return matmul("matmul_int8", nullptr, A, lda, a_scales, rows, codes, ldb, scales, out, in, bias, y_dtype, Y, ldy,
+                  workspace, workspace_bytes, stream);
+}
+
+int ptq_test_matmul_int8_plan(int64_t rows, int64_t out, int64_t in, int* shape, int* nsplit) {
+    if (rows < 1 || out < 1 || in < 8 || in % 8 || in > MAX_IN || !shape || !nsplit)
+        REFUSE("ptq_test_matmul_int8_plan: bad arguments");
+    const Int8Plan p = matmul_int8_plan(rows, out, in);
+    *shape = p.few ? -1 : p.shape;
+    *nsplit = p.nsplit;
+    return PTQ_OK;
+}
+
+size_t ptq_test_matmul_int8_workspace_bytes(int shape, int nsplit, int64_t rows, int64_t out, int64_t in) {
+    return rows > 0 && out > 0 && in > 0 && shape < INT8_SHAPES
+               ? matmul_int8_ws_bytes(Int8Plan{shape < 0, std::max(shape, 0), nsplit}, rows, out, in)
+               : 0;
+}
+
+int ptq_test_matmul_int8(int shape, int nsplit, const int8_t* A, int64_t lda, const float* a_scales, int64_t rows,
+                         const int8_t* codes, int64_t ldb, const float* scales, int64_t out, int64_t in,
+                         const float* bias, int y_dtype, void* Y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+    const char* fn = "ptq_test_matmul_int8";
+    // a tile holds whole stages of 128, and a share of the depth one at least
+    if (shape < -1 || shape >= INT8_SHAPES || nsplit < 1 || nsplit > 16 ||
+        (shape < 0 ? nsplit > 1 : in < 128 || nsplit > cdiv(in, 128)))
+        REFUSE("%s: shape = %d, nsplit = %d", fn, shape, nsplit);
+    const Int8Plan p{shape < 0, std::max(shape, 0), nsplit};
+    return matmul(fn, &p, A, lda, a_scales, rows, codes, ldb, scales, out, in, bias, y_dtype, Y, ldy, workspace,
+                  workspace_bytes, stream);
 }
 
 size_t linear_int8_workspace_bytes(int64_t rows, int64_t out, int64_t in) {
@@ -215,32 +285,49 @@ int attention_int8_cache(const void* Q, int64_t ldq, void* O, int64_t ldo, float
                          const float* k_scales, const float* v_scales, int64_t num_blocks, int kv_heads, int head_dim,
                          int block_size, float scale, int causal, int64_t window, void* workspace,
                          size_t workspace_bytes, void* stream) {
-    const char* fn = "attention_int8_cache";
     const KVCacheInt8 c{const_cast<int8_t*>(k_codes), const_cast<int8_t*>(v_codes), const_cast<float*>(k_scales),
                         const_cast<float*>(v_scales), num_blocks, kv_heads, head_dim, block_size};
     const RaggedRows r{rows, batch, offsets, seq_lens, block_table, table_width};
-    PTQ_TRY(check_cache(fn, c));
-    if (heads < 1 || heads > 65535 || heads % kv_heads)
-        REFUSE("%s: heads = %d must be a multiple of kv_heads = %d, at most 65535", fn, heads, kv_heads);
-    PTQ_TRY(check_ragged(fn, r, "seq_lens", heads));
-    if (!std::isfinite(scale)) REFUSE("%s: scale is not finite", fn);
-    if (causal != 0 && causal != 1) REFUSE("%s: causal = %d is neither 0 nor 1", fn, causal);
-    if (window < 0) REFUSE("%s: window = %lld < 0", fn, (long long)window);
-    if (window > 0 && !causal) REFUSE("%s: a window needs causal = 1", fn);
-    if (rows == 0 || batch == 0) return PTQ_OK;
-    PTQ_TRY(check_cache_pointers(fn, c));
-    if (num_blocks < 1) REFUSE("%s: num_blocks = 0", fn);
-    const int64_t n = (int64_t)heads * head_dim;
-    PTQ_TRY(check_float_rows(fn, "Q", Q, dtype, n, ldq));
-    PTQ_TRY(check_float_rows(fn, "O", O, dtype, n, ldo));
-    const size_t need = attention_int8_ws_bytes(rows, batch, heads, kv_heads, head_dim, block_size, table_width);
-    if (need && (!workspace || workspace_bytes < need)) {
-        set_error("%s: workspace %zu bytes, need %zu", fn, workspace ? workspace_bytes : (size_t)0, need);
-        return PTQ_EWORKSPACE;
-    }
-    if (need && !aligned16(workspace)) REFUSE("%s: workspace is not 16-byte aligned", fn);
-    return run_attention_int8(c, r, dtype, Q, ldq, heads, scale, causal, window, O, ldo, lse, workspace,
-                              workspace_bytes, (hipStream_t)stream);
+    return attention("attention_int8_cache", nullptr, c, r, dtype, Q, ldq, heads, scale, causal, window, O, ldo, lse,
+                     workspace, workspace_bytes, stream);
+}
+
+int ptq_test_attention_int8_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim, int block_size,
+                                 int64_t table_width, int64_t window, int* tiles, int* waves, int* nsplit) {
+    const char* fn = "ptq_test_attention_int8_plan";
+    PTQ_TRY(check_cache(fn, KVCacheInt8{nullptr, nullptr, nullptr, nullptr, 0, kv_heads, head_dim, block_size}));
+    if (rows < 1 || batch < 1 || heads < kv_heads || heads % kv_heads || table_width < 0 || window < 0 || !tiles ||
+        !waves || !nsplit)
+        REFUSE("%s: bad arguments", fn);
+    const AttnPlan p = attention_int8_plan(rows, batch, heads, kv_heads, head_dim, block_size, table_width, window);
+    *tiles = p.tr == ATTN_TILE;
+    *waves = p.nw;
+    *nsplit = p.nsplit;
+    return PTQ_OK;
+}
+
+size_t ptq_test_attention_int8_workspace_bytes(int nsplit, int64_t rows, int heads, int head_dim) {
+    return nsplit > 0 && rows > 0 && heads > 0 && head_dim > 0 ? attention_int8_part_bytes(nsplit, rows, heads, head_dim)
+                                                               : 0;
+}
+
+int ptq_test_attention_int8_cache(int tiles, int waves, int nsplit, const void* Q, int64_t ldq, void* O, int64_t ldo,
+                                  float* lse, int dtype, int64_t rows, int heads, const int32_t* offsets,
+                                  const int32_t* seq_lens, int64_t batch, const int32_t* block_table,
+                                  int64_t table_width, const int8_t* k_codes, const int8_t* v_codes,
+                                  const float* k_scales, const float* v_scales, int64_t num_blocks, int kv_heads,
+                                  int head_dim, int block_size, float scale, int causal, int64_t window,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "ptq_test_attention_int8_cache";
+    if ((tiles != 0 && tiles != 1) || (tiles && head_dim > 128) || nsplit < 1 || nsplit > 64 ||
+        (waves != 4 && (waves != 8 || tiles || nsplit > 1 || head_dim > 128)) || rows > 1 << 16 || batch > 1 << 10)
+        REFUSE("%s: tiles = %d, waves = %d, nsplit = %d", fn, tiles, waves, nsplit);
+    const KVCacheInt8 c{const_cast<int8_t*>(k_codes), const_cast<int8_t*>(v_codes), const_cast<float*>(k_scales),
+                        const_cast<float*>(v_scales), num_blocks, kv_heads, head_dim, block_size};
+    const RaggedRows r{rows, batch, offsets, seq_lens, block_table, table_width};
+    const AttnPlan p{tiles ? ATTN_TILE : ATTN_ROWS, waves, nsplit};
+    return attention(fn, &p, c, r, dtype, Q, ldq, heads, scale, causal, window, O, ldo, lse, workspace,
+                     workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -23,7 +23,7 @@ namespace {
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int TR = 16;       // query rows (tokens x grouped heads) of a tile
+constexpr int TR = ATTN_ROWS;     // query rows (tokens x grouped heads) of a tile
 constexpr int TK = 64;       // tokens per step of a wave
 constexpr float PSHIFT = 8.f;   // p up to 2^8: fp16 keeps 11 bits down to 2^-22 of the largest
 // The reference m of a row follows its maximum only when that exceeds it by
@@ -964,19 +964,15 @@ int64_t tile_units(int64_t rows, int64_t batch, int group, int tr) { return rows
 // Waves of a tile: two per SIMD. At 256 channels the output and query
 // fragments of 32 rows leave no registers for the rest: those go through
 // attention_rows_kernel whatever the number of rows.
-constexpr int TILE_WAVES = 8;
+constexpr int TILE_WAVES = ATTN_TILE / 32;
 
-// Which kernel, and how many splits of the keys. Lengths are not known here:
-// keys is the most there may be, and every sequence but one is taken to end half
-// way through a tile.
-struct Plan {
-    int tr;        // rows of a tile: TR, or 32 TILE_WAVES
-    int nw;        // waves of attention_rows_kernel
-    int nsplit;
-};
+// The choice of an AttnPlan. Lengths are not known here: keys is the most there
+// may be, and every sequence but one is taken to end half way through a tile.
 int64_t likely_tiles(int64_t rows, int64_t batch, int group, int tr) {
     return std::max<int64_t>({1, batch, cdiv(rows * group, tr) + (batch - 1) / 2});
 }
+// As long as the longest sequence there can be: none (and positions less a window stay far from 2^63).
+int64_t bounded_window(int64_t window, int block, int64_t width) { return window >= width * block ? 0 : window; }
 int64_t most_keys(int64_t rows, int64_t batch, int block, int64_t width, int64_t window) {
     const int64_t keys = width * block;
     return window > 0 ? std::min(keys, window + cdiv(rows, std::max<int64_t>(batch, 1))) : keys;
@@ -992,9 +988,9 @@ int64_t most_keys(int64_t rows, int64_t batch, int block, int64_t width, int64_t
 // Up to 2048 keys eight waves share a tile instead, and there is no join: 1000
 // keys 14.3 us, split 19; 16 sequences of 2000 keys 20.9 and 25.3. At 4000 keys
 // of one sequence it is 29 against 19.
-Plan plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int64_t keys, bool tiles) {
-    Plan p;
-    p.tr = tiles ? 32 * TILE_WAVES : TR;
+AttnPlan plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int64_t keys, bool tiles) {
+    AttnPlan p;
+    p.tr = tiles ? ATTN_TILE : TR;
     const int64_t units = likely_tiles(rows, batch, heads / kv_heads, p.tr) * kv_heads;
     const int64_t want = tiles ? 256 / units : std::max(512 / units, std::min(1536 / units, cdiv(keys, 32 * TK)));
     const int64_t most = std::min<int64_t>(cdiv(keys, 8 * TK), 64);
@@ -1016,12 +1012,12 @@ bool use_tiles(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, in
     const int group = heads / kv_heads;
     const double steps = (double)keys / TK * kv_heads * dim / 128;
     const double few = 18 + 1.85 / 1024 * steps * likely_tiles(rows, batch, group, TR);
-    const double many = 38 + 2.1 / 256 * steps * likely_tiles(rows, batch, group, 32 * TILE_WAVES);
+    const double many = 38 + 2.1 / 256 * steps * likely_tiles(rows, batch, group, ATTN_TILE);
     return many < few;
 }
 
 template <typename T, int D>
-int launch(const AttnArgs& a, const Plan& p, hipStream_t st) {
+int launch(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
     const int tr = p.tr;
     const int64_t units = tile_units(a.g.rows, a.g.batch, a.group, tr) * a.kv_heads;
     const dim3 grid((unsigned)(units * a.nsplit));
@@ -1052,7 +1048,7 @@ int launch(const AttnArgs& a, const Plan& p, hipStream_t st) {
 }
 
 template <typename T>
-int launch_dim(const AttnArgs& a, const Plan& p, hipStream_t st) {
+int launch_dim(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
     switch (a.dim) {
         case 64: return launch<T, 64>(a, p, st);
         case 128: return launch<T, 128>(a, p, st);
@@ -1069,19 +1065,28 @@ size_t attention_int8_ws_bytes(int64_t rows, int64_t batch, int heads, int kv_he
     int n = plan(rows, batch, heads, kv_heads, dim, keys, false).nsplit;
     if (use_tiles(rows, batch, heads, kv_heads, dim, keys))
         n = std::max(n, plan(rows, batch, heads, kv_heads, dim, keys, true).nsplit);
-    if (n == 1) return 0;
+    return attention_int8_part_bytes(n, rows, heads, dim);
+}
+
+size_t attention_int8_part_bytes(int nsplit, int64_t rows, int heads, int dim) {
+    if (nsplit == 1) return 0;
     Sizer z;
-    z.take<float>((size_t)n * rows * heads * dim);
-    z.take<float>((size_t)n * rows * heads);
+    z.take<float>((size_t)nsplit * rows * heads * dim);
+    z.take<float>((size_t)nsplit * rows * heads);
     return z.bytes();
 }
 
-int run_attention_int8(const KVCacheInt8& c, const RaggedRows& r, int dtype, const void* Q, int64_t ldq, int heads,
-                       float scale, int causal, int64_t window, void* O, int64_t ldo, float* lse, void* ws,
-                       size_t ws_bytes, hipStream_t st) {
+AttnPlan attention_int8_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int block, int64_t width,
+                             int64_t window) {
+    const int64_t keys = most_keys(rows, batch, block, width, bounded_window(window, block, width));
+    return plan(rows, batch, heads, kv_heads, dim, keys, use_tiles(rows, batch, heads, kv_heads, dim, keys));
+}
+
+int run_attention_int8(const AttnPlan& p, const KVCacheInt8& c, const RaggedRows& r, int dtype, const void* Q,
+                       int64_t ldq, int heads, float scale, int causal, int64_t window, void* O, int64_t ldo,
+                       float* lse, void* ws, size_t ws_bytes, hipStream_t st) {
     if (r.rows == 0 || r.batch == 0) return PTQ_OK;
-    // as long as the longest sequence there can be: none (and positions less a window stay far from 2^63)
-    if (window >= r.width * c.block) window = 0;
+    window = bounded_window(window, c.block, r.width);
     AttnArgs a{};
     a.g.offsets = r.offsets; a.g.starts = r.starts; a.g.batch = (int)r.batch; a.g.rows = r.rows;
     a.table = r.table; a.width = r.width;
@@ -1091,9 +1096,6 @@ int run_attention_int8(const KVCacheInt8& c, const RaggedRows& r, int dtype, con
     a.Q = Q; a.ldq = ldq; a.O = O; a.ldo = ldo; a.lse = lse;
     a.scale2 = (float)(scale * 1.4426950408889634);
     a.causal = causal; a.window = window;
-    const int64_t keys = most_keys(r.rows, r.batch, c.block, r.width, window);
-    const Plan p = plan(r.rows, r.batch, heads, c.heads, c.dim, keys,
-                        use_tiles(r.rows, r.batch, heads, c.heads, c.dim, keys));
     a.nsplit = p.nsplit;
     if (a.nsplit > 1) {
         Arena ar(ws, ws_bytes);

@@ -211,10 +211,18 @@ int run_awq(const void* W, int w_dtype, int64_t out, int64_t n, int64_t ldw, con
 // Int8 linear layers (linear_int8.hip)
 int launch_quantize_tokens_int8(const void* X, int x_dtype, int64_t rows, int64_t in, int64_t ldx, const float* s,
                                 int8_t* codes, int64_t ldc, float* scales, hipStream_t st);
-size_t matmul_int8_ws_bytes(int64_t rows, int64_t out, int64_t in);
-int run_matmul_int8(const int8_t* A, int64_t lda, const float* a_scales, int64_t rows, const int8_t* B, int64_t ldb,
-                    const float* b_scales, int64_t out, int64_t in, const float* bias, int y_dtype, void* Y,
-                    int64_t ldy, void* ws, size_t ws_bytes, hipStream_t st);
+// How a product runs: few = the streaming kernel, else tiles of shape `shape`
+// (0 .. INT8_SHAPES - 1) with the depth in nsplit shares.
+struct Int8Plan {
+    bool few;
+    int shape, nsplit;
+};
+constexpr int INT8_SHAPES = 6;
+Int8Plan matmul_int8_plan(int64_t rows, int64_t out, int64_t in);
+size_t matmul_int8_ws_bytes(const Int8Plan& p, int64_t rows, int64_t out, int64_t in);
+int run_matmul_int8(const Int8Plan& p, const int8_t* A, int64_t lda, const float* a_scales, int64_t rows,
+                    const int8_t* B, int64_t ldb, const float* b_scales, int64_t out, int64_t in, const float* bias,
+                    int y_dtype, void* Y, int64_t ldy, void* ws, size_t ws_bytes, hipStream_t st);
 size_t linear_int8_ws_bytes(int64_t rows, int64_t out, int64_t in);
 int run_linear_int8(const void* X, int x_dtype, int64_t rows, int64_t ldx, const float* s, const int8_t* codes,
                     int64_t ldb, const float* scales, int64_t out, int64_t in, const float* bias, int y_dtype, void* Y,
@@ -237,10 +245,21 @@ int launch_kv_write(const KVCacheInt8& c, const RaggedRows& r, int dtype, const 
                     int64_t ldv, hipStream_t st);
 int launch_kv_read(const KVCacheInt8& c, const RaggedRows& r, int dtype, void* K, int64_t ldk, void* V, int64_t ldv,
                    hipStream_t st);
+// Which kernel, and how many splits of the keys.
+struct AttnPlan {
+    int tr;        // query rows of a tile: ATTN_ROWS (attention_rows_kernel), or ATTN_TILE (attention_tile_kernel)
+    int nw;        // waves of attention_rows_kernel: 4, or 8 up to 128 channels without splits
+    int nsplit;
+};
+constexpr int ATTN_ROWS = 16, ATTN_TILE = 256;
+AttnPlan attention_int8_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int block, int64_t width,
+                             int64_t window);
+// of a plan with nsplit splits, and the most that any window needs
+size_t attention_int8_part_bytes(int nsplit, int64_t rows, int heads, int dim);
 size_t attention_int8_ws_bytes(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int block,
                                int64_t width);
-int run_attention_int8(const KVCacheInt8& c, const RaggedRows& r, int dtype, const void* Q, int64_t ldq, int heads,
-                       float scale, int causal, int64_t window, void* O, int64_t ldo, float* lse, void* ws,
-                       size_t ws_bytes, hipStream_t st);
+int run_attention_int8(const AttnPlan& p, const KVCacheInt8& c, const RaggedRows& r, int dtype, const void* Q,
+                       int64_t ldq, int heads, float scale, int causal, int64_t window, void* O, int64_t ldo,
+                       float* lse, void* ws, size_t ws_bytes, hipStream_t st);
 
 }  // namespace ptq

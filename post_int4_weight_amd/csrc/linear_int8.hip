@@ -606,12 +606,6 @@ int launch_quantize(const void* X, int x_dtype, int64_t rows, int64_t in, int64_
     return PTQ_OK;
 }
 
-// How a product runs: few = the streaming kernel, else tiles of shape `shape`
-// with the depth in nsplit shares.
-struct Plan {
-    bool few;
-    int shape, nsplit;
-};
 // Tile shapes; us: time of a stage of one workgroup per CU. Rings are as deep
 // as LDS allows without losing a second workgroup to it (small tiles wait for
 // their copies, so 5 stages against 3 at 64 x 64: 4096 x 4096 weights, 200
@@ -622,49 +616,19 @@ struct Shape {
 };
 constexpr Shape SHAPES[] = {{256, 256, 2.55f}, {128, 256, 1.47f}, {128, 128, 1.38f},
                             {64, 64, 0.449f},  {64, 32, 0.336f},  {32, 32, 0.193f}};
-
-// The streaming kernel serves up to 16 tokens on weights of up to 2^25 codes
-// (4096 x 4096, 1 token: 6.2 us against 6.9 for 32 x 32 tiles; 8192 x 8192, 8
-// tokens: 16.0 against 14.6) and depths below one stage. Otherwise the shape
-// and the split with the least estimate: workgroups per CU times the stages of
-// one, at least the weights at 3.88 TB/s, and for splits 5 us and the partial
-// sums written and read at 2.04 TB/s. The constants are fitted to 4107 timings
-// of 170 products, 1 to 4096 tokens, 255 x 2056 to 28672 x 8192 weights; the
-// choice is 0.8% slower than the best of each in the mean, 14% at worst (512
-// tokens, 5003 x 4104: 34.4 against 30.3 us).
-Plan plan(int64_t rows, int64_t out, int64_t in) {
-    Plan p{in < KT || (rows <= 16 && out * in <= ((int64_t)1 << 25)), 0, 1};
-    if (p.few) return p;
-    const int64_t stages = cdiv(in, KT);
-    double least = 1e300;
-    for (int k = 0; k < (int)(sizeof(SHAPES) / sizeof(SHAPES[0])); ++k) {
-        const Shape& h = SHAPES[k];
-        const int64_t tiles = cdiv(out, h.to) * cdiv(rows, h.tt);
-        for (int ns : {1, 2, 3, 4, 6, 8, 12, 16}) {
-            if (ns > 1 && (stages < 4 * ns || tiles * ns > 2048)) break;
-            double us = std::max((double)cdiv(tiles * ns, 256) * cdiv(stages, ns) * h.us, out * in / 3.88e6);
-            if (ns > 1) us += 5.0 + (double)tiles * ns * h.to * h.tt * 8 / 2.04e6;
-            if (us < least) {
-                least = us;
-                p.shape = k;
-                p.nsplit = ns;
-            }
-        }
-    }
-    return p;
-}
+static_assert(sizeof(SHAPES) / sizeof(SHAPES[0]) == INT8_SHAPES, "a launch for each shape");
 
 // Row stride of the tokens' codes in stages.
 int64_t tile_ldc(int64_t in) { return cdiv(in, KT) * KT; }
 
-size_t part_elems(const Plan& p, int64_t rows, int64_t out) {
+size_t part_elems(const Int8Plan& p, int64_t rows, int64_t out) {
     if (p.few || p.nsplit == 1) return 0;
     const Shape s = SHAPES[p.shape];
     return (size_t)p.nsplit * cdiv(out, s.to) * cdiv(rows, s.tt) * s.to * s.tt;
 }
 
 // C: the tokens' codes as the plan wants them (in stages for tiles)
-int run_product(const Plan& p, const int8_t* C, int64_t ldc, const float* sx, int64_t rows, const int8_t* B, int64_t ldb,
+int run_product(const Int8Plan& p, const int8_t* C, int64_t ldc, const float* sx, int64_t rows, const int8_t* B, int64_t ldb,
                 const float* sw, int64_t out, int64_t in, const float* bias, int y_dtype, void* Y, int64_t ldy, int* part,
                 hipStream_t st) {
     Int8GemmArgs g{};
@@ -692,23 +656,52 @@ int run_product(const Plan& p, const int8_t* C, int64_t ldc, const float* sx, in
 
 }  // namespace
 
+// The streaming kernel serves up to 16 tokens on weights of up to 2^25 codes
+// (4096 x 4096, 1 token: 6.2 us against 6.9 for 32 x 32 tiles; 8192 x 8192, 8
+// tokens: 16.0 against 14.6) and depths below one stage. Otherwise the shape
+// and the split with the least estimate: workgroups per CU times the stages of
+// one, at least the weights at 3.88 TB/s, and for splits 5 us and the partial
+// sums written and read at 2.04 TB/s. The constants are fitted to 4107 timings
+// of 170 products, 1 to 4096 tokens, 255 x 2056 to 28672 x 8192 weights; the
+// choice is 0.8% slower than the best of each in the mean, 14% at worst (512
+// tokens, 5003 x 4104: 34.4 against 30.3 us).
+Int8Plan matmul_int8_plan(int64_t rows, int64_t out, int64_t in) {
+    Int8Plan p{in < KT || (rows <= 16 && out * in <= ((int64_t)1 << 25)), 0, 1};
+    if (p.few) return p;
+    const int64_t stages = cdiv(in, KT);
+    double least = 1e300;
+    for (int k = 0; k < INT8_SHAPES; ++k) {
+        const Shape& h = SHAPES[k];
+        const int64_t tiles = cdiv(out, h.to) * cdiv(rows, h.tt);
+        for (int ns : {1, 2, 3, 4, 6, 8, 12, 16}) {
+            if (ns > 1 && (stages < 4 * ns || tiles * ns > 2048)) break;
+            double us = std::max((double)cdiv(tiles * ns, 256) * cdiv(stages, ns) * h.us, out * in / 3.88e6);
+            if (ns > 1) us += 5.0 + (double)tiles * ns * h.to * h.tt * 8 / 2.04e6;
+            if (us < least) {
+                least = us;
+                p.shape = k;
+                p.nsplit = ns;
+            }
+        }
+    }
+    return p;
+}
+
 int launch_quantize_tokens_int8(const void* X, int x_dtype, int64_t rows, int64_t in, int64_t ldx, const float* s,
                                 int8_t* codes, int64_t ldc, float* scales, hipStream_t st) {
     return launch_quantize(X, x_dtype, rows, in, ldx, s, codes, ldc, 0, scales, st);
 }
 
-size_t matmul_int8_ws_bytes(int64_t rows, int64_t out, int64_t in) {
-    const Plan p = plan(rows, out, in);
+size_t matmul_int8_ws_bytes(const Int8Plan& p, int64_t rows, int64_t out, int64_t in) {
     Sizer z;
     z.take<int>(part_elems(p, rows, out));
     if (!p.few && in % KT) z.take<int8_t>((size_t)(rows * tile_ldc(in)));
     return z.bytes();
 }
 
-int run_matmul_int8(const int8_t* A, int64_t lda, const float* a_scales, int64_t rows, const int8_t* B, int64_t ldb,
-                    const float* b_scales, int64_t out, int64_t in, const float* bias, int y_dtype, void* Y,
-                    int64_t ldy, void* ws, size_t ws_bytes, hipStream_t st) {
-    const Plan p = plan(rows, out, in);
+int run_matmul_int8(const Int8Plan& p, const int8_t* A, int64_t lda, const float* a_scales, int64_t rows,
+                    const int8_t* B, int64_t ldb, const float* b_scales, int64_t out, int64_t in, const float* bias,
+                    int y_dtype, void* Y, int64_t ldy, void* ws, size_t ws_bytes, hipStream_t st) {
     Arena a(ws, ws_bytes);
     int* part = a.take<int>(part_elems(p, rows, out));
     if (!p.few && in % KT) {
@@ -727,14 +720,14 @@ size_t linear_int8_ws_bytes(int64_t rows, int64_t out, int64_t in) {
     Sizer z;
     z.take<int8_t>((size_t)(rows * tile_ldc(in)));
     z.take<float>((size_t)rows);
-    z.take<int>(part_elems(plan(rows, out, in), rows, out));
+    z.take<int>(part_elems(matmul_int8_plan(rows, out, in), rows, out));
     return z.bytes();
 }
 
 int run_linear_int8(const void* X, int x_dtype, int64_t rows, int64_t ldx, const float* s, const int8_t* codes,
                     int64_t ldb, const float* scales, int64_t out, int64_t in, const float* bias, int y_dtype, void* Y,
                     int64_t ldy, void* ws, size_t ws_bytes, hipStream_t st) {
-    const Plan p = plan(rows, out, in);
+    const Int8Plan p = matmul_int8_plan(rows, out, in);
     Arena a(ws, ws_bytes);
     const int64_t ldc = tile_ldc(in);
     int8_t* c = a.take<int8_t>((size_t)(rows * ldc));
