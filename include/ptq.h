@@ -421,10 +421,11 @@ int kv_cache_read_int8(const int8_t* k_codes, const int8_t* v_codes, const float
  *
  * The codes enter the products exactly; sums, maxima and the output
  * accumulate in fp32. Probabilities are held in 11 significant bits for bf16
- * queries, 22 for fp32 queries, times S_v over the largest S_v that the 16 or
- * 32 rows computed together have met: a value whose block's S_v is below 2^-20
- * of that one's loses them. S_v that is not finite makes O NaN, lse depends on
- * S_k alone. Asynchronous.
+ * queries, 22 for fp32 queries, times S_v over the largest S_v of the blocks
+ * that the row attends to: a value whose block's S_v is below 2^-20 of that
+ * one's loses them. Blocks that it does not attend to have no part in a row.
+ * Scales are not negative (the cache's writer makes none that are). S_v that is
+ * not finite makes O NaN, lse depends on S_k alone. Asynchronous.
  * Errors: EINVAL, EWORKSPACE, EHIP.
  * ---------------------------------------------------------------------- */
 size_t attention_int8_cache_workspace_bytes(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim,

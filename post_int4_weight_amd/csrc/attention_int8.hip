@@ -9,8 +9,10 @@
 // to [8, 16) (a bf16 q is then exact; an fp32 q is split into two fp16 terms),
 // S_k and the softmax scale multiply the fp32 sums, and S_v multiplies the
 // probabilities: w_j = p_j S_v[block(j)] / R in fp16 (two terms for fp32
-// queries), R a running maximum of S_v over what the wave has read, so w_j <=
-// p_j whatever the scales are. Sums, maxima and the output accumulate in fp32.
+// queries), R the row's running maximum of S_v over the blocks it attends to, so
+// w_j <= p_j whatever the scales are, and a block that a window or the diagonal
+// hides from a row, which may hold anything, has no part in the row's rounding.
+// Sums, maxima and the output accumulate in fp32.
 #include "int8.hpp"
 
 #include <algorithm>
@@ -259,8 +261,8 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
             }
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
-        // R: largest finite S_v so far, the same for every lane
-        float big = c.sv < INFINITY ? c.sv : 0.f;
+        // R: largest finite S_v of the row's blocks so far
+        float big = c.sv < INFINITY && (whole || (r_lo < 16 && r_hi > 0)) ? c.sv : 0.f;
         big = fmaxf(big, __shfl_xor(big, 16, 64));
         big = fmaxf(big, __shfl_xor(big, 32, 64));
         if (__any(top > m + LAZY || big > R)) {
@@ -458,6 +460,7 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
     // of step it, at (it - s0) % 4: S_k of the lane half's group in either block, then log2 S_v of them (NaN: S_v is
     // not finite); the largest finite S_v, negative if one is not finite
     __shared__ __attribute__((aligned(16))) float ssc[4][2][4], sbig[4];
+    __shared__ float ssv[4][2][2];      // S_v of them, 0 if it is not finite
 
     const int split = (int)(blockIdx.x % (unsigned)a.nsplit);
     const int64_t tile = blockIdx.x / (unsigned)a.nsplit;
@@ -555,6 +558,7 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
             to[0] = sk;
             to[2] = bad ? __builtin_nanf("") : __builtin_amdgcn_logf(sv);     // v_log_f32: base 2
             float big = bad ? 0.f : sv;
+            ssv[(it - s0) & 3][lane & 1][lane >> 1] = big;
             big = fmaxf(big, swap_lanes<0xB1>(big));        // quad_perm [1, 0, 3, 2]
             big = fmaxf(big, swap_lanes<0x4E>(big));        // quad_perm [2, 3, 0, 1]
             const bool any_bad = __ballot(bad) != 0;
@@ -609,19 +613,21 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[n][k][e] = (_Float16)0.f;
     };
-    // A row moves to another reference when its largest score mx exceeds limit, all rows when S_v exceeds R; big: of sbig,
-    // as bits, so that a negative one is large, too. What was pending at the old references is in acc already.
-    auto over_R = [&](unsigned big) { return big > __float_as_uint(R); };
-    auto move = [&](float mx, unsigned big_bits) __attribute__((always_inline)) {
-        const float m_new = fmaxf(m, mx), big = fabsf(__uint_as_float(big_bits));
+    // A row moves to another reference when its largest score mx exceeds limit or S_v of a block it attends to exceeds R.
+    // What was pending at the old references is in acc already. Blocks that all rows attend to are compared with all_R, a
+    // scalar that no row's R is below: with R itself the bf16 kernel spills 47 registers. As bits, so that a negative one
+    // of sbig is large, too.
+    unsigned all_R = 0;
+    auto move = [&](float mx, float big) __attribute__((always_inline)) {
+        const float m_new = fmaxf(m, mx);
         float fall = m_new == m ? 1.f : exp2_fast(m - m_new);
         m = m_new;
         ref = (m == -INFINITY ? 0.f : m) - PSHIFT;
         limit = m + LAZY;
         l *= fall;
-        if (big > R) {     // the same for every lane
+        if (big > R) {
             fall *= big < FLT_MIN ? 0.f : __fdiv_rn(R, big);
-            R = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(big)));
+            R = big;
             log2_R = big < FLT_MIN ? 0.f : __builtin_amdgcn_logf(big);
         }
 #pragma unroll
@@ -672,9 +678,9 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
             for (int r = 0; r < 16; r += 2) top_of(s, top, r);
         }
         const float mx = max_halves(top * ck);
-        const unsigned big = bits(big_of(it));
-        if (over_R(big) || __any(mx > limit)) move(mx, big);
         const bool mine = !decltype(masked)::value || (lo < 16 && hi > 0);
+        const float big = max_halves(mine ? ssv[(it - s0) & 3][hf][u] : 0.f);
+        if (__any(mx > limit || big > R)) move(mx, big);
         if (mine && sc[2 + u] != sc[2 + u]) poison = sc[2 + u];
         const float lr = log2_rv(sc[2 + u]), off = ref - lr;
         Probs w;
@@ -695,7 +701,7 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
         h.ck = sk * qs;
         h.mx = max_halves(top * h.ck);
         h.big = big;
-        h.moves = (first && over_R(big)) || __any(h.mx > limit);      // S_v's are the step's
+        h.moves = (first && big > all_R) || __any(h.mx > limit);      // S_v's are the step's
         h.lr = log2_rv(lv);
         h.off = ref - h.lr;
         return h;
@@ -711,7 +717,8 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
         if (h.moves) {
             output(pv, pu, wp);
             forget(wp);
-            move(h.mx, h.big);
+            move(h.mx, fabsf(__uint_as_float(h.big)));
+            all_R = std::max(all_R, h.big & 0x7fffffffu);
             if (u == 0 && sc[2] + sc[3] != sc[2] + sc[3]) poison = __builtin_nanf("");
             h.lr = log2_rv(sc[2 + u]);
             h.off = ref - h.lr;
