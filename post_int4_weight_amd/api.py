@@ -440,7 +440,8 @@ def _product_output(Y, rows, out, dtype, device):
         Y = torch.empty(rows, out, dtype=dtype, device=device)
     elif tuple(Y.shape) != (rows, out):
         raise ValueError("Y must be [rows, out]")
-    return Y, _rowmajor(Y, "Y") if rows > 1 else max(out, 1)
+    ldy = _rowmajor(Y, "Y")
+    return Y, ldy if rows > 1 else max(out, 1)
 
 
 def matmul_int8(A, a_scales, codes, scales, bias=None, out_dtype=torch.bfloat16, Y=None, workspace=None):
