@@ -399,10 +399,16 @@ def layer_output_error(X, W, codes, scales, g_idx=None, zeros=None, s=None, grou
 
 # ---------------------------------------------------------- int8 serving ---
 
+def _on_gpu(t, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU, not on {t.device}")
+
+
 def _vector(t, n: int, dtype, name: str):
     """t as n dense values of dtype (any shape with that many), or None."""
     if t is None:
         return None
+    _on_gpu(t, name)
     if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be {n} contiguous {dtype} values")
     return t.data_ptr()
@@ -411,14 +417,26 @@ def _vector(t, n: int, dtype, name: str):
 def _codes(t: torch.Tensor, name: str):
     if t.dtype != torch.int8:
         raise TypeError(f"{name} must be int8, not {t.dtype}")
-    return _rowmajor(t, name)
+    return _rows(t, name)
+
+
+def _rows(t: torch.Tensor, name: str):
+    ld = _rowmajor(t, name)
+    _on_gpu(t, name)
+    return ld
+
+
+def _scratch(nbytes: int, device, given):
+    if given is not None:
+        _on_gpu(given, "workspace")
+    return _workspace(nbytes, device, given)
 
 
 def quantize_tokens_int8(X: torch.Tensor, s=None, codes=None, scales=None):
     """quantize_tokens_int8 (include/ptq.h): X [rows, in] -> (codes int8 [rows, in], scales fp32 [rows]); s divides
     the columns first."""
     rows, n = X.shape
-    ldx = _rowmajor(X, "X")
+    ldx = _rows(X, "X")
     if codes is None:
         codes = torch.empty(rows, n, dtype=torch.int8, device=X.device)
     if scales is None:
@@ -437,10 +455,10 @@ def matmul_int8_workspace_bytes(rows: int, out: int, n: int) -> int:
 
 def _product_output(Y, rows, out, dtype, device):
     if Y is None:
-        Y = torch.empty(rows, out, dtype=dtype, device=device)
-    elif tuple(Y.shape) != (rows, out):
+        return torch.empty(rows, out, dtype=dtype, device=device), max(out, 1)
+    if tuple(Y.shape) != (rows, out):
         raise ValueError("Y must be [rows, out]")
-    ldy = _rowmajor(Y, "Y")
+    ldy = _rows(Y, "Y")
     return Y, ldy if rows > 1 else max(out, 1)
 
 
@@ -451,7 +469,7 @@ def matmul_int8(A, a_scales, codes, scales, bias=None, out_dtype=torch.bfloat16,
     if codes.shape[1] != n:
         raise ValueError(f"codes has {codes.shape[1]} columns, A has {n}")
     Y, ldy = _product_output(Y, rows, out, out_dtype, A.device)
-    ws, wsb = _workspace(matmul_int8_workspace_bytes(rows, out, n), A.device, workspace)
+    ws, wsb = _scratch(matmul_int8_workspace_bytes(rows, out, n), A.device, workspace)
     _check(_lib.matmul_int8(_ptr(A), _codes(A, "A"), _vector(a_scales, rows, torch.float32, "a_scales"), rows,
                             _ptr(codes), _codes(codes, "codes"), _vector(scales, out, torch.float32, "scales"), out, n,
                             _vector(bias, out, torch.float32, "bias"), _dtype_code(Y), _ptr(Y), ldy, _ptr(ws), wsb,
@@ -472,8 +490,8 @@ def linear_int8(X, codes, scales, bias=None, s=None, out_dtype=None, Y=None, wor
     if codes.shape[1] != n:
         raise ValueError(f"codes has {codes.shape[1]} columns, X has {n}")
     Y, ldy = _product_output(Y, rows, out, out_dtype or X.dtype, X.device)
-    ws, wsb = _workspace(linear_int8_workspace_bytes(rows, out, n), X.device, workspace)
-    _check(_lib.linear_int8(_ptr(X), _dtype_code(X), rows, _rowmajor(X, "X"), _vector(s, n, torch.float32, "s"),
+    ws, wsb = _scratch(linear_int8_workspace_bytes(rows, out, n), X.device, workspace)
+    _check(_lib.linear_int8(_ptr(X), _dtype_code(X), rows, _rows(X, "X"), _vector(s, n, torch.float32, "s"),
                             _ptr(codes), _codes(codes, "codes"), _vector(scales, out, torch.float32, "scales"), out, n,
                             _vector(bias, out, torch.float32, "bias"), _dtype_code(Y), _ptr(Y), ldy, _ptr(ws), wsb,
                             _stream()))
@@ -501,6 +519,8 @@ class KVCacheInt8(NamedTuple):
                 or not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous())):
             raise ValueError("cache tensors must be contiguous: int8 k [blocks, heads, block_size, dim] and v "
                              "[blocks, heads, dim, block_size], fp32 scales [blocks, heads]")
+        for t, name in zip(self, ("cache.k", "cache.v", "cache.k_scales", "cache.v_scales")):
+            _on_gpu(t, name)
         return nb, h, d, bs
 
 
@@ -511,6 +531,7 @@ def _heads3(t, rows, heads, dim, name):
     s0, s1, s2 = t.stride()
     if s2 != 1 or (heads > 1 and s1 != dim):
         raise ValueError(f"{name}: the heads of a row must follow each other")
+    _on_gpu(t, name)
     return s0 if rows > 1 else heads * dim
 
 
@@ -574,8 +595,7 @@ def attention_int8_cache(Q, cache: KVCacheInt8, offsets, seq_lens, block_table, 
     if O.dtype != Q.dtype:
         raise TypeError("O must have Q's dtype")
     off, lens, batch, table, width = _ragged(offsets, seq_lens, block_table, "seq_lens")
-    ws, wsb = _workspace(attention_int8_cache_workspace_bytes(rows, batch, heads, h, d, bs, width), Q.device,
-                         workspace)
+    ws, wsb = _scratch(attention_int8_cache_workspace_bytes(rows, batch, heads, h, d, bs, width), Q.device, workspace)
     _check(_lib.attention_int8_cache(_ptr(Q), ldq, _ptr(O), ldo, _vector(lse, rows * heads, torch.float32, "lse"),
                                      _dtype_code(Q), rows, heads, off, lens, batch, table, width, _ptr(cache.k),
                                      _ptr(cache.v), _ptr(cache.k_scales), _ptr(cache.v_scales), nb, h, d, bs,
