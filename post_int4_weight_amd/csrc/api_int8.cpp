@@ -117,6 +117,7 @@ int matmul(const char* fn, const Int8Plan* given, const int8_t* A, int64_t lda, 
         set_error("%s: workspace %zu bytes, need %zu", fn, workspace ? workspace_bytes : (size_t)0, need);
         return PTQ_EWORKSPACE;
     }
+    if (need && !aligned16(workspace)) REFUSE("%s: workspace is not 16-byte aligned", fn);
     return run_matmul_int8(p, A, lda, a_scales, rows, codes, ldb, scales, out, in, bias, y_dtype, Y, ldy, workspace,
                            workspace_bytes, (hipStream_t)stream);
 }
