@@ -597,12 +597,15 @@ void launch_tokens(const T* X, int64_t rows, int in, int64_t ldx, const float* s
 
 int launch_quantize(const void* X, int x_dtype, int64_t rows, int64_t in, int64_t ldx, const float* s, int8_t* codes,
                     int64_t ldc, int shift, float* scales, hipStream_t st) {
-    if (rows == 0) return PTQ_OK;
-    if (x_dtype == PTQ_F32)
-        launch_tokens((const float*)X, rows, (int)in, ldx, s, codes, ldc, shift, scales, st);
-    else
-        launch_tokens((const uint16_t*)X, rows, (int)in, ldx, s, codes, ldc, shift, scales, st);
-    PTQ_LAUNCH_CHECK();
+    constexpr int64_t MOST = (int64_t)1 << 21;      // rows of a launch, which has fewer than 2^32 threads
+    for (int64_t r = 0; r < rows; r += MOST) {
+        const int64_t n = std::min(rows - r, MOST);
+        if (x_dtype == PTQ_F32)
+            launch_tokens((const float*)X + r * ldx, n, (int)in, ldx, s, codes + r * ldc, ldc, shift, scales + r, st);
+        else
+            launch_tokens((const uint16_t*)X + r * ldx, n, (int)in, ldx, s, codes + r * ldc, ldc, shift, scales + r, st);
+        PTQ_LAUNCH_CHECK();
+    }
     return PTQ_OK;
 }
 
