@@ -526,10 +526,33 @@ __global__ __launch_bounds__(64 * WO * WT) void matmul_int8_join_kernel(Int8Gemm
     store_rows<WA>(g, o0, r0, lds + wave * rows_bytes<WA>(), [&](int a) { return sum[a]; });
 }
 
+// f(part) for parts of the product, of whole tiles of to x tt, that a launch with one workgroup of that many threads a
+// tile takes (it has to have fewer than 2^32): one part, but for billions of outputs.
+template <typename F>
+void for_parts(const Int8GemmArgs& g, int to, int tt, int threads, F&& f) {
+    const int64_t most = ((int64_t)1 << 31) / threads, e = g.y_dtype == PTQ_F32 ? 4 : 2;
+    const int64_t no = std::min(cdiv(g.out, to), most), step_o = no * to, step_t = std::max<int64_t>(1, most / no) * tt;
+    for (int64_t r = 0; r < g.rows; r += step_t)
+        for (int64_t o = 0; o < g.out; o += step_o) {
+            Int8GemmArgs part = g;
+            part.W += o * g.ldw;
+            part.sw += o;
+            if (g.bias) part.bias += o;
+            part.out = std::min(g.out - o, step_o);
+            if (g.C) part.C += r * g.ldc;
+            if (g.sx) part.sx += r;
+            part.rows = std::min(g.rows - r, step_t);
+            part.Y = (char*)g.Y + (r * g.ldy + o) * e;
+            f(part);
+        }
+}
+
 void launch_few(const Int8GemmArgs& g, hipStream_t st) {
-    const int64_t strips = cdiv(g.out, 16);
-    hipLaunchKernelGGL(matmul_int8_few_kernel, dim3((unsigned)(strips * cdiv(g.rows, 16))), dim3(64 * FW), 0, st, g,
-                       (unsigned)strips);
+    for_parts(g, 16, 16, 64 * FW, [&](const Int8GemmArgs& part) {
+        const int64_t strips = cdiv(part.out, 16);
+        hipLaunchKernelGGL(matmul_int8_few_kernel, dim3((unsigned)(strips * cdiv(part.rows, 16))), dim3(64 * FW), 0, st,
+                           part, (unsigned)strips);
+    });
 }
 
 // ceil(log2(rows)) if the fused kernel takes them, else -1
@@ -547,8 +570,10 @@ int launch_fused(const Int8GemmArgs& g, const T* X, int64_t ldx, const float* s,
                                     hipFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024));
         ready = true;
     }
-    hipLaunchKernelGGL((linear_int8_few_kernel<T, SMOOTH>), dim3((unsigned)cdiv(g.out, 16)), dim3(64 * FW),
-                       (unsigned)(g.rows * fused_pitch(g.in)), st, g, X, ldx, s, rl);
+    for_parts(g, 16, 16, 64 * FW, [&](const Int8GemmArgs& part) {      // up to 16 tokens: parts of the outputs
+        hipLaunchKernelGGL((linear_int8_few_kernel<T, SMOOTH>), dim3((unsigned)cdiv(part.out, 16)), dim3(64 * FW),
+                           (unsigned)(part.rows * fused_pitch(part.in)), st, part, X, ldx, s, rl);
+    });
     return PTQ_OK;
 }
 
@@ -561,12 +586,16 @@ int launch_tile(const Int8GemmArgs& g, hipStream_t st) {
                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds));
         ready = true;
     }
-    const int64_t to = cdiv(g.out, TO), tt = cdiv(g.rows, TT);
-    hipLaunchKernelGGL((matmul_int8_tile_kernel<TO, TT, WO, WT, NST>),
-                       dim3((unsigned)(cdiv(to * tt, NXCD) * NXCD), g.nsplit), dim3(64 * WO * WT), lds, st, g, (int)to, (int)tt);
-    if (g.nsplit > 1)
-        hipLaunchKernelGGL((matmul_int8_join_kernel<TO, TT, WO, WT>), dim3((unsigned)(to * tt * (TT / WT / 16))),
-                           dim3(64 * WO * WT), 0, st, g, (int)to, (int)tt);
+    constexpr int joins = TT / WT / 16;             // workgroups of the join for each of the product's
+    for_parts(g, TO, TT, 64 * WO * WT * (g.nsplit > 1 ? joins : 1), [&](const Int8GemmArgs& part) {
+        const int64_t to = cdiv(part.out, TO), tt = cdiv(part.rows, TT);
+        hipLaunchKernelGGL((matmul_int8_tile_kernel<TO, TT, WO, WT, NST>),
+                           dim3((unsigned)(cdiv(to * tt, NXCD) * NXCD), part.nsplit), dim3(64 * WO * WT), lds, st, part,
+                           (int)to, (int)tt);
+        if (part.nsplit > 1)
+            hipLaunchKernelGGL((matmul_int8_join_kernel<TO, TT, WO, WT>), dim3((unsigned)(to * tt * joins)),
+                               dim3(64 * WO * WT), 0, st, part, (int)to, (int)tt);
+    });
     return PTQ_OK;
 }
 
