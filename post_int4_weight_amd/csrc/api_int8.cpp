@@ -89,7 +89,8 @@ int check_cache_pointers(const char* fn, const KVCacheInt8& c) {
 int check_ragged(const char* fn, const RaggedRows& r, const char* starts, int heads) {
     if (r.rows < 0 || r.batch < 0 || r.width < 0)
         REFUSE("%s: rows, batch and table_width must not be negative", fn);
-    // launches count work units of at least one row and head in 32 bits
+    // launches count work units of at least one row and head in 32 bits (attention: at most one workgroup of 256 threads
+    // for 16 rows and one for each sequence, or half as many of 512, so below 2^32 threads)
     if ((r.rows + 2 * r.batch) > MAX_ROWS / (64 * (int64_t)heads))
         REFUSE("%s: rows = %lld, batch = %lld too large for %d heads", fn, (long long)r.rows, (long long)r.batch, heads);
     if (r.width > MAX_ROWS / 128) REFUSE("%s: table_width = %lld too large", fn, (long long)r.width);

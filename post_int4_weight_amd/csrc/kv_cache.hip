@@ -253,13 +253,19 @@ struct Launch {
     dim3 grid, block;
     int per;
 };
-Launch block_launch(const KVCacheInt8& c, const RaggedRows& r, int nv) {
-    Launch l;
+int block_launch(const char* fn, const KVCacheInt8& c, const RaggedRows& r, int nv, Launch& l) {
     l.per = c.block * c.dim / (16 * nv);
     const int nt = std::max(l.per, std::min(256, (int)cdiv((int64_t)l.per * c.heads, 64) * 64));
+    const int64_t units = r.rows / c.block + 2 * r.batch;
+    // a launch of 2^32 threads or more wraps without an error: only some of its workgroups run
+    if (units > (((int64_t)1 << 32) - 1) / nt) {
+        set_error("%s: rows = %lld, batch = %lld: %lld workgroups of %d threads are too many for a launch", fn,
+                  (long long)r.rows, (long long)r.batch, (long long)units, nt);
+        return PTQ_EINVAL;
+    }
     l.block = dim3((unsigned)nt);
-    l.grid = dim3((unsigned)(r.rows / c.block + 2 * r.batch), (unsigned)cdiv(c.heads, nt / l.per), 2);
-    return l;
+    l.grid = dim3((unsigned)units, (unsigned)cdiv(c.heads, nt / l.per), 2);
+    return PTQ_OK;
 }
 
 }  // namespace
@@ -268,7 +274,8 @@ int launch_kv_write(const KVCacheInt8& c, const RaggedRows& r, int dtype, const 
                     int64_t ldv, hipStream_t st) {
     if (r.rows == 0 || r.batch == 0) return PTQ_OK;
     const CacheArgs a = cache_args(c, r);
-    const Launch l = block_launch(c, r, dtype == PTQ_F32 ? write_nv<float>() : write_nv<uint16_t>());
+    Launch l;
+    PTQ_TRY(block_launch("kv_cache_write_int8", c, r, dtype == PTQ_F32 ? write_nv<float>() : write_nv<uint16_t>(), l));
     if (dtype == PTQ_F32)
         hipLaunchKernelGGL(kv_write_kernel<float>, l.grid, l.block, 0, st, a, l.per, (const float*)K, ldk, (const float*)V,
                            ldv);
@@ -283,7 +290,8 @@ int launch_kv_read(const KVCacheInt8& c, const RaggedRows& r, int dtype, void* K
                    hipStream_t st) {
     if (r.rows == 0 || r.batch == 0) return PTQ_OK;
     const CacheArgs a = cache_args(c, r);
-    const Launch l = block_launch(c, r, READ_NV);
+    Launch l;
+    PTQ_TRY(block_launch("kv_cache_read_int8", c, r, READ_NV, l));
     if (dtype == PTQ_F32)
         hipLaunchKernelGGL(kv_read_kernel<float>, l.grid, l.block, 0, st, a, l.per, (float*)K, ldk, (float*)V, ldv);
     else

@@ -19,3 +19,11 @@ def test_matmul_workspace_alignment():
         need = lib.matmul_int8_workspace_bytes(rows, out, n)
         assert need > 0
         _refused(lib.matmul_int8(P, n, P, rows, P, n, P, out, n, None, 0, P, out, ODD, need, None), "workspace is not")
+
+
+def test_launches_of_2_32_threads():
+    """Sequences are looked up in the launch, which has workgroups for each: as many as wrap its size are refused."""
+    for name in ("kv_cache_write_int8", "kv_cache_read_int8"):
+        for dtype in (0, 1):
+            _refused(getattr(lib, name)(P, P, P, P, 10, 1, 256, 128, P, 256, P, 256, dtype, 5, P, P, (1 << 24) - 8, P, 1,
+                                        None), "too many for a launch")
