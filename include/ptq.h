@@ -345,7 +345,9 @@ int layer_output_error(const void* X, int x_dtype, int64_t rows, int64_t ldx,
  * (>= in, a multiple of 8), scales fp32[rows].
  *
  * matmul_int8: Y[t][o] = (sum_j A[t][j] codes[o][j]) * a_scales[t] * scales[o]
- * + bias[o], the sums exact in int32, one rounding to Y's type (y_dtype).
+ * + bias[o], the sums exact in int32; a sum as fp32, the product of the two
+ * scales, their product and the bias sum are fp32 numbers, rounded to Y's type
+ * (y_dtype).
  * codes int8[out, in], scales fp32[out], bias fp32[out] or NULL; Y bf16 or
  * fp32 [rows, out] with row stride ldy >= out.
  *
@@ -412,7 +414,10 @@ int kv_cache_read_int8(const int8_t* k_codes, const int8_t* v_codes, const float
  * the keys of each sequence, the call's own tokens included; with n rows,
  * query i of sequence b is at position p = seq_lens[b] - n + i. It attends to
  * keys [max(0, p - window + 1), p] with causal = 1 (window 0: no lower
- * limit), to all seq_lens[b] keys with causal = 0 (window must be 0).
+ * limit), to all seq_lens[b] keys with causal = 0 (window must be 0). The host
+ * does not read the lengths: kernel and splits are chosen for sequences as
+ * long as table_width allows, so a table no wider than the longest sequence
+ * serves short ones best.
  *   O = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * q.k_j)
  *   lse[rows, heads] (fp32, may be NULL) = ln sum_j w_j
  * A query that attends to nothing gives O = 0, lse = -inf. A sequence longer

@@ -158,9 +158,11 @@ __device__ __forceinline__ float load_query(const T* p, float scale2, f16x8 (&q)
 // (its size is a multiple of 16), so a lane needs one S_k and one S_v a step.
 // The waves of a workgroup take every NW-th step; block ids come a step early.
 // What bounds it is memory: each step's 16 KB (D = 128) are requested at once,
-// and the other waves of the CU, four a SIMD, work meanwhile. A second buffer
-// for the next step's codes halves those waves: 280 us against 253. 64
-// sequences of 100 .. 16000 keys, 64 query heads on 8: 227 us, 4.7 TB/s.
+// and the other waves of the CU work meanwhile: a SIMD holds four at D = 64 (111
+// + 16 registers), two at 128 (159 + 32 of bf16, 175 + 32 of fp32 queries), one
+// at 256 (256 + 76, 256 + 108), where nothing is in flight while it computes. 64
+// sequences of 100 .. 16000 keys, 64 query heads on 8, D = 128: 227 us, 4.7
+// TB/s. 16 sequences of 100 .. 4000 keys, 16 on 4, D = 256: 34 us, 2.0 TB/s.
 template <int D>
 struct StepCodes {
     uint4 k[4][D / 64], v[D / 16];
@@ -401,7 +403,8 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
 // (fetching and staging the next ones, its only barrier, the head of the next
 // block) lies between products, too. A fragment is read AHEAD products early.
 // Measured, 4 prompts of 2000 .. 4096 tokens over 5000 keys, 32 query heads on
-// 8: 652 us, 43% of the matrix cycles; phases one after the other were 785. 64
+// 8: 661 .. 691 us on three cards, about 42% of the matrix cycles; phases one
+// after the other were 785 where this order was 652. 64
 // rows a wave halve the LDS reads, but then one wave a SIMD has to issue
 // everything, and a sixth more of it to move accumulators between register
 // files: 917 us against 773 on the same card. Fragments 6 products early, or
@@ -1022,6 +1025,13 @@ AttnPlan plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int
 // 64 keys, 4 at a time on a CU or one. At 8 sequences on 8 kv heads of 4 query
 // heads over 2000 keys: 16 queries 22.7 us with few rows at a time and 34.6 with
 // tiles, 32 queries 39.3 and 38.7, 64 queries 73.6 and 53.1.
+// fp32 queries take twice the products in both kernels, and the same rule: over
+// 192 sizes each of 2 .. 512 queries on 1024 .. 16000 keys the choice is 0.7%
+// slower than the better kernel in the mean, for bf16 and for fp32, 23% and 19%
+// at worst (8 sequences of 32 heads of 64 on 8: 128 queries on 1024 keys bf16,
+// few rows 38.2 us where tiles take 31.1; 64 on 4096 fp32, tiles 86.7, few rows
+// 73.1). Above that fp32 tiles win as bf16 ones do: 8 sequences of 512 queries
+// of 16 heads of 128 on 2 over 16000 keys, 874 us against 1668.
 bool use_tiles(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int64_t keys) {
     if (dim > 128) return false;
     const int group = heads / kv_heads;

@@ -639,9 +639,10 @@ int launch_quantize(const void* X, int x_dtype, int64_t rows, int64_t in, int64_
 }
 
 // Tile shapes; us: time of a stage of one workgroup per CU. Rings are as deep
-// as LDS allows without losing a second workgroup to it (small tiles wait for
-// their copies, so 5 stages against 3 at 64 x 64: 4096 x 4096 weights, 200
-// tokens 10.8 against 14.4 us; 8 against 2 at 32 x 32).
+// as 160 KB of LDS allow for one workgroup a CU from 128 x 128 on (128, 144 and
+// 128 KB), and for two below (60 to 80 KB each): small tiles wait for their
+// copies, so 5 stages against 3 at 64 x 64: 4096 x 4096 weights, 200 tokens
+// 10.8 against 14.4 us; 8 against 2 at 32 x 32.
 struct Shape {
     int to, tt;
     float us;
