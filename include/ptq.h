@@ -442,6 +442,95 @@ int attention_int8_cache(const void* Q, int64_t ldq, void* O, int64_t ldo, float
                          int block_size, float scale, int causal, int64_t window, void* workspace,
                          size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A decode step with drafted tokens: rotary positions, appending to the cache,
+ * attention of a tree of drafted tokens, and which of them are kept.
+ *
+ * Rotary positions: the first rotary_dim channels of a head (even, at most
+ * head_dim) turn in pairs, n = rotary_dim / 2 of them, pair i being channels
+ * (2 i, 2 i + 1) with interleaved = 1 and (i, i + n) with 0:
+ *   y_a = m (x_a cos t - x_b sin t),  y_b = m (x_b cos t + x_a sin t),
+ *   t = position * inv_freq[i], m = magnitude
+ * inv_freq: fp64[n] (device; scaled for long contexts by the caller, or by the
+ * Python binding's Rotary.make), the angle in fp64, the rest in fp32; a value
+ * is rounded once, to its type. positions: int32, any value.
+ *
+ * rotary_apply: Y = X turned, [rows, heads, head_dim] bf16 or fp32 (row strides
+ * ldx and ldy, head_dim a multiple of 8), positions[rows]; channels from
+ * rotary_dim on are copied. Y may be X (with its stride), and must not overlap
+ * it otherwise.
+ *
+ * kv_cache_append_int8: kv_cache_write_int8 of turned keys, which are not
+ * rounded before they are quantized. positions[rows], or NULL: each row's own
+ * position in its sequence (the nodes of a tree have their depths' instead).
+ *
+ * Asynchronous. Errors: EINVAL, EHIP.
+ * ---------------------------------------------------------------------- */
+int rotary_apply(const void* X, int64_t ldx, void* Y, int64_t ldy, int dtype, int64_t rows, int heads, int head_dim,
+                 const int32_t* positions, const double* inv_freq, int rotary_dim, int interleaved, float magnitude,
+                 void* stream);
+int kv_cache_append_int8(int8_t* k_codes, int8_t* v_codes, float* k_scales, float* v_scales, int64_t num_blocks,
+                         int kv_heads, int head_dim, int block_size, const void* K, int64_t ldk, const void* V,
+                         int64_t ldv, int dtype, int64_t rows, const int32_t* offsets, const int32_t* starts,
+                         int64_t batch, const int32_t* block_table, int64_t table_width, const int32_t* positions,
+                         const double* inv_freq, int rotary_dim, int interleaved, float magnitude, void* stream);
+
+/* ------------------------------------------------------------------------
+ * attention_int8_tree: attention_int8_cache for sequences whose last n keys
+ * (n = offsets[b + 1] - offsets[b], at most 512) are the nodes of a tree, with
+ * one query each. parents int32[rows]: the parent of a node, an index within
+ * its sequence's nodes and below its own, or -1. Node i attends to all
+ * seq_lens[b] - n keys before the tree, to its ancestors and to itself; with a
+ * window > 0 only to those of them fewer than window positions back, its own
+ * position being seq_lens[b] - n + its depth (0 for a parent of -1).
+ * O, lse and the rest as for attention_int8_cache. NaN for all of a sequence's
+ * queries: fewer keys than nodes, more than 512 nodes, or longer than its row of
+ * block_table. NaN for a query: a parent on its way up that is not below its
+ * node or less than -1, or a key in a block without a valid id.
+ *
+ * Q is held in 15 significant bits of its row's largest element (bf16) or 22
+ * (fp32), its products with the codes of K are exact; probabilities, sums and
+ * scales as for attention_int8_cache. Asynchronous.
+ * Errors: EINVAL, EWORKSPACE, EHIP.
+ * ---------------------------------------------------------------------- */
+size_t attention_int8_tree_workspace_bytes(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim,
+                                           int block_size, int64_t table_width, int64_t window);
+int attention_int8_tree(const void* Q, int64_t ldq, void* O, int64_t ldo, float* lse, int dtype, int64_t rows,
+                        int heads, const int32_t* offsets, const int32_t* seq_lens, const int32_t* parents,
+                        int64_t batch, const int32_t* block_table, int64_t table_width, const int8_t* k_codes,
+                        const int8_t* v_codes, const float* k_scales, const float* v_scales, int64_t num_blocks,
+                        int kv_heads, int head_dim, int block_size, float scale, int64_t window, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * verify_drafts: which nodes of each sequence's tree are kept, so that the
+ * tokens that come out are distributed as the target's. Node 0 of a sequence is
+ * its last token, the others are drafted: tokens[rows] and parents[rows]
+ * (int32, rows as in attention_int8_tree, at most 512 a sequence). Row i of
+ * target [rows, vocab] (row stride ldt) holds the target's probabilities of the
+ * token after node i, row i of draft (ldd) those that i's children were drawn
+ * from; both bf16 or fp32. Random numbers u[rows] and r[batch], fp32 in [0, 1).
+ *
+ * From node 0, with p its row of target, q of draft, w = max(p, 0) and z = 1:
+ * its children x in index order,
+ *   u[x] z q(token x) < w(token x):  x is kept, and the walk goes on from x;
+ *   otherwise:                       w <- max(w - z q, 0), z <- sum w.
+ * Where no child is kept, the next token is the first one whose running sum of
+ * w exceeds r[b] times the whole sum (w = max(p, 0) again if nothing is left).
+ * draft NULL: drafts that were chosen, not drawn; q is 1 at the child's token
+ * and z <- z - w(token x), w(token x) <- 0. Nodes with a token outside
+ * [0, vocab) or a parent not below them are passed over. Sums and products of
+ * probabilities are formed in fp64.
+ *
+ * path[rows]: node 0 and the kept nodes in order, then -1; counts[batch]: how
+ * many; next[batch]: the token, or -1 if the sum is not positive and finite. A
+ * sequence without rows, or with more than 512, has counts 0 and next -1.
+ * Rows of no sequence are left as they are. Asynchronous. Errors: EINVAL, EHIP.
+ * ---------------------------------------------------------------------- */
+int verify_drafts(const void* target, int64_t ldt, const void* draft, int64_t ldd, int dtype, int64_t rows,
+                  int64_t vocab, const int32_t* tokens, const int32_t* parents, const int32_t* offsets, int64_t batch,
+                  const float* u, const float* r, int32_t* path, int32_t* counts, int32_t* next, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,7 +12,8 @@ from .api import (PTQError, PTQ_BF16, PTQ_F32, library_path, hessian_workspace_b
                   dequantize_int4, layer_output_error_workspace_bytes, layer_output_error, quantize_tokens_int8,
                   matmul_int8_workspace_bytes, matmul_int8, linear_int8_workspace_bytes, linear_int8, KVCacheInt8,
                   kv_cache_write_int8, kv_cache_read_int8, attention_int8_cache_workspace_bytes,
-                  attention_int8_cache)
+                  attention_int8_cache, Rotary, rotary_apply, kv_cache_append_int8,
+                  attention_int8_tree_workspace_bytes, attention_int8_tree, verify_drafts)
 
 __all__ = [
     "PTQError", "PTQ_BF16", "PTQ_F32", "library_path", "hessian_workspace_bytes", "hessian_accumulate",
@@ -22,4 +23,6 @@ __all__ = [
     "layer_output_error_workspace_bytes", "layer_output_error", "quantize_tokens_int8",
     "matmul_int8_workspace_bytes", "matmul_int8", "linear_int8_workspace_bytes", "linear_int8", "KVCacheInt8",
     "kv_cache_write_int8", "kv_cache_read_int8", "attention_int8_cache_workspace_bytes", "attention_int8_cache",
+    "Rotary", "rotary_apply", "kv_cache_append_int8", "attention_int8_tree_workspace_bytes", "attention_int8_tree",
+    "verify_drafts",
 ]

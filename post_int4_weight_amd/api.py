@@ -10,6 +10,7 @@ PyTorch fallback, and a missing library is an ImportError.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import NamedTuple
 
@@ -91,6 +92,13 @@ def _load() -> ctypes.CDLL:
         "attention_int8_cache_workspace_bytes": (sz, [i64, i64, i32, i32, i32, i32, i64]),
         "attention_int8_cache": (i32, [vp, i64, vp, i64, vp, i32, i64, i32, vp, vp, i64, vp, i64, vp, vp, vp, vp,
                                        i64, i32, i32, i32, ctypes.c_float, i32, i64, vp, sz, vp]),
+        "rotary_apply": (i32, [vp, i64, vp, i64, i32, i64, i32, i32, vp, vp, i32, i32, ctypes.c_float, vp]),
+        "kv_cache_append_int8": (i32, [vp, vp, vp, vp, i64, i32, i32, i32, vp, i64, vp, i64, i32, i64, vp, vp, i64,
+                                       vp, i64, vp, vp, i32, i32, ctypes.c_float, vp]),
+        "attention_int8_tree_workspace_bytes": (sz, [i64, i64, i32, i32, i32, i32, i64, i64]),
+        "attention_int8_tree": (i32, [vp, i64, vp, i64, vp, i32, i64, i32, vp, vp, vp, i64, vp, i64, vp, vp, vp, vp,
+                                      i64, i32, i32, i32, ctypes.c_float, i64, vp, sz, vp]),
+        "verify_drafts": (i32, [vp, i64, vp, i64, i32, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp]),
         "ptq_test_matmul_int8_plan": (i32, [i64, i64, i64, ctypes.POINTER(i32), ctypes.POINTER(i32)]),
         "ptq_test_matmul_int8_workspace_bytes": (sz, [i32, i32, i64, i64, i64]),
         "ptq_test_matmul_int8": (i32, [i32, i32, vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, i32, vp, i64, vp, sz,
@@ -601,6 +609,150 @@ def attention_int8_cache(Q, cache: KVCacheInt8, offsets, seq_lens, block_table, 
                                      _ptr(cache.v), _ptr(cache.k_scales), _ptr(cache.v_scales), nb, h, d, bs,
                                      float(scale), int(bool(causal)), window, _ptr(ws), wsb, _stream()))
     return O if lse is None else (O, lse)
+
+
+class Rotary(NamedTuple):
+    """Rotary positions (include/ptq.h): how the pairs of a head lie, and how fast each of them turns."""
+    inv_freq: torch.Tensor       # fp64 [rotary_dim / 2], radians per position
+    magnitude: float = 1.0       # factor of the channels that turn
+    interleaved: bool = False    # pairs (2i, 2i + 1); else (i, i + rotary_dim / 2)
+
+    @classmethod
+    def make(cls, rotary_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str | None = None,
+             factor: float = 1.0, original_length: int = 0, low: float = 1.0, high: float | None = None, device="cuda"):
+        """Frequencies base^(-2i / rotary_dim), for contexts `factor` times original_length positions scaled by
+
+        * "linear": all divided by factor;
+        * "ntk": base times factor^(rotary_dim / (rotary_dim - 2)), so that the slowest pair turns factor times slower;
+        * "yarn": pairs of up to `low` turns (1) in original_length divided by factor, those of `high` turns (32) and more
+          kept, a ramp over the pairs between, and magnitude 1 + 0.1 ln factor;
+        * "wavelength": the same ends (1 and 4), a ramp over the turns between.
+        """
+        if rotary_dim < 2 or rotary_dim % 2:
+            raise ValueError(f"rotary_dim = {rotary_dim} must be even and positive")
+        if not (base > 1 and factor > 0):
+            raise ValueError("base must be above 1 and factor positive")
+        if scaling not in (None, "linear", "ntk", "yarn", "wavelength"):
+            raise ValueError(f"unknown scaling {scaling!r}")
+        n, magnitude = rotary_dim // 2, 1.0
+        if scaling == "ntk":
+            if n < 2:
+                raise ValueError("ntk scaling needs rotary_dim above 2")
+            base = base * factor ** (n / (n - 1))
+        freq = [base ** (-i / n) for i in range(n)]
+        if scaling == "linear":
+            freq = [f / factor for f in freq]
+        elif scaling in ("yarn", "wavelength"):
+            high = high or (32.0 if scaling == "yarn" else 4.0)
+            if original_length < 1 or not 0 < low < high:
+                raise ValueError("original_length must be positive, and 0 < low < high")
+            turns = lambda i: original_length * base ** (-i / n) / (2 * math.pi)
+            if scaling == "yarn":
+                pair = lambda t: n * math.log(original_length / (2 * math.pi * t)) / math.log(base)   # that turns t times
+                first, last = max(math.floor(pair(high)), 0), min(math.ceil(pair(low)), rotary_dim - 1)
+                keep = lambda i: 1 - min(max((i - first) / max(last - first, 0.001), 0), 1)
+                magnitude = 1.0 + 0.1 * math.log(factor) if factor > 1 else 1.0
+            else:
+                keep = lambda i: min(max((turns(i) - low) / (high - low), 0), 1)
+            freq = [f * (keep(i) + (1 - keep(i)) / factor) for i, f in enumerate(freq)]
+        return cls(torch.tensor(freq, dtype=torch.float64, device=device), magnitude, interleaved)
+
+    def _args(self):
+        n = self.inv_freq.numel()
+        return _vector(self.inv_freq, n, torch.float64, "inv_freq"), 2 * n, int(bool(self.interleaved)), self.magnitude
+
+
+def rotary_apply(X, rotary: Rotary, positions, Y=None):
+    """rotary_apply (include/ptq.h): X [rows, heads, head_dim] turned by positions [rows]; Y may be X."""
+    if X.dim() != 3:
+        raise ValueError("X must be [rows, heads, head_dim]")
+    rows, heads, dim = X.shape
+    if Y is None:
+        Y = torch.empty(rows, heads, dim, dtype=X.dtype, device=X.device)
+    if Y.dtype != X.dtype:
+        raise TypeError("Y must have X's dtype")
+    ldx, ldy = _heads3(X, rows, heads, dim, "X"), _heads3(Y, rows, heads, dim, "Y")
+    _check(_lib.rotary_apply(_ptr(X), ldx, _ptr(Y), ldy, _dtype_code(X), rows, heads, dim,
+                             _vector(positions, rows, torch.int32, "positions"), *rotary._args(), _stream()))
+    return Y
+
+
+def kv_cache_append_int8(cache: KVCacheInt8, K, V, offsets, starts, block_table, rotary: Rotary, positions=None):
+    """kv_cache_append_int8 (include/ptq.h): kv_cache_write_int8 with the keys turned on the way, by positions [rows] or
+    by their own positions in their sequences."""
+    nb, h, d, bs = cache._sizes()
+    rows = K.shape[0]
+    ldk, ldv = _heads3(K, rows, h, d, "K"), _heads3(V, rows, h, d, "V")
+    if V.dtype != K.dtype:
+        raise TypeError("K and V must have one dtype")
+    _check(_lib.kv_cache_append_int8(_ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scales), _ptr(cache.v_scales), nb, h, d,
+                                     bs, _ptr(K), ldk, _ptr(V), ldv, _dtype_code(K), rows,
+                                     *_ragged(offsets, starts, block_table, "starts"),
+                                     _vector(positions, rows, torch.int32, "positions"), *rotary._args(), _stream()))
+
+
+def attention_int8_tree_workspace_bytes(rows: int, batch: int, heads: int, kv_heads: int, head_dim: int,
+                                        block_size: int, table_width: int, window: int = 0) -> int:
+    return int(_lib.attention_int8_tree_workspace_bytes(rows, batch, heads, kv_heads, head_dim, block_size, table_width,
+                                                        window))
+
+
+def attention_int8_tree(Q, cache: KVCacheInt8, offsets, seq_lens, block_table, parents, scale=None, window=0, O=None,
+                        lse=None, return_lse=False, workspace=None):
+    """attention_int8_tree (include/ptq.h): attention of trees of drafted tokens, Q [rows, heads, head_dim] with
+    parents [rows]; seq_lens counts each sequence's keys, its nodes included. Returns O, or (O, lse) with return_lse or a
+    given lse."""
+    nb, h, d, bs = cache._sizes()
+    if Q.dim() != 3:
+        raise ValueError("Q must be [rows, heads, head_dim]")
+    rows, heads = Q.shape[0], Q.shape[1]
+    if scale is None:
+        scale = d ** -0.5
+    if O is None:
+        O = torch.empty(rows, heads, d, dtype=Q.dtype, device=Q.device)
+    if lse is None and return_lse:
+        lse = torch.empty(rows, heads, dtype=torch.float32, device=Q.device)
+    ldq, ldo = _heads3(Q, rows, heads, d, "Q"), _heads3(O, rows, heads, d, "O")
+    if O.dtype != Q.dtype:
+        raise TypeError("O must have Q's dtype")
+    off, lens, batch, table, width = _ragged(offsets, seq_lens, block_table, "seq_lens")
+    ws, wsb = _scratch(attention_int8_tree_workspace_bytes(rows, batch, heads, h, d, bs, width, window), Q.device, workspace)
+    _check(_lib.attention_int8_tree(_ptr(Q), ldq, _ptr(O), ldo, _vector(lse, rows * heads, torch.float32, "lse"),
+                                    _dtype_code(Q), rows, heads, off, lens,
+                                    _vector(parents, rows, torch.int32, "parents"), batch, table, width, _ptr(cache.k),
+                                    _ptr(cache.v), _ptr(cache.k_scales), _ptr(cache.v_scales), nb, h, d, bs,
+                                    float(scale), window, _ptr(ws), wsb, _stream()))
+    return O if lse is None else (O, lse)
+
+
+def _probabilities(t, rows, vocab, name):
+    if t.dim() != 2 or tuple(t.shape) != (rows, vocab):
+        raise ValueError(f"{name} must be {(rows, vocab)}, got {tuple(t.shape)}")
+    return max(_rows(t, name), vocab)
+
+
+def verify_drafts(target, tokens, parents, offsets, u, r, draft=None, path=None, counts=None, next=None):
+    """verify_drafts (include/ptq.h): (path [rows], counts [batch], next [batch]) of each sequence's tree, from target
+    and draft probabilities [rows, vocab] (draft None: drafts that were chosen) and random numbers u [rows], r [batch]."""
+    if target.dim() != 2:
+        raise ValueError("target must be [rows, vocab]")
+    rows, vocab = target.shape
+    batch = r.numel()
+    ldt = _probabilities(target, rows, vocab, "target")
+    ldd = 0
+    if draft is not None:
+        ldd = _probabilities(draft, rows, vocab, "draft")
+        if draft.dtype != target.dtype:
+            raise TypeError("draft must have target's dtype")
+    ints = lambda t, n: torch.empty(n, dtype=torch.int32, device=target.device) if t is None else t
+    path, counts, next = ints(path, rows), ints(counts, batch), ints(next, batch)
+    vec = lambda t, n, name, dtype=torch.int32: _vector(t, n, dtype, name)
+    _check(_lib.verify_drafts(_ptr(target), ldt, _ptr(draft), ldd, _dtype_code(target), rows, vocab,
+                              vec(tokens, rows, "tokens"), vec(parents, rows, "parents"),
+                              vec(offsets, batch + 1, "offsets"), batch, vec(u, rows, "u", torch.float32),
+                              vec(r, batch, "r", torch.float32), vec(path, rows, "path"), vec(counts, batch, "counts"),
+                              vec(next, batch, "next"), _stream()))
+    return path, counts, next
 
 
 # ------------------------------------------------------------- test hook ---

@@ -1,6 +1,7 @@
 // C ABI of the int8 serving operators (declared in include/ptq.h): argument
 // checks, before any HIP call, and the calls into linear_int8.hip,
-// kv_cache.hip and attention_int8.hip.
+// kv_cache.hip, attention_int8.hip, rotary.hip, attention_tree.hip and
+// verify.hip.
 #include <algorithm>
 #include <cmath>
 
@@ -152,6 +153,56 @@ int attention(const char* fn, const AttnPlan* given, const KVCacheInt8& c, const
     if (need && !aligned16(workspace)) REFUSE("%s: workspace is not 16-byte aligned", fn);
     return run_attention_int8(p, c, r, dtype, Q, ldq, heads, scale, causal, window, O, ldo, lse, workspace,
                               workspace_bytes, (hipStream_t)stream);
+}
+
+int check_rotary(const char* fn, const Rotary& p, int rotary_dim, int head_dim) {
+    if (rotary_dim < 2 || rotary_dim % 2 || rotary_dim > head_dim)
+        REFUSE("%s: rotary_dim = %d must be even, in [2, head_dim = %d]", fn, rotary_dim, head_dim);
+    if (p.interleaved != 0 && p.interleaved != 1) REFUSE("%s: interleaved = %d is neither 0 nor 1", fn, p.interleaved);
+    if (!std::isfinite(p.magnitude)) REFUSE("%s: magnitude is not finite", fn);
+    return PTQ_OK;
+}
+
+int check_frequencies(const char* fn, const double* freq) {
+    if (!freq) REFUSE("%s: inv_freq is NULL", fn);
+    if ((uintptr_t)freq & 7u) REFUSE("%s: inv_freq is not 8-byte aligned", fn);
+    return PTQ_OK;
+}
+
+// attention_int8_tree with the plan given, or chosen
+int attention_tree(const char* fn, const TreePlan* given, const KVCacheInt8& c, const RaggedRows& r,
+                   const int32_t* parents, int dtype, const void* Q, int64_t ldq, int heads, float scale, int64_t window,
+                   void* O, int64_t ldo, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    PTQ_TRY(check_cache(fn, c));
+    if (heads < 1 || heads > 65535 || heads % c.heads)
+        REFUSE("%s: heads = %d must be a multiple of kv_heads = %d, at most 65535", fn, heads, c.heads);
+    PTQ_TRY(check_ragged(fn, r, "seq_lens", heads));
+    if (!std::isfinite(scale)) REFUSE("%s: scale is not finite", fn);
+    if (window < 0) REFUSE("%s: window = %lld < 0", fn, (long long)window);
+    if (r.rows == 0 || r.batch == 0) return PTQ_OK;
+    PTQ_TRY(check_cache_pointers(fn, c));
+    if (c.num_blocks < 1) REFUSE("%s: num_blocks = 0", fn);
+    if (!parents) REFUSE("%s: parents is NULL", fn);
+    const int64_t n = (int64_t)heads * c.dim;
+    PTQ_TRY(check_float_rows(fn, "Q", Q, dtype, n, ldq));
+    PTQ_TRY(check_float_rows(fn, "O", O, dtype, n, ldo));
+    const TreePlan p =
+        given ? *given : attention_tree_plan(r.rows, r.batch, heads, c.heads, c.block, r.width, window);
+    const size_t need = attention_tree_part_bytes(p.nsplit, r.rows, heads, c.dim);
+    if (need && (!workspace || workspace_bytes < need)) {
+        set_error("%s: workspace %zu bytes, need %zu", fn, workspace ? workspace_bytes : (size_t)0, need);
+        return PTQ_EWORKSPACE;
+    }
+    if (need && !aligned16(workspace)) REFUSE("%s: workspace is not 16-byte aligned", fn);
+    return run_attention_tree(p, c, r, parents, dtype, Q, ldq, heads, scale, window, O, ldo, lse, workspace,
+                              workspace_bytes, (hipStream_t)stream);
+}
+
+int check_probabilities(const char* fn, const char* name, const void* P, int dtype, int64_t vocab, int64_t ld) {
+    if (!P) REFUSE("%s: %s is NULL", fn, name);
+    if ((uintptr_t)P & (dtype == PTQ_BF16 ? 1u : 3u)) REFUSE("%s: %s is not aligned to its elements", fn, name);
+    if (ld < vocab) REFUSE("%s: row stride %lld of %s < vocab = %lld", fn, (long long)ld, name, (long long)vocab);
+    return PTQ_OK;
 }
 
 }  // namespace
@@ -330,6 +381,95 @@ int ptq_test_attention_int8_cache(int tiles, int waves, int nsplit, const void* 
     const AttnPlan p{tiles ? ATTN_TILE : ATTN_ROWS, waves, nsplit};
     return attention(fn, &p, c, r, dtype, Q, ldq, heads, scale, causal, window, O, ldo, lse, workspace,
                      workspace_bytes, stream);
+}
+
+int rotary_apply(const void* X, int64_t ldx, void* Y, int64_t ldy, int dtype, int64_t rows, int heads, int head_dim,
+                 const int32_t* positions, const double* inv_freq, int rotary_dim, int interleaved, float magnitude,
+                 void* stream) {
+    const char* fn = "rotary_apply";
+    if (rows < 0 || rows > MAX_ROWS) REFUSE("%s: rows = %lld outside [0, 2^31)", fn, (long long)rows);
+    if (heads < 1 || heads > 65535) REFUSE("%s: heads = %d outside [1, 65535]", fn, heads);
+    if (head_dim < 8 || head_dim % 8 || head_dim > 65536)
+        REFUSE("%s: head_dim = %d must be a multiple of 8 in [8, 65536]", fn, head_dim);
+    const Rotary p{inv_freq, rotary_dim / 2, interleaved, magnitude};
+    PTQ_TRY(check_rotary(fn, p, rotary_dim, head_dim));
+    if (rows == 0) return PTQ_OK;
+    const int64_t n = (int64_t)heads * head_dim;
+    PTQ_TRY(check_float_rows(fn, "X", X, dtype, n, ldx));
+    PTQ_TRY(check_float_rows(fn, "Y", Y, dtype, n, ldy));
+    if (!positions) REFUSE("%s: positions is NULL", fn);
+    PTQ_TRY(check_frequencies(fn, inv_freq));
+    // rows of Y are written while others of X are still read
+    const uintptr_t x0 = (uintptr_t)X, y0 = (uintptr_t)Y, es = dtype == PTQ_BF16 ? 2 : 4;
+    const uintptr_t xn = ((uintptr_t)(rows - 1) * ldx + n) * es, yn = ((uintptr_t)(rows - 1) * ldy + n) * es;
+    if (x0 == y0 ? ldx != ldy && rows > 1 : x0 < y0 + yn && y0 < x0 + xn)
+        REFUSE("%s: Y overlaps X without being X", fn);
+    return launch_rotary(X, ldx, Y, ldy, dtype, rows, heads, head_dim, p, positions, (hipStream_t)stream);
+}
+
+int kv_cache_append_int8(int8_t* k_codes, int8_t* v_codes, float* k_scales, float* v_scales, int64_t num_blocks,
+                         int kv_heads, int head_dim, int block_size, const void* K, int64_t ldk, const void* V,
+                         int64_t ldv, int dtype, int64_t rows, const int32_t* offsets, const int32_t* starts,
+                         int64_t batch, const int32_t* block_table, int64_t table_width, const int32_t* positions,
+                         const double* inv_freq, int rotary_dim, int interleaved, float magnitude, void* stream) {
+    const char* fn = "kv_cache_append_int8";
+    const KVCacheInt8 c{k_codes, v_codes, k_scales, v_scales, num_blocks, kv_heads, head_dim, block_size};
+    const RaggedRows r{rows, batch, offsets, starts, block_table, table_width};
+    const Rotary p{inv_freq, rotary_dim / 2, interleaved, magnitude};
+    PTQ_TRY(check_cache(fn, c));
+    PTQ_TRY(check_ragged(fn, r, "starts", kv_heads));
+    PTQ_TRY(check_rotary(fn, p, rotary_dim, head_dim));
+    if (rows == 0 || batch == 0) return PTQ_OK;
+    PTQ_TRY(check_cache_pointers(fn, c));
+    const int64_t n = (int64_t)kv_heads * head_dim;
+    PTQ_TRY(check_float_rows(fn, "K", K, dtype, n, ldk));
+    PTQ_TRY(check_float_rows(fn, "V", V, dtype, n, ldv));
+    PTQ_TRY(check_frequencies(fn, inv_freq));
+    return launch_kv_append(c, r, dtype, K, ldk, V, ldv, p, positions, (hipStream_t)stream);
+}
+
+size_t attention_int8_tree_workspace_bytes(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim,
+                                           int block_size, int64_t table_width, int64_t window) {
+    const KVCacheInt8 c{nullptr, nullptr, nullptr, nullptr, 0, kv_heads, head_dim, block_size};
+    if (check_cache("attention_int8_tree_workspace_bytes", c) != PTQ_OK || rows <= 0 || batch <= 0 ||
+        heads < kv_heads || heads % kv_heads || table_width < 0 || window < 0)
+        return 0;
+    const TreePlan p = attention_tree_plan(rows, batch, heads, kv_heads, block_size, table_width, window);
+    return attention_tree_part_bytes(p.nsplit, rows, heads, head_dim);
+}
+
+int attention_int8_tree(const void* Q, int64_t ldq, void* O, int64_t ldo, float* lse, int dtype, int64_t rows,
+                        int heads, const int32_t* offsets, const int32_t* seq_lens, const int32_t* parents,
+                        int64_t batch, const int32_t* block_table, int64_t table_width, const int8_t* k_codes,
+                        const int8_t* v_codes, const float* k_scales, const float* v_scales, int64_t num_blocks,
+                        int kv_heads, int head_dim, int block_size, float scale, int64_t window, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    const KVCacheInt8 c{const_cast<int8_t*>(k_codes), const_cast<int8_t*>(v_codes), const_cast<float*>(k_scales),
+                        const_cast<float*>(v_scales), num_blocks, kv_heads, head_dim, block_size};
+    const RaggedRows r{rows, batch, offsets, seq_lens, block_table, table_width};
+    return attention_tree("attention_int8_tree", nullptr, c, r, parents, dtype, Q, ldq, heads, scale, window, O, ldo,
+                          lse, workspace, workspace_bytes, stream);
+}
+
+int verify_drafts(const void* target, int64_t ldt, const void* draft, int64_t ldd, int dtype, int64_t rows,
+                  int64_t vocab, const int32_t* tokens, const int32_t* parents, const int32_t* offsets, int64_t batch,
+                  const float* u, const float* r, int32_t* path, int32_t* counts, int32_t* next, void* stream) {
+    const char* fn = "verify_drafts";
+    if (rows < 0 || rows > MAX_ROWS) REFUSE("%s: rows = %lld outside [0, 2^31)", fn, (long long)rows);
+    // a workgroup of 1024 threads each, and fewer than 2^32 threads
+    if (batch < 0 || batch >= (int64_t)1 << 22) REFUSE("%s: batch = %lld outside [0, 2^22)", fn, (long long)batch);
+    if (vocab < 1 || vocab > MAX_ROWS) REFUSE("%s: vocab = %lld outside [1, 2^31)", fn, (long long)vocab);
+    if (!dtype_ok(dtype)) REFUSE("%s: dtype = %d is neither PTQ_BF16 nor PTQ_F32", fn, dtype);
+    if (batch == 0) return PTQ_OK;
+    if (!offsets) REFUSE("%s: offsets is NULL", fn);
+    if (!counts || !next) REFUSE("%s: counts or next is NULL", fn);
+    if (rows > 0) {
+        PTQ_TRY(check_probabilities(fn, "target", target, dtype, vocab, ldt));
+        if (draft) PTQ_TRY(check_probabilities(fn, "draft", draft, dtype, vocab, ldd));
+        if (!tokens || !parents || !u || !r || !path) REFUSE("%s: tokens, parents, u, r or path is NULL", fn);
+    }
+    const Drafts d{rows, batch, tokens, parents, offsets, u, r};
+    return launch_verify_drafts(target, ldt, draft, ldd, dtype, vocab, d, path, counts, next, (hipStream_t)stream);
 }
 
 }  // extern "C"

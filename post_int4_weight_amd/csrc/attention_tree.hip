@@ -1,0 +1,590 @@
+// Softmax attention of trees of drafted tokens over the int8 block cache
+// (layout in kv_cache.hip): the last n keys of a sequence are the nodes of a
+// tree, its queries are theirs. Node i attends to every key before the tree and
+// to its ancestors and itself,
+//
+//   o_i = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q_i.k_j - m)
+//   k_j = S_k[block(j)] c_j,  v_j = S_v[block(j)] c'_j
+//
+// Arithmetic. Scores are int8 products: a row of q is a fixed-point number of
+// its largest element, q = (max|q| / 16256) (128 hi + lo) for bf16 and 21 bits in
+// three terms for fp32 queries, so the codes of K go into the matrix cores as
+// they lie in memory and the sums are exact in int32. P V runs on the fp16
+// matrix cores, where codes are exact: w_j = p_j S_v[block(j)] / R in fp16 (two
+// terms for fp32 queries), R the running maximum of S_v over the blocks that the
+// row attends to. Maxima, sums and the output accumulate in fp32.
+#include "attention.hpp"
+
+#include <algorithm>
+#include <cmath>
+
+namespace ptq {
+namespace {
+
+constexpr int WAVE_ROWS = 32;            // query rows (nodes x grouped heads) of a wave
+constexpr int WAVES = 4;
+constexpr int NODES = TREE_NODES;
+// Words of a node's line of keys: 64 ones for what comes before the tree, then
+// a bit for each node (its ancestors and itself), then 64 zeros.
+constexpr int WORDS = 2 + NODES / 32 + 2;
+
+struct TreeArgs {
+    Ragged g;                             // g.starts: the lengths
+    const int32_t* parents;
+    const int32_t* table; int64_t width;
+    int heads, kv_heads, group, bs, bs_log2;
+    int64_t num_blocks;
+    const int8_t* k; const int8_t* v; const float* ks; const float* vs;
+    const void* Q; int64_t ldq;
+    void* O; int64_t ldo;
+    float* lse;                    // [rows, heads] or null
+    float scale2;                  // softmax scale * log2(e)
+    int64_t window;
+    int nsplit;
+    float* part; float* part_lse;  // [nsplit][rows * heads][dim], [nsplit][rows * heads]
+};
+
+// One tile of query rows: flat rows f0 .. f0 + tr of sequence b, flat row =
+// node * group + head within the group.
+struct TreeTile {
+    int b;
+    int64_t off;           // first row of the sequence
+    int nodes, rows;       // nodes, and flat rows, of the sequence
+    int f0;
+    int base, end;         // keys before the tree; end of the keys that a row of the tile attends to
+    int it0, it1;          // steps of tk keys that some row of the tile attends to
+    bool bad;              // longer than its row of the table can hold, or more nodes than a line has: NaN
+};
+
+__device__ __forceinline__ bool find_tile(const TreeArgs& a, int64_t unit, int tr, int tk, TreeTile& t) {
+    const RaggedUnit u = ragged_find(a.g, unit, a.group, tr, 1);
+    t.b = u.b;
+    t.off = u.off;
+    const int64_t rows = u.rows * a.group, f0 = u.local * tr;
+    if (u.rows <= 0 || f0 >= rows) return false;
+    t.nodes = (int)u.rows;
+    t.rows = (int)rows;
+    t.f0 = (int)f0;
+    const int64_t len = std::max(u.start, 0), base = std::max<int64_t>(len - u.rows, 0);
+    t.bad = len > a.width * a.bs || len < u.rows || u.rows > NODES;
+    t.base = (int)base;
+    t.end = (int)std::min<int64_t>(base + std::min<int64_t>(f0 + tr - 1, rows - 1) / a.group + 1, len);
+    const int64_t lo = a.window > 0 ? std::max<int64_t>(0, base - a.window + 1) : 0;      // of the root, the lowest
+    t.it0 = (int)(lo / tk);
+    t.it1 = t.bad ? t.it0 : (t.end + tk - 1) / tk;
+    return true;
+}
+
+// Steps of a split of a tile: an even share, but not so few that the start of a
+// workgroup and the join would outweigh them.
+__device__ __forceinline__ int split_steps(const TreeTile& t, int nsplit) {
+    return std::max(4, (t.it1 - t.it0 + nsplit - 1) / nsplit);
+}
+
+// 16 elements of a row
+__device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
+    load8(p, *(float (*)[8])&v[0]);
+    load8(p + 8, *(float (*)[8])&v[8]);
+}
+__device__ __forceinline__ void load16(const uint16_t* p, float (&v)[16]) {
+    load8(p, *(float (*)[8])&v[0]);
+    load8(p + 8, *(float (*)[8])&v[8]);
+}
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+// One query row as NT terms of 7 bits and a factor: q = factor sum_t term_t 2^(7 (NT - 1 - t)). Lane half hf holds
+// channels 32 c + 16 hf .. + 15 of fragment c; the two lanes that differ in bit 5 share the row. The sign of the softmax
+// scale goes into the terms. A row with a NaN or an infinity gets the factor NaN.
+template <typename T, int NC, int NT>
+__device__ __forceinline__ float load_query(const T* p, float scale2, i32x4 (&q)[NT][NC]) {
+    const int hf = (threadIdx.x >> 5) & 1;
+    float x[NC][16], m = 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        load16(p + 32 * c + 16 * hf, x[c]);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) m = amax_acc(m, x[c][k]);
+    }
+    m = amax_acc(m, __shfl_xor(m, 32, 64));
+    constexpr float LARGEST = NT == 2 ? 127 * 128 : 127 * 128 * 128;
+    const float up = m < 0x1p-100f ? 0x1p100f : 1.f;       // 1 / m is finite
+    const bool fine = m <= FLT_MAX;
+    const float inv = fine && m > 0.f ? __fdiv_rn(scale2 < 0.f ? -LARGEST : LARGEST, m * up) : 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            uint32_t d[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) d[t] = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                int n = fine ? (int)rintf(x[c][4 * w + k] * up * inv) : 0;
+#pragma unroll
+                for (int t = NT - 1; t > 0; --t) {
+                    const int low = ((n + 64) & 127) - 64;
+                    d[t] |= (uint32_t)(uint8_t)low << (8 * k);
+                    n = (n - low) >> 7;
+                }
+                d[0] |= (uint32_t)(uint8_t)n << (8 * k);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) q[t][c][w] = (int)d[t];
+        }
+    return fine ? fabsf(scale2) * (__fdiv_rn(m * up, LARGEST) * (up == 1.f ? 1.f : 0x1p-100f)) : __builtin_nanf("");
+}
+
+// A wave takes 32 query rows; RG waves of a workgroup share the keys, and the
+// 4 / RG groups of RG waves take every (4 / RG)-th step of 64 keys. Scores are
+// computed transposed, S^T = K Q^T, so that a lane ends up with scores of one
+// row and the probabilities are already the operand of O^T = V^T P^T: operand
+// row r of a block of 32 keys is key 16 (r / 4 % 2) + 4 (r / 8) + r % 4, so lane
+// half hf holds keys 16 hf .. 16 hf + 15, in one block of the cache.
+// A step is 64 keys, or 32 where 64 do not fit the registers of the waves that a
+// SIMD shall hold.
+template <typename T>
+constexpr int blocks_of(int dim) { return dim <= (sizeof(T) == 4 ? 64 : 128) ? 2 : 1; }
+constexpr int waves_of(int dim) { return dim <= 128 ? 2 : 1; }
+template <int D, int U>
+struct TreeCodes {
+    uint4 k[U][D / 32], v[U][D / 32];
+    float sk[U], sv[U];
+};
+
+template <typename T, int D, int RG>
+__global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel(TreeArgs a) {
+    constexpr int U = blocks_of<T>(D), TK = 32 * U;
+    constexpr int NQ = sizeof(T) == 4 ? 3 : 2;    // int8 terms of q
+    constexpr int NT = sizeof(T) == 4 ? 2 : 1;    // fp16 terms of the probabilities
+    constexpr int NC = D / 32, TG = WAVES / RG, ROWS = WAVE_ROWS * RG;
+    __shared__ uint32_t line[ROWS][WORDS + 1];      // an odd stride
+    __shared__ int16_t parent[NODES], level[ROWS];      // level: depth of a node, negative: no valid way up
+
+    const int split = (int)(blockIdx.x % (unsigned)a.nsplit);
+    const int64_t tile = blockIdx.x / (unsigned)a.nsplit;
+    const int h = (int)(tile % a.kv_heads);
+    TreeTile tl;
+    if (!find_tile(a, tile / a.kv_heads, ROWS, TK, tl)) return;
+    const int per = split_steps(tl, a.nsplit);
+    const int s0 = tl.it0 + split * per, s1 = std::min(s0 + per, tl.it1);
+    if (split > 0 && s0 >= s1) return;
+
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int rg = wave % RG, tg = wave / RG;
+    const int li = lane & 31, hf = lane >> 5;
+    const int first_node = tl.f0 / a.group;
+    auto row_of = [&](int i) { return std::min(tl.f0 + WAVE_ROWS * rg + i, tl.rows - 1); };
+    const int node = row_of(li) / a.group;
+
+    // lines of the tile's nodes, where this split has keys of the tree or a window asks for depths
+    const bool lines = !tl.bad && (a.window > 0 || s1 * TK > tl.base);
+    int lo = 0;
+    bool broken = tl.bad;
+    if (lines) {
+        for (int i = t; i < tl.nodes; i += 64 * WAVES) {
+            const int p = a.parents[tl.off + i];
+            parent[i] = (int16_t)(p >= -1 && p < NODES ? p : NODES);
+        }
+        const int count = std::min(tl.f0 + ROWS - 1, tl.rows - 1) / a.group - first_node + 1;
+        for (int i = t; i < count * WORDS; i += 64 * WAVES) line[i / WORDS][i % WORDS] = i % WORDS < 2 ? ~0u : 0u;
+        __syncthreads();
+        if (t < count) {
+            // ancestors come in falling order: a word is done when the walk leaves it
+            int j = first_node + t, depth = 0, word = j >> 5;
+            uint32_t bits = 0;
+            bool fine = true;
+            while (true) {
+                if (j >> 5 != word) {
+                    line[t][2 + word] = bits;
+                    word = j >> 5;
+                    bits = 0;
+                }
+                if (a.window <= 0 || depth < a.window) bits |= 1u << (j & 31);
+                const int p = parent[j];
+                if (p >= j) fine = false;
+                if (p >= j || p < 0) break;
+                j = p;
+                ++depth;
+            }
+            line[t][2 + word] = bits;
+            level[t] = (int16_t)(fine ? depth : -1);
+        }
+        __syncthreads();
+        const int depth = level[node - first_node];
+        broken = depth < 0;
+        // of the keys before the tree: the walk has left out the ancestors that the window does
+        if (a.window > 0)
+            lo = (int)std::min<int64_t>(tl.base, std::max<int64_t>(0, tl.base + std::max(depth, 0) - a.window + 1));
+    }
+    const int lo_max = a.window > 0 ? (int)std::max<int64_t>(0, tl.base + (int64_t)tl.nodes - a.window) : 0;   // of the deepest row
+
+    const int32_t* table = a.table + (int64_t)tl.b * a.width;
+    const int64_t pool = (int64_t)a.bs * D, stride = (int64_t)a.kv_heads * pool;
+    const int8_t* kp = a.k + (int64_t)h * pool;
+    const int8_t* vp = a.v + (int64_t)h * pool;
+    const int end = tl.end, bmask = a.bs - 1;
+    const int ktok = 16 * (li >> 2 & 1) + 4 * (li >> 3) + (li & 3), kgrp = ktok & 16, vgrp = 16 * hf;
+    // block of position p: one without a valid id, and positions past the keys, stand for some other block of the
+    // pool, whose codes are as good as any (the scale says NaN, or the mask leaves them out)
+    auto entry = [&](int p) { return table[std::min(p, end - 1) >> a.bs_log2]; };
+    auto ok = [&](int id) { return (unsigned)id < (unsigned)a.num_blocks; };
+    int idk[U] = {}, idv[U] = {};                 // of the step to load next
+    auto ids = [&](int it) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            idk[u] = entry(it * TK + 32 * u + kgrp);
+            idv[u] = entry(it * TK + 32 * u + vgrp);
+        }
+    };
+    auto load = [&](int it, TreeCodes<D, U>& c) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int tk = it * TK + 32 * u + ktok;
+            const int8_t* p = kp + (ok(idk[u]) ? idk[u] : 0) * stride + ((tk & bmask) * D + 16 * hf);
+#pragma unroll
+            for (int e = 0; e < NC; ++e) c.k[u][e] = *(const uint4*)(p + 32 * e);
+            const int tv = it * TK + 32 * u + vgrp, bv = ok(idv[u]) ? idv[u] : 0;
+            const int8_t* q = vp + bv * stride + (li * a.bs + (tv & bmask));
+#pragma unroll
+            for (int i = 0; i < NC; ++i) c.v[u][i] = *(const uint4*)(q + 32 * i * a.bs);
+            const int64_t at = (int64_t)bv * a.kv_heads + h;
+            c.sk[u] = a.ks[at];
+            c.sv[u] = a.vs[at];
+            if (!ok(idv[u])) c.sk[u] = c.sv[u] = __builtin_nanf("");
+            // infinite ones, too: times codes of one sign they would stay infinite
+            if (!(c.sk[u] < INFINITY)) c.sk[u] = __builtin_nanf("");
+            if (!(c.sv[u] < INFINITY)) c.sv[u] = __builtin_nanf("");
+            if (tv >= end) c.sk[u] = c.sv[u] = 0.f;
+        }
+    };
+
+    i32x4 q[NQ][NC];
+    f32x16 acc[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
+    float m = -INFINITY, l = broken ? __builtin_nanf("") : 0.f, R = 0.f, rcp_R = 0.f;
+    const float qs = load_query<T, NC, NQ>(
+        (const T*)a.Q + (tl.off + node) * a.ldq + (int64_t)(h * a.group + row_of(li) % a.group) * D, a.scale2, q);
+
+    auto work = [&](int it, TreeCodes<D, U>& c) {
+        const bool whole = it * TK >= lo_max && it * TK + TK <= tl.base;      // no row masks anything here
+        f32x16 s[U];
+        uint32_t seen[U];
+        float top = -INFINITY, big = 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            // the leading terms of q make one whole number below 2^30, a third one another
+            auto product = [&](int n) {
+                i32x16 x;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) x[r] = 0;
+#pragma unroll
+                for (int e = 0; e < NC; ++e) {
+                    const uint4 w = c.k[u][e];
+                    x = __builtin_amdgcn_mfma_i32_32x32x32_i8(i32x4{(int)w.x, (int)w.y, (int)w.z, (int)w.w}, q[n][e], x, 0, 0, 0);
+                }
+                return x;
+            };
+            i32x16 hi = product(0), lo_terms = product(1);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) hi[r] = hi[r] * 128 + lo_terms[r];
+            if constexpr (NQ == 3) {
+                lo_terms = product(2);
+            }
+            const float ck = c.sk[u] * qs;
+            const int tv = it * TK + 32 * u + vgrp;
+            seen[u] = 0xffffu;
+            if (!whole) {
+                const int o = std::min(std::max(tv - tl.base, -64) + 64, 32 * (WORDS - 2));      // the last two words are 0
+                const uint32_t* w = &line[node - first_node][o >> 5];
+                seen[u] = (uint32_t)((((uint64_t)w[1] << 32 | w[0]) >> (o & 31)) & 0xffffu);
+                if (tv < lo) seen[u] &= lo - tv < 16 ? 0xffffu << (lo - tv) : 0u;
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                float y = (float)hi[r];
+                if constexpr (NQ == 3) y = fmaf(y, 128.f, (float)lo_terms[r]);
+                y *= ck;
+                if (!whole && !(seen[u] >> r & 1)) y = -INFINITY;
+                s[u][r] = y;
+                top = fmaxf(top, y);
+            }
+            // R: largest finite S_v of the row's blocks so far
+            if (c.sv[u] < INFINITY && seen[u]) big = fmaxf(big, c.sv[u]);
+        }
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        big = fmaxf(big, __shfl_xor(big, 32, 64));
+        if (__any(top > m + LAZY || big > R)) {
+            // each row by itself: what one row sees changes no other row's roundings
+            float fall = 1.f;
+            if (top > m + LAZY) {
+                fall = exp2_fast(m - top);
+                m = top;
+                l *= fall;
+            }
+            if (big > R) {
+                rcp_R = big < FLT_MIN ? 0.f : __fdiv_rn(1.f, big);
+                fall *= R * rcp_R;
+                R = big;
+            }
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][r] *= fall;
+        }
+        const float m_sub = (m == -INFINITY ? 0.f : m) - PSHIFT;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float rv = c.sv[u] * rcp_R;
+            f16x8 w[NT][2];
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) {
+                const float p0 = exp2_fast(s[u][r] - m_sub), p1 = exp2_fast(s[u][r + 1] - m_sub);
+                l += p0;
+                l += p1;
+                f32x2 y = {p0 * rv, p1 * rv};
+                if (!whole) {      // S_v of a block that is not this row's may be NaN
+                    if (!(seen[u] >> r & 1)) y[0] = 0.f;
+                    if (!(seen[u] >> r & 2)) y[1] = 0.f;
+                }
+                const f16x2 x = __builtin_convertvector(y, f16x2);
+                w[0][r >> 3][r & 7] = x[0];
+                w[0][r >> 3][(r & 7) + 1] = x[1];
+                if constexpr (NT == 2) {
+                    const f16x2 z = __builtin_convertvector((f32x2{y[0] - (float)x[0], y[1] - (float)x[1]}), f16x2);
+                    w[1][r >> 3][r & 7] = z[0];
+                    w[1][r >> 3][(r & 7) + 1] = z[1];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const f16x8 v0 = half8(c.v[u][i].x, c.v[u][i].y), v1 = half8(c.v[u][i].z, c.v[u][i].w);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v0, w[n][0], acc[i], 0, 0, 0);
+                    acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1, w[n][1], acc[i], 0, 0, 0);
+                }
+            }
+        }
+    };
+
+    if (tl.f0 + WAVE_ROWS * rg < tl.rows) {
+        int it = s0 + tg;
+        if (it < s1) ids(it);
+        for (; it < s1; it += TG) {
+            TreeCodes<D, U> c;
+            load(it, c);
+            if (it + TG < s1) ids(it + TG);
+            work(it, c);
+        }
+    }
+
+    l += __shfl_xor(l, 32, 64);
+    // this lane's row is worked out again: its registers are the loop's
+    int again = li;
+    asm volatile("" : "+v"(again));
+    const int f = row_of(again), qh = h * a.group + f % a.group;
+    const bool there = tl.f0 + WAVE_ROWS * rg + again < tl.rows;
+    const int64_t token = tl.off + f / a.group;
+    const bool split_out = a.nsplit > 1;
+    const int64_t nflat = a.g.rows * a.heads, at = token * a.heads + qh;
+    float M = m, M0 = m == -INFINITY ? 0.f : m, L = l;
+    if constexpr (TG > 1) {
+        // join the groups of waves: factors to the common maximum
+        __shared__ float sm[WAVES][WAVE_ROWS], sl[WAVES][WAVE_ROWS];
+        if (hf == 0) {
+            sm[wave][li] = m;
+            sl[wave][li] = l;
+        }
+        __syncthreads();
+        M = sm[rg][li];
+#pragma unroll
+        for (int g = 1; g < TG; ++g) M = fmaxf(M, sm[rg + g * RG][li]);
+        M0 = M == -INFINITY ? 0.f : M;
+        L = 0.f;
+#pragma unroll
+        for (int g = 0; g < TG; ++g) L += sl[rg + g * RG][li] * exp2_fast(sm[rg + g * RG][li] - M0);
+    }
+    const float mine = (R > 0.f ? R : 1.f) * exp2_fast(m - M0) / (L == 0.f ? 1.f : L);
+    auto put = [&](int64_t row, int head, int d, const f32x4& o) {
+        if (split_out)
+            *(f32x4*)(a.part + (split * nflat + row * a.heads + head) * D + d) = o;
+        else
+            store4((T*)a.O + row * a.ldo + (int64_t)head * D + d, o[0], o[1], o[2], o[3]);
+    };
+    if constexpr (TG == 1) {
+        if (there)
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    put(token, qh, 32 * i + 8 * b + 4 * hf,
+                        f32x4{acc[i][4 * b] * mine, acc[i][4 * b + 1] * mine, acc[i][4 * b + 2] * mine, acc[i][4 * b + 3] * mine});
+    } else {
+        __shared__ __attribute__((aligned(16))) float so[WAVES][WAVE_ROWS][36];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            if (i) __syncthreads();
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                *(f32x4*)&so[wave][li][8 * b + 4 * hf] =
+                    f32x4{acc[i][4 * b] * mine, acc[i][4 * b + 1] * mine, acc[i][4 * b + 2] * mine, acc[i][4 * b + 3] * mine};
+            __syncthreads();
+            for (int c = t; c < ROWS * 8; c += 64 * WAVES) {
+                const int r = c / 8, d = 4 * (c % 8), fr = tl.f0 + r;
+                if (fr >= tl.rows) continue;
+                f32x4 o = *(const f32x4*)&so[r / WAVE_ROWS][r % WAVE_ROWS][d];
+#pragma unroll
+                for (int g = 1; g < TG; ++g) o += *(const f32x4*)&so[r / WAVE_ROWS + g * RG][r % WAVE_ROWS][d];
+                put(tl.off + fr / a.group, h * a.group + fr % a.group, 32 * i + d, o);
+            }
+        }
+    }
+    if (tg == 0 && hf == 0 && there && (split_out || a.lse)) {
+        // L carries 2^PSHIFT
+        const float lse2 = L == 0.f ? -INFINITY : M0 - PSHIFT + __log2f(L);
+        if (split_out)
+            a.part_lse[split * nflat + at] = lse2;
+        else
+            a.lse[at] = lse2 * 0.6931471805599453f;
+    }
+}
+
+// Join of the splits: 16 rows a workgroup, 16 threads a row, JB splits at a
+// time with all their loads at once; tr: rows of the tiles that were split.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void attention_tree_join_kernel(TreeArgs a, int tr) {
+    const int64_t part = blockIdx.x % (unsigned)(tr / 16), tile = blockIdx.x / (unsigned)(tr / 16);
+    const int h = (int)(tile % a.kv_heads);
+    TreeTile tl;
+    if (!find_tile(a, tile / a.kv_heads, tr, 32 * blocks_of<T>(D), tl)) return;
+    const int per = split_steps(tl, a.nsplit);
+    const int n = std::max(1, (tl.it1 - tl.it0 + per - 1) / per);    // split 0 is always written
+    const int r = threadIdx.x / 16, c = threadIdx.x % 16, f = tl.f0 + (int)part * 16 + r;
+    if (f >= tl.rows) return;
+    const int64_t row = tl.off + f / a.group, nflat = a.g.rows * a.heads;
+    const int head = h * a.group + f % a.group;
+    const int64_t at = row * a.heads + head;
+    constexpr int JB = 8;
+    float M = -INFINITY, M0 = 0.f, L = 0.f;
+    f32x4 o[D / 64];
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < n; s += JB) {
+        float lse[JB];
+        f32x4 v[JB][D / 64];
+#pragma unroll
+        for (int j = 0; j < JB; ++j) {
+            const int64_t from = std::min(s + j, n - 1) * nflat + at;
+            lse[j] = s + j < n ? a.part_lse[from] : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) v[j][i] = *(const f32x4*)(a.part + from * D + 64 * i + 4 * c);
+        }
+        const float before = M;
+#pragma unroll
+        for (int j = 0; j < JB; ++j) M = fmaxf(M, lse[j]);
+        M0 = M == -INFINITY ? 0.f : M;
+        const float fall = exp2_fast(before - M0);
+        L *= fall;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) o[i] *= fall;
+#pragma unroll
+        for (int j = 0; j < JB; ++j) {
+            const float w = exp2_fast(lse[j] - M0);
+            L += w;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) o[i] += (s + j < n ? w : 0.f) * v[j][i];
+        }
+    }
+    const float inv = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i)
+        store4((T*)a.O + row * a.ldo + (int64_t)head * D + 64 * i + 4 * c, o[i][0] * inv, o[i][1] * inv,
+               o[i][2] * inv, o[i][3] * inv);
+    if (a.lse && c == 0) a.lse[at] = L == 0.f ? -INFINITY : (M0 + __log2f(L)) * 0.6931471805599453f;
+}
+
+int64_t tile_units(int64_t rows, int64_t batch, int group, int tr) { return rows * group / tr + batch; }
+
+template <typename T, int D>
+int launch(const TreeArgs& a, const TreePlan& p, hipStream_t st) {
+    constexpr bool TWO = D < 256 || sizeof(T) == 2;      // fp32 at 256 channels: two row waves spill registers, four do not
+    const int rg = p.rg == 2 && !TWO ? 4 : p.rg, tr = WAVE_ROWS * rg;
+    const int64_t units = tile_units(a.g.rows, a.g.batch, a.group, tr) * a.kv_heads;
+    const dim3 grid((unsigned)(units * a.nsplit)), block(64 * WAVES);
+    if (rg == 1) {
+        hipLaunchKernelGGL((attention_tree_kernel<T, D, 1>), grid, block, 0, st, a);
+    } else if (rg == 4) {
+        hipLaunchKernelGGL((attention_tree_kernel<T, D, 4>), grid, block, 0, st, a);
+    } else if constexpr (TWO) {
+        hipLaunchKernelGGL((attention_tree_kernel<T, D, 2>), grid, block, 0, st, a);
+    }
+    PTQ_LAUNCH_CHECK();
+    if (a.nsplit > 1) {
+        hipLaunchKernelGGL((attention_tree_join_kernel<T, D>), dim3((unsigned)(units * (tr / 16))), dim3(256), 0, st, a, tr);
+        PTQ_LAUNCH_CHECK();
+    }
+    return PTQ_OK;
+}
+
+template <typename T>
+int launch_dim(const TreeArgs& a, int dim, const TreePlan& p, hipStream_t st) {
+    switch (dim) {
+        case 64: return launch<T, 64>(a, p, st);
+        case 128: return launch<T, 128>(a, p, st);
+        default: return launch<T, 256>(a, p, st);
+    }
+}
+
+}  // namespace
+
+size_t attention_tree_part_bytes(int nsplit, int64_t rows, int heads, int dim) {
+    if (nsplit == 1) return 0;
+    Sizer z;
+    z.take<float>((size_t)nsplit * rows * heads * dim);
+    z.take<float>((size_t)nsplit * rows * heads);
+    return z.bytes();
+}
+
+// Lengths are not known here: keys is the most there may be.
+TreePlan attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int block, int64_t width,
+                             int64_t window) {
+    const int group = heads / kv_heads;
+    const int64_t keys = window > 0 && window < width * block ? std::min(width * block, window + cdiv(rows, batch)) : width * block;
+    TreePlan p;
+    const int64_t each = cdiv(rows * group, batch);
+    p.rg = each <= WAVE_ROWS ? 1 : each <= 2 * WAVE_ROWS ? 2 : 4;
+    const int tr = WAVE_ROWS * p.rg;
+    const int64_t units = std::max<int64_t>({1, batch, cdiv(rows * group, tr) + (batch - 1) / 2}) * kv_heads;
+    p.nsplit = (int)std::max<int64_t>(1, std::min({cdiv(1024, units), cdiv(keys, 256), (int64_t)64}));
+    return p;
+}
+
+int run_attention_tree(const TreePlan& p, const KVCacheInt8& c, const RaggedRows& r, const int32_t* parents, int dtype,
+                       const void* Q, int64_t ldq, int heads, float scale, int64_t window, void* O, int64_t ldo,
+                       float* lse, void* ws, size_t ws_bytes, hipStream_t st) {
+    if (r.rows == 0 || r.batch == 0) return PTQ_OK;
+    TreeArgs a{};
+    a.g.offsets = r.offsets; a.g.starts = r.starts; a.g.batch = (int)r.batch; a.g.rows = r.rows;
+    a.parents = parents;
+    a.table = r.table; a.width = r.width;
+    a.heads = heads; a.kv_heads = c.heads; a.group = heads / c.heads;
+    a.bs = c.block; a.bs_log2 = __builtin_ctz((unsigned)c.block); a.num_blocks = c.num_blocks;
+    a.k = c.k; a.v = c.v; a.ks = c.k_scales; a.vs = c.v_scales;
+    a.Q = Q; a.ldq = ldq; a.O = O; a.ldo = ldo; a.lse = lse;
+    a.scale2 = (float)(scale * 1.4426950408889634);
+    a.window = window >= r.width * c.block ? 0 : window;      // as long as the longest sequence there can be: none
+    a.nsplit = p.nsplit;
+    if (a.nsplit > 1) {
+        Arena ar(ws, ws_bytes);
+        a.part = ar.take<float>((size_t)a.nsplit * r.rows * heads * c.dim);
+        a.part_lse = ar.take<float>((size_t)a.nsplit * r.rows * heads);
+    }
+    return dtype == PTQ_F32 ? launch_dim<float>(a, c.dim, p, st) : launch_dim<uint16_t>(a, c.dim, p, st);
+}
+
+}  // namespace ptq

@@ -228,6 +228,17 @@ int run_linear_int8(const void* X, int x_dtype, int64_t rows, int64_t ldx, const
                     int64_t ldb, const float* scales, int64_t out, int64_t in, const float* bias, int y_dtype, void* Y,
                     int64_t ldy, void* ws, size_t ws_bytes, hipStream_t st);
 
+// Rotary positions (rotary.hip): the first 2 n channels of a head turn in pairs,
+// (2 i, 2 i + 1) interleaved or (i, i + n), by position * freq[i].
+struct Rotary {
+    const double* freq;
+    int n;
+    int interleaved;
+    float magnitude;
+};
+int launch_rotary(const void* X, int64_t ldx, void* Y, int64_t ldy, int dtype, int64_t rows, int heads, int dim,
+                  const Rotary& p, const int32_t* positions, hipStream_t st);
+
 // Int8 key/value cache (kv_cache.hip) and attention over it (attention_int8.hip)
 struct KVCacheInt8 {
     int8_t* k; int8_t* v; float* k_scales; float* v_scales;
@@ -243,6 +254,9 @@ struct RaggedRows {
 };
 int launch_kv_write(const KVCacheInt8& c, const RaggedRows& r, int dtype, const void* K, int64_t ldk, const void* V,
                     int64_t ldv, hipStream_t st);
+// K turned on the way, by the positions of the rows (null: of their slots)
+int launch_kv_append(const KVCacheInt8& c, const RaggedRows& r, int dtype, const void* K, int64_t ldk, const void* V,
+                     int64_t ldv, const Rotary& p, const int32_t* positions, hipStream_t st);
 int launch_kv_read(const KVCacheInt8& c, const RaggedRows& r, int dtype, void* K, int64_t ldk, void* V, int64_t ldv,
                    hipStream_t st);
 // Which kernel, and how many splits of the keys.
@@ -261,5 +275,27 @@ size_t attention_int8_ws_bytes(int64_t rows, int64_t batch, int heads, int kv_he
 int run_attention_int8(const AttnPlan& p, const KVCacheInt8& c, const RaggedRows& r, int dtype, const void* Q,
                        int64_t ldq, int heads, float scale, int causal, int64_t window, void* O, int64_t ldo,
                        float* lse, void* ws, size_t ws_bytes, hipStream_t st);
+
+// Attention of trees of drafted tokens over the cache (attention_tree.hip):
+// rg waves of 32 query rows share the keys of a workgroup.
+constexpr int TREE_NODES = 512;     // of a sequence, at most
+struct TreePlan {
+    int rg, nsplit;
+};
+TreePlan attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int block, int64_t width,
+                             int64_t window);
+size_t attention_tree_part_bytes(int nsplit, int64_t rows, int heads, int dim);
+int run_attention_tree(const TreePlan& p, const KVCacheInt8& c, const RaggedRows& r, const int32_t* parents, int dtype,
+                       const void* Q, int64_t ldq, int heads, float scale, int64_t window, void* O, int64_t ldo,
+                       float* lse, void* ws, size_t ws_bytes, hipStream_t st);
+
+// Which drafted tokens are kept (verify.hip)
+struct Drafts {
+    int64_t rows, batch;
+    const int32_t* tokens; const int32_t* parents; const int32_t* offsets;
+    const float* u; const float* r;
+};
+int launch_verify_drafts(const void* P, int64_t ldp, const void* Q, int64_t ldq, int dtype, int64_t vocab,
+                         const Drafts& d, int32_t* path, int32_t* counts, int32_t* next, hipStream_t st);
 
 }  // namespace ptq

@@ -85,6 +85,15 @@ __device__ __forceinline__ void store4(float* p, float a, float b, float c, floa
 __device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, float d) {
     *(uint2*)p = make_uint2(bf16_pair(a, b), bf16_pair(c, d));
 }
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+    store4(p, v[0], v[1], v[2], v[3]);
+    store4(p + 4, v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
+    *(uint4*)p = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+}
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(uint16_t* p, float v) { *p = (uint16_t)bf16_of(v); }
 
 // ----------------------------------------------------------- ragged batch --
 // Sequence b of a ragged batch owns rows offsets[b] .. offsets[b + 1], and has

@@ -12,7 +12,10 @@
 // recoded, rint(c (S_old / S)), and the new values get rint(x / S)
 // ("int8.hpp"). One workgroup owns a (block, head) pair, so nothing is
 // summed or raced over, and the same call twice leaves the same cache.
-#include "int8.hpp"
+//
+// Appending with rotary positions is the same write of keys that turn on the
+// way (rotary.hpp), in fp32: they are not rounded before they are quantized.
+#include "rotary.hpp"
 
 namespace ptq {
 namespace {
@@ -89,11 +92,24 @@ __device__ __forceinline__ HeadThreads head_threads(const CacheArgs& a, int per)
     return x;
 }
 
-// grid (units, groups of heads, 2): z = 0 keys, 1 values
-template <typename T>
+// A thread's chunks of K where pairs turn: the two chunks of 8 channels that
+// hold 8 pairs, or two neighbours past the pairs, so that a sine and a cosine
+// are formed once for both. Item t of a token (0 .. dim / 16 - 1) is chunk
+// first(t) and its partner.
+template <int TURN>
+__device__ __forceinline__ int turned_chunk(int t, int n, int second) {
+    if (TURN == PAIR_HALVES && t < n / 8) return t + (second ? n / 8 : 0);
+    return 2 * t + second;
+}
+
+constexpr int NO_TURN = -1;
+
+// grid (units, groups of heads, 2): z = 0 keys, 1 values. TURN: a PairLayout, or NO_TURN
+template <typename T, int TURN>
 __global__ __launch_bounds__(sizeof(T) == 4 ? 1024 : 512) void kv_write_kernel(CacheArgs a, int per, const T* __restrict__ K, int64_t ldk,
-                                                       const T* __restrict__ V, int64_t ldv) {
+                                                       const T* __restrict__ V, int64_t ldv, RotaryArgs r) {
     constexpr int NV = write_nv<T>();
+    constexpr bool PAIRS = TURN == PAIR_HALVES || TURN == PAIR_NEIGHBOURS;
     __shared__ float red[16];
     BlockSpan s;
     if (!find_block(a.g, a.table, a.width, a.num_blocks, a.bs, blockIdx.x, s) || s.id < 0) return;
@@ -103,13 +119,59 @@ __global__ __launch_bounds__(sizeof(T) == 4 ? 1024 : 512) void kv_write_kernel(C
     const int64_t ld = val ? ldv : ldk;
     const T* X = (val ? V : K) + s.row0 * ld + (int64_t)std::min(x.h, a.heads - 1) * a.dim;
     const int cpr = a.dim / 8;
+    auto chunk_of = [&](int i) {      // chunk i of this thread: slot times cpr, and its place in the token
+        if constexpr (PAIRS) {
+            const int t = x.q + (i >> 1) * per, half = cpr / 2;
+            return t / half * cpr + turned_chunk<TURN>(t % half, r.n, i & 1);
+        }
+        return x.q + i * per;
+    };
     // all loads at once: a slot that is not the call's reads the nearest one that is (the maximum is the same)
     float v[16 * NV];      // K: [chunk][channel], V: [slot][channel]
     if (!val) {
 #pragma unroll
         for (int i = 0; i < 2 * NV; ++i) {
-            const int c = x.q + i * per, slot = std::min(std::max(c / cpr, s.lo), s.hi - 1);
+            const int c = chunk_of(i), slot = std::min(std::max(c / cpr, s.lo), s.hi - 1);
             load8(X + slot * ld + 8 * (c % cpr), *(float (*)[8])&v[8 * i]);
+        }
+        if constexpr (TURN != NO_TURN) {
+            // the turned keys of this call's slots; the others count for nothing
+            auto position = [&](int slot) { return r.positions ? r.positions[s.row0 + slot] : (int)(s.p0 + slot); };
+            if constexpr (PAIRS) {
+#pragma unroll
+                for (int i = 0; i < 2 * NV; i += 2) {
+                    const int c = chunk_of(i), slot = c / cpr, i0 = TURN == PAIR_HALVES ? 8 * (c % cpr) : 4 * (c % cpr);
+                    float (&p)[8] = *(float (*)[8])&v[8 * i], (&q)[8] = *(float (*)[8])&v[8 * i + 8];
+                    if (slot < s.lo || slot >= s.hi) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) p[k] = q[k] = 0.f;
+                    } else if (i0 < r.n) {
+                        turn_chunks<TURN>(r, position(slot), i0, p, q);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2 * NV; ++i) {
+                    const int c = chunk_of(i), slot = c / cpr, c0 = 8 * (c % cpr);
+                    float (&p)[8] = *(float (*)[8])&v[8 * i];
+                    if (slot < s.lo || slot >= s.hi) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) p[k] = 0.f;
+                        continue;
+                    }
+                    const int at = position(slot);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int d = c0 + k;
+                        if (d >= 2 * r.n) break;
+                        float cs, sn;
+                        turn_of(at, r.freq[d < r.n ? d : d - r.n], r.magnitude, cs, sn);
+                        float u = load_as_float(X + slot * ld, d < r.n ? d : d - r.n), w = load_as_float(X + slot * ld, d < r.n ? d + r.n : d);
+                        turn_pair(u, w, cs, sn);
+                        p[k] = d < r.n ? u : w;
+                    }
+                }
+            }
         }
     } else {
 #pragma unroll
@@ -142,7 +204,7 @@ __global__ __launch_bounds__(sizeof(T) == 4 ? 1024 : 512) void kv_write_kernel(C
     if (!val) {
 #pragma unroll
         for (int i = 0; i < 2 * NV; ++i) {
-            const int c = x.q + i * per, slot = c / cpr;
+            const int c = chunk_of(i), slot = c / cpr;
             uint2* p = (uint2*)(codes + 8 * c);
             if (slot >= s.lo && slot < s.hi) {
                 *p = int8_code8(*(float (*)[8])&v[8 * i], inv);
@@ -270,20 +332,42 @@ int block_launch(const char* fn, const KVCacheInt8& c, const RaggedRows& r, int 
 
 }  // namespace
 
+namespace {
+
+template <int TURN>
+int launch_write(const char* fn, const KVCacheInt8& c, const RaggedRows& r, int dtype, const void* K, int64_t ldk,
+                 const void* V, int64_t ldv, const RotaryArgs& rot, hipStream_t st) {
+    const CacheArgs a = cache_args(c, r);
+    Launch l;
+    PTQ_TRY(block_launch(fn, c, r, dtype == PTQ_F32 ? write_nv<float>() : write_nv<uint16_t>(), l));
+    if (dtype == PTQ_F32)
+        hipLaunchKernelGGL((kv_write_kernel<float, TURN>), l.grid, l.block, 0, st, a, l.per, (const float*)K, ldk,
+                           (const float*)V, ldv, rot);
+    else
+        hipLaunchKernelGGL((kv_write_kernel<uint16_t, TURN>), l.grid, l.block, 0, st, a, l.per, (const uint16_t*)K, ldk,
+                           (const uint16_t*)V, ldv, rot);
+    PTQ_LAUNCH_CHECK();
+    return PTQ_OK;
+}
+
+}  // namespace
+
 int launch_kv_write(const KVCacheInt8& c, const RaggedRows& r, int dtype, const void* K, int64_t ldk, const void* V,
                     int64_t ldv, hipStream_t st) {
     if (r.rows == 0 || r.batch == 0) return PTQ_OK;
-    const CacheArgs a = cache_args(c, r);
-    Launch l;
-    PTQ_TRY(block_launch("kv_cache_write_int8", c, r, dtype == PTQ_F32 ? write_nv<float>() : write_nv<uint16_t>(), l));
-    if (dtype == PTQ_F32)
-        hipLaunchKernelGGL(kv_write_kernel<float>, l.grid, l.block, 0, st, a, l.per, (const float*)K, ldk, (const float*)V,
-                           ldv);
-    else
-        hipLaunchKernelGGL(kv_write_kernel<uint16_t>, l.grid, l.block, 0, st, a, l.per, (const uint16_t*)K, ldk,
-                           (const uint16_t*)V, ldv);
-    PTQ_LAUNCH_CHECK();
-    return PTQ_OK;
+    return launch_write<NO_TURN>("kv_cache_write_int8", c, r, dtype, K, ldk, V, ldv, RotaryArgs{}, st);
+}
+
+int launch_kv_append(const KVCacheInt8& c, const RaggedRows& r, int dtype, const void* K, int64_t ldk, const void* V,
+                     int64_t ldv, const Rotary& p, const int32_t* positions, hipStream_t st) {
+    if (r.rows == 0 || r.batch == 0) return PTQ_OK;
+    const char* fn = "kv_cache_append_int8";
+    const RotaryArgs rot{p.freq, positions, p.n, p.magnitude};
+    switch (pair_layout(p.n, p.interleaved)) {
+        case PAIR_HALVES: return launch_write<PAIR_HALVES>(fn, c, r, dtype, K, ldk, V, ldv, rot, st);
+        case PAIR_NEIGHBOURS: return launch_write<PAIR_NEIGHBOURS>(fn, c, r, dtype, K, ldk, V, ldv, rot, st);
+        default: return launch_write<PAIR_ANY_HALVES>(fn, c, r, dtype, K, ldk, V, ldv, rot, st);
+    }
 }
 
 int launch_kv_read(const KVCacheInt8& c, const RaggedRows& r, int dtype, void* K, int64_t ldk, void* V, int64_t ldv,
