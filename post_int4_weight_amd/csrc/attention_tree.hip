@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 namespace ptq {
 namespace {
@@ -136,29 +137,41 @@ __device__ __forceinline__ float load_query(const T* p, float scale2, i32x4 (&q)
     return fine ? fabsf(scale2) * (__fdiv_rn(m * up, LARGEST) * (up == 1.f ? 1.f : 0x1p-100f)) : __builtin_nanf("");
 }
 
-// A wave takes 32 query rows; RG waves of a workgroup share the keys, and the
-// 4 / RG groups of RG waves take every (4 / RG)-th step of 64 keys. Scores are
-// computed transposed, S^T = K Q^T, so that a lane ends up with scores of one
-// row and the probabilities are already the operand of O^T = V^T P^T: operand
-// row r of a block of 32 keys is key 16 (r / 4 % 2) + 4 (r / 8) + r % 4, so lane
-// half hf holds keys 16 hf .. 16 hf + 15, in one block of the cache.
+// A wave takes 32 query rows. Scores are computed transposed, S^T = K Q^T, so
+// that a lane ends up with scores of one row and the probabilities are already
+// the operand of O^T = V^T P^T: operand row r of a block of 32 keys is key
+// 16 (r / 4 % 2) + 4 (r / 8) + r % 4, so lane half hf holds keys 16 hf .. 16 hf +
+// 15, in one block of the cache: one S_k and one S_v a lane.
+//
+// RG waves of a workgroup take rows that differ, and share the keys. With few
+// rows (RG < 4) the 4 / RG groups of waves take every (4 / RG)-th step, and a
+// wave loads its own operands. With four row waves the workgroup stages each
+// step in LDS, K as it is and V converted to fp16: a wave that converts V for
+// its 32 rows alone spends as much on that as on the exponentials.
+//
 // A step is 64 keys, or 32 where 64 do not fit the registers of the waves that a
 // SIMD shall hold.
-template <typename T>
+template <typename T, int RG>
 constexpr int blocks_of(int dim) { return dim <= (sizeof(T) == 4 ? 64 : 128) ? 2 : 1; }
 constexpr int waves_of(int dim) { return dim <= 128 ? 2 : 1; }
+
+// One step of keys in LDS: K in the order of the operand's rows, in chunks of 16 channels, and V in chunks of 8 keys of a
+// channel, chunk c of row r at c ^ (r % 8) (r % 4 where a row has four): 8 neighbours' chunks lie in all banks.
 template <int D, int U>
-struct TreeCodes {
-    uint4 k[U][D / 32], v[U][D / 32];
-    float sk[U], sv[U];
+struct TreeStep {
+    uint4 k[32 * U][D / 16];
+    f16x8 v[D][4 * U];
+    float scale[2 * U][4];       // of 16 keys: S_k, S_v, log2 S_v
 };
 
 template <typename T, int D, int RG>
 __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel(TreeArgs a) {
-    constexpr int U = blocks_of<T>(D), TK = 32 * U;
+    constexpr int U = blocks_of<T, RG>(D), TK = 32 * U;
     constexpr int NQ = sizeof(T) == 4 ? 3 : 2;    // int8 terms of q
     constexpr int NT = sizeof(T) == 4 ? 2 : 1;    // fp16 terms of the probabilities
-    constexpr int NC = D / 32, TG = WAVES / RG, ROWS = WAVE_ROWS * RG;
+    constexpr int NC = D / 32, TG = WAVES / RG, ROWS = WAVE_ROWS * RG, NTH = 64 * WAVES;
+    constexpr bool STAGED = RG == WAVES;
+    constexpr bool FOLD = NT == 1;       // S_v / R goes into the exponent
     __shared__ uint32_t line[ROWS][WORDS + 1];      // an odd stride
     __shared__ int16_t parent[NODES], level[ROWS];      // level: depth of a node, negative: no valid way up
 
@@ -183,12 +196,12 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
     int lo = 0;
     bool broken = tl.bad;
     if (lines) {
-        for (int i = t; i < tl.nodes; i += 64 * WAVES) {
+        for (int i = t; i < tl.nodes; i += NTH) {
             const int p = a.parents[tl.off + i];
             parent[i] = (int16_t)(p >= -1 && p < NODES ? p : NODES);
         }
         const int count = std::min(tl.f0 + ROWS - 1, tl.rows - 1) / a.group - first_node + 1;
-        for (int i = t; i < count * WORDS; i += 64 * WAVES) line[i / WORDS][i % WORDS] = i % WORDS < 2 ? ~0u : 0u;
+        for (int i = t; i < count * WORDS; i += NTH) line[i / WORDS][i % WORDS] = i % WORDS < 2 ? ~0u : 0u;
         __syncthreads();
         if (t < count) {
             // ancestors come in falling order: a word is done when the walk leaves it
@@ -219,46 +232,22 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
             lo = (int)std::min<int64_t>(tl.base, std::max<int64_t>(0, tl.base + std::max(depth, 0) - a.window + 1));
     }
     const int lo_max = a.window > 0 ? (int)std::max<int64_t>(0, tl.base + (int64_t)tl.nodes - a.window) : 0;   // of the deepest row
+    // steps that no row masks: [whole, last)
+    const int whole = std::min(__builtin_amdgcn_readfirstlane((lo_max + TK - 1) / TK), s1);
+    const int last = std::min(__builtin_amdgcn_readfirstlane(tl.base / TK), s1);
 
     const int32_t* table = a.table + (int64_t)tl.b * a.width;
     const int64_t pool = (int64_t)a.bs * D, stride = (int64_t)a.kv_heads * pool;
     const int8_t* kp = a.k + (int64_t)h * pool;
     const int8_t* vp = a.v + (int64_t)h * pool;
     const int end = tl.end, bmask = a.bs - 1;
-    const int ktok = 16 * (li >> 2 & 1) + 4 * (li >> 3) + (li & 3), kgrp = ktok & 16, vgrp = 16 * hf;
     // block of position p: one without a valid id, and positions past the keys, stand for some other block of the
     // pool, whose codes are as good as any (the scale says NaN, or the mask leaves them out)
     auto entry = [&](int p) { return table[std::min(p, end - 1) >> a.bs_log2]; };
     auto ok = [&](int id) { return (unsigned)id < (unsigned)a.num_blocks; };
-    int idk[U] = {}, idv[U] = {};                 // of the step to load next
-    auto ids = [&](int it) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            idk[u] = entry(it * TK + 32 * u + kgrp);
-            idv[u] = entry(it * TK + 32 * u + vgrp);
-        }
-    };
-    auto load = [&](int it, TreeCodes<D, U>& c) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int tk = it * TK + 32 * u + ktok;
-            const int8_t* p = kp + (ok(idk[u]) ? idk[u] : 0) * stride + ((tk & bmask) * D + 16 * hf);
-#pragma unroll
-            for (int e = 0; e < NC; ++e) c.k[u][e] = *(const uint4*)(p + 32 * e);
-            const int tv = it * TK + 32 * u + vgrp, bv = ok(idv[u]) ? idv[u] : 0;
-            const int8_t* q = vp + bv * stride + (li * a.bs + (tv & bmask));
-#pragma unroll
-            for (int i = 0; i < NC; ++i) c.v[u][i] = *(const uint4*)(q + 32 * i * a.bs);
-            const int64_t at = (int64_t)bv * a.kv_heads + h;
-            c.sk[u] = a.ks[at];
-            c.sv[u] = a.vs[at];
-            if (!ok(idv[u])) c.sk[u] = c.sv[u] = __builtin_nanf("");
-            // infinite ones, too: times codes of one sign they would stay infinite
-            if (!(c.sk[u] < INFINITY)) c.sk[u] = __builtin_nanf("");
-            if (!(c.sv[u] < INFINITY)) c.sv[u] = __builtin_nanf("");
-            if (tv >= end) c.sk[u] = c.sv[u] = 0.f;
-        }
-    };
+    // infinite scales, too, count as NaN: times codes of one sign they would stay infinite
+    auto clean = [&](float s, int id, int p) { return p >= end ? 0.f : ok(id) && s < INFINITY ? s : __builtin_nanf(""); };
+    auto key_of_row = [](int r) { return 16 * (r >> 2 & 1) + 4 * (r >> 3) + (r & 3); };      // r < 32
 
     i32x4 q[NQ][NC];
     f32x16 acc[NC];
@@ -266,58 +255,60 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
     for (int i = 0; i < NC; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
-    float m = -INFINITY, l = broken ? __builtin_nanf("") : 0.f, R = 0.f, rcp_R = 0.f;
+    // ref: what the scores' maximum m stands for in the exponents
+    float m = -INFINITY, l = broken ? __builtin_nanf("") : 0.f, R = 0.f, rcp_R = 0.f, log2_R = 0.f, poison = 0.f;
     const float qs = load_query<T, NC, NQ>(
         (const T*)a.Q + (tl.off + node) * a.ldq + (int64_t)(h * a.group + row_of(li) % a.group) * D, a.scale2, q);
 
-    auto work = [&](int it, TreeCodes<D, U>& c) {
-        const bool whole = it * TK >= lo_max && it * TK + TK <= tl.base;      // no row masks anything here
+    // One step. kf(u, e): codes of K, operand e of block u; vf(u, i, j): V of keys 8 j .. of the lane's 16, channels 32 i ..;
+    // sk, sv, lv: S_k, S_v and log2 S_v of the lane's keys of each block
+    auto work = [&](auto masked, int it, auto&& kf, auto&& vf, const float (&sk)[U], const float (&sv)[U],
+                    const float (&lv)[U]) __attribute__((always_inline)) {
+        constexpr bool MASK = decltype(masked)::value;
         f32x16 s[U];
         uint32_t seen[U];
-        float top = -INFINITY, big = 0.f;
+        float ck[U], top = -INFINITY, big = 0.f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             // the leading terms of q make one whole number below 2^30, a third one another
-            auto product = [&](int n) {
-                i32x16 x;
+            i32x16 x[NQ];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) x[r] = 0;
+            for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                for (int e = 0; e < NC; ++e) {
-                    const uint4 w = c.k[u][e];
-                    x = __builtin_amdgcn_mfma_i32_32x32x32_i8(i32x4{(int)w.x, (int)w.y, (int)w.z, (int)w.w}, q[n][e], x, 0, 0, 0);
-                }
-                return x;
-            };
-            i32x16 hi = product(0), lo_terms = product(1);
+                for (int r = 0; r < 16; ++r) x[n][r] = 0;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) hi[r] = hi[r] * 128 + lo_terms[r];
-            if constexpr (NQ == 3) {
-                lo_terms = product(2);
+            for (int e = 0; e < NC; ++e) {
+                const i32x4 k = kf(u, e);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) x[n] = __builtin_amdgcn_mfma_i32_32x32x32_i8(k, q[n][e], x[n], 0, 0, 0);
             }
-            const float ck = c.sk[u] * qs;
-            const int tv = it * TK + 32 * u + vgrp;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[u][r] = (float)(x[0][r] * 128 + x[1][r]);
+                if constexpr (NQ == 3) s[u][r] = fmaf(s[u][r], 128.f, (float)x[NQ - 1][r]);
+            }
+            ck[u] = sk[u] * qs;
             seen[u] = 0xffffu;
-            if (!whole) {
+            if constexpr (MASK) {
+                const int tv = it * TK + 32 * u + 16 * hf;
                 const int o = std::min(std::max(tv - tl.base, -64) + 64, 32 * (WORDS - 2));      // the last two words are 0
                 const uint32_t* w = &line[node - first_node][o >> 5];
                 seen[u] = (uint32_t)((((uint64_t)w[1] << 32 | w[0]) >> (o & 31)) & 0xffffu);
                 if (tv < lo) seen[u] &= lo - tv < 16 ? 0xffffu << (lo - tv) : 0u;
-            }
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                float y = (float)hi[r];
-                if constexpr (NQ == 3) y = fmaf(y, 128.f, (float)lo_terms[r]);
-                y *= ck;
-                if (!whole && !(seen[u] >> r & 1)) y = -INFINITY;
-                s[u][r] = y;
-                top = fmaxf(top, y);
+                for (int r = 0; r < 16; ++r) s[u][r] = seen[u] >> r & 1 ? s[u][r] * ck[u] : -INFINITY;
+                ck[u] = 1.f;
             }
+            float most = s[u][0];
+#pragma unroll
+            for (int r = 1; r < 16; ++r) most = fmaxf(most, s[u][r]);
+            top = fmaxf(top, most * ck[u]);
             // R: largest finite S_v of the row's blocks so far
-            if (c.sv[u] < INFINITY && seen[u]) big = fmaxf(big, c.sv[u]);
+            if (sv[u] < INFINITY && (!MASK || seen[u])) big = fmaxf(big, sv[u]);
+            if (FOLD && sv[u] != sv[u] && (!MASK || seen[u])) poison = sv[u];
         }
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        big = fmaxf(big, __shfl_xor(big, 32, 64));
+        top = max_halves(top);
+        big = max_halves(big);
         if (__any(top > m + LAZY || big > R)) {
             // each row by itself: what one row sees changes no other row's roundings
             float fall = 1.f;
@@ -330,6 +321,7 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
                 rcp_R = big < FLT_MIN ? 0.f : __fdiv_rn(1.f, big);
                 fall *= R * rcp_R;
                 R = big;
+                log2_R = big < FLT_MIN ? 0.f : __builtin_amdgcn_logf(big);
             }
 #pragma unroll
             for (int i = 0; i < NC; ++i)
@@ -339,17 +331,25 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
         const float m_sub = (m == -INFINITY ? 0.f : m) - PSHIFT;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float rv = c.sv[u] * rcp_R;
+            const float rv = sv[u] * rcp_R, lr = FOLD ? fmaxf(lv[u] - log2_R, LOG2_RV_MIN) : 0.f;      // of NaN, too
+            const float off = m_sub - lr;
+            float sum = 0.f;
             f16x8 w[NT][2];
 #pragma unroll
             for (int r = 0; r < 16; r += 2) {
-                const float p0 = exp2_fast(s[u][r] - m_sub), p1 = exp2_fast(s[u][r + 1] - m_sub);
-                l += p0;
-                l += p1;
-                f32x2 y = {p0 * rv, p1 * rv};
-                if (!whole) {      // S_v of a block that is not this row's may be NaN
-                    if (!(seen[u] >> r & 1)) y[0] = 0.f;
-                    if (!(seen[u] >> r & 2)) y[1] = 0.f;
+                f32x2 y;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float p = exp2_fast(fmaf(s[u][r + k], ck[u], -off));
+                    const bool in = !MASK || (seen[u] >> (r + k) & 1);      // S_v of a block that is not this row's may be NaN
+                    if constexpr (FOLD) {
+                        if (!in) p = 0.f;
+                        sum += p;
+                        y[k] = p;
+                    } else {
+                        sum += p;
+                        y[k] = in ? p * rv : 0.f;
+                    }
                 }
                 const f16x2 x = __builtin_convertvector(y, f16x2);
                 w[0][r >> 3][r & 7] = x[0];
@@ -360,30 +360,151 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
                     w[1][r >> 3][(r & 7) + 1] = z[1];
                 }
             }
+            l += FOLD ? sum * exp2_fast(-lr) : sum;
 #pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                const f16x8 v0 = half8(c.v[u][i].x, c.v[u][i].y), v1 = half8(c.v[u][i].z, c.v[u][i].w);
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v0, w[n][0], acc[i], 0, 0, 0);
-                    acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1, w[n][1], acc[i], 0, 0, 0);
+                for (int i = 0; i < NC; ++i) {
+                    const f16x8 v = vf(u, i, j);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[n][j], acc[i], 0, 0, 0);
                 }
-            }
         }
     };
+    const bool busy = tl.f0 + WAVE_ROWS * rg < tl.rows;      // some row is this wave's
 
-    if (tl.f0 + WAVE_ROWS * rg < tl.rows) {
-        int it = s0 + tg;
-        if (it < s1) ids(it);
-        for (; it < s1; it += TG) {
-            TreeCodes<D, U> c;
-            load(it, c);
+    if constexpr (STAGED) {
+        using Step = TreeStep<D, U>;
+        __shared__ __attribute__((aligned(16))) Step step[2];
+        constexpr int KC = D / 16, VC = 2 * U;                       // chunks of a row of K, groups of 16 keys of a channel of V
+        constexpr int KN = 32 * U * KC / NTH, VN = D * VC / NTH;     // chunks of a thread
+        static_assert(KN * NTH == 32 * U * KC && VN * NTH == D * VC && NTH % (32 * U * KC / KN) == 0, "whole shares");
+        constexpr int KM = KC < 8 ? KC - 1 : 7, VM = 4 * U < 8 ? 4 * U - 1 : 7;
+        // chunk i of K of this thread: row t / KC + i NTH / KC; of V: group t % VC, channel t / VC + i NTH / VC
+        const int kc = t % KC, kr = t / KC, vg = t % VC, vd = t / VC;
+        auto krow = [&](int i) { return kr + i * (NTH / KC); };
+        auto kkey = [&](int i) { return (krow(i) & ~31) + key_of_row(krow(i) & 31); };
+        uint4 rk[KN], rv[VN];
+        float rsk = 0.f, rsv = 0.f;
+        int idk[KN], idv, ids_of = 0;       // blocks of the step to fetch next; idv of the step in registers
+        auto ids = [&](int it) {
+#pragma unroll
+            for (int i = 0; i < KN; ++i) idk[i] = entry(it * TK + kkey(i));
+            idv = entry(it * TK + 16 * vg);
+        };
+        auto fetch = [&](int it) {
+#pragma unroll
+            for (int i = 0; i < KN; ++i) {
+                const int p = it * TK + kkey(i);
+                rk[i] = *(const uint4*)(kp + (ok(idk[i]) ? idk[i] : 0) * stride + ((p & bmask) * D + 16 * kc));
+            }
+            const int p = it * TK + 16 * vg;
+            const int64_t id = ok(idv) ? idv : 0;
+#pragma unroll
+            for (int i = 0; i < VN; ++i)
+                rv[i] = *(const uint4*)(vp + id * stride + ((vd + i * (NTH / VC)) * a.bs + (p & bmask)));
+            rsk = a.ks[id * a.kv_heads + h];
+            rsv = a.vs[id * a.kv_heads + h];
+            ids_of = idv;
+        };
+        auto stage = [&](int it) {
+            Step& to = step[it & 1];
+#pragma unroll
+            for (int i = 0; i < KN; ++i) to.k[krow(i)][kc ^ (krow(i) & KM)] = rk[i];
+#pragma unroll
+            for (int i = 0; i < VN; ++i) {
+                const int d = vd + i * (NTH / VC);
+                to.v[d][(2 * vg) ^ (d & VM)] = half8(rv[i].x, rv[i].y);
+                to.v[d][(2 * vg + 1) ^ (d & VM)] = half8(rv[i].z, rv[i].w);
+            }
+            if (t < VC) {
+                const float sv = clean(rsv, ids_of, it * TK + 16 * vg);
+                *(f32x4*)to.scale[t] = f32x4{clean(rsk, ids_of, it * TK + 16 * vg), sv, __builtin_amdgcn_logf(sv), 0.f};
+            }
+        };
+        // Step it finds its keys in LDS; those of it + 1 are in registers or on their way, the ids of it + 2 known.
+        auto turn = [&](auto masked, int it) __attribute__((always_inline)) {
+            __syncthreads();
+            if (it + 1 < s1) {
+                stage(it + 1);
+                if (it + 2 < s1) {
+                    fetch(it + 2);
+                    ids(std::min(it + 3, s1 - 1));
+                }
+            }
+            if (!busy) return;
+            const Step& from = step[it & 1];
+            float sk[U], sv[U], lv[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const f32x4 x = *(const f32x4*)from.scale[2 * u + hf];
+                sk[u] = x[0], sv[u] = x[1], lv[u] = x[2];
+            }
+            work(masked, it,
+                 [&](int u, int e) {
+                     const uint4 w = from.k[32 * u + li][(2 * e + hf) ^ (li & KM)];
+                     return i32x4{(int)w.x, (int)w.y, (int)w.z, (int)w.w};
+                 },
+                 [&](int u, int i, int j) { return from.v[32 * i + li][(4 * u + 2 * hf + j) ^ (li & VM)]; }, sk, sv, lv);
+        };
+        int it = s0;
+        if (it < s1) {
+            ids(it);
+            fetch(it);
+            ids(std::min(it + 1, s1 - 1));
+            stage(it);
+            if (it + 1 < s1) {
+                fetch(it + 1);
+                ids(std::min(it + 2, s1 - 1));
+            }
+        }
+        for (; it < whole; ++it) turn(std::true_type{}, it);
+        for (; it < last; ++it) turn(std::false_type{}, it);
+        for (; it < s1; ++it) turn(std::true_type{}, it);
+    } else {
+        // operands straight from the cache, everything of a step requested at once; block ids a step early
+        const int key = key_of_row(li);
+        int idk[U], idv[U];
+        auto ids = [&](int it) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                idk[u] = entry(it * TK + 32 * u + (key & 16));
+                idv[u] = entry(it * TK + 32 * u + 16 * hf);
+            }
+        };
+        auto turn = [&](auto masked, int it) __attribute__((always_inline)) {
+            uint4 k[U][NC], v[U][NC];
+            float sk[U], sv[U], lv[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int8_t* p = kp + (ok(idk[u]) ? idk[u] : 0) * stride + (((it * TK + 32 * u + key) & bmask) * D + 16 * hf);
+#pragma unroll
+                for (int e = 0; e < NC; ++e) k[u][e] = *(const uint4*)(p + 32 * e);
+                const int tv = it * TK + 32 * u + 16 * hf;
+                const int64_t id = ok(idv[u]) ? idv[u] : 0;
+                const int8_t* x = vp + id * stride + (li * a.bs + (tv & bmask));
+#pragma unroll
+                for (int i = 0; i < NC; ++i) v[u][i] = *(const uint4*)(x + 32 * i * a.bs);
+                sk[u] = clean(a.ks[id * a.kv_heads + h], idv[u], tv);
+                sv[u] = clean(a.vs[id * a.kv_heads + h], idv[u], tv);
+                lv[u] = FOLD ? __builtin_amdgcn_logf(sv[u]) : 0.f;
+            }
             if (it + TG < s1) ids(it + TG);
-            work(it, c);
+            work(masked, it,
+                 [&](int u, int e) { return i32x4{(int)k[u][e].x, (int)k[u][e].y, (int)k[u][e].z, (int)k[u][e].w}; },
+                 [&](int u, int i, int j) { return j ? half8(v[u][i].z, v[u][i].w) : half8(v[u][i].x, v[u][i].y); }, sk, sv, lv);
+        };
+        int it = s0 + tg;
+        if (busy && it < s1) {
+            ids(it);
+            for (; it < whole; it += TG) turn(std::true_type{}, it);
+            for (; it < last; it += TG) turn(std::false_type{}, it);
+            for (; it < s1; it += TG) turn(std::true_type{}, it);
         }
     }
 
     l += __shfl_xor(l, 32, 64);
+    if (FOLD) poison += __shfl_xor(poison, 32, 64);
     // this lane's row is worked out again: its registers are the loop's
     int again = li;
     asm volatile("" : "+v"(again));
@@ -409,32 +530,31 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
 #pragma unroll
         for (int g = 0; g < TG; ++g) L += sl[rg + g * RG][li] * exp2_fast(sm[rg + g * RG][li] - M0);
     }
-    const float mine = (R > 0.f ? R : 1.f) * exp2_fast(m - M0) / (L == 0.f ? 1.f : L);
+    const float mine = (R > 0.f ? R : 1.f) * exp2_fast(m - M0) / (L == 0.f ? 1.f : L) + poison;
     auto put = [&](int64_t row, int head, int d, const f32x4& o) {
         if (split_out)
             *(f32x4*)(a.part + (split * nflat + row * a.heads + head) * D + d) = o;
         else
             store4((T*)a.O + row * a.ldo + (int64_t)head * D + d, o[0], o[1], o[2], o[3]);
     };
+    auto channels = [&](int i, int b) {
+        return f32x4{acc[i][4 * b] * mine, acc[i][4 * b + 1] * mine, acc[i][4 * b + 2] * mine, acc[i][4 * b + 3] * mine};
+    };
     if constexpr (TG == 1) {
         if (there)
 #pragma unroll
             for (int i = 0; i < NC; ++i)
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    put(token, qh, 32 * i + 8 * b + 4 * hf,
-                        f32x4{acc[i][4 * b] * mine, acc[i][4 * b + 1] * mine, acc[i][4 * b + 2] * mine, acc[i][4 * b + 3] * mine});
+                for (int b = 0; b < 4; ++b) put(token, qh, 32 * i + 8 * b + 4 * hf, channels(i, b));
     } else {
         __shared__ __attribute__((aligned(16))) float so[WAVES][WAVE_ROWS][36];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             if (i) __syncthreads();
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-                *(f32x4*)&so[wave][li][8 * b + 4 * hf] =
-                    f32x4{acc[i][4 * b] * mine, acc[i][4 * b + 1] * mine, acc[i][4 * b + 2] * mine, acc[i][4 * b + 3] * mine};
+            for (int b = 0; b < 4; ++b) *(f32x4*)&so[wave][li][8 * b + 4 * hf] = channels(i, b);
             __syncthreads();
-            for (int c = t; c < ROWS * 8; c += 64 * WAVES) {
+            for (int c = t; c < ROWS * 8; c += NTH) {
                 const int r = c / 8, d = 4 * (c % 8), fr = tl.f0 + r;
                 if (fr >= tl.rows) continue;
                 f32x4 o = *(const f32x4*)&so[r / WAVE_ROWS][r % WAVE_ROWS][d];
@@ -456,12 +576,13 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
 
 // Join of the splits: 16 rows a workgroup, 16 threads a row, JB splits at a
 // time with all their loads at once; tr: rows of the tiles that were split.
-template <typename T, int D>
-__global__ __launch_bounds__(256) void attention_tree_join_kernel(TreeArgs a, int tr) {
+template <typename T, int D, int RG>
+__global__ __launch_bounds__(256) void attention_tree_join_kernel(TreeArgs a) {
+    constexpr int tr = WAVE_ROWS * RG, TK = 32 * blocks_of<T, RG>(D);
     const int64_t part = blockIdx.x % (unsigned)(tr / 16), tile = blockIdx.x / (unsigned)(tr / 16);
     const int h = (int)(tile % a.kv_heads);
     TreeTile tl;
-    if (!find_tile(a, tile / a.kv_heads, tr, 32 * blocks_of<T>(D), tl)) return;
+    if (!find_tile(a, tile / a.kv_heads, tr, TK, tl)) return;
     const int per = split_steps(tl, a.nsplit);
     const int n = std::max(1, (tl.it1 - tl.it0 + per - 1) / per);    // split 0 is always written
     const int r = threadIdx.x / 16, c = threadIdx.x % 16, f = tl.f0 + (int)part * 16 + r;
@@ -510,25 +631,25 @@ __global__ __launch_bounds__(256) void attention_tree_join_kernel(TreeArgs a, in
 
 int64_t tile_units(int64_t rows, int64_t batch, int group, int tr) { return rows * group / tr + batch; }
 
-template <typename T, int D>
-int launch(const TreeArgs& a, const TreePlan& p, hipStream_t st) {
-    constexpr bool TWO = D < 256 || sizeof(T) == 2;      // fp32 at 256 channels: two row waves spill registers, four do not
-    const int rg = p.rg == 2 && !TWO ? 4 : p.rg, tr = WAVE_ROWS * rg;
+template <typename T, int D, int RG>
+int launch_tiles(const TreeArgs& a, hipStream_t st) {
+    const int tr = WAVE_ROWS * RG;
     const int64_t units = tile_units(a.g.rows, a.g.batch, a.group, tr) * a.kv_heads;
-    const dim3 grid((unsigned)(units * a.nsplit)), block(64 * WAVES);
-    if (rg == 1) {
-        hipLaunchKernelGGL((attention_tree_kernel<T, D, 1>), grid, block, 0, st, a);
-    } else if (rg == 4) {
-        hipLaunchKernelGGL((attention_tree_kernel<T, D, 4>), grid, block, 0, st, a);
-    } else if constexpr (TWO) {
-        hipLaunchKernelGGL((attention_tree_kernel<T, D, 2>), grid, block, 0, st, a);
-    }
+    hipLaunchKernelGGL((attention_tree_kernel<T, D, RG>), dim3((unsigned)(units * a.nsplit)), dim3(64 * WAVES), 0, st, a);
     PTQ_LAUNCH_CHECK();
     if (a.nsplit > 1) {
-        hipLaunchKernelGGL((attention_tree_join_kernel<T, D>), dim3((unsigned)(units * (tr / 16))), dim3(256), 0, st, a, tr);
+        hipLaunchKernelGGL((attention_tree_join_kernel<T, D, RG>), dim3((unsigned)(units * (tr / 16))), dim3(256), 0, st, a);
         PTQ_LAUNCH_CHECK();
     }
     return PTQ_OK;
+}
+
+template <typename T, int D>
+int launch(const TreeArgs& a, const TreePlan& p, hipStream_t st) {
+    if (p.rg == 1) return launch_tiles<T, D, 1>(a, st);
+    if constexpr (D < 256 || sizeof(T) == 2)      // fp32 at 256 channels: two row waves would spill registers
+        if (p.rg == 2) return launch_tiles<T, D, 2>(a, st);
+    return launch_tiles<T, D, 4>(a, st);
 }
 
 template <typename T>
