@@ -187,7 +187,7 @@ int attention_tree(const char* fn, const TreePlan* given, const KVCacheInt8& c, 
     PTQ_TRY(check_float_rows(fn, "Q", Q, dtype, n, ldq));
     PTQ_TRY(check_float_rows(fn, "O", O, dtype, n, ldo));
     const TreePlan p =
-        given ? *given : attention_tree_plan(r.rows, r.batch, heads, c.heads, c.block, r.width, window);
+        given ? *given : attention_tree_plan(r.rows, r.batch, heads, c.heads, c.dim, c.block, r.width, window);
     const size_t need = attention_tree_part_bytes(p.nsplit, r.rows, heads, c.dim);
     if (need && (!workspace || workspace_bytes < need)) {
         set_error("%s: workspace %zu bytes, need %zu", fn, workspace ? workspace_bytes : (size_t)0, need);
@@ -434,7 +434,7 @@ size_t attention_int8_tree_workspace_bytes(int64_t rows, int64_t batch, int head
     if (check_cache("attention_int8_tree_workspace_bytes", c) != PTQ_OK || rows <= 0 || batch <= 0 ||
         heads < kv_heads || heads % kv_heads || table_width < 0 || window < 0)
         return 0;
-    const TreePlan p = attention_tree_plan(rows, batch, heads, kv_heads, block_size, table_width, window);
+    const TreePlan p = attention_tree_plan(rows, batch, heads, kv_heads, head_dim, block_size, table_width, window);
     return attention_tree_part_bytes(p.nsplit, rows, heads, head_dim);
 }
 
@@ -449,6 +449,43 @@ int attention_int8_tree(const void* Q, int64_t ldq, void* O, int64_t ldo, float*
     const RaggedRows r{rows, batch, offsets, seq_lens, block_table, table_width};
     return attention_tree("attention_int8_tree", nullptr, c, r, parents, dtype, Q, ldq, heads, scale, window, O, ldo,
                           lse, workspace, workspace_bytes, stream);
+}
+
+int ptq_test_attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim, int block_size,
+                                 int64_t table_width, int64_t window, int* rg, int* nw, int* nsplit) {
+    const char* fn = "ptq_test_attention_tree_plan";
+    PTQ_TRY(check_cache(fn, KVCacheInt8{nullptr, nullptr, nullptr, nullptr, 0, kv_heads, head_dim, block_size}));
+    if (rows < 1 || batch < 1 || heads < kv_heads || heads % kv_heads || table_width < 0 || window < 0 || !rg || !nw ||
+        !nsplit)
+        REFUSE("%s: bad arguments", fn);
+    const TreePlan p = attention_tree_plan(rows, batch, heads, kv_heads, head_dim, block_size, table_width, window);
+    *rg = p.rg;
+    *nw = p.nw;
+    *nsplit = p.nsplit;
+    return PTQ_OK;
+}
+
+size_t ptq_test_attention_tree_workspace_bytes(int nsplit, int64_t rows, int heads, int head_dim) {
+    return nsplit > 0 && rows > 0 && heads > 0 && head_dim > 0 ? attention_tree_part_bytes(nsplit, rows, heads, head_dim) : 0;
+}
+
+int ptq_test_attention_int8_tree(int rg, int nw, int nsplit, const void* Q, int64_t ldq, void* O, int64_t ldo, float* lse,
+                                 int dtype, int64_t rows, int heads, const int32_t* offsets, const int32_t* seq_lens,
+                                 const int32_t* parents, int64_t batch, const int32_t* block_table,
+                                 int64_t table_width, const int8_t* k_codes, const int8_t* v_codes,
+                                 const float* k_scales, const float* v_scales, int64_t num_blocks, int kv_heads,
+                                 int head_dim, int block_size, float scale, int64_t window, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+    const char* fn = "ptq_test_attention_int8_tree";
+    if ((rg != 1 && rg != 2 && rg != 4) || (nw != 4 && (nw != 8 || rg != 1 || head_dim > 128)) || nsplit < 1 || nsplit > 64 ||
+        rows > 1 << 16 || batch > 1 << 10)
+        REFUSE("%s: rg = %d, nw = %d, nsplit = %d", fn, rg, nw, nsplit);
+    const KVCacheInt8 c{const_cast<int8_t*>(k_codes), const_cast<int8_t*>(v_codes), const_cast<float*>(k_scales),
+                        const_cast<float*>(v_scales), num_blocks, kv_heads, head_dim, block_size};
+    const RaggedRows r{rows, batch, offsets, seq_lens, block_table, table_width};
+    const TreePlan p{rg, nw, nsplit};
+    return attention_tree(fn, &p, c, r, parents, dtype, Q, ldq, heads, scale, window, O, ldo, lse, workspace,
+                          workspace_bytes, stream);
 }
 
 int verify_drafts(const void* target, int64_t ldt, const void* draft, int64_t ldd, int dtype, int64_t rows,

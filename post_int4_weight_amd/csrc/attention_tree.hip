@@ -6,9 +6,9 @@
 //   o_i = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q_i.k_j - m)
 //   k_j = S_k[block(j)] c_j,  v_j = S_v[block(j)] c'_j
 //
-// Arithmetic. Scores are int8 products: a row of q is a fixed-point number of
-// its largest element, q = (max|q| / 16256) (128 hi + lo) for bf16 and 21 bits in
-// three terms for fp32 queries, so the codes of K go into the matrix cores as
+// Arithmetic. Scores are int8 products: a row of q is whole numbers of steps of
+// its largest element, q = (max|q| / 16256) (128 hi + lo) for bf16 and three such
+// terms, max|q| / 2080768, for fp32 queries, so the codes of K go into the matrix cores as
 // they lie in memory and the sums are exact in int32. P V runs on the fp16
 // matrix cores, where codes are exact: w_j = p_j S_v[block(j)] / R in fp16 (two
 // terms for fp32 queries), R the running maximum of S_v over the blocks that the
@@ -23,7 +23,6 @@ namespace ptq {
 namespace {
 
 constexpr int WAVE_ROWS = 32;            // query rows (nodes x grouped heads) of a wave
-constexpr int WAVES = 4;
 constexpr int NODES = TREE_NODES;
 // Words of a node's line of keys: 64 ones for what comes before the tree, then
 // a bit for each node (its ancestors and itself), then 64 zeros.
@@ -57,22 +56,22 @@ struct TreeTile {
     bool bad;              // longer than its row of the table can hold, or more nodes than a line has: NaN
 };
 
-__device__ __forceinline__ bool find_tile(const TreeArgs& a, int64_t unit, int tr, int tk, TreeTile& t) {
+__device__ __forceinline__ bool find_tile(const TreeArgs& a, unsigned unit, int tr, int tk, TreeTile& t) {
     const RaggedUnit u = ragged_find(a.g, unit, a.group, tr, 1);
     t.b = u.b;
     t.off = u.off;
-    const int64_t rows = u.rows * a.group, f0 = u.local * tr;
+    const int64_t rows = u.rows * a.group, f0 = u.local * tr;      // below 2^25 (rows x heads)
     if (u.rows <= 0 || f0 >= rows) return false;
     t.nodes = (int)u.rows;
     t.rows = (int)rows;
     t.f0 = (int)f0;
-    const int64_t len = std::max(u.start, 0), base = std::max<int64_t>(len - u.rows, 0);
-    t.bad = len > a.width * a.bs || len < u.rows || u.rows > NODES;
-    t.base = (int)base;
-    t.end = (int)std::min<int64_t>(base + std::min<int64_t>(f0 + tr - 1, rows - 1) / a.group + 1, len);
-    const int64_t lo = a.window > 0 ? std::max<int64_t>(0, base - a.window + 1) : 0;      // of the root, the lowest
-    t.it0 = (int)(lo / tk);
-    t.it1 = t.bad ? t.it0 : (t.end + tk - 1) / tk;
+    const int len = std::max(u.start, 0);
+    t.base = std::max(len - t.nodes, 0);
+    t.bad = len > a.width * a.bs || len < t.nodes || t.nodes > NODES;
+    t.end = std::min(t.base + std::min(t.f0 + tr - 1, t.rows - 1) / a.group + 1, len);
+    const int lo = a.window > 0 ? (int)std::max<int64_t>(0, t.base - a.window + 1) : 0;      // of the root, the lowest
+    t.it0 = lo / tk;
+    t.it1 = t.bad ? t.it0 : (int)(((unsigned)t.end + tk - 1) / tk);
     return true;
 }
 
@@ -82,60 +81,77 @@ __device__ __forceinline__ int split_steps(const TreeTile& t, int nsplit) {
     return std::max(4, (t.it1 - t.it0 + nsplit - 1) / nsplit);
 }
 
-// 16 elements of a row
-__device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
-    load8(p, *(float (*)[8])&v[0]);
-    load8(p + 8, *(float (*)[8])&v[8]);
-}
-__device__ __forceinline__ void load16(const uint16_t* p, float (&v)[16]) {
-    load8(p, *(float (*)[8])&v[0]);
-    load8(p + 8, *(float (*)[8])&v[8]);
-}
+// |x| as bits, in the order of the values: a NaN's are the largest
+__device__ __forceinline__ uint32_t size_of(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
-// One query row as NT terms of 7 bits and a factor: q = factor sum_t term_t 2^(7 (NT - 1 - t)). Lane half hf holds
-// channels 32 c + 16 hf .. + 15 of fragment c; the two lanes that differ in bit 5 share the row. The sign of the softmax
-// scale goes into the terms. A row with a NaN or an infinity gets the factor NaN.
-template <typename T, int NC, int NT>
-__device__ __forceinline__ float load_query(const T* p, float scale2, i32x4 (&q)[NT][NC]) {
-    const int hf = (threadIdx.x >> 5) & 1;
-    float x[NC][16], m = 0.f;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        load16(p + 32 * c + 16 * hf, x[c]);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) m = amax_acc(m, x[c][k]);
-    }
-    m = amax_acc(m, __shfl_xor(m, 32, 64));
-    constexpr float LARGEST = NT == 2 ? 127 * 128 : 127 * 128 * 128;
-    const float up = m < 0x1p-100f ? 0x1p100f : 1.f;       // 1 / m is finite
-    const bool fine = m <= FLT_MAX;
-    const float inv = fine && m > 0.f ? __fdiv_rn(scale2 < 0.f ? -LARGEST : LARGEST, m * up) : 0.f;
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            uint32_t d[NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) d[t] = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                int n = fine ? (int)rintf(x[c][4 * w + k] * up * inv) : 0;
-#pragma unroll
-                for (int t = NT - 1; t > 0; --t) {
-                    const int low = ((n + 64) & 127) - 64;
-                    d[t] |= (uint32_t)(uint8_t)low << (8 * k);
-                    n = (n - low) >> 7;
-                }
-                d[0] |= (uint32_t)(uint8_t)n << (8 * k);
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) q[t][c][w] = (int)d[t];
-        }
-    return fine ? fabsf(scale2) * (__fdiv_rn(m * up, LARGEST) * (up == 1.f ? 1.f : 0x1p-100f)) : __builtin_nanf("");
+// Bytes SHIFT .. SHIFT + 7 of four numbers, as the bytes of one word
+template <int SHIFT>
+__device__ __forceinline__ uint32_t bytes_of(const uint32_t (&n)[4]) {
+    const uint32_t lo = __builtin_amdgcn_perm(n[1] >> SHIFT, n[0] >> SHIFT, 0x0c0c0400u);
+    return lo | __builtin_amdgcn_perm(n[3] >> SHIFT, n[2] >> SHIFT, 0x04000c0cu);
 }
+
+// One query row: 32 channels of it for each of the NC fragments, as they come from memory.
+template <typename T, int NC>
+struct QueryRow {
+    static constexpr int WORDS = 16 * sizeof(T) / 16;      // 16-byte words of 16 channels
+    uint4 raw[NC][WORDS];
+    // lane half hf holds channels 32 c + 16 hf .. + 15 of fragment c; the lanes that differ in bit 5 share the row
+    __device__ __forceinline__ void load(const T* p) {
+        const int hf = (threadIdx.x >> 5) & 1;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int w = 0; w < WORDS; ++w) raw[c][w] = *(const uint4*)(p + 32 * c + 16 * hf + w * (16 / sizeof(T)));
+    }
+    __device__ __forceinline__ void values(int c, float (&x)[16]) const {
+        load8((const T*)&raw[c][0], *(float (*)[8])&x[0]);
+        load8((const T*)&raw[c][WORDS / 2], *(float (*)[8])&x[8]);
+    }
+    // As whole numbers n of NT terms, n = sum_t q_t 2^(7 (NT - 1 - t)), the first signed and the others in [0, 128), and
+    // the factor with which they stand for the row times the softmax scale, whose sign goes into the numbers. A row with a
+    // NaN or an infinity gets the factor NaN. Adding 3 * 2^22 leaves n, half to even, in the low bits of the sum.
+    template <int NT>
+    __device__ __forceinline__ float terms(float scale2, i32x4 (&q)[NT][NC]) {
+        uint32_t size = 0;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            float x[16];
+            values(c, x);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) size = std::max(size, size_of(x[k]));
+        }
+        size = std::max(size, (uint32_t)__shfl_xor((int)size, 32, 64));
+        float m = __uint_as_float(size);
+        constexpr float LARGEST = NT == 2 ? 127 * 128 : 127 * 128 * 128, MAGIC = 12582912.f;
+        const float up = m < 0x1p-100f ? 0x1p100f : 1.f, down = m < 0x1p-100f ? 0x1p-100f : 1.f;      // 1 / m is finite
+        m *= up;
+        const bool fine = m <= FLT_MAX;
+        const float inv = fine && m > 0.f ? __fdiv_rn(scale2 < 0.f ? -LARGEST : LARGEST, m) : 0.f;
+        const bool tiny = __any(up != 1.f);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            float x[16];
+            values(c, x);
+            if (tiny)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) x[k] *= up;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                uint32_t n[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) n[k] = __float_as_uint(fmaf(x[4 * w + k], inv, MAGIC));
+                q[NT - 1][c][w] = (int)(bytes_of<0>(n) & 0x7f7f7f7fu);
+                if constexpr (NT == 3) q[1][c][w] = (int)(bytes_of<7>(n) & 0x7f7f7f7fu);
+                q[0][c][w] = (int)bytes_of<7 * (NT - 1)>(n);
+            }
+        }
+        return fine ? fabsf(scale2) * (__fdiv_rn(m, LARGEST) * down) : __builtin_nanf("");
+    }
+};
 
 // A wave takes 32 query rows. Scores are computed transposed, S^T = K Q^T, so
 // that a lane ends up with scores of one row and the probabilities are already
@@ -143,43 +159,66 @@ __device__ __forceinline__ float load_query(const T* p, float scale2, i32x4 (&q)
 // 16 (r / 4 % 2) + 4 (r / 8) + r % 4, so lane half hf holds keys 16 hf .. 16 hf +
 // 15, in one block of the cache: one S_k and one S_v a lane.
 //
-// RG waves of a workgroup take rows that differ, and share the keys. With few
-// rows (RG < 4) the 4 / RG groups of waves take every (4 / RG)-th step, and a
-// wave loads its own operands. With four row waves the workgroup stages each
-// step in LDS, K as it is and V converted to fp16: a wave that converts V for
-// its 32 rows alone spends as much on that as on the exponentials.
+// RG waves take 32 rows each of a tile and share the keys; NW / RG such groups
+// take every (NW / RG)-th step. Up to two row waves the codes of a step are copied
+// into the group's part of LDS as they are, and each wave converts V for itself;
+// a wave alone overwrites its part when it has read it, two have two parts. With
+// four row waves (RG = NW = 4) the workgroup stages each step, K as it is and V
+// converted to fp16: a wave that converts V for its 32 rows alone spends as much
+// on that as on the exponentials.
 //
 // A step is 64 keys, or 32 where 64 do not fit the registers of the waves that a
 // SIMD shall hold.
-template <typename T, int RG>
+template <typename T>
 constexpr int blocks_of(int dim) { return dim <= (sizeof(T) == 4 ? 64 : 128) ? 2 : 1; }
 constexpr int waves_of(int dim) { return dim <= 128 ? 2 : 1; }
 
+// Chunks of 16 bytes in LDS, C a row: chunk c of row r lies at c ^ swizzle(r), so that the same chunk of 8 neighbours is in
+// all banks.
+template <int C>
+__device__ __forceinline__ int swizzle(int r) {
+    return C >= 8 ? r & 7 : (r / (8 / C)) & (C - 1);
+}
+
 // One step of keys in LDS: K in the order of the operand's rows, in chunks of 16 channels, and V in chunks of 8 keys of a
-// channel, chunk c of row r at c ^ (r % 8) (r % 4 where a row has four): 8 neighbours' chunks lie in all banks.
+// channel.
 template <int D, int U>
 struct TreeStep {
     uint4 k[32 * U][D / 16];
     f16x8 v[D][4 * U];
     float scale[2 * U][4];       // of 16 keys: S_k, S_v, log2 S_v
 };
+// The same with the codes of V, chunks of 16 keys.
+template <int D, int U>
+struct TreeCodes {
+    uint4 k[32 * U][D / 16];
+    uint4 v[D][2 * U];
+};
 
-template <typename T, int D, int RG>
-__global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel(TreeArgs a) {
-    constexpr int U = blocks_of<T, RG>(D), TK = 32 * U;
+typedef __attribute__((address_space(3))) void* lds_ptr;
+typedef const __attribute__((address_space(1))) void* global_ptr;
+// 16 bytes a lane from `from` into LDS at to + 16 lane (`to` the same for the wave); done when vmcnt says so
+__device__ __forceinline__ void copy16(const void* from, void* to) {
+    __builtin_amdgcn_global_load_lds((global_ptr)from, (lds_ptr)to, 16, 0, 0);
+}
+
+template <typename T, int D, int RG, int NW>
+__global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(TreeArgs a) {
+    constexpr int U = blocks_of<T>(D), TK = 32 * U;
     constexpr int NQ = sizeof(T) == 4 ? 3 : 2;    // int8 terms of q
     constexpr int NT = sizeof(T) == 4 ? 2 : 1;    // fp16 terms of the probabilities
-    constexpr int NC = D / 32, TG = WAVES / RG, ROWS = WAVE_ROWS * RG, NTH = 64 * WAVES;
-    constexpr bool STAGED = RG == WAVES;
+    constexpr int NC = D / 32, TG = NW / RG, ROWS = WAVE_ROWS * RG, NTH = 64 * NW;
+    constexpr bool STAGED = RG == 4;
+    static_assert(RG * TG == NW && (!STAGED || TG == 1), "rows and steps are dealt to waves");
     constexpr bool FOLD = NT == 1;       // S_v / R goes into the exponent
     __shared__ uint32_t line[ROWS][WORDS + 1];      // an odd stride
     __shared__ int16_t parent[NODES], level[ROWS];      // level: depth of a node, negative: no valid way up
 
     const int split = (int)(blockIdx.x % (unsigned)a.nsplit);
-    const int64_t tile = blockIdx.x / (unsigned)a.nsplit;
-    const int h = (int)(tile % a.kv_heads);
+    const unsigned tile = blockIdx.x / (unsigned)a.nsplit;
+    const int h = (int)(tile % (unsigned)a.kv_heads);
     TreeTile tl;
-    if (!find_tile(a, tile / a.kv_heads, ROWS, TK, tl)) return;
+    if (!find_tile(a, tile / (unsigned)a.kv_heads, ROWS, TK, tl)) return;
     const int per = split_steps(tl, a.nsplit);
     const int s0 = tl.it0 + split * per, s1 = std::min(s0 + per, tl.it1);
     if (split > 0 && s0 >= s1) return;
@@ -190,16 +229,100 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
     const int first_node = tl.f0 / a.group;
     auto row_of = [&](int i) { return std::min(tl.f0 + WAVE_ROWS * rg + i, tl.rows - 1); };
     const int node = row_of(li) / a.group;
+    const int32_t* table = a.table + (int64_t)tl.b * a.width;
+    const unsigned pool = (unsigned)a.bs * D, stride = (unsigned)a.kv_heads * pool;      // codes of a (block, head), of a block
+    const int8_t* kp = a.k + (int64_t)h * pool;
+    const int8_t* vp = a.v + (int64_t)h * pool;
+    const int end = tl.end, bmask = a.bs - 1;
+    // block of position p: one without a valid id, and positions past the keys, stand for some other block of the
+    // pool, whose codes are as good as any (the scale says NaN, or the mask leaves them out)
+    auto entry = [&](int p) __attribute__((always_inline)) { return table[std::min(p, end - 1) >> a.bs_log2]; };
+    auto ok = [&](int id) { return (unsigned)id < (unsigned)a.num_blocks; };
+    auto place = [&](int id, int off) __attribute__((always_inline)) { return (uint64_t)(ok(id) ? (unsigned)id : 0u) * stride + (unsigned)off; };
+    auto scale_at = [&](int id) { return (uint64_t)(ok(id) ? (unsigned)id : 0u) * (unsigned)a.kv_heads + (unsigned)h; };
+    // infinite scales, too, count as NaN: times codes of one sign they would stay infinite
+    auto clean = [&](float s, int id, int p) { return p >= end ? 0.f : ok(id) && s < INFINITY ? s : __builtin_nanf(""); };
+    auto key_of_row = [](int r) { return 16 * (r >> 2 & 1) + 4 * (r >> 3) + (r & 3); };      // r < 32
+
+    const bool busy = tl.f0 + WAVE_ROWS * rg < tl.rows;      // some row is this wave's
+
+    // what the rest waits for is requested first, and answered in that order: parents, the query row, the first keys
+    const bool lines = !tl.bad && (a.window > 0 || s1 * TK > tl.base);
+    constexpr int PN = NODES / NTH + (NODES % NTH != 0);
+    int up[PN];
+    if (lines)
+#pragma unroll
+        for (int i = 0; i < PN; ++i) up[i] = a.parents[tl.off + std::min(t + i * NTH, tl.nodes - 1)];
+    QueryRow<T, NC> row;
+    row.load((const T*)a.Q + (tl.off + node) * a.ldq + (int64_t)(h * a.group + row_of(li) % a.group) * D);
+
+    // the group's part of LDS, and the copies of one step into it
+    constexpr int KC = D / 16, VC = 2 * U;      // chunks of a row of K, groups of 16 keys of a channel of V
+    constexpr int PARTS = RG == 1 ? 1 : 2;
+    using Codes = TreeCodes<D, U>;
+    __shared__ __attribute__((aligned(16))) unsigned char own[STAGED ? 16 : TG * PARTS * sizeof(Codes)];
+    auto part = [&](int k) -> Codes& { return ((Codes*)own)[STAGED ? 0 : tg * PARTS + k]; };
+    float rsk[U], rsv[U];
+    int ids_of[U];
+    const bool one_block = a.bs >= TK;      // a step lies in one block of the cache: addresses are scalar
+    auto copy = [&](int it, Codes& to) __attribute__((always_inline)) {
+        constexpr int KI = 32 * U * KC / 64, VI = D * VC / 64;      // copies of 64 chunks
+        auto krow = [&](int i) { return (i * 64 + lane) / KC; };
+        auto koff = [&](int i) {      // from the first key of a step in one block
+            return ((krow(i) & ~31) + key_of_row(krow(i) & 31)) * D + 16 * ((lane % KC) ^ swizzle<KC>(krow(i)));
+        };
+        const int vd = lane / VC, vg = (lane % VC) ^ swizzle<VC>(vd);      // 64 / VC channels a copy, a multiple of 8
+        const int voff = vd * a.bs + 16 * vg;
+        if (one_block) {
+            const int id = __builtin_amdgcn_readfirstlane(entry(it * TK)), from = (it * TK) & bmask;
+            const int8_t* kb = kp + place(id, from * D);
+            const int8_t* vb = vp + place(id, from);
+#pragma unroll
+            for (int i = 0; i < KI; ++i)
+                if (i % RG == rg % RG) copy16(kb + (unsigned)koff(i), (char*)to.k + 1024 * i);
+#pragma unroll
+            for (int i = 0; i < VI; ++i)
+                if (i % RG == rg % RG) copy16(vb + (unsigned)(voff + i * (64 / VC) * a.bs), (char*)to.v + 1024 * i);
+#pragma unroll
+            for (int u = 0; u < U; ++u) ids_of[u] = id;
+            rsk[0] = a.ks[scale_at(id)];
+            rsv[0] = a.vs[scale_at(id)];
+            if constexpr (U == 2) rsk[1] = rsk[0], rsv[1] = rsv[0];
+            return;
+        }
+        // blocks of 16 keys each
+        const int id0 = entry(it * TK), id1 = entry(it * TK + 16);
+        const int id2 = U == 1 ? 0 : entry(it * TK + 32), id3 = U == 1 ? 0 : entry(it * TK + 48);
+        const int idv = entry(it * TK + 16 * vg);
+        ids_of[0] = hf ? id1 : id0;
+        if constexpr (U == 2) ids_of[1] = hf ? id3 : id2;
+#pragma unroll
+        for (int i = 0; i < KI; ++i) {
+            const int key = key_of_row(krow(i) & 31);
+            const int id = i * 64 / KC < 32 ? (key & 16 ? id1 : id0) : (key & 16 ? id3 : id2);      // rows of one 32
+            const int p = it * TK + (krow(i) & ~31) + key;
+            if (i % RG == rg % RG)
+                copy16(kp + place(id, (p & bmask) * D + 16 * ((lane % KC) ^ swizzle<KC>(krow(i)))), (char*)to.k + 1024 * i);
+        }
+        const int8_t* from = vp + place(idv, vd * a.bs + ((it * TK + 16 * vg) & bmask));
+#pragma unroll
+        for (int i = 0; i < VI; ++i)
+            if (i % RG == rg % RG) copy16(from + i * (64 / VC) * a.bs, (char*)to.v + 1024 * i);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            rsk[u] = a.ks[scale_at(ids_of[u])];
+            rsv[u] = a.vs[scale_at(ids_of[u])];
+        }
+    };
+    if (!STAGED && s0 + tg < s1) copy(s0 + tg, part(0));
 
     // lines of the tile's nodes, where this split has keys of the tree or a window asks for depths
-    const bool lines = !tl.bad && (a.window > 0 || s1 * TK > tl.base);
     int lo = 0;
     bool broken = tl.bad;
     if (lines) {
-        for (int i = t; i < tl.nodes; i += NTH) {
-            const int p = a.parents[tl.off + i];
-            parent[i] = (int16_t)(p >= -1 && p < NODES ? p : NODES);
-        }
+#pragma unroll
+        for (int i = 0; i < PN; ++i)
+            if (t + i * NTH < tl.nodes) parent[t + i * NTH] = (int16_t)(up[i] >= -1 && up[i] < NODES ? up[i] : NODES);
         const int count = std::min(tl.f0 + ROWS - 1, tl.rows - 1) / a.group - first_node + 1;
         for (int i = t; i < count * WORDS; i += NTH) line[i / WORDS][i % WORDS] = i % WORDS < 2 ? ~0u : 0u;
         __syncthreads();
@@ -209,13 +332,13 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
             uint32_t bits = 0;
             bool fine = true;
             while (true) {
+                const int p = parent[j];
                 if (j >> 5 != word) {
                     line[t][2 + word] = bits;
                     word = j >> 5;
                     bits = 0;
                 }
                 if (a.window <= 0 || depth < a.window) bits |= 1u << (j & 31);
-                const int p = parent[j];
                 if (p >= j) fine = false;
                 if (p >= j || p < 0) break;
                 j = p;
@@ -232,22 +355,16 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
             lo = (int)std::min<int64_t>(tl.base, std::max<int64_t>(0, tl.base + std::max(depth, 0) - a.window + 1));
     }
     const int lo_max = a.window > 0 ? (int)std::max<int64_t>(0, tl.base + (int64_t)tl.nodes - a.window) : 0;   // of the deepest row
-    // steps that no row masks: [whole, last)
-    const int whole = std::min(__builtin_amdgcn_readfirstlane((lo_max + TK - 1) / TK), s1);
-    const int last = std::min(__builtin_amdgcn_readfirstlane(tl.base / TK), s1);
-
-    const int32_t* table = a.table + (int64_t)tl.b * a.width;
-    const int64_t pool = (int64_t)a.bs * D, stride = (int64_t)a.kv_heads * pool;
-    const int8_t* kp = a.k + (int64_t)h * pool;
-    const int8_t* vp = a.v + (int64_t)h * pool;
-    const int end = tl.end, bmask = a.bs - 1;
-    // block of position p: one without a valid id, and positions past the keys, stand for some other block of the
-    // pool, whose codes are as good as any (the scale says NaN, or the mask leaves them out)
-    auto entry = [&](int p) { return table[std::min(p, end - 1) >> a.bs_log2]; };
-    auto ok = [&](int id) { return (unsigned)id < (unsigned)a.num_blocks; };
-    // infinite scales, too, count as NaN: times codes of one sign they would stay infinite
-    auto clean = [&](float s, int id, int p) { return p >= end ? 0.f : ok(id) && s < INFINITY ? s : __builtin_nanf(""); };
-    auto key_of_row = [](int r) { return 16 * (r >> 2 & 1) + 4 * (r >> 3) + (r & 3); };      // r < 32
+    // a round is one step of each group; rounds [whole, last) have steps that no row masks alone
+    const int rounds = s1 > s0 ? (s1 - s0 + TG - 1) / TG : 0;
+    const int whole = std::min(std::max((lo_max + TK - 1) / TK - s0 + TG - 1, 0) / TG, rounds);
+    const int last = std::min(std::max(tl.base / TK - s0, 0) / TG, rounds);
+    auto every_round = [&](auto&& round) __attribute__((always_inline)) {
+        int i = 0;
+        for (; i < whole; ++i) round(std::true_type{}, i);
+        for (; i < last; ++i) round(std::false_type{}, i);
+        for (; i < rounds; ++i) round(std::true_type{}, i);
+    };
 
     i32x4 q[NQ][NC];
     f32x16 acc[NC];
@@ -257,8 +374,7 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
         for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
     // ref: what the scores' maximum m stands for in the exponents
     float m = -INFINITY, l = broken ? __builtin_nanf("") : 0.f, R = 0.f, rcp_R = 0.f, log2_R = 0.f, poison = 0.f;
-    const float qs = load_query<T, NC, NQ>(
-        (const T*)a.Q + (tl.off + node) * a.ldq + (int64_t)(h * a.group + row_of(li) % a.group) * D, a.scale2, q);
+    const float qs = row.template terms<NQ>(a.scale2, q);
 
     // One step. kf(u, e): codes of K, operand e of block u; vf(u, i, j): V of keys 8 j .. of the lane's 16, channels 32 i ..;
     // sk, sv, lv: S_k, S_v and log2 S_v of the lane's keys of each block
@@ -294,6 +410,7 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
                 const int o = std::min(std::max(tv - tl.base, -64) + 64, 32 * (WORDS - 2));      // the last two words are 0
                 const uint32_t* w = &line[node - first_node][o >> 5];
                 seen[u] = (uint32_t)((((uint64_t)w[1] << 32 | w[0]) >> (o & 31)) & 0xffffu);
+                if (tv + 16 <= tl.base) seen[u] = 0xffffu;      // there need be no lines
                 if (tv < lo) seen[u] &= lo - tv < 16 ? 0xffffu << (lo - tv) : 0u;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[u][r] = seen[u] >> r & 1 ? s[u][r] * ck[u] : -INFINITY;
@@ -371,59 +488,74 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
                 }
         }
     };
-    const bool busy = tl.f0 + WAVE_ROWS * rg < tl.rows;      // some row is this wave's
-
     if constexpr (STAGED) {
         using Step = TreeStep<D, U>;
         __shared__ __attribute__((aligned(16))) Step step[2];
-        constexpr int KC = D / 16, VC = 2 * U;                       // chunks of a row of K, groups of 16 keys of a channel of V
         constexpr int KN = 32 * U * KC / NTH, VN = D * VC / NTH;     // chunks of a thread
         static_assert(KN * NTH == 32 * U * KC && VN * NTH == D * VC && NTH % (32 * U * KC / KN) == 0, "whole shares");
-        constexpr int KM = KC < 8 ? KC - 1 : 7, VM = 4 * U < 8 ? 4 * U - 1 : 7;
         // chunk i of K of this thread: row t / KC + i NTH / KC; of V: group t % VC, channel t / VC + i NTH / VC
         const int kc = t % KC, kr = t / KC, vg = t % VC, vd = t / VC;
         auto krow = [&](int i) { return kr + i * (NTH / KC); };
         auto kkey = [&](int i) { return (krow(i) & ~31) + key_of_row(krow(i) & 31); };
         uint4 rk[KN], rv[VN];
-        float rsk = 0.f, rsv = 0.f;
-        int idk[KN], idv, ids_of = 0;       // blocks of the step to fetch next; idv of the step in registers
-        auto ids = [&](int it) {
-#pragma unroll
-            for (int i = 0; i < KN; ++i) idk[i] = entry(it * TK + kkey(i));
+        int idk[KN] = {}, idv = 0, id_of = 0;       // blocks of the step to fetch next; idv of the step in registers
+        auto ids = [&](int it) __attribute__((always_inline)) {
             idv = entry(it * TK + 16 * vg);
-        };
-        auto fetch = [&](int it) {
+            if (!one_block)
 #pragma unroll
-            for (int i = 0; i < KN; ++i) {
-                const int p = it * TK + kkey(i);
-                rk[i] = *(const uint4*)(kp + (ok(idk[i]) ? idk[i] : 0) * stride + ((p & bmask) * D + 16 * kc));
+                for (int i = 0; i < KN; ++i) idk[i] = entry(it * TK + kkey(i));
+        };
+        auto fetch = [&](int it) __attribute__((always_inline)) {
+            if (one_block) {
+                const int id = __builtin_amdgcn_readfirstlane(idv), from = (it * TK) & bmask;
+                const int8_t* kb = kp + place(id, from * D);
+                const int8_t* vb = vp + place(id, from);
+#pragma unroll
+                for (int i = 0; i < KN; ++i) rk[i] = *(const uint4*)(kb + (unsigned)(kkey(i) * D + 16 * kc));
+#pragma unroll
+                for (int i = 0; i < VN; ++i)
+                    rv[i] = *(const uint4*)(vb + (unsigned)((vd + i * (NTH / VC)) * a.bs + 16 * vg));
+            } else {
+#pragma unroll
+                for (int i = 0; i < KN; ++i)
+                    rk[i] = *(const uint4*)(kp + place(idk[i], ((it * TK + kkey(i)) & bmask) * D + 16 * kc));
+                const int8_t* from = vp + place(idv, vd * a.bs + ((it * TK + 16 * vg) & bmask));
+#pragma unroll
+                for (int i = 0; i < VN; ++i) rv[i] = *(const uint4*)(from + i * (NTH / VC) * a.bs);
             }
-            const int p = it * TK + 16 * vg;
-            const int64_t id = ok(idv) ? idv : 0;
-#pragma unroll
-            for (int i = 0; i < VN; ++i)
-                rv[i] = *(const uint4*)(vp + id * stride + ((vd + i * (NTH / VC)) * a.bs + (p & bmask)));
-            rsk = a.ks[id * a.kv_heads + h];
-            rsv = a.vs[id * a.kv_heads + h];
-            ids_of = idv;
+            rsk[0] = a.ks[scale_at(idv)];
+            rsv[0] = a.vs[scale_at(idv)];
+            id_of = idv;
         };
-        auto stage = [&](int it) {
+        auto stage = [&](int it) __attribute__((always_inline)) {
             Step& to = step[it & 1];
 #pragma unroll
-            for (int i = 0; i < KN; ++i) to.k[krow(i)][kc ^ (krow(i) & KM)] = rk[i];
+            for (int i = 0; i < KN; ++i) to.k[krow(i)][kc ^ swizzle<KC>(krow(i))] = rk[i];
 #pragma unroll
             for (int i = 0; i < VN; ++i) {
                 const int d = vd + i * (NTH / VC);
-                to.v[d][(2 * vg) ^ (d & VM)] = half8(rv[i].x, rv[i].y);
-                to.v[d][(2 * vg + 1) ^ (d & VM)] = half8(rv[i].z, rv[i].w);
+                to.v[d][(2 * vg) ^ swizzle<4 * U>(d)] = half8(rv[i].x, rv[i].y);
+                to.v[d][(2 * vg + 1) ^ swizzle<4 * U>(d)] = half8(rv[i].z, rv[i].w);
             }
             if (t < VC) {
-                const float sv = clean(rsv, ids_of, it * TK + 16 * vg);
-                *(f32x4*)to.scale[t] = f32x4{clean(rsk, ids_of, it * TK + 16 * vg), sv, __builtin_amdgcn_logf(sv), 0.f};
+                const float sv = clean(rsv[0], id_of, it * TK + 16 * vg);
+                *(f32x4*)to.scale[t] = f32x4{clean(rsk[0], id_of, it * TK + 16 * vg), sv, __builtin_amdgcn_logf(sv), 0.f};
             }
         };
-        // Step it finds its keys in LDS; those of it + 1 are in registers or on their way, the ids of it + 2 known.
-        auto turn = [&](auto masked, int it) __attribute__((always_inline)) {
+        int it = s0;
+        if (it < s1) {
+            ids(it);
+            fetch(it);
+            ids(std::min(it + 1, s1 - 1));
+            stage(it);
+            if (it + 1 < s1) {
+                fetch(it + 1);
+                ids(std::min(it + 2, s1 - 1));
+            }
+        }
+        // step it finds its keys in LDS; those of it + 1 are in registers or on their way, the ids of it + 2 known
+        every_round([&](auto masked, int i) __attribute__((always_inline)) {
+            const int it = s0 + i;
             __syncthreads();
             if (it + 1 < s1) {
                 stage(it + 1);
@@ -442,65 +574,43 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
             }
             work(masked, it,
                  [&](int u, int e) {
-                     const uint4 w = from.k[32 * u + li][(2 * e + hf) ^ (li & KM)];
+                     const uint4 w = from.k[32 * u + li][(2 * e + hf) ^ swizzle<KC>(li)];
                      return i32x4{(int)w.x, (int)w.y, (int)w.z, (int)w.w};
                  },
-                 [&](int u, int i, int j) { return from.v[32 * i + li][(4 * u + 2 * hf + j) ^ (li & VM)]; }, sk, sv, lv);
-        };
-        int it = s0;
-        if (it < s1) {
-            ids(it);
-            fetch(it);
-            ids(std::min(it + 1, s1 - 1));
-            stage(it);
-            if (it + 1 < s1) {
-                fetch(it + 1);
-                ids(std::min(it + 2, s1 - 1));
-            }
-        }
-        for (; it < whole; ++it) turn(std::true_type{}, it);
-        for (; it < last; ++it) turn(std::false_type{}, it);
-        for (; it < s1; ++it) turn(std::true_type{}, it);
+                 [&](int u, int i, int j) { return from.v[32 * i + li][(4 * u + 2 * hf + j) ^ swizzle<4 * U>(li)]; }, sk, sv, lv);
+        });
     } else {
-        // operands straight from the cache, everything of a step requested at once; block ids a step early
-        const int key = key_of_row(li);
-        int idk[U], idv[U];
-        auto ids = [&](int it) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                idk[u] = entry(it * TK + 32 * u + (key & 16));
-                idv[u] = entry(it * TK + 32 * u + 16 * hf);
-            }
-        };
-        auto turn = [&](auto masked, int it) __attribute__((always_inline)) {
-            uint4 k[U][NC], v[U][NC];
+        every_round([&](auto masked, int i) __attribute__((always_inline)) {
+            const int it = s0 + i * TG + tg;
+            __builtin_amdgcn_s_waitcnt(0x0f70);      // vmcnt = 0: the copies have landed
+            asm volatile("" ::: "memory");
+            if constexpr (PARTS == 2) __syncthreads();      // the other wave's, too, and it has read what is copied over now
+            const Codes& from = part(i % PARTS);
             float sk[U], sv[U], lv[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int8_t* p = kp + (ok(idk[u]) ? idk[u] : 0) * stride + (((it * TK + 32 * u + key) & bmask) * D + 16 * hf);
-#pragma unroll
-                for (int e = 0; e < NC; ++e) k[u][e] = *(const uint4*)(p + 32 * e);
                 const int tv = it * TK + 32 * u + 16 * hf;
-                const int64_t id = ok(idv[u]) ? idv[u] : 0;
-                const int8_t* x = vp + id * stride + (li * a.bs + (tv & bmask));
-#pragma unroll
-                for (int i = 0; i < NC; ++i) v[u][i] = *(const uint4*)(x + 32 * i * a.bs);
-                sk[u] = clean(a.ks[id * a.kv_heads + h], idv[u], tv);
-                sv[u] = clean(a.vs[id * a.kv_heads + h], idv[u], tv);
+                sk[u] = clean(rsk[u], ids_of[u], tv);
+                sv[u] = clean(rsv[u], ids_of[u], tv);
                 lv[u] = FOLD ? __builtin_amdgcn_logf(sv[u]) : 0.f;
             }
-            if (it + TG < s1) ids(it + TG);
-            work(masked, it,
-                 [&](int u, int e) { return i32x4{(int)k[u][e].x, (int)k[u][e].y, (int)k[u][e].z, (int)k[u][e].w}; },
-                 [&](int u, int i, int j) { return j ? half8(v[u][i].z, v[u][i].w) : half8(v[u][i].x, v[u][i].y); }, sk, sv, lv);
-        };
-        int it = s0 + tg;
-        if (busy && it < s1) {
-            ids(it);
-            for (; it < whole; it += TG) turn(std::true_type{}, it);
-            for (; it < last; it += TG) turn(std::false_type{}, it);
-            for (; it < s1; it += TG) turn(std::true_type{}, it);
-        }
+            if (PARTS == 2 && it + TG < s1) copy(it + TG, part((i + 1) % PARTS));
+            if (busy && it < s1)
+                work(masked, it,
+                     [&](int u, int e) {
+                         const uint4 w = from.k[32 * u + li][(2 * e + hf) ^ swizzle<KC>(li)];
+                         return i32x4{(int)w.x, (int)w.y, (int)w.z, (int)w.w};
+                     },
+                     [&](int u, int i, int j) {
+                         const uint4 w = from.v[32 * i + li][(2 * u + hf) ^ swizzle<VC>(li)];
+                         return j ? half8(w.z, w.w) : half8(w.x, w.y);
+                     }, sk, sv, lv);
+            if constexpr (PARTS == 1) {
+                __builtin_amdgcn_s_waitcnt(0xc07f);      // lgkmcnt = 0: everything has been read
+                asm volatile("" ::: "memory");
+                if (it + TG < s1) copy(it + TG, part(0));
+            }
+        });
     }
 
     l += __shfl_xor(l, 32, 64);
@@ -516,7 +626,7 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
     float M = m, M0 = m == -INFINITY ? 0.f : m, L = l;
     if constexpr (TG > 1) {
         // join the groups of waves: factors to the common maximum
-        __shared__ float sm[WAVES][WAVE_ROWS], sl[WAVES][WAVE_ROWS];
+        __shared__ float sm[NW][WAVE_ROWS], sl[NW][WAVE_ROWS];
         if (hf == 0) {
             sm[wave][li] = m;
             sl[wave][li] = l;
@@ -531,7 +641,7 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
         for (int g = 0; g < TG; ++g) L += sl[rg + g * RG][li] * exp2_fast(sm[rg + g * RG][li] - M0);
     }
     const float mine = (R > 0.f ? R : 1.f) * exp2_fast(m - M0) / (L == 0.f ? 1.f : L) + poison;
-    auto put = [&](int64_t row, int head, int d, const f32x4& o) {
+    auto put = [&](int64_t row, int head, int d, const f32x4& o) __attribute__((always_inline)) {
         if (split_out)
             *(f32x4*)(a.part + (split * nflat + row * a.heads + head) * D + d) = o;
         else
@@ -547,20 +657,24 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
 #pragma unroll
                 for (int b = 0; b < 4; ++b) put(token, qh, 32 * i + 8 * b + 4 * hf, channels(i, b));
     } else {
-        __shared__ __attribute__((aligned(16))) float so[WAVES][WAVE_ROWS][36];
+        constexpr int JC = sizeof(own) >= sizeof(float) * NW * WAVE_ROWS * 68 ? 64 : 32;      // channels at a time
+        static_assert(sizeof(own) >= sizeof(float) * NW * WAVE_ROWS * (JC + 4), "the join goes where the keys were");
+        float(*so)[WAVE_ROWS][JC + 4] = (float(*)[WAVE_ROWS][JC + 4])own;      // behind the barrier above
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            if (i) __syncthreads();
+        for (int i0 = 0; i0 < NC; i0 += JC / 32) {
+            if (i0) __syncthreads();
 #pragma unroll
-            for (int b = 0; b < 4; ++b) *(f32x4*)&so[wave][li][8 * b + 4 * hf] = channels(i, b);
+            for (int i = 0; i < JC / 32; ++i)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) *(f32x4*)&so[wave][li][32 * i + 8 * b + 4 * hf] = channels(i0 + i, b);
             __syncthreads();
-            for (int c = t; c < ROWS * 8; c += NTH) {
-                const int r = c / 8, d = 4 * (c % 8), fr = tl.f0 + r;
+            for (int c = t; c < ROWS * JC / 4; c += NTH) {
+                const int r = c / (JC / 4), d = 4 * (c % (JC / 4)), fr = tl.f0 + r;
                 if (fr >= tl.rows) continue;
                 f32x4 o = *(const f32x4*)&so[r / WAVE_ROWS][r % WAVE_ROWS][d];
 #pragma unroll
                 for (int g = 1; g < TG; ++g) o += *(const f32x4*)&so[r / WAVE_ROWS + g * RG][r % WAVE_ROWS][d];
-                put(tl.off + fr / a.group, h * a.group + fr % a.group, 32 * i + d, o);
+                put(tl.off + fr / a.group, h * a.group + fr % a.group, 32 * i0 + d, o);
             }
         }
     }
@@ -578,11 +692,11 @@ __global__ __launch_bounds__(64 * WAVES, waves_of(D)) void attention_tree_kernel
 // time with all their loads at once; tr: rows of the tiles that were split.
 template <typename T, int D, int RG>
 __global__ __launch_bounds__(256) void attention_tree_join_kernel(TreeArgs a) {
-    constexpr int tr = WAVE_ROWS * RG, TK = 32 * blocks_of<T, RG>(D);
-    const int64_t part = blockIdx.x % (unsigned)(tr / 16), tile = blockIdx.x / (unsigned)(tr / 16);
-    const int h = (int)(tile % a.kv_heads);
+    constexpr int tr = WAVE_ROWS * RG, TK = 32 * blocks_of<T>(D);
+    const unsigned part = blockIdx.x % (unsigned)(tr / 16), tile = blockIdx.x / (unsigned)(tr / 16);
+    const int h = (int)(tile % (unsigned)a.kv_heads);
     TreeTile tl;
-    if (!find_tile(a, tile / a.kv_heads, tr, TK, tl)) return;
+    if (!find_tile(a, tile / (unsigned)a.kv_heads, tr, TK, tl)) return;
     const int per = split_steps(tl, a.nsplit);
     const int n = std::max(1, (tl.it1 - tl.it0 + per - 1) / per);    // split 0 is always written
     const int r = threadIdx.x / 16, c = threadIdx.x % 16, f = tl.f0 + (int)part * 16 + r;
@@ -631,11 +745,11 @@ __global__ __launch_bounds__(256) void attention_tree_join_kernel(TreeArgs a) {
 
 int64_t tile_units(int64_t rows, int64_t batch, int group, int tr) { return rows * group / tr + batch; }
 
-template <typename T, int D, int RG>
+template <typename T, int D, int RG, int NW>
 int launch_tiles(const TreeArgs& a, hipStream_t st) {
     const int tr = WAVE_ROWS * RG;
     const int64_t units = tile_units(a.g.rows, a.g.batch, a.group, tr) * a.kv_heads;
-    hipLaunchKernelGGL((attention_tree_kernel<T, D, RG>), dim3((unsigned)(units * a.nsplit)), dim3(64 * WAVES), 0, st, a);
+    hipLaunchKernelGGL((attention_tree_kernel<T, D, RG, NW>), dim3((unsigned)(units * a.nsplit)), dim3(64 * NW), 0, st, a);
     PTQ_LAUNCH_CHECK();
     if (a.nsplit > 1) {
         hipLaunchKernelGGL((attention_tree_join_kernel<T, D, RG>), dim3((unsigned)(units * (tr / 16))), dim3(256), 0, st, a);
@@ -646,10 +760,11 @@ int launch_tiles(const TreeArgs& a, hipStream_t st) {
 
 template <typename T, int D>
 int launch(const TreeArgs& a, const TreePlan& p, hipStream_t st) {
-    if (p.rg == 1) return launch_tiles<T, D, 1>(a, st);
-    if constexpr (D < 256 || sizeof(T) == 2)      // fp32 at 256 channels: two row waves would spill registers
-        if (p.rg == 2) return launch_tiles<T, D, 2>(a, st);
-    return launch_tiles<T, D, 4>(a, st);
+    if (p.rg == 4) return launch_tiles<T, D, 4, 4>(a, st);
+    if (p.rg == 2) return launch_tiles<T, D, 2, 4>(a, st);
+    if constexpr (D <= 128)
+        if (p.nw == 8) return launch_tiles<T, D, 1, 8>(a, st);
+    return launch_tiles<T, D, 1, 4>(a, st);
 }
 
 template <typename T>
@@ -671,18 +786,33 @@ size_t attention_tree_part_bytes(int nsplit, int64_t rows, int heads, int dim) {
     return z.bytes();
 }
 
-// Lengths are not known here: keys is the most there may be.
-TreePlan attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int block, int64_t width,
+// Lengths are not known here: keys is the most there may be, and every sequence
+// is taken to have the mean number of rows. The time of a choice, in steps of 64
+// keys that a wave does while another one of its SIMD does the same: rounds of
+// as many workgroups as the card holds, each a start and its steps, and the join.
+TreePlan attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int block, int64_t width,
                              int64_t window) {
-    const int group = heads / kv_heads;
-    const int64_t keys = window > 0 && window < width * block ? std::min(width * block, window + cdiv(rows, batch)) : width * block;
-    TreePlan p;
+    const int64_t group = heads / kv_heads, most = width * block;
+    const int64_t keys = window > 0 && window < most ? std::min(most, window + cdiv(rows, batch)) : most;
     const int64_t each = cdiv(rows * group, batch);
-    p.rg = each <= WAVE_ROWS ? 1 : each <= 2 * WAVE_ROWS ? 2 : 4;
-    const int tr = WAVE_ROWS * p.rg;
-    const int64_t units = std::max<int64_t>({1, batch, cdiv(rows * group, tr) + (batch - 1) / 2}) * kv_heads;
-    p.nsplit = (int)std::max<int64_t>(1, std::min({cdiv(1024, units), cdiv(keys, 256), (int64_t)64}));
-    return p;
+    const double steps = std::max(1.0, (double)keys / 64);
+    TreePlan best{};
+    double least = 0;
+    for (const TreePlan p : {TreePlan{1, 4, 0}, TreePlan{1, 8, 0}, TreePlan{2, 4, 0}, TreePlan{4, 4, 0}}) {
+        if (p.nw == 8 && dim > 128) continue;
+        const int64_t tiles = batch * cdiv(each, WAVE_ROWS * p.rg) * kv_heads;
+        const int64_t slots = 256 * (dim <= 128 ? 2 : 1) * 4 / p.nw;
+        for (int ns = 1; ns <= 64 && (ns == 1 || ns * 4 <= steps); ++ns) {
+            const double mine = std::ceil(steps / ns * p.rg / p.nw);
+            const double join = ns == 1 ? 0 : 3 + ns * (double)rows * heads * dim * 8 / 6e6;
+            const double time = std::max(1.0, (double)(tiles * ns) / slots) * (3 + mine) + join;
+            if (best.nsplit == 0 || time < least) {
+                least = time;
+                best = TreePlan{p.rg, p.nw, ns};
+            }
+        }
+    }
+    return best;
 }
 
 int run_attention_tree(const TreePlan& p, const KVCacheInt8& c, const RaggedRows& r, const int32_t* parents, int dtype,

@@ -277,12 +277,13 @@ int run_attention_int8(const AttnPlan& p, const KVCacheInt8& c, const RaggedRows
                        float* lse, void* ws, size_t ws_bytes, hipStream_t st);
 
 // Attention of trees of drafted tokens over the cache (attention_tree.hip):
-// rg waves of 32 query rows share the keys of a workgroup.
+// tiles of 32 rg query rows (rg 1, 2 or 4), workgroups of nw waves (4; for rg 1
+// 8, too, up to 128 channels), nsplit splits of the keys.
 constexpr int TREE_NODES = 512;     // of a sequence, at most
 struct TreePlan {
-    int rg, nsplit;
+    int rg, nw, nsplit;
 };
-TreePlan attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int block, int64_t width,
+TreePlan attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int block, int64_t width,
                              int64_t window);
 size_t attention_tree_part_bytes(int nsplit, int64_t rows, int heads, int dim);
 int run_attention_tree(const TreePlan& p, const KVCacheInt8& c, const RaggedRows& r, const int32_t* parents, int dtype,
