@@ -85,8 +85,8 @@ int ptq_test_attention_int8_cache(int tiles, int waves, int nsplit, const void* 
                                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* attention_int8_tree with the kernel given instead of chosen: tiles of 32
- * query rows (rg 1; nw = 4 waves, or 8 with head_dim up to 128), of 64 (rg 2, nw 4)
- * or of 128 (rg 4, nw 4), and the splits of the keys (1 .. 64). _plan says what
+ * query rows (rg 1; nw = 4 waves, or 8 with head_dim up to 128), of 64 (rg 2, nw
+ * 4), of 128 (rg 4, nw 4) or of 256 (rg 8, nw 8; head_dim up to 128), and the splits of the keys (1 .. 64). _plan says what
  * attention_int8_tree chooses. Returns PTQ_OK, PTQ_EINVAL, PTQ_EWORKSPACE or
  * PTQ_EHIP. */
 int ptq_test_attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim, int block_size,

@@ -477,7 +477,8 @@ int ptq_test_attention_int8_tree(int rg, int nw, int nsplit, const void* Q, int6
                                  int head_dim, int block_size, float scale, int64_t window, void* workspace,
                                  size_t workspace_bytes, void* stream) {
     const char* fn = "ptq_test_attention_int8_tree";
-    if ((rg != 1 && rg != 2 && rg != 4) || (nw != 4 && (nw != 8 || rg != 1 || head_dim > 128)) || nsplit < 1 || nsplit > 64 ||
+    if ((rg != 1 && rg != 2 && rg != 4 && rg != 8) || (nw != 4 && nw != 8) ||
+        (nw == 8 ? (rg != 1 && rg != 8) || head_dim > 128 : rg == 8) || nsplit < 1 || nsplit > 64 ||
         rows > 1 << 16 || batch > 1 << 10)
         REFUSE("%s: rg = %d, nw = %d, nsplit = %d", fn, rg, nw, nsplit);
     const KVCacheInt8 c{const_cast<int8_t*>(k_codes), const_cast<int8_t*>(v_codes), const_cast<float*>(k_scales),

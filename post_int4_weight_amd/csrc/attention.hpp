@@ -42,4 +42,86 @@ __device__ __forceinline__ float max_halves(float x) {
     return larger;
 }
 
+// ------------------------------------------------------------------ trees --
+struct TreeArgs {
+    Ragged g;                             // g.starts: the lengths
+    const int32_t* parents;
+    const int32_t* table; int64_t width;
+    int heads, kv_heads, group, bs, bs_log2;
+    int64_t num_blocks;
+    const int8_t* k; const int8_t* v; const float* ks; const float* vs;
+    const void* Q; int64_t ldq;
+    void* O; int64_t ldo;
+    float* lse;                    // [rows, heads] or null
+    float scale2;                  // softmax scale * log2(e)
+    int64_t window;
+    int nsplit;
+    float* part; float* part_lse;  // [nsplit][rows * heads][dim], [nsplit][rows * heads]
+};
+// The tiles of 256 rows of attention_int8.hip (head_dim up to 128): writes O and lse, or the splits' parts.
+int launch_attention_tree_tiles(const TreeArgs& a, int dtype, int dim, hipStream_t st);
+
+// What the nodes of a tile of ROWS query rows attend to, of keys in the order of
+// a sequence: a line of bits for each node, 64 ones for keys before the tree, a
+// bit for each node (its ancestors and itself), 64 zeros.
+constexpr int NODES = TREE_NODES;
+constexpr int LINE_WORDS = 2 + NODES / 32 + 2;
+
+template <int ROWS>
+struct TreeLines {
+    uint32_t line[ROWS][LINE_WORDS + 1];      // an odd stride
+    int16_t parent[NODES];
+    int16_t level[ROWS];                      // depth of a node, negative: no valid way up
+};
+
+// All NTH threads, t of them this one: nodes first .. first + count of a tree of n; up[i]: parents[t + i NTH], requested
+// before. A window > 0 leaves out ancestors window levels up and more.
+template <int NTH, int ROWS, int PN>
+__device__ __forceinline__ void build_lines(TreeLines<ROWS>& s, const int (&up)[PN], int n, int first, int count,
+                                            int64_t window, int t) {
+#pragma unroll
+    for (int i = 0; i < PN; ++i)
+        if (t + i * NTH < n) s.parent[t + i * NTH] = (int16_t)(up[i] >= -1 && up[i] < NODES ? up[i] : NODES);
+    for (int i = t; i < count * LINE_WORDS; i += NTH) s.line[i / LINE_WORDS][i % LINE_WORDS] = i % LINE_WORDS < 2 ? ~0u : 0u;
+    __syncthreads();
+    if (t < count) {
+        // ancestors come in falling order: a word is done when the walk leaves it
+        int j = first + t, depth = 0, word = j >> 5;
+        uint32_t bits = 0;
+        bool fine = true;
+        while (true) {
+            const int p = s.parent[j];
+            if (j >> 5 != word) {
+                s.line[t][2 + word] = bits;
+                word = j >> 5;
+                bits = 0;
+            }
+            if (window <= 0 || depth < window) bits |= 1u << (j & 31);
+            if (p >= j) fine = false;
+            if (p >= j || p < 0) break;
+            j = p;
+            ++depth;
+        }
+        s.line[t][2 + word] = bits;
+        s.level[t] = (int16_t)(fine ? depth : -1);
+    }
+    __syncthreads();
+}
+
+// Which of the 16 keys from key on (of which the tree's begin at base, the row's at lo <= base) a row with this line
+// attends to. Where all 16 lie before the tree there need be no lines.
+__device__ __forceinline__ uint32_t seen16(const uint32_t* line, int key, int base, int lo) {
+    const int o = std::min(std::max(key - base, -64) + 64, 32 * (LINE_WORDS - 2));      // the last two words are 0
+    const uint32_t* w = line + (o >> 5);
+    uint32_t seen = (uint32_t)((((uint64_t)w[1] << 32 | w[0]) >> (o & 31)) & 0xffffu);
+    if (key + 16 <= base) seen = 0xffffu;
+    if (key < lo) seen &= lo - key < 16 ? 0xffffu << (lo - key) : 0u;
+    return seen;
+}
+
+// First key of a node at this depth, of those before the tree
+__device__ __forceinline__ int first_key(int base, int depth, int64_t window) {
+    return window > 0 ? (int)std::min<int64_t>(base, std::max<int64_t>(0, base + std::max(depth, 0) - window + 1)) : 0;
+}
+
 }  // namespace ptq

@@ -35,6 +35,7 @@ struct AttnArgs {
     float* lse;                    // [rows, heads] or null
     float scale2;                  // softmax scale * log2(e)
     int causal; int64_t window;
+    const int32_t* parents;        // trees only
     int nsplit;
     float* part; float* part_lse;  // [nsplit][rows * heads][dim], [nsplit][rows * heads]
 };
@@ -81,6 +82,28 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t unit, int t
     const int64_t lo = row_lo(a, first);
     t.it0 = (int)(lo / TK);
     t.it1 = t.hi > lo ? (int)((t.hi + TK - 1) / TK) : t.it0;
+    return true;
+}
+
+// The same of a sequence whose last rows are the nodes of a tree: all see the keys before it (a window may hide the first),
+// and what a row sees from hi_min on is in its line.
+__device__ __forceinline__ bool find_tree_tile(const AttnArgs& a, int64_t unit, int tr, Tile& t) {
+    const RaggedUnit u = ragged_find(a.g, unit, a.group, tr, 1);
+    t.b = u.b;
+    t.off = u.off;
+    const int64_t n = u.rows, rows = n * a.group, f0 = u.local * tr;
+    if (n <= 0 || f0 >= rows) return false;
+    t.rows = (int)rows;
+    t.f0 = (int)f0;
+    t.len = std::max(u.start, 0);
+    t.over = t.len > a.width * a.bs || t.len < n || n > NODES;
+    t.pos0 = std::max<int64_t>(t.len - n, 0);
+    t.lo_max = a.window > 0 ? std::max<int64_t>(0, t.pos0 + n - a.window) : 0;
+    t.hi_min = t.pos0;
+    t.hi = std::min(t.pos0 + std::min<int64_t>(f0 + tr - 1, rows - 1) / a.group + 1, t.len);
+    const int64_t lo = a.window > 0 ? std::max<int64_t>(0, t.pos0 - a.window + 1) : 0;
+    t.it0 = (int)(lo / TK);
+    t.it1 = t.over ? t.it0 : (int)((t.hi + TK - 1) / TK);
     return true;
 }
 
@@ -415,7 +438,10 @@ struct TileLds {
     }
 };
 
-template <typename T, int D, int WAVES>
+//
+// TREE: the queries are the nodes of trees of drafted tokens (attention_tree.hip);
+// steps with keys of the tree take their masks from the nodes' lines.
+template <typename T, int D, int WAVES, bool TREE>
 __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) {
     constexpr int NT = sizeof(T) == 4 ? 2 : 1;
     constexpr bool PIPE = NT == 1;                 // two terms of everything would not fit the registers
@@ -435,7 +461,8 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
     const int h = (int)(tile % a.kv_heads);
     Tile tl;
     // later tiles of a sequence have more keys: they go first
-    if (!find_tile(a, gridDim.x / (unsigned)a.nsplit / a.kv_heads - 1 - tile / a.kv_heads, 32 * WAVES, tl)) return;
+    const int64_t unit = gridDim.x / (unsigned)a.nsplit / a.kv_heads - 1 - tile / a.kv_heads;
+    if (!(TREE ? find_tree_tile(a, unit, 32 * WAVES, tl) : find_tile(a, unit, 32 * WAVES, tl))) return;
     const int per = split_steps(tl, a.nsplit, 32 * WAVES);
     const int s0 = __builtin_amdgcn_readfirstlane(tl.it0 + split * per);
     const int s1 = __builtin_amdgcn_readfirstlane(std::min(s0 + per, tl.it1));
@@ -448,10 +475,30 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
     const int64_t token = tl.off + f / a.group;
     const int qh = h * a.group + f % a.group;
     const int64_t pos = tl.pos0 + f / a.group;
-    // keys of this lane's row; the wave's rows have none from w_max on
-    const int my_lo = (int)row_lo(a, pos), my_hi = (int)row_hi(a, pos, tl.len);
+    // keys of this lane's row (of a tree's node: the first, and the end of those before the tree); the wave's rows have
+    // none from w_max on
+    int my_lo = 0, my_hi = (int)tl.pos0;
+    bool broken = tl.over;
+    const int first_node = tl.f0 / a.group;
+    __shared__ TreeLines<TREE ? 32 * WAVES : 1> lines_of;
+    if constexpr (TREE) {
+        if (!tl.over && (a.window > 0 || (int64_t)s1 * TK > tl.pos0)) {
+            const int n = tl.rows / a.group;
+            int up[1];
+            static_assert(NODES <= NTH, "a node a thread");
+            up[0] = a.parents[tl.off + std::min(t, n - 1)];
+            const int count = std::min(tl.f0 + 32 * WAVES - 1, tl.rows - 1) / a.group - first_node + 1;
+            build_lines<NTH>(lines_of, up, n, first_node, count, a.window, t);
+            const int depth = lines_of.level[f / a.group - first_node];
+            broken = depth < 0;
+            my_lo = first_key((int)tl.pos0, depth, a.window);
+        }
+    } else {
+        my_lo = (int)row_lo(a, pos), my_hi = (int)row_hi(a, pos, tl.len);
+    }
     const int fb = std::min(tl.f0 + 32 * wave + 31, tl.rows - 1);
-    const int w_max = idle ? 0 : __builtin_amdgcn_readfirstlane((int)row_hi(a, tl.pos0 + fb / a.group, tl.len));
+    const int64_t last_pos = tl.pos0 + fb / a.group;
+    const int w_max = idle ? 0 : __builtin_amdgcn_readfirstlane((int)(TREE ? last_pos + 1 : row_hi(a, last_pos, tl.len)));
 
     f16x8 q[NT][NC];
     const float qs = load_query<T, NC, 32>((const T*)a.Q + token * a.ldq + (int64_t)qh * D, a.scale2, q,
@@ -463,7 +510,7 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
     // ref, limit: what m comes down to for the exponents, the score from which it moves
-    float m = -INFINITY, ref = -PSHIFT, limit = -INFINITY, l = tl.over ? __builtin_nanf("") : 0.f;
+    float m = -INFINITY, ref = -PSHIFT, limit = -INFINITY, l = broken ? __builtin_nanf("") : 0.f;
     float R = 0.f, log2_R = 0.f, poison = 0.f;
 
     // Staging: one 16-byte chunk of K (16 channels of a token) and one of V (16 tokens of a channel) per thread and
@@ -519,7 +566,7 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
     auto stage_scales = [&](int it, int ids) {
         if (wave == 0 && lane < 4) {
             const bool past = (unsigned)it * TK + 16 * lane >= (unsigned)end, known = (unsigned)ids < (unsigned)a.num_blocks;
-            const float sk = past ? 0.f : known ? sk_r : __builtin_nanf("");
+            const float sk = past ? 0.f : known && (!TREE || sk_r < INFINITY) ? sk_r : __builtin_nanf("");
             const float sv = past || !known ? 0.f : sv_r;
             const bool bad = !(sv < INFINITY);
             float* to = ssc[(it - s0) & 3][lane & 1] + (lane >> 1);
@@ -587,7 +634,7 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
     // of sbig is large, too.
     unsigned all_R = 0;
     auto move = [&](float mx, float big) __attribute__((always_inline)) {
-        const float m_new = fmaxf(m, mx);
+        const float m_new = !TREE || mx > limit ? fmaxf(m, mx) : m;      // a tree's rows each by itself
         float fall = m_new == m ? 1.f : exp2_fast(m - m_new);
         m = m_new;
         ref = (m == -INFINITY ? 0.f : m) - PSHIFT;
@@ -607,14 +654,14 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
     auto big_of = [&](int it) { return sbig[(it - s0) & 3]; };
     auto bits = [](float big) { return (unsigned)__builtin_amdgcn_readfirstlane(__float_as_uint(big)); };
     auto log2_rv = [&](float log2_sv) { return fmaxf(log2_sv - log2_R, LOG2_RV_MIN); };      // of NaN, too
-    // two probabilities of block (it, u), into w and sum; lo, hi: the row's keys within the lane's 16
-    auto pair = [&](auto masked, const f32x16& s, float ck, float off, int r, Probs& w, float& sum, int lo, int hi) {
+    // two probabilities of block (it, u), into w and sum; in(r): whether the row attends to key r of the lane's 16
+    auto pair = [&](auto masked, const f32x16& s, float ck, float off, int r, Probs& w, float& sum, auto&& in) {
         f32x2 e;
         e[0] = exp2_fast(fmaf(s[r], ck, -off));
         e[1] = exp2_fast(fmaf(s[r + 1], ck, -off));
         if constexpr (decltype(masked)::value) {     // S_v of a block that is not this row's may be NaN
-            if (r < lo || r >= hi) e[0] = 0.f;
-            if (r + 1 < lo || r + 1 >= hi) e[1] = 0.f;
+            if (!in(r)) e[0] = 0.f;
+            if (!in(r + 1)) e[1] = 0.f;
         }
         sum += e[0];
         sum += e[1];
@@ -638,15 +685,19 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
         const f32x4 sc = scales_of(it);
         float ck = sc[u] * qs;
         const int g0 = it * TK + 32 * u + 16 * hf, lo = my_lo - g0, hi = my_hi - g0;
+        uint32_t seen = 0;
+        if constexpr (TREE && decltype(masked)::value)
+            seen = seen16(lines_of.line[f / a.group - first_node], g0, (int)tl.pos0, my_lo);
+        auto in = [&](int r) { return TREE ? (seen >> r & 1) != 0 : r >= lo && r < hi; };
         if constexpr (decltype(masked)::value) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] = (r >= lo && r < hi) ? s[r] * ck : -INFINITY;
+            for (int r = 0; r < 16; ++r) s[r] = in(r) ? s[r] * ck : -INFINITY;
             ck = 1.f;
 #pragma unroll
             for (int r = 0; r < 16; r += 2) top_of(s, top, r);
         }
         const float mx = max_halves(top * ck);
-        const bool mine = !decltype(masked)::value || (lo < 16 && hi > 0);
+        const bool mine = !decltype(masked)::value || (TREE ? seen != 0 : lo < 16 && hi > 0);
         const float big = max_halves(mine ? ssv[(it - s0) & 3][hf][u] : 0.f);
         if (__any(mx > limit || big > R)) move(mx, big);
         if (mine && sc[2 + u] != sc[2 + u]) poison = sc[2 + u];
@@ -654,7 +705,7 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
         Probs w;
         float sum = 0.f;
 #pragma unroll
-        for (int r = 0; r < 16; r += 2) pair(masked, s, ck, off, r, w, sum, lo, hi);
+        for (int r = 0; r < 16; r += 2) pair(masked, s, ck, off, r, w, sum, in);
         l += sum * exp2_fast(-lr);
         output(v0, u, w);
     };
@@ -1015,11 +1066,11 @@ int launch(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
         if (tr != TR) {
             static bool ready = false;    // more than 64 KB of LDS
             if (!ready) {
-                PTQ_HIP(hipFuncSetAttribute((const void*)attention_tile_kernel<T, D, TILE_WAVES>,
+                PTQ_HIP(hipFuncSetAttribute((const void*)attention_tile_kernel<T, D, TILE_WAVES, false>,
                                             hipFuncAttributeMaxDynamicSharedMemorySize, TileLds<D>::BYTES));
                 ready = true;
             }
-            hipLaunchKernelGGL((attention_tile_kernel<T, D, TILE_WAVES>), grid, dim3(64 * TILE_WAVES), TileLds<D>::BYTES, st,
+            hipLaunchKernelGGL((attention_tile_kernel<T, D, TILE_WAVES, false>), grid, dim3(64 * TILE_WAVES), TileLds<D>::BYTES, st,
                                a);
         } else if (p.nw == 8) {
             hipLaunchKernelGGL((attention_rows_kernel<T, D, 8>), grid, dim3(512), 0, st, a);
@@ -1093,6 +1144,40 @@ int run_attention_int8(const AttnPlan& p, const KVCacheInt8& c, const RaggedRows
         a.part_lse = ar.take<float>((size_t)a.nsplit * r.rows * heads);
     }
     return dtype == PTQ_F32 ? launch_dim<float>(a, p, st) : launch_dim<uint16_t>(a, p, st);
+}
+
+namespace {
+
+template <typename T, int D>
+int launch_tree(const AttnArgs& a, hipStream_t st) {
+    static bool ready = false;    // more than 64 KB of LDS
+    if (!ready) {
+        PTQ_HIP(hipFuncSetAttribute((const void*)attention_tile_kernel<T, D, TILE_WAVES, true>,
+                                    hipFuncAttributeMaxDynamicSharedMemorySize, TileLds<D>::BYTES));
+        ready = true;
+    }
+    const int64_t units = tile_units(a.g.rows, a.g.batch, a.group, ATTN_TILE) * a.kv_heads;
+    hipLaunchKernelGGL((attention_tile_kernel<T, D, TILE_WAVES, true>), dim3((unsigned)(units * a.nsplit)),
+                       dim3(64 * TILE_WAVES), TileLds<D>::BYTES, st, a);
+    PTQ_LAUNCH_CHECK();
+    return PTQ_OK;
+}
+
+}  // namespace
+
+int launch_attention_tree_tiles(const TreeArgs& t, int dtype, int dim, hipStream_t st) {
+    AttnArgs a{};
+    a.g = t.g;
+    a.table = t.table; a.width = t.width;
+    a.heads = t.heads; a.kv_heads = t.kv_heads; a.group = t.group;
+    a.dim = dim; a.bs = t.bs; a.bs_log2 = t.bs_log2; a.num_blocks = t.num_blocks;
+    a.k = t.k; a.v = t.v; a.ks = t.ks; a.vs = t.vs;
+    a.Q = t.Q; a.ldq = t.ldq; a.O = t.O; a.ldo = t.ldo; a.lse = t.lse;
+    a.scale2 = t.scale2;
+    a.causal = 1; a.window = t.window; a.parents = t.parents;
+    a.nsplit = t.nsplit; a.part = t.part; a.part_lse = t.part_lse;
+    if (dtype == PTQ_F32) return dim == 64 ? launch_tree<float, 64>(a, st) : launch_tree<float, 128>(a, st);
+    return dim == 64 ? launch_tree<uint16_t, 64>(a, st) : launch_tree<uint16_t, 128>(a, st);
 }
 
 }  // namespace ptq

@@ -23,26 +23,7 @@ namespace ptq {
 namespace {
 
 constexpr int WAVE_ROWS = 32;            // query rows (nodes x grouped heads) of a wave
-constexpr int NODES = TREE_NODES;
-// Words of a node's line of keys: 64 ones for what comes before the tree, then
-// a bit for each node (its ancestors and itself), then 64 zeros.
-constexpr int WORDS = 2 + NODES / 32 + 2;
-
-struct TreeArgs {
-    Ragged g;                             // g.starts: the lengths
-    const int32_t* parents;
-    const int32_t* table; int64_t width;
-    int heads, kv_heads, group, bs, bs_log2;
-    int64_t num_blocks;
-    const int8_t* k; const int8_t* v; const float* ks; const float* vs;
-    const void* Q; int64_t ldq;
-    void* O; int64_t ldo;
-    float* lse;                    // [rows, heads] or null
-    float scale2;                  // softmax scale * log2(e)
-    int64_t window;
-    int nsplit;
-    float* part; float* part_lse;  // [nsplit][rows * heads][dim], [nsplit][rows * heads]
-};
+constexpr int TILE_RG = ATTN_TILE / WAVE_ROWS;      // tiles of attention_int8.hip
 
 // One tile of query rows: flat rows f0 .. f0 + tr of sequence b, flat row =
 // node * group + head within the group.
@@ -173,11 +154,11 @@ template <typename T>
 constexpr int blocks_of(int dim) { return dim <= (sizeof(T) == 4 ? 64 : 128) ? 2 : 1; }
 constexpr int waves_of(int dim) { return dim <= 128 ? 2 : 1; }
 
-// Chunks of 16 bytes in LDS, C a row: chunk c of row r lies at c ^ swizzle(r), so that the same chunk of 8 neighbours is in
-// all banks.
+// Chunks of 16 bytes in LDS, C a row: chunk c of row r lies at c ^ swizzle(r), so that the same chunk of 16 neighbours is
+// in all 64 banks.
 template <int C>
 __device__ __forceinline__ int swizzle(int r) {
-    return C >= 8 ? r & 7 : (r / (8 / C)) & (C - 1);
+    return (r / (16 / C)) & (C - 1);
 }
 
 // One step of keys in LDS: K in the order of the operand's rows, in chunks of 16 channels, and V in chunks of 8 keys of a
@@ -211,8 +192,7 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
     constexpr bool STAGED = RG == 4;
     static_assert(RG * TG == NW && (!STAGED || TG == 1), "rows and steps are dealt to waves");
     constexpr bool FOLD = NT == 1;       // S_v / R goes into the exponent
-    __shared__ uint32_t line[ROWS][WORDS + 1];      // an odd stride
-    __shared__ int16_t parent[NODES], level[ROWS];      // level: depth of a node, negative: no valid way up
+    __shared__ TreeLines<ROWS> lines_of;
 
     const int split = (int)(blockIdx.x % (unsigned)a.nsplit);
     const unsigned tile = blockIdx.x / (unsigned)a.nsplit;
@@ -271,7 +251,7 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
         auto koff = [&](int i) {      // from the first key of a step in one block
             return ((krow(i) & ~31) + key_of_row(krow(i) & 31)) * D + 16 * ((lane % KC) ^ swizzle<KC>(krow(i)));
         };
-        const int vd = lane / VC, vg = (lane % VC) ^ swizzle<VC>(vd);      // 64 / VC channels a copy, a multiple of 8
+        const int vd = lane / VC, vg = (lane % VC) ^ swizzle<VC>(vd);      // 64 / VC channels a copy, a multiple of 16
         const int voff = vd * a.bs + 16 * vg;
         if (one_block) {
             const int id = __builtin_amdgcn_readfirstlane(entry(it * TK)), from = (it * TK) & bmask;
@@ -320,39 +300,11 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
     int lo = 0;
     bool broken = tl.bad;
     if (lines) {
-#pragma unroll
-        for (int i = 0; i < PN; ++i)
-            if (t + i * NTH < tl.nodes) parent[t + i * NTH] = (int16_t)(up[i] >= -1 && up[i] < NODES ? up[i] : NODES);
         const int count = std::min(tl.f0 + ROWS - 1, tl.rows - 1) / a.group - first_node + 1;
-        for (int i = t; i < count * WORDS; i += NTH) line[i / WORDS][i % WORDS] = i % WORDS < 2 ? ~0u : 0u;
-        __syncthreads();
-        if (t < count) {
-            // ancestors come in falling order: a word is done when the walk leaves it
-            int j = first_node + t, depth = 0, word = j >> 5;
-            uint32_t bits = 0;
-            bool fine = true;
-            while (true) {
-                const int p = parent[j];
-                if (j >> 5 != word) {
-                    line[t][2 + word] = bits;
-                    word = j >> 5;
-                    bits = 0;
-                }
-                if (a.window <= 0 || depth < a.window) bits |= 1u << (j & 31);
-                if (p >= j) fine = false;
-                if (p >= j || p < 0) break;
-                j = p;
-                ++depth;
-            }
-            line[t][2 + word] = bits;
-            level[t] = (int16_t)(fine ? depth : -1);
-        }
-        __syncthreads();
-        const int depth = level[node - first_node];
+        build_lines<NTH>(lines_of, up, tl.nodes, first_node, count, a.window, t);
+        const int depth = lines_of.level[node - first_node];
         broken = depth < 0;
-        // of the keys before the tree: the walk has left out the ancestors that the window does
-        if (a.window > 0)
-            lo = (int)std::min<int64_t>(tl.base, std::max<int64_t>(0, tl.base + std::max(depth, 0) - a.window + 1));
+        lo = first_key(tl.base, depth, a.window);
     }
     const int lo_max = a.window > 0 ? (int)std::max<int64_t>(0, tl.base + (int64_t)tl.nodes - a.window) : 0;   // of the deepest row
     // a round is one step of each group; rounds [whole, last) have steps that no row masks alone
@@ -406,12 +358,7 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
             ck[u] = sk[u] * qs;
             seen[u] = 0xffffu;
             if constexpr (MASK) {
-                const int tv = it * TK + 32 * u + 16 * hf;
-                const int o = std::min(std::max(tv - tl.base, -64) + 64, 32 * (WORDS - 2));      // the last two words are 0
-                const uint32_t* w = &line[node - first_node][o >> 5];
-                seen[u] = (uint32_t)((((uint64_t)w[1] << 32 | w[0]) >> (o & 31)) & 0xffffu);
-                if (tv + 16 <= tl.base) seen[u] = 0xffffu;      // there need be no lines
-                if (tv < lo) seen[u] &= lo - tv < 16 ? 0xffffu << (lo - tv) : 0u;
+                seen[u] = seen16(lines_of.line[node - first_node], it * TK + 32 * u + 16 * hf, tl.base, lo);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[u][r] = seen[u] >> r & 1 ? s[u][r] * ck[u] : -INFINITY;
                 ck[u] = 1.f;
@@ -500,29 +447,17 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
         uint4 rk[KN], rv[VN];
         int idk[KN] = {}, idv = 0, id_of = 0;       // blocks of the step to fetch next; idv of the step in registers
         auto ids = [&](int it) __attribute__((always_inline)) {
-            idv = entry(it * TK + 16 * vg);
-            if (!one_block)
 #pragma unroll
-                for (int i = 0; i < KN; ++i) idk[i] = entry(it * TK + kkey(i));
+            for (int i = 0; i < KN; ++i) idk[i] = entry(it * TK + kkey(i));
+            idv = entry(it * TK + 16 * vg);
         };
         auto fetch = [&](int it) __attribute__((always_inline)) {
-            if (one_block) {
-                const int id = __builtin_amdgcn_readfirstlane(idv), from = (it * TK) & bmask;
-                const int8_t* kb = kp + place(id, from * D);
-                const int8_t* vb = vp + place(id, from);
 #pragma unroll
-                for (int i = 0; i < KN; ++i) rk[i] = *(const uint4*)(kb + (unsigned)(kkey(i) * D + 16 * kc));
+            for (int i = 0; i < KN; ++i)
+                rk[i] = *(const uint4*)(kp + place(idk[i], ((it * TK + kkey(i)) & bmask) * D + 16 * kc));
+            const int8_t* from = vp + place(idv, vd * a.bs + ((it * TK + 16 * vg) & bmask));
 #pragma unroll
-                for (int i = 0; i < VN; ++i)
-                    rv[i] = *(const uint4*)(vb + (unsigned)((vd + i * (NTH / VC)) * a.bs + 16 * vg));
-            } else {
-#pragma unroll
-                for (int i = 0; i < KN; ++i)
-                    rk[i] = *(const uint4*)(kp + place(idk[i], ((it * TK + kkey(i)) & bmask) * D + 16 * kc));
-                const int8_t* from = vp + place(idv, vd * a.bs + ((it * TK + 16 * vg) & bmask));
-#pragma unroll
-                for (int i = 0; i < VN; ++i) rv[i] = *(const uint4*)(from + i * (NTH / VC) * a.bs);
-            }
+            for (int i = 0; i < VN; ++i) rv[i] = *(const uint4*)(from + i * (NTH / VC) * a.bs);
             rsk[0] = a.ks[scale_at(idv)];
             rsv[0] = a.vs[scale_at(idv)];
             id_of = idv;
@@ -692,7 +627,7 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
 // time with all their loads at once; tr: rows of the tiles that were split.
 template <typename T, int D, int RG>
 __global__ __launch_bounds__(256) void attention_tree_join_kernel(TreeArgs a) {
-    constexpr int tr = WAVE_ROWS * RG, TK = 32 * blocks_of<T>(D);
+    constexpr int tr = WAVE_ROWS * RG, TK = RG == TILE_RG ? ptq::TK : 32 * blocks_of<T>(D);
     const unsigned part = blockIdx.x % (unsigned)(tr / 16), tile = blockIdx.x / (unsigned)(tr / 16);
     const int h = (int)(tile % (unsigned)a.kv_heads);
     TreeTile tl;
@@ -749,8 +684,12 @@ template <typename T, int D, int RG, int NW>
 int launch_tiles(const TreeArgs& a, hipStream_t st) {
     const int tr = WAVE_ROWS * RG;
     const int64_t units = tile_units(a.g.rows, a.g.batch, a.group, tr) * a.kv_heads;
-    hipLaunchKernelGGL((attention_tree_kernel<T, D, RG, NW>), dim3((unsigned)(units * a.nsplit)), dim3(64 * NW), 0, st, a);
-    PTQ_LAUNCH_CHECK();
+    if constexpr (RG == TILE_RG) {
+        PTQ_TRY(launch_attention_tree_tiles(a, sizeof(T) == 4 ? PTQ_F32 : PTQ_BF16, D, st));
+    } else {
+        hipLaunchKernelGGL((attention_tree_kernel<T, D, RG, NW>), dim3((unsigned)(units * a.nsplit)), dim3(64 * NW), 0, st, a);
+        PTQ_LAUNCH_CHECK();
+    }
     if (a.nsplit > 1) {
         hipLaunchKernelGGL((attention_tree_join_kernel<T, D, RG>), dim3((unsigned)(units * (tr / 16))), dim3(256), 0, st, a);
         PTQ_LAUNCH_CHECK();
@@ -760,10 +699,12 @@ int launch_tiles(const TreeArgs& a, hipStream_t st) {
 
 template <typename T, int D>
 int launch(const TreeArgs& a, const TreePlan& p, hipStream_t st) {
+    if constexpr (D <= 128) {
+        if (p.rg == TILE_RG) return launch_tiles<T, D, TILE_RG, TILE_RG>(a, st);
+        if (p.nw == 8) return launch_tiles<T, D, 1, 8>(a, st);
+    }
     if (p.rg == 4) return launch_tiles<T, D, 4, 4>(a, st);
     if (p.rg == 2) return launch_tiles<T, D, 2, 4>(a, st);
-    if constexpr (D <= 128)
-        if (p.nw == 8) return launch_tiles<T, D, 1, 8>(a, st);
     return launch_tiles<T, D, 1, 4>(a, st);
 }
 

@@ -277,8 +277,9 @@ int run_attention_int8(const AttnPlan& p, const KVCacheInt8& c, const RaggedRows
                        float* lse, void* ws, size_t ws_bytes, hipStream_t st);
 
 // Attention of trees of drafted tokens over the cache (attention_tree.hip):
-// tiles of 32 rg query rows (rg 1, 2 or 4), workgroups of nw waves (4; for rg 1
-// 8, too, up to 128 channels), nsplit splits of the keys.
+// tiles of 32 rg query rows (rg 1, 2, 4; up to 128 channels 8, the tiles of
+// attention_int8.hip), workgroups of nw waves (4; 8 for rg 8 and, up to 128
+// channels, for rg 1, too), nsplit splits of the keys.
 constexpr int TREE_NODES = 512;     // of a sequence, at most
 struct TreePlan {
     int rg, nw, nsplit;

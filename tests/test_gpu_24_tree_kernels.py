@@ -1,0 +1,80 @@
+"""GPU: every kernel of attention_int8_tree by name (the hook in include/ptq_testing.h), with and without splits, against the
+fp64 oracle within the bounds of test_gpu_22_attention_tree.py, which reaches the ones that the estimates choose."""
+import pytest
+import torch
+
+from gpu_util import announce
+from test_gpu_22_attention_tree import _check, _make, _trees
+
+pytestmark = pytest.mark.gpu
+
+PLANS = [(1, 4, 1), (1, 4, 5), (1, 8, 1), (1, 8, 3), (2, 4, 1), (2, 4, 4), (4, 4, 1), (4, 4, 3), (8, 8, 1), (8, 8, 3)]
+SHAPES = [(64, 16), (64, 64), (128, 16), (128, 128), (256, 16), (256, 32)]
+
+
+def _fits(plan, dim):
+    return dim <= 128 or plan[1] == 4
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [0, 90])
+@pytest.mark.parametrize("plan,dim,bs", [(p, d, b) for p in PLANS for d, b in SHAPES if _fits(p, d)])
+def test_kernel(gpu, plan, dim, bs, window, dtype):
+    from post_int4_weight_amd import api
+    announce(f"attention tree kernel={plan} dim={dim} bs={bs} window={window} {dtype}")
+    # trees over the edges of steps, blocks and tiles; single nodes, no nodes, no keys before the tree
+    prefix, nodes = [1000, 0, 250, 63, 31, 129], [45, 70, 1, 0, 17, 3]
+    trees = _trees(nodes, 4, dim + window)
+    Q, cache, args, vals = _make(api, gpu, prefix, trees, 6, 2, dim, bs, dtype, 7)
+    O, lse = api._test_attention_int8_tree(*plan, Q, cache, *args, window=window)
+    again, _ = api._test_attention_int8_tree(*plan, Q, cache, *args, window=window)
+    torch.cuda.synchronize()
+    _check(O, lse, Q, vals, trees, 6, 2, dim ** -0.5, window)
+    assert torch.equal(O, again)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("plan,dim", [(p, d) for p in PLANS for d in (64, 128, 256) if _fits(p, d)])
+def test_rows_by_themselves(gpu, plan, dim, dtype):
+    """NaN queries, bad parents, scales that are not finite or huge: they reach the rows that see them, and no bit of others."""
+    from post_int4_weight_amd import api
+    announce(f"attention tree kernel={plan} dim={dim} {dtype}, rows by themselves")
+    parents = [-1] + [i // 2 for i in range(15)] + [3] * 16      # two blocks of the cache
+    Q, cache, args, _ = _make(api, gpu, [496, 80], [parents, parents[:16]], 4, 2, dim, 16, dtype, 9)
+    run = lambda q=Q, flat=args[3]: api._test_attention_int8_tree(*plan, q, cache, *args[:3], flat)
+    want, wl = run()
+    torch.cuda.synchronize()
+    assert torch.isfinite(want).all()
+
+    def others(hit, got):
+        hit = hit[:, None].expand(48, 4) if hit.dim() == 1 else hit
+        assert torch.isnan(got[0][hit]).all() and torch.equal(got[0][~hit], want[~hit]) and torch.equal(got[1][~hit], wl[~hit])
+    hit = torch.zeros(48, 4, dtype=torch.bool, device=gpu)
+    q = Q.clone()
+    q[5, 2, 7], q[40, 0, 0] = float("nan"), float("inf")
+    hit[5, 2] = hit[40, 0] = True
+    others(hit, run(q=q))
+    flat = args[3].clone()
+    flat[8] = 8      # and no node hangs below it
+    others(torch.arange(48, device=gpu) == 8, run(flat=flat))
+    at = int(args[2][0, 32])       # keys 512 .. 527: nodes 16 .. 31 of the first tree
+    low = (torch.arange(48, device=gpu) >= 16) & (torch.arange(48, device=gpu) < 32)
+    for scales in (cache.k_scales, cache.v_scales):
+        for value in (float("nan"), float("inf"), 1e30):
+            keep = scales[at].clone()
+            scales[at] = value
+            got = run()
+            torch.cuda.synchronize()
+            scales[at] = keep
+            if value == 1e30:
+                assert torch.equal(got[0][~low], want[~low]) and torch.equal(got[1][~low], wl[~low])
+            else:
+                others(low, got)
+
+
+def test_hook_refuses(gpu):
+    from post_int4_weight_amd import api
+    Q, cache, args, _ = _make(api, gpu, [30], [[-1, 0]], 2, 1, 256, 16, "bf16", 3)
+    for plan in ((3, 4, 1), (1, 2, 1), (2, 8, 1), (8, 4, 1), (1, 8, 1), (8, 8, 1), (1, 4, 0), (1, 4, 65)):
+        with pytest.raises(api.PTQError):
+            api._test_attention_int8_tree(*plan, Q, cache, *args)
