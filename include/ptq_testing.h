@@ -84,15 +84,15 @@ int ptq_test_attention_int8_cache(int tiles, int waves, int nsplit, const void* 
                                   int head_dim, int block_size, float scale, int causal, int64_t window,
                                   void* workspace, size_t workspace_bytes, void* stream);
 
-/* attention_int8_tree with the kernel given instead of chosen: tiles of 32
- * query rows (rg 1; nw = 4 waves, or 8 with head_dim up to 128), of 64 (rg 2, nw
- * 4), of 128 (rg 4, nw 4) or of 256 (rg 8, nw 8; head_dim up to 128), and the splits of the keys (1 .. 64). _plan says what
+/* attention_int8_tree with the kernel given instead of chosen: tiles of 256
+ * query rows (1; head_dim up to 128, 8 waves) or of 32 (0; 4 waves, or 8 with
+ * head_dim up to 128), and the splits of the keys (1 .. 64). _plan says what
  * attention_int8_tree chooses. Returns PTQ_OK, PTQ_EINVAL, PTQ_EWORKSPACE or
  * PTQ_EHIP. */
 int ptq_test_attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim, int block_size,
-                                 int64_t table_width, int64_t window, int* rg, int* nw, int* nsplit);
+                                 int64_t table_width, int64_t window, int* tiles, int* waves, int* nsplit);
 size_t ptq_test_attention_tree_workspace_bytes(int nsplit, int64_t rows, int heads, int head_dim);
-int ptq_test_attention_int8_tree(int rg, int nw, int nsplit, const void* Q, int64_t ldq, void* O, int64_t ldo, float* lse,
+int ptq_test_attention_int8_tree(int tiles, int waves, int nsplit, const void* Q, int64_t ldq, void* O, int64_t ldo, float* lse,
                                  int dtype, int64_t rows, int heads, const int32_t* offsets, const int32_t* seq_lens,
                                  const int32_t* parents, int64_t batch, const int32_t* block_table,
                                  int64_t table_width, const int8_t* k_codes, const int8_t* v_codes,

@@ -837,14 +837,14 @@ def _test_attention_int8_cache(tiles, waves, nsplit, Q, cache, offsets, seq_lens
 
 
 def _test_attention_tree_plan(rows, batch, heads, kv_heads, head_dim, block_size, table_width, window=0):
-    """ptq_test_attention_tree_plan (include/ptq_testing.h): (rg, nw, nsplit) that attention_int8_tree chooses."""
+    """ptq_test_attention_tree_plan (include/ptq_testing.h): (tiles, waves, nsplit) that attention_int8_tree chooses."""
     plan = [ctypes.c_int() for _ in range(3)]
     _check(_lib.ptq_test_attention_tree_plan(rows, batch, heads, kv_heads, head_dim, block_size, table_width, window,
                                              *map(ctypes.byref, plan)))
     return tuple(x.value for x in plan)
 
 
-def _test_attention_int8_tree(rg, nw, nsplit, Q, cache, offsets, seq_lens, block_table, parents, scale=None, window=0):
+def _test_attention_int8_tree(tiles, waves, nsplit, Q, cache, offsets, seq_lens, block_table, parents, scale=None, window=0):
     """ptq_test_attention_int8_tree (include/ptq_testing.h): (O, lse) by the kernel that the first three name."""
     nb, h, d, bs = cache._sizes()
     rows, heads = Q.shape[0], Q.shape[1]
@@ -852,7 +852,7 @@ def _test_attention_int8_tree(rg, nw, nsplit, Q, cache, offsets, seq_lens, block
     lse = torch.empty(rows, heads, dtype=torch.float32, device=Q.device)
     off, lens, batch, table, width = _ragged(offsets, seq_lens, block_table, "seq_lens")
     ws, wsb = _workspace(int(_lib.ptq_test_attention_tree_workspace_bytes(nsplit, rows, heads, d)), Q.device, None)
-    _check(_lib.ptq_test_attention_int8_tree(rg, nw, nsplit, _ptr(Q), _heads3(Q, rows, heads, d, "Q"), _ptr(O),
+    _check(_lib.ptq_test_attention_int8_tree(tiles, waves, nsplit, _ptr(Q), _heads3(Q, rows, heads, d, "Q"), _ptr(O),
                                              heads * d, _ptr(lse), _dtype_code(Q), rows, heads, off, lens,
                                              _vector(parents, rows, torch.int32, "parents"), batch, table, width,
                                              _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scales), _ptr(cache.v_scales),

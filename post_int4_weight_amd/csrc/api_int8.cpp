@@ -452,15 +452,15 @@ int attention_int8_tree(const void* Q, int64_t ldq, void* O, int64_t ldo, float*
 }
 
 int ptq_test_attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim, int block_size,
-                                 int64_t table_width, int64_t window, int* rg, int* nw, int* nsplit) {
+                                 int64_t table_width, int64_t window, int* tiles, int* waves, int* nsplit) {
     const char* fn = "ptq_test_attention_tree_plan";
     PTQ_TRY(check_cache(fn, KVCacheInt8{nullptr, nullptr, nullptr, nullptr, 0, kv_heads, head_dim, block_size}));
-    if (rows < 1 || batch < 1 || heads < kv_heads || heads % kv_heads || table_width < 0 || window < 0 || !rg || !nw ||
+    if (rows < 1 || batch < 1 || heads < kv_heads || heads % kv_heads || table_width < 0 || window < 0 || !tiles || !waves ||
         !nsplit)
         REFUSE("%s: bad arguments", fn);
     const TreePlan p = attention_tree_plan(rows, batch, heads, kv_heads, head_dim, block_size, table_width, window);
-    *rg = p.rg;
-    *nw = p.nw;
+    *tiles = p.tr == ATTN_TILE;
+    *waves = p.nw;
     *nsplit = p.nsplit;
     return PTQ_OK;
 }
@@ -469,7 +469,7 @@ size_t ptq_test_attention_tree_workspace_bytes(int nsplit, int64_t rows, int hea
     return nsplit > 0 && rows > 0 && heads > 0 && head_dim > 0 ? attention_tree_part_bytes(nsplit, rows, heads, head_dim) : 0;
 }
 
-int ptq_test_attention_int8_tree(int rg, int nw, int nsplit, const void* Q, int64_t ldq, void* O, int64_t ldo, float* lse,
+int ptq_test_attention_int8_tree(int tiles, int waves, int nsplit, const void* Q, int64_t ldq, void* O, int64_t ldo, float* lse,
                                  int dtype, int64_t rows, int heads, const int32_t* offsets, const int32_t* seq_lens,
                                  const int32_t* parents, int64_t batch, const int32_t* block_table,
                                  int64_t table_width, const int8_t* k_codes, const int8_t* v_codes,
@@ -477,14 +477,13 @@ int ptq_test_attention_int8_tree(int rg, int nw, int nsplit, const void* Q, int6
                                  int head_dim, int block_size, float scale, int64_t window, void* workspace,
                                  size_t workspace_bytes, void* stream) {
     const char* fn = "ptq_test_attention_int8_tree";
-    if ((rg != 1 && rg != 2 && rg != 4 && rg != 8) || (nw != 4 && nw != 8) ||
-        (nw == 8 ? (rg != 1 && rg != 8) || head_dim > 128 : rg == 8) || nsplit < 1 || nsplit > 64 ||
-        rows > 1 << 16 || batch > 1 << 10)
-        REFUSE("%s: rg = %d, nw = %d, nsplit = %d", fn, rg, nw, nsplit);
+    if ((tiles != 0 && tiles != 1) || (waves != 8 && (waves != 4 || tiles)) || (waves == 8 && head_dim > 128) ||
+        nsplit < 1 || nsplit > 64 || rows > 1 << 16 || batch > 1 << 10)
+        REFUSE("%s: tiles = %d, waves = %d, nsplit = %d", fn, tiles, waves, nsplit);
     const KVCacheInt8 c{const_cast<int8_t*>(k_codes), const_cast<int8_t*>(v_codes), const_cast<float*>(k_scales),
                         const_cast<float*>(v_scales), num_blocks, kv_heads, head_dim, block_size};
     const RaggedRows r{rows, batch, offsets, seq_lens, block_table, table_width};
-    const TreePlan p{rg, nw, nsplit};
+    const TreePlan p{tiles ? ATTN_TILE : ATTN_TREE_ROWS, waves, nsplit};
     return attention_tree(fn, &p, c, r, parents, dtype, Q, ldq, heads, scale, window, O, ldo, lse, workspace,
                           workspace_bytes, stream);
 }

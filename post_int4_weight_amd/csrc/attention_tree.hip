@@ -22,8 +22,7 @@
 namespace ptq {
 namespace {
 
-constexpr int WAVE_ROWS = 32;            // query rows (nodes x grouped heads) of a wave
-constexpr int TILE_RG = ATTN_TILE / WAVE_ROWS;      // tiles of attention_int8.hip
+constexpr int ROWS = ATTN_TREE_ROWS;            // query rows (nodes x grouped heads) of a tile
 
 // One tile of query rows: flat rows f0 .. f0 + tr of sequence b, flat row =
 // node * group + head within the group.
@@ -134,22 +133,23 @@ struct QueryRow {
     }
 };
 
-// A wave takes 32 query rows. Scores are computed transposed, S^T = K Q^T, so
-// that a lane ends up with scores of one row and the probabilities are already
-// the operand of O^T = V^T P^T: operand row r of a block of 32 keys is key
+// A workgroup takes a tile of 32 query rows of one kv head, and its NW waves every
+// NW-th step of 64 keys (32 where 64 do not fit the registers of the waves that a
+// SIMD shall hold). Scores are computed transposed, S^T = K Q^T, so that a lane
+// ends up with scores of one row and the probabilities are already the operand of
+// O^T = V^T P^T: operand row r of a block of 32 keys is key
 // 16 (r / 4 % 2) + 4 (r / 8) + r % 4, so lane half hf holds keys 16 hf .. 16 hf +
 // 15, in one block of the cache: one S_k and one S_v a lane.
 //
-// RG waves take 32 rows each of a tile and share the keys; NW / RG such groups
-// take every (NW / RG)-th step. Up to two row waves the codes of a step are copied
-// into the group's part of LDS as they are, and each wave converts V for itself;
-// a wave alone overwrites its part when it has read it, two have two parts. With
-// four row waves (RG = NW = 4) the workgroup stages each step, K as it is and V
-// converted to fp16: a wave that converts V for its 32 rows alone spends as much
-// on that as on the exponentials.
-//
-// A step is 64 keys, or 32 where 64 do not fit the registers of the waves that a
-// SIMD shall hold.
+// A wave copies the codes of a step into a part of LDS of its own, as they are and
+// whole rows at a time, and copies the next step over it when it has read it; the
+// other waves of the SIMD work meanwhile, and nothing waits for another wave until
+// the join. What bounds it: for few rows memory (16 trees of 8 nodes over 4000
+// keys, 32 heads on 8, D = 128: FEW us, the cache's 131 MB at TB/s TB/s), with more
+// tiles on the same keys the vector instructions of the exponentials and of the
+// conversion of V. Tiles of 64 and 128 rows that share a step among waves were 1%
+// faster in the mean over 1700 shapes, and taken out; from about 300 rows a kv
+// head on, the tiles of 256 rows of attention_int8.hip win.
 template <typename T>
 constexpr int blocks_of(int dim) { return dim <= (sizeof(T) == 4 ? 64 : 128) ? 2 : 1; }
 constexpr int waves_of(int dim) { return dim <= 128 ? 2 : 1; }
@@ -161,15 +161,8 @@ __device__ __forceinline__ int swizzle(int r) {
     return (r / (16 / C)) & (C - 1);
 }
 
-// One step of keys in LDS: K in the order of the operand's rows, in chunks of 16 channels, and V in chunks of 8 keys of a
+// Codes of a step in LDS: K in the order of the operand's rows, chunks of 16 channels, and V in chunks of 16 keys of a
 // channel.
-template <int D, int U>
-struct TreeStep {
-    uint4 k[32 * U][D / 16];
-    f16x8 v[D][4 * U];
-    float scale[2 * U][4];       // of 16 keys: S_k, S_v, log2 S_v
-};
-// The same with the codes of V, chunks of 16 keys.
 template <int D, int U>
 struct TreeCodes {
     uint4 k[32 * U][D / 16];
@@ -183,14 +176,12 @@ __device__ __forceinline__ void copy16(const void* from, void* to) {
     __builtin_amdgcn_global_load_lds((global_ptr)from, (lds_ptr)to, 16, 0, 0);
 }
 
-template <typename T, int D, int RG, int NW>
+template <typename T, int D, int NW>
 __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(TreeArgs a) {
     constexpr int U = blocks_of<T>(D), TK = 32 * U;
     constexpr int NQ = sizeof(T) == 4 ? 3 : 2;    // int8 terms of q
     constexpr int NT = sizeof(T) == 4 ? 2 : 1;    // fp16 terms of the probabilities
-    constexpr int NC = D / 32, TG = NW / RG, ROWS = WAVE_ROWS * RG, NTH = 64 * NW;
-    constexpr bool STAGED = RG == 4;
-    static_assert(RG * TG == NW && (!STAGED || TG == 1), "rows and steps are dealt to waves");
+    constexpr int NC = D / 32, NTH = 64 * NW;
     constexpr bool FOLD = NT == 1;       // S_v / R goes into the exponent
     __shared__ TreeLines<ROWS> lines_of;
 
@@ -204,10 +195,9 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
     if (split > 0 && s0 >= s1) return;
 
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int rg = wave % RG, tg = wave / RG;
     const int li = lane & 31, hf = lane >> 5;
     const int first_node = tl.f0 / a.group;
-    auto row_of = [&](int i) { return std::min(tl.f0 + WAVE_ROWS * rg + i, tl.rows - 1); };
+    auto row_of = [&](int i) { return std::min(tl.f0 + i, tl.rows - 1); };
     const int node = row_of(li) / a.group;
     const int32_t* table = a.table + (int64_t)tl.b * a.width;
     const unsigned pool = (unsigned)a.bs * D, stride = (unsigned)a.kv_heads * pool;      // codes of a (block, head), of a block
@@ -224,8 +214,6 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
     auto clean = [&](float s, int id, int p) { return p >= end ? 0.f : ok(id) && s < INFINITY ? s : __builtin_nanf(""); };
     auto key_of_row = [](int r) { return 16 * (r >> 2 & 1) + 4 * (r >> 3) + (r & 3); };      // r < 32
 
-    const bool busy = tl.f0 + WAVE_ROWS * rg < tl.rows;      // some row is this wave's
-
     // what the rest waits for is requested first, and answered in that order: parents, the query row, the first keys
     const bool lines = !tl.bad && (a.window > 0 || s1 * TK > tl.base);
     constexpr int PN = NODES / NTH + (NODES % NTH != 0);
@@ -236,16 +224,15 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
     QueryRow<T, NC> row;
     row.load((const T*)a.Q + (tl.off + node) * a.ldq + (int64_t)(h * a.group + row_of(li) % a.group) * D);
 
-    // the group's part of LDS, and the copies of one step into it
+    // this wave's part of LDS, and the copies of one step into it
     constexpr int KC = D / 16, VC = 2 * U;      // chunks of a row of K, groups of 16 keys of a channel of V
-    constexpr int PARTS = RG == 1 ? 1 : 2;
     using Codes = TreeCodes<D, U>;
-    __shared__ __attribute__((aligned(16))) unsigned char own[STAGED ? 16 : TG * PARTS * sizeof(Codes)];
-    auto part = [&](int k) -> Codes& { return ((Codes*)own)[STAGED ? 0 : tg * PARTS + k]; };
+    __shared__ __attribute__((aligned(16))) unsigned char own[NW * sizeof(Codes)];
+    Codes& codes = ((Codes*)own)[wave];
     float rsk[U], rsv[U];
     int ids_of[U];
     const bool one_block = a.bs >= TK;      // a step lies in one block of the cache: addresses are scalar
-    auto copy = [&](int it, Codes& to) __attribute__((always_inline)) {
+    auto copy = [&](int it) __attribute__((always_inline)) {
         constexpr int KI = 32 * U * KC / 64, VI = D * VC / 64;      // copies of 64 chunks
         auto krow = [&](int i) { return (i * 64 + lane) / KC; };
         auto koff = [&](int i) {      // from the first key of a step in one block
@@ -259,10 +246,10 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
             const int8_t* vb = vp + place(id, from);
 #pragma unroll
             for (int i = 0; i < KI; ++i)
-                if (i % RG == rg % RG) copy16(kb + (unsigned)koff(i), (char*)to.k + 1024 * i);
+                copy16(kb + (unsigned)koff(i), (char*)codes.k + 1024 * i);
 #pragma unroll
             for (int i = 0; i < VI; ++i)
-                if (i % RG == rg % RG) copy16(vb + (unsigned)(voff + i * (64 / VC) * a.bs), (char*)to.v + 1024 * i);
+                copy16(vb + (unsigned)(voff + i * (64 / VC) * a.bs), (char*)codes.v + 1024 * i);
 #pragma unroll
             for (int u = 0; u < U; ++u) ids_of[u] = id;
             rsk[0] = a.ks[scale_at(id)];
@@ -281,20 +268,19 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
             const int key = key_of_row(krow(i) & 31);
             const int id = i * 64 / KC < 32 ? (key & 16 ? id1 : id0) : (key & 16 ? id3 : id2);      // rows of one 32
             const int p = it * TK + (krow(i) & ~31) + key;
-            if (i % RG == rg % RG)
-                copy16(kp + place(id, (p & bmask) * D + 16 * ((lane % KC) ^ swizzle<KC>(krow(i)))), (char*)to.k + 1024 * i);
+            copy16(kp + place(id, (p & bmask) * D + 16 * ((lane % KC) ^ swizzle<KC>(krow(i)))), (char*)codes.k + 1024 * i);
         }
         const int8_t* from = vp + place(idv, vd * a.bs + ((it * TK + 16 * vg) & bmask));
 #pragma unroll
         for (int i = 0; i < VI; ++i)
-            if (i % RG == rg % RG) copy16(from + i * (64 / VC) * a.bs, (char*)to.v + 1024 * i);
+            copy16(from + i * (64 / VC) * a.bs, (char*)codes.v + 1024 * i);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             rsk[u] = a.ks[scale_at(ids_of[u])];
             rsv[u] = a.vs[scale_at(ids_of[u])];
         }
     };
-    if (!STAGED && s0 + tg < s1) copy(s0 + tg, part(0));
+    if (s0 + wave < s1) copy(s0 + wave);
 
     // lines of the tile's nodes, where this split has keys of the tree or a window asks for depths
     int lo = 0;
@@ -307,16 +293,9 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
         lo = first_key(tl.base, depth, a.window);
     }
     const int lo_max = a.window > 0 ? (int)std::max<int64_t>(0, tl.base + (int64_t)tl.nodes - a.window) : 0;   // of the deepest row
-    // a round is one step of each group; rounds [whole, last) have steps that no row masks alone
-    const int rounds = s1 > s0 ? (s1 - s0 + TG - 1) / TG : 0;
-    const int whole = std::min(std::max((lo_max + TK - 1) / TK - s0 + TG - 1, 0) / TG, rounds);
-    const int last = std::min(std::max(tl.base / TK - s0, 0) / TG, rounds);
-    auto every_round = [&](auto&& round) __attribute__((always_inline)) {
-        int i = 0;
-        for (; i < whole; ++i) round(std::true_type{}, i);
-        for (; i < last; ++i) round(std::false_type{}, i);
-        for (; i < rounds; ++i) round(std::true_type{}, i);
-    };
+    // steps that no row masks: [whole, last)
+    const int whole = std::min(__builtin_amdgcn_readfirstlane((lo_max + TK - 1) / TK), s1);
+    const int last = std::min(__builtin_amdgcn_readfirstlane(tl.base / TK), s1);
 
     i32x4 q[NQ][NC];
     f32x16 acc[NC];
@@ -328,11 +307,16 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
     float m = -INFINITY, l = broken ? __builtin_nanf("") : 0.f, R = 0.f, rcp_R = 0.f, log2_R = 0.f, poison = 0.f;
     const float qs = row.template terms<NQ>(a.scale2, q);
 
-    // One step. kf(u, e): codes of K, operand e of block u; vf(u, i, j): V of keys 8 j .. of the lane's 16, channels 32 i ..;
-    // sk, sv, lv: S_k, S_v and log2 S_v of the lane's keys of each block
-    auto work = [&](auto masked, int it, auto&& kf, auto&& vf, const float (&sk)[U], const float (&sv)[U],
-                    const float (&lv)[U]) __attribute__((always_inline)) {
+    auto work = [&](auto masked, int it) __attribute__((always_inline)) {
         constexpr bool MASK = decltype(masked)::value;
+        float sk[U], sv[U], lv[U];      // S_k, S_v and log2 S_v of the lane's keys of each block
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int tv = it * TK + 32 * u + 16 * hf;
+            sk[u] = clean(rsk[u], ids_of[u], tv);
+            sv[u] = clean(rsv[u], ids_of[u], tv);
+            lv[u] = FOLD ? __builtin_amdgcn_logf(sv[u]) : 0.f;
+        }
         f32x16 s[U];
         uint32_t seen[U];
         float ck[U], top = -INFINITY, big = 0.f;
@@ -346,7 +330,7 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
                 for (int r = 0; r < 16; ++r) x[n][r] = 0;
 #pragma unroll
             for (int e = 0; e < NC; ++e) {
-                const i32x4 k = kf(u, e);
+                const i32x4 k = *(const i32x4*)&codes.k[32 * u + li][(2 * e + hf) ^ swizzle<KC>(li)];
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) x[n] = __builtin_amdgcn_mfma_i32_32x32x32_i8(k, q[n][e], x[n], 0, 0, 0);
             }
@@ -426,127 +410,29 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
             }
             l += FOLD ? sum * exp2_fast(-lr) : sum;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int i = 0; i < NC; ++i) {
+                const uint4 v = codes.v[32 * i + li][(2 * u + hf) ^ swizzle<VC>(li)];
+                const f16x8 v0 = half8(v.x, v.y), v1 = half8(v.z, v.w);
 #pragma unroll
-                for (int i = 0; i < NC; ++i) {
-                    const f16x8 v = vf(u, i, j);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[n][j], acc[i], 0, 0, 0);
+                for (int n = 0; n < NT; ++n) {
+                    acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v0, w[n][0], acc[i], 0, 0, 0);
+                    acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1, w[n][1], acc[i], 0, 0, 0);
                 }
+            }
         }
     };
-    if constexpr (STAGED) {
-        using Step = TreeStep<D, U>;
-        __shared__ __attribute__((aligned(16))) Step step[2];
-        constexpr int KN = 32 * U * KC / NTH, VN = D * VC / NTH;     // chunks of a thread
-        static_assert(KN * NTH == 32 * U * KC && VN * NTH == D * VC && NTH % (32 * U * KC / KN) == 0, "whole shares");
-        // chunk i of K of this thread: row t / KC + i NTH / KC; of V: group t % VC, channel t / VC + i NTH / VC
-        const int kc = t % KC, kr = t / KC, vg = t % VC, vd = t / VC;
-        auto krow = [&](int i) { return kr + i * (NTH / KC); };
-        auto kkey = [&](int i) { return (krow(i) & ~31) + key_of_row(krow(i) & 31); };
-        uint4 rk[KN], rv[VN];
-        int idk[KN] = {}, idv = 0, id_of = 0;       // blocks of the step to fetch next; idv of the step in registers
-        auto ids = [&](int it) __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < KN; ++i) idk[i] = entry(it * TK + kkey(i));
-            idv = entry(it * TK + 16 * vg);
-        };
-        auto fetch = [&](int it) __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < KN; ++i)
-                rk[i] = *(const uint4*)(kp + place(idk[i], ((it * TK + kkey(i)) & bmask) * D + 16 * kc));
-            const int8_t* from = vp + place(idv, vd * a.bs + ((it * TK + 16 * vg) & bmask));
-#pragma unroll
-            for (int i = 0; i < VN; ++i) rv[i] = *(const uint4*)(from + i * (NTH / VC) * a.bs);
-            rsk[0] = a.ks[scale_at(idv)];
-            rsv[0] = a.vs[scale_at(idv)];
-            id_of = idv;
-        };
-        auto stage = [&](int it) __attribute__((always_inline)) {
-            Step& to = step[it & 1];
-#pragma unroll
-            for (int i = 0; i < KN; ++i) to.k[krow(i)][kc ^ swizzle<KC>(krow(i))] = rk[i];
-#pragma unroll
-            for (int i = 0; i < VN; ++i) {
-                const int d = vd + i * (NTH / VC);
-                to.v[d][(2 * vg) ^ swizzle<4 * U>(d)] = half8(rv[i].x, rv[i].y);
-                to.v[d][(2 * vg + 1) ^ swizzle<4 * U>(d)] = half8(rv[i].z, rv[i].w);
-            }
-            if (t < VC) {
-                const float sv = clean(rsv[0], id_of, it * TK + 16 * vg);
-                *(f32x4*)to.scale[t] = f32x4{clean(rsk[0], id_of, it * TK + 16 * vg), sv, __builtin_amdgcn_logf(sv), 0.f};
-            }
-        };
-        int it = s0;
-        if (it < s1) {
-            ids(it);
-            fetch(it);
-            ids(std::min(it + 1, s1 - 1));
-            stage(it);
-            if (it + 1 < s1) {
-                fetch(it + 1);
-                ids(std::min(it + 2, s1 - 1));
-            }
-        }
-        // step it finds its keys in LDS; those of it + 1 are in registers or on their way, the ids of it + 2 known
-        every_round([&](auto masked, int i) __attribute__((always_inline)) {
-            const int it = s0 + i;
-            __syncthreads();
-            if (it + 1 < s1) {
-                stage(it + 1);
-                if (it + 2 < s1) {
-                    fetch(it + 2);
-                    ids(std::min(it + 3, s1 - 1));
-                }
-            }
-            if (!busy) return;
-            const Step& from = step[it & 1];
-            float sk[U], sv[U], lv[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const f32x4 x = *(const f32x4*)from.scale[2 * u + hf];
-                sk[u] = x[0], sv[u] = x[1], lv[u] = x[2];
-            }
-            work(masked, it,
-                 [&](int u, int e) {
-                     const uint4 w = from.k[32 * u + li][(2 * e + hf) ^ swizzle<KC>(li)];
-                     return i32x4{(int)w.x, (int)w.y, (int)w.z, (int)w.w};
-                 },
-                 [&](int u, int i, int j) { return from.v[32 * i + li][(4 * u + 2 * hf + j) ^ swizzle<4 * U>(li)]; }, sk, sv, lv);
-        });
-    } else {
-        every_round([&](auto masked, int i) __attribute__((always_inline)) {
-            const int it = s0 + i * TG + tg;
-            __builtin_amdgcn_s_waitcnt(0x0f70);      // vmcnt = 0: the copies have landed
-            asm volatile("" ::: "memory");
-            if constexpr (PARTS == 2) __syncthreads();      // the other wave's, too, and it has read what is copied over now
-            const Codes& from = part(i % PARTS);
-            float sk[U], sv[U], lv[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int tv = it * TK + 32 * u + 16 * hf;
-                sk[u] = clean(rsk[u], ids_of[u], tv);
-                sv[u] = clean(rsv[u], ids_of[u], tv);
-                lv[u] = FOLD ? __builtin_amdgcn_logf(sv[u]) : 0.f;
-            }
-            if (PARTS == 2 && it + TG < s1) copy(it + TG, part((i + 1) % PARTS));
-            if (busy && it < s1)
-                work(masked, it,
-                     [&](int u, int e) {
-                         const uint4 w = from.k[32 * u + li][(2 * e + hf) ^ swizzle<KC>(li)];
-                         return i32x4{(int)w.x, (int)w.y, (int)w.z, (int)w.w};
-                     },
-                     [&](int u, int i, int j) {
-                         const uint4 w = from.v[32 * i + li][(2 * u + hf) ^ swizzle<VC>(li)];
-                         return j ? half8(w.z, w.w) : half8(w.x, w.y);
-                     }, sk, sv, lv);
-            if constexpr (PARTS == 1) {
-                __builtin_amdgcn_s_waitcnt(0xc07f);      // lgkmcnt = 0: everything has been read
-                asm volatile("" ::: "memory");
-                if (it + TG < s1) copy(it + TG, part(0));
-            }
-        });
-    }
+    auto step = [&](auto masked, int it) __attribute__((always_inline)) {
+        __builtin_amdgcn_s_waitcnt(0x0f70);      // vmcnt = 0: the copies have landed
+        asm volatile("" ::: "memory");
+        work(masked, it);
+        __builtin_amdgcn_s_waitcnt(0xc07f);      // lgkmcnt = 0: everything has been read
+        asm volatile("" ::: "memory");
+        if (it + NW < s1) copy(it + NW);
+    };
+    int it = s0 + wave;
+    for (; it < whole; it += NW) step(std::true_type{}, it);
+    for (; it < last; it += NW) step(std::false_type{}, it);
+    for (; it < s1; it += NW) step(std::true_type{}, it);
 
     l += __shfl_xor(l, 32, 64);
     if (FOLD) poison += __shfl_xor(poison, 32, 64);
@@ -554,66 +440,55 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
     int again = li;
     asm volatile("" : "+v"(again));
     const int f = row_of(again), qh = h * a.group + f % a.group;
-    const bool there = tl.f0 + WAVE_ROWS * rg + again < tl.rows;
+    const bool there = tl.f0 + again < tl.rows;
     const int64_t token = tl.off + f / a.group;
     const bool split_out = a.nsplit > 1;
     const int64_t nflat = a.g.rows * a.heads, at = token * a.heads + qh;
-    float M = m, M0 = m == -INFINITY ? 0.f : m, L = l;
-    if constexpr (TG > 1) {
-        // join the groups of waves: factors to the common maximum
-        __shared__ float sm[NW][WAVE_ROWS], sl[NW][WAVE_ROWS];
-        if (hf == 0) {
-            sm[wave][li] = m;
-            sl[wave][li] = l;
-        }
-        __syncthreads();
-        M = sm[rg][li];
-#pragma unroll
-        for (int g = 1; g < TG; ++g) M = fmaxf(M, sm[rg + g * RG][li]);
-        M0 = M == -INFINITY ? 0.f : M;
-        L = 0.f;
-#pragma unroll
-        for (int g = 0; g < TG; ++g) L += sl[rg + g * RG][li] * exp2_fast(sm[rg + g * RG][li] - M0);
+    // join the waves: factors to the common maximum, then sums through LDS
+    __shared__ float sm[NW][ROWS], sl[NW][ROWS];
+    if (hf == 0) {
+        sm[wave][li] = m;
+        sl[wave][li] = l;
     }
+    __syncthreads();
+    float M = sm[0][li];
+#pragma unroll
+    for (int g = 1; g < NW; ++g) M = fmaxf(M, sm[g][li]);
+    const float M0 = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+#pragma unroll
+    for (int g = 0; g < NW; ++g) L += sl[g][li] * exp2_fast(sm[g][li] - M0);
     const float mine = (R > 0.f ? R : 1.f) * exp2_fast(m - M0) / (L == 0.f ? 1.f : L) + poison;
-    auto put = [&](int64_t row, int head, int d, const f32x4& o) __attribute__((always_inline)) {
-        if (split_out)
-            *(f32x4*)(a.part + (split * nflat + row * a.heads + head) * D + d) = o;
-        else
-            store4((T*)a.O + row * a.ldo + (int64_t)head * D + d, o[0], o[1], o[2], o[3]);
-    };
-    auto channels = [&](int i, int b) {
-        return f32x4{acc[i][4 * b] * mine, acc[i][4 * b + 1] * mine, acc[i][4 * b + 2] * mine, acc[i][4 * b + 3] * mine};
-    };
-    if constexpr (TG == 1) {
-        if (there)
+    constexpr int JC = sizeof(own) >= sizeof(float) * NW * ROWS * 68 ? 64 : 32;      // channels at a time
+    static_assert(sizeof(own) >= sizeof(float) * NW * ROWS * (JC + 4), "the join goes where the keys were");
+    float(*so)[ROWS][JC + 4] = (float(*)[ROWS][JC + 4])own;      // behind the barrier above
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
+    for (int i0 = 0; i0 < NC; i0 += JC / 32) {
+        if (i0) __syncthreads();
 #pragma unroll
-                for (int b = 0; b < 4; ++b) put(token, qh, 32 * i + 8 * b + 4 * hf, channels(i, b));
-    } else {
-        constexpr int JC = sizeof(own) >= sizeof(float) * NW * WAVE_ROWS * 68 ? 64 : 32;      // channels at a time
-        static_assert(sizeof(own) >= sizeof(float) * NW * WAVE_ROWS * (JC + 4), "the join goes where the keys were");
-        float(*so)[WAVE_ROWS][JC + 4] = (float(*)[WAVE_ROWS][JC + 4])own;      // behind the barrier above
+        for (int i = 0; i < JC / 32; ++i)
 #pragma unroll
-        for (int i0 = 0; i0 < NC; i0 += JC / 32) {
-            if (i0) __syncthreads();
-#pragma unroll
-            for (int i = 0; i < JC / 32; ++i)
-#pragma unroll
-                for (int b = 0; b < 4; ++b) *(f32x4*)&so[wave][li][32 * i + 8 * b + 4 * hf] = channels(i0 + i, b);
-            __syncthreads();
-            for (int c = t; c < ROWS * JC / 4; c += NTH) {
-                const int r = c / (JC / 4), d = 4 * (c % (JC / 4)), fr = tl.f0 + r;
-                if (fr >= tl.rows) continue;
-                f32x4 o = *(const f32x4*)&so[r / WAVE_ROWS][r % WAVE_ROWS][d];
-#pragma unroll
-                for (int g = 1; g < TG; ++g) o += *(const f32x4*)&so[r / WAVE_ROWS + g * RG][r % WAVE_ROWS][d];
-                put(tl.off + fr / a.group, h * a.group + fr % a.group, 32 * i0 + d, o);
+            for (int b = 0; b < 4; ++b) {
+                const f32x16& x = acc[i0 + i];
+                *(f32x4*)&so[wave][li][32 * i + 8 * b + 4 * hf] =
+                    f32x4{x[4 * b] * mine, x[4 * b + 1] * mine, x[4 * b + 2] * mine, x[4 * b + 3] * mine};
             }
+        __syncthreads();
+        for (int c = t; c < ROWS * JC / 4; c += NTH) {
+            const int r = c / (JC / 4), d = 4 * (c % (JC / 4)), fr = tl.f0 + r;
+            if (fr >= tl.rows) continue;
+            f32x4 o = *(const f32x4*)&so[0][r][d];
+#pragma unroll
+            for (int g = 1; g < NW; ++g) o += *(const f32x4*)&so[g][r][d];
+            const int64_t row = tl.off + fr / a.group;
+            const int head = h * a.group + fr % a.group;
+            if (split_out)
+                *(f32x4*)(a.part + (split * nflat + row * a.heads + head) * D + 32 * i0 + d) = o;
+            else
+                store4((T*)a.O + row * a.ldo + (int64_t)head * D + 32 * i0 + d, o[0], o[1], o[2], o[3]);
         }
     }
-    if (tg == 0 && hf == 0 && there && (split_out || a.lse)) {
+    if (wave == 0 && hf == 0 && there && (split_out || a.lse)) {
         // L carries 2^PSHIFT
         const float lse2 = L == 0.f ? -INFINITY : M0 - PSHIFT + __log2f(L);
         if (split_out)
@@ -625,9 +500,9 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
 
 // Join of the splits: 16 rows a workgroup, 16 threads a row, JB splits at a
 // time with all their loads at once; tr: rows of the tiles that were split.
-template <typename T, int D, int RG>
+template <typename T, int D, int tr>
 __global__ __launch_bounds__(256) void attention_tree_join_kernel(TreeArgs a) {
-    constexpr int tr = WAVE_ROWS * RG, TK = RG == TILE_RG ? ptq::TK : 32 * blocks_of<T>(D);
+    constexpr int TK = tr == ATTN_TILE ? ptq::TK : 32 * blocks_of<T>(D);
     const unsigned part = blockIdx.x % (unsigned)(tr / 16), tile = blockIdx.x / (unsigned)(tr / 16);
     const int h = (int)(tile % (unsigned)a.kv_heads);
     TreeTile tl;
@@ -680,32 +555,29 @@ __global__ __launch_bounds__(256) void attention_tree_join_kernel(TreeArgs a) {
 
 int64_t tile_units(int64_t rows, int64_t batch, int group, int tr) { return rows * group / tr + batch; }
 
-template <typename T, int D, int RG, int NW>
-int launch_tiles(const TreeArgs& a, hipStream_t st) {
-    const int tr = WAVE_ROWS * RG;
-    const int64_t units = tile_units(a.g.rows, a.g.batch, a.group, tr) * a.kv_heads;
-    if constexpr (RG == TILE_RG) {
-        PTQ_TRY(launch_attention_tree_tiles(a, sizeof(T) == 4 ? PTQ_F32 : PTQ_BF16, D, st));
-    } else {
-        hipLaunchKernelGGL((attention_tree_kernel<T, D, RG, NW>), dim3((unsigned)(units * a.nsplit)), dim3(64 * NW), 0, st, a);
-        PTQ_LAUNCH_CHECK();
+template <typename T, int D>
+int launch(const TreeArgs& a, const TreePlan& p, hipStream_t st) {
+    const int64_t units = tile_units(a.g.rows, a.g.batch, a.group, p.tr) * a.kv_heads;
+    const dim3 grid((unsigned)(units * a.nsplit)), join((unsigned)(units * (p.tr / 16)));
+    if constexpr (D <= 128) {
+        if (p.tr == ATTN_TILE) {
+            PTQ_TRY(launch_attention_tree_tiles(a, sizeof(T) == 4 ? PTQ_F32 : PTQ_BF16, D, st));
+            if (a.nsplit > 1) hipLaunchKernelGGL((attention_tree_join_kernel<T, D, ATTN_TILE>), join, dim3(256), 0, st, a);
+            PTQ_LAUNCH_CHECK();
+            return PTQ_OK;
+        }
     }
+    if (D <= 128 && p.nw == 8) {
+        if constexpr (D <= 128) hipLaunchKernelGGL((attention_tree_kernel<T, D, 8>), grid, dim3(512), 0, st, a);
+    } else {
+        hipLaunchKernelGGL((attention_tree_kernel<T, D, 4>), grid, dim3(256), 0, st, a);
+    }
+    PTQ_LAUNCH_CHECK();
     if (a.nsplit > 1) {
-        hipLaunchKernelGGL((attention_tree_join_kernel<T, D, RG>), dim3((unsigned)(units * (tr / 16))), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((attention_tree_join_kernel<T, D, ROWS>), join, dim3(256), 0, st, a);
         PTQ_LAUNCH_CHECK();
     }
     return PTQ_OK;
-}
-
-template <typename T, int D>
-int launch(const TreeArgs& a, const TreePlan& p, hipStream_t st) {
-    if constexpr (D <= 128) {
-        if (p.rg == TILE_RG) return launch_tiles<T, D, TILE_RG, TILE_RG>(a, st);
-        if (p.nw == 8) return launch_tiles<T, D, 1, 8>(a, st);
-    }
-    if (p.rg == 4) return launch_tiles<T, D, 4, 4>(a, st);
-    if (p.rg == 2) return launch_tiles<T, D, 2, 4>(a, st);
-    return launch_tiles<T, D, 1, 4>(a, st);
 }
 
 template <typename T>
@@ -739,17 +611,17 @@ TreePlan attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_head
     const double steps = std::max(1.0, (double)keys / 64);
     TreePlan best{};
     double least = 0;
-    for (const TreePlan p : {TreePlan{1, 4, 0}, TreePlan{1, 8, 0}, TreePlan{2, 4, 0}, TreePlan{4, 4, 0}}) {
+    for (const TreePlan p : {TreePlan{ROWS, 4, 0}, TreePlan{ROWS, 8, 0}, TreePlan{ATTN_TILE, 8, 0}}) {
         if (p.nw == 8 && dim > 128) continue;
-        const int64_t tiles = batch * cdiv(each, WAVE_ROWS * p.rg) * kv_heads;
+        const int64_t tiles = batch * cdiv(each, p.tr) * kv_heads;
         const int64_t slots = 256 * (dim <= 128 ? 2 : 1) * 4 / p.nw;
         for (int ns = 1; ns <= 64 && (ns == 1 || ns * 4 <= steps); ++ns) {
-            const double mine = std::ceil(steps / ns * p.rg / p.nw);
+            const double mine = std::ceil(steps / ns / (p.tr == ROWS ? p.nw : 1));
             const double join = ns == 1 ? 0 : 3 + ns * (double)rows * heads * dim * 8 / 6e6;
             const double time = std::max(1.0, (double)(tiles * ns) / slots) * (3 + mine) + join;
             if (best.nsplit == 0 || time < least) {
                 least = time;
-                best = TreePlan{p.rg, p.nw, ns};
+                best = TreePlan{p.tr, p.nw, ns};
             }
         }
     }

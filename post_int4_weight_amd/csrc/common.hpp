@@ -276,13 +276,13 @@ int run_attention_int8(const AttnPlan& p, const KVCacheInt8& c, const RaggedRows
                        int64_t ldq, int heads, float scale, int causal, int64_t window, void* O, int64_t ldo,
                        float* lse, void* ws, size_t ws_bytes, hipStream_t st);
 
-// Attention of trees of drafted tokens over the cache (attention_tree.hip):
-// tiles of 32 rg query rows (rg 1, 2, 4; up to 128 channels 8, the tiles of
-// attention_int8.hip), workgroups of nw waves (4; 8 for rg 8 and, up to 128
-// channels, for rg 1, too), nsplit splits of the keys.
+// Attention of trees of drafted tokens over the cache (attention_tree.hip): tiles
+// of ATTN_TREE_ROWS query rows with nw = 4 waves, or 8 up to 128 channels, or of
+// ATTN_TILE (up to 128 channels, nw 8); nsplit splits of the keys.
 constexpr int TREE_NODES = 512;     // of a sequence, at most
+constexpr int ATTN_TREE_ROWS = 32;
 struct TreePlan {
-    int rg, nw, nsplit;
+    int tr, nw, nsplit;
 };
 TreePlan attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int block, int64_t width,
                              int64_t window);

@@ -8,7 +8,7 @@ from test_gpu_22_attention_tree import _check, _make, _trees
 
 pytestmark = pytest.mark.gpu
 
-PLANS = [(1, 4, 1), (1, 4, 5), (1, 8, 1), (1, 8, 3), (2, 4, 1), (2, 4, 4), (4, 4, 1), (4, 4, 3), (8, 8, 1), (8, 8, 3)]
+PLANS = [(0, 4, 1), (0, 4, 5), (0, 8, 1), (0, 8, 3), (1, 8, 1), (1, 8, 3)]      # tiles, waves, splits
 SHAPES = [(64, 16), (64, 64), (128, 16), (128, 128), (256, 16), (256, 32)]
 
 
@@ -75,6 +75,6 @@ def test_rows_by_themselves(gpu, plan, dim, dtype):
 def test_hook_refuses(gpu):
     from post_int4_weight_amd import api
     Q, cache, args, _ = _make(api, gpu, [30], [[-1, 0]], 2, 1, 256, 16, "bf16", 3)
-    for plan in ((3, 4, 1), (1, 2, 1), (2, 8, 1), (8, 4, 1), (1, 8, 1), (8, 8, 1), (1, 4, 0), (1, 4, 65)):
+    for plan in ((2, 8, 1), (0, 2, 1), (1, 4, 1), (0, 8, 1), (1, 8, 1), (0, 4, 0), (0, 4, 65)):
         with pytest.raises(api.PTQError):
             api._test_attention_int8_tree(*plan, Q, cache, *args)
