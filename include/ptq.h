@@ -488,13 +488,14 @@ int kv_cache_append_int8(int8_t* k_codes, int8_t* v_codes, float* k_scales, floa
  * block_table. NaN for a query: a parent on its way up that is not below its
  * node or less than -1, or a key in a block without a valid id.
  *
- * Q is held in 15 significant bits of its row's largest element (bf16) or 22
- * (fp32), its products with the codes of K are exact; probabilities, sums and
- * scales as for attention_int8_cache. Asynchronous.
+ * A row of Q is held in steps of 1 / 16256 of its largest element (bf16) or of
+ * 1 / 2080768 (fp32), or in the fp16 terms of attention_int8_cache, whichever the
+ * sizes choose; its products with the codes of K are exact. Probabilities, sums
+ * and scales as for attention_int8_cache. Asynchronous.
  * Errors: EINVAL, EWORKSPACE, EHIP.
  * ---------------------------------------------------------------------- */
 size_t attention_int8_tree_workspace_bytes(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim,
-                                           int block_size, int64_t table_width, int64_t window);
+                                           int dtype, int block_size, int64_t table_width, int64_t window);
 int attention_int8_tree(const void* Q, int64_t ldq, void* O, int64_t ldo, float* lse, int dtype, int64_t rows,
                         int heads, const int32_t* offsets, const int32_t* seq_lens, const int32_t* parents,
                         int64_t batch, const int32_t* block_table, int64_t table_width, const int8_t* k_codes,

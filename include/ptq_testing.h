@@ -89,8 +89,8 @@ int ptq_test_attention_int8_cache(int tiles, int waves, int nsplit, const void* 
  * head_dim up to 128), and the splits of the keys (1 .. 64). _plan says what
  * attention_int8_tree chooses. Returns PTQ_OK, PTQ_EINVAL, PTQ_EWORKSPACE or
  * PTQ_EHIP. */
-int ptq_test_attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim, int block_size,
-                                 int64_t table_width, int64_t window, int* tiles, int* waves, int* nsplit);
+int ptq_test_attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim, int dtype,
+                                 int block_size, int64_t table_width, int64_t window, int* tiles, int* waves, int* nsplit);
 size_t ptq_test_attention_tree_workspace_bytes(int nsplit, int64_t rows, int heads, int head_dim);
 int ptq_test_attention_int8_tree(int tiles, int waves, int nsplit, const void* Q, int64_t ldq, void* O, int64_t ldo, float* lse,
                                  int dtype, int64_t rows, int heads, const int32_t* offsets, const int32_t* seq_lens,

@@ -95,7 +95,7 @@ def _load() -> ctypes.CDLL:
         "rotary_apply": (i32, [vp, i64, vp, i64, i32, i64, i32, i32, vp, vp, i32, i32, ctypes.c_float, vp]),
         "kv_cache_append_int8": (i32, [vp, vp, vp, vp, i64, i32, i32, i32, vp, i64, vp, i64, i32, i64, vp, vp, i64,
                                        vp, i64, vp, vp, i32, i32, ctypes.c_float, vp]),
-        "attention_int8_tree_workspace_bytes": (sz, [i64, i64, i32, i32, i32, i32, i64, i64]),
+        "attention_int8_tree_workspace_bytes": (sz, [i64, i64, i32, i32, i32, i32, i32, i64, i64]),
         "attention_int8_tree": (i32, [vp, i64, vp, i64, vp, i32, i64, i32, vp, vp, vp, i64, vp, i64, vp, vp, vp, vp,
                                       i64, i32, i32, i32, ctypes.c_float, i64, vp, sz, vp]),
         "verify_drafts": (i32, [vp, i64, vp, i64, i32, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp]),
@@ -109,7 +109,7 @@ def _load() -> ctypes.CDLL:
         "ptq_test_attention_int8_cache": (i32, [i32, i32, i32, vp, i64, vp, i64, vp, i32, i64, i32, vp, vp, i64, vp,
                                                 i64, vp, vp, vp, vp, i64, i32, i32, i32, ctypes.c_float, i32, i64,
                                                 vp, sz, vp]),
-        "ptq_test_attention_tree_plan": (i32, [i64, i64, i32, i32, i32, i32, i64, i64, ctypes.POINTER(i32),
+        "ptq_test_attention_tree_plan": (i32, [i64, i64, i32, i32, i32, i32, i32, i64, i64, ctypes.POINTER(i32),
                                                ctypes.POINTER(i32), ctypes.POINTER(i32)]),
         "ptq_test_attention_tree_workspace_bytes": (sz, [i32, i64, i32, i32]),
         "ptq_test_attention_int8_tree": (i32, [i32, i32, i32, vp, i64, vp, i64, vp, i32, i64, i32, vp, vp, vp, i64, vp,
@@ -697,10 +697,10 @@ def kv_cache_append_int8(cache: KVCacheInt8, K, V, offsets, starts, block_table,
                                      _vector(positions, rows, torch.int32, "positions"), *rotary._args(), _stream()))
 
 
-def attention_int8_tree_workspace_bytes(rows: int, batch: int, heads: int, kv_heads: int, head_dim: int,
+def attention_int8_tree_workspace_bytes(rows: int, batch: int, heads: int, kv_heads: int, head_dim: int, dtype: int,
                                         block_size: int, table_width: int, window: int = 0) -> int:
-    return int(_lib.attention_int8_tree_workspace_bytes(rows, batch, heads, kv_heads, head_dim, block_size, table_width,
-                                                        window))
+    return int(_lib.attention_int8_tree_workspace_bytes(rows, batch, heads, kv_heads, head_dim, dtype, block_size,
+                                                        table_width, window))
 
 
 def attention_int8_tree(Q, cache: KVCacheInt8, offsets, seq_lens, block_table, parents, scale=None, window=0, O=None,
@@ -722,7 +722,8 @@ def attention_int8_tree(Q, cache: KVCacheInt8, offsets, seq_lens, block_table, p
     if O.dtype != Q.dtype:
         raise TypeError("O must have Q's dtype")
     off, lens, batch, table, width = _ragged(offsets, seq_lens, block_table, "seq_lens")
-    ws, wsb = _scratch(attention_int8_tree_workspace_bytes(rows, batch, heads, h, d, bs, width, window), Q.device, workspace)
+    ws, wsb = _scratch(attention_int8_tree_workspace_bytes(rows, batch, heads, h, d, _dtype_code(Q), bs, width, window),
+                       Q.device, workspace)
     _check(_lib.attention_int8_tree(_ptr(Q), ldq, _ptr(O), ldo, _vector(lse, rows * heads, torch.float32, "lse"),
                                     _dtype_code(Q), rows, heads, off, lens,
                                     _vector(parents, rows, torch.int32, "parents"), batch, table, width, _ptr(cache.k),
@@ -836,10 +837,10 @@ def _test_attention_int8_cache(tiles, waves, nsplit, Q, cache, offsets, seq_lens
     return O, lse
 
 
-def _test_attention_tree_plan(rows, batch, heads, kv_heads, head_dim, block_size, table_width, window=0):
+def _test_attention_tree_plan(rows, batch, heads, kv_heads, head_dim, dtype, block_size, table_width, window=0):
     """ptq_test_attention_tree_plan (include/ptq_testing.h): (tiles, waves, nsplit) that attention_int8_tree chooses."""
     plan = [ctypes.c_int() for _ in range(3)]
-    _check(_lib.ptq_test_attention_tree_plan(rows, batch, heads, kv_heads, head_dim, block_size, table_width, window,
+    _check(_lib.ptq_test_attention_tree_plan(rows, batch, heads, kv_heads, head_dim, dtype, block_size, table_width, window,
                                              *map(ctypes.byref, plan)))
     return tuple(x.value for x in plan)
 

@@ -187,7 +187,7 @@ int attention_tree(const char* fn, const TreePlan* given, const KVCacheInt8& c, 
     PTQ_TRY(check_float_rows(fn, "Q", Q, dtype, n, ldq));
     PTQ_TRY(check_float_rows(fn, "O", O, dtype, n, ldo));
     const TreePlan p =
-        given ? *given : attention_tree_plan(r.rows, r.batch, heads, c.heads, c.dim, c.block, r.width, window);
+        given ? *given : attention_tree_plan(r.rows, r.batch, heads, c.heads, c.dim, dtype, c.block, r.width, window);
     const size_t need = attention_tree_part_bytes(p.nsplit, r.rows, heads, c.dim);
     if (need && (!workspace || workspace_bytes < need)) {
         set_error("%s: workspace %zu bytes, need %zu", fn, workspace ? workspace_bytes : (size_t)0, need);
@@ -429,12 +429,12 @@ int kv_cache_append_int8(int8_t* k_codes, int8_t* v_codes, float* k_scales, floa
 }
 
 size_t attention_int8_tree_workspace_bytes(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim,
-                                           int block_size, int64_t table_width, int64_t window) {
+                                           int dtype, int block_size, int64_t table_width, int64_t window) {
     const KVCacheInt8 c{nullptr, nullptr, nullptr, nullptr, 0, kv_heads, head_dim, block_size};
-    if (check_cache("attention_int8_tree_workspace_bytes", c) != PTQ_OK || rows <= 0 || batch <= 0 ||
+    if (check_cache("attention_int8_tree_workspace_bytes", c) != PTQ_OK || !dtype_ok(dtype) || rows <= 0 || batch <= 0 ||
         heads < kv_heads || heads % kv_heads || table_width < 0 || window < 0)
         return 0;
-    const TreePlan p = attention_tree_plan(rows, batch, heads, kv_heads, head_dim, block_size, table_width, window);
+    const TreePlan p = attention_tree_plan(rows, batch, heads, kv_heads, head_dim, dtype, block_size, table_width, window);
     return attention_tree_part_bytes(p.nsplit, rows, heads, head_dim);
 }
 
@@ -451,14 +451,14 @@ int attention_int8_tree(const void* Q, int64_t ldq, void* O, int64_t ldo, float*
                           lse, workspace, workspace_bytes, stream);
 }
 
-int ptq_test_attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim, int block_size,
-                                 int64_t table_width, int64_t window, int* tiles, int* waves, int* nsplit) {
+int ptq_test_attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim, int dtype,
+                                 int block_size, int64_t table_width, int64_t window, int* tiles, int* waves, int* nsplit) {
     const char* fn = "ptq_test_attention_tree_plan";
     PTQ_TRY(check_cache(fn, KVCacheInt8{nullptr, nullptr, nullptr, nullptr, 0, kv_heads, head_dim, block_size}));
-    if (rows < 1 || batch < 1 || heads < kv_heads || heads % kv_heads || table_width < 0 || window < 0 || !tiles || !waves ||
-        !nsplit)
+    if (rows < 1 || batch < 1 || heads < kv_heads || heads % kv_heads || !dtype_ok(dtype) || table_width < 0 || window < 0 ||
+        !tiles || !waves || !nsplit)
         REFUSE("%s: bad arguments", fn);
-    const TreePlan p = attention_tree_plan(rows, batch, heads, kv_heads, head_dim, block_size, table_width, window);
+    const TreePlan p = attention_tree_plan(rows, batch, heads, kv_heads, head_dim, dtype, block_size, table_width, window);
     *tiles = p.tr == ATTN_TILE;
     *waves = p.nw;
     *nsplit = p.nsplit;

@@ -145,7 +145,7 @@ struct QueryRow {
 // whole rows at a time, and copies the next step over it when it has read it; the
 // other waves of the SIMD work meanwhile, and nothing waits for another wave until
 // the join. What bounds it: for few rows memory (16 trees of 8 nodes over 4000
-// keys, 32 heads on 8, D = 128: FEW us, the cache's 131 MB at TB/s TB/s), with more
+// keys, 32 heads on 8, D = 128: 37 us, the cache's 131 MB at 3.5 TB/s), with more
 // tiles on the same keys the vector instructions of the exponentials and of the
 // conversion of V. Tiles of 64 and 128 rows that share a step among waves were 1%
 // faster in the mean over 1700 shapes, and taken out; from about 300 rows a kv
@@ -599,29 +599,43 @@ size_t attention_tree_part_bytes(int nsplit, int64_t rows, int heads, int dim) {
     return z.bytes();
 }
 
-// Lengths are not known here: keys is the most there may be, and every sequence
-// is taken to have the mean number of rows. The time of a choice, in steps of 64
-// keys that a wave does while another one of its SIMD does the same: rounds of
-// as many workgroups as the card holds, each a start and its steps, and the join.
-TreePlan attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int block, int64_t width,
-                             int64_t window) {
+// The choice of a TreePlan: the least of estimated times, in microseconds,
+//   start + rounds (first + steps each) + [join + bytes of the parts],
+// fitted to 1950 shapes with all their plans (1 .. 64 sequences of 1 .. 64 nodes, 1
+// .. 8 kv heads, groups of 1 .. 8, 64 .. 16000 keys); the choice is 3% slower than
+// the best plan in the mean, 10% at nine shapes of ten, 58% at worst. Lengths are
+// not known here: keys is the most there may be, and every sequence is taken to
+// have the mean number of rows. A round is as many workgroups as the card holds.
+TreePlan attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int dtype, int block,
+                             int64_t width, int64_t window) {
     const int64_t group = heads / kv_heads, most = width * block;
     const int64_t keys = window > 0 && window < most ? std::min(most, window + cdiv(rows, batch)) : most;
     const int64_t each = cdiv(rows * group, batch);
-    const double steps = std::max(1.0, (double)keys / 64);
+    const bool f32 = dtype == PTQ_F32;
+    const int d = dim == 64 ? 0 : dim == 128 ? 1 : 2;
+    struct Kind {
+        TreePlan plan;
+        double start, first, step[2][3];      // step: bf16, fp32 at 64, 128, 256 channels
+    };
+    const Kind kinds[] = {{{ROWS, 4, 1}, 7.8, dim <= 128 ? 4.1 : 6.9, {{1.3, 2.25, 2.1}, {1.7, 1.4, 2.75}}},
+                                 {{ROWS, 8, 1}, 6.7, 5.9, {{1.55, 2.85, 0}, {2.15, 2.1, 0}}},
+                                 {{ATTN_TILE, 8, 1}, 7.2, 3.5, {{1.3, 1.8, 0}, {1.9, 2.9, 0}}}};
     TreePlan best{};
     double least = 0;
-    for (const TreePlan p : {TreePlan{ROWS, 4, 0}, TreePlan{ROWS, 8, 0}, TreePlan{ATTN_TILE, 8, 0}}) {
-        if (p.nw == 8 && dim > 128) continue;
-        const int64_t tiles = batch * cdiv(each, p.tr) * kv_heads;
-        const int64_t slots = 256 * (dim <= 128 ? 2 : 1) * 4 / p.nw;
+    for (const Kind& k : kinds) {
+        if (k.plan.nw == 8 && dim > 128) continue;
+        const bool own_steps = k.plan.tr == ROWS;
+        const int tk = own_steps ? 32 * (f32 ? blocks_of<float>(dim) : blocks_of<uint16_t>(dim)) : TK;
+        const int64_t steps = std::max<int64_t>(1, cdiv(keys, tk)), tiles = batch * cdiv(each, k.plan.tr) * kv_heads;
+        const int64_t slots = k.plan.nw == 4 && dim <= 128 ? 512 : 256;
         for (int ns = 1; ns <= 64 && (ns == 1 || ns * 4 <= steps); ++ns) {
-            const double mine = std::ceil(steps / ns / (p.tr == ROWS ? p.nw : 1));
-            const double join = ns == 1 ? 0 : 3 + ns * (double)rows * heads * dim * 8 / 6e6;
-            const double time = std::max(1.0, (double)(tiles * ns) / slots) * (3 + mine) + join;
+            const int64_t per = std::max<int64_t>(4, cdiv(steps, ns));
+            const double full = (double)(tiles * cdiv(steps, per)) / slots, rounds = std::max(1., (full + std::ceil(full)) / 2);
+            const double time = k.start + rounds * (k.first + k.step[f32][d] * cdiv(per, own_steps ? k.plan.nw : 1)) +
+                                (ns == 1 ? 0. : 3.5 + 0.35e-6 * ns * (double)rows * heads * dim * 8);
             if (best.nsplit == 0 || time < least) {
                 least = time;
-                best = TreePlan{p.tr, p.nw, ns};
+                best = TreePlan{k.plan.tr, k.plan.nw, ns};
             }
         }
     }

@@ -284,8 +284,8 @@ constexpr int ATTN_TREE_ROWS = 32;
 struct TreePlan {
     int tr, nw, nsplit;
 };
-TreePlan attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int block, int64_t width,
-                             int64_t window);
+TreePlan attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int dtype, int block,
+                             int64_t width, int64_t window);
 size_t attention_tree_part_bytes(int nsplit, int64_t rows, int heads, int dim);
 int run_attention_tree(const TreePlan& p, const KVCacheInt8& c, const RaggedRows& r, const int32_t* parents, int dtype,
                        const void* Q, int64_t ldq, int heads, float scale, int64_t window, void* O, int64_t ldo,

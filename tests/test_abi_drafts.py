@@ -63,12 +63,12 @@ def test_tree():
                      ("Q is not", dict(Q=ODD)), ("row stride", dict(ldo=250)), ("dtype", dict(dt=9)),
                      ("too large", dict(rows=1 << 40)), ("table_width", dict(width=1 << 31))):
         _refused(call(**kw), word)
-    need = lib.attention_int8_tree_workspace_bytes(5, 2, 4, 2, 64, 16, 300, 0)
+    need = lib.attention_int8_tree_workspace_bytes(5, 2, 4, 2, 64, 0, 16, 300, 0)
     assert need > 0
     assert call(wsb=need - 1) == 4 and call(ws=None) == 4
     _refused(call(ws=ctypes.c_void_p((1 << 20) + 8)), "workspace is not")
     assert call(rows=0) == 0 and call(batch=0) == 0
-    assert lib.attention_int8_tree_workspace_bytes(5, 2, 4, 3, 64, 16, 300, 0) == 0
+    assert lib.attention_int8_tree_workspace_bytes(5, 2, 4, 3, 64, 0, 16, 300, 0) == 0
 
 
 def test_verify():

@@ -272,7 +272,7 @@ def test_streams_and_graphs(gpu):
     assert torch.equal(got, want[0])
     q, c = made[0][0].clone(), api.KVCacheInt8(*(t.clone() for t in made[0][1]))
     args = [t.clone() for t in made[0][2]]
-    need = api.attention_int8_tree_workspace_bytes(34, 2, 8, 2, 128, 64, args[2].shape[1])
+    need = api.attention_int8_tree_workspace_bytes(34, 2, 8, 2, 128, api.PTQ_BF16, 64, args[2].shape[1])
     assert need > 0
     ws, O1, O2 = torch.empty(need, dtype=torch.uint8, device=gpu), torch.empty_like(q), torch.empty_like(q)
     g = torch.cuda.CUDAGraph()
