@@ -73,7 +73,7 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
 // prompts of 1000 .. 4099 tokens, 8 heads of 128, bf16: 109 us, 4.6 TB/s; 16
 // such sequences read back: 108 us, 5.0 TB/s; one token appended to each of 64
 // sequences: 6 us. With NV = 2 the bf16 write took 118 us.
-// Threads of a workgroup: `per` for each head, as many heads as make 256.
+// Threads of a workgroup: `per` for each head, as many heads as make 256 (512 where keys turn).
 template <typename T>
 constexpr int write_nv() { return sizeof(T) == 4 ? 2 : 4; }
 constexpr int READ_NV = 4;
@@ -93,21 +93,30 @@ __device__ __forceinline__ HeadThreads head_threads(const CacheArgs& a, int per)
 }
 
 // A thread's chunks of K where pairs turn: the two chunks of 8 channels that
-// hold 8 pairs, or two neighbours past the pairs, so that a sine and a cosine
-// are formed once for both. Item t of a token (0 .. dim / 16 - 1) is chunk
-// first(t) and its partner.
+// hold 8 pairs, or two neighbours past the pairs. Item t of a token (0 .. dim / 16
+// - 1) is chunk first(t) and its partner.
 template <int TURN>
 __device__ __forceinline__ int turned_chunk(int t, int n, int second) {
     if (TURN == PAIR_HALVES && t < n / 8) return t + (second ? n / 8 : 0);
     return 2 * t + second;
 }
 
+// Cosines, then sines, are formed in LDS once for all heads of a workgroup, rows
+// of turn_stride(n) for the slots of `steps` steps at a time, a step being the
+// slots of a thread's next two chunks (or one). 16 prompts of 2500 tokens, 8 heads
+// of 128, bf16, blocks of 64: 66 us where the write alone takes 50 (each thread its
+// own sines: 88); halves of 45 pairs, whose partners are loaded once more: 96.
+__host__ __device__ __forceinline__ int turn_stride(int n) { return (n + 7) / 8 * 8; }
+template <typename T>
+constexpr int turn_steps(int layout) { return layout == PAIR_ANY_HALVES ? 2 * write_nv<T>() : write_nv<T>(); }
+constexpr int TURN_LDS = 32768;      // two workgroups of 512 threads fill a CU by their registers
+
 constexpr int NO_TURN = -1;
 
 // grid (units, groups of heads, 2): z = 0 keys, 1 values. TURN: a PairLayout, or NO_TURN
 template <typename T, int TURN>
 __global__ __launch_bounds__(sizeof(T) == 4 ? 1024 : 512) void kv_write_kernel(CacheArgs a, int per, const T* __restrict__ K, int64_t ldk,
-                                                       const T* __restrict__ V, int64_t ldv, RotaryArgs r) {
+                                                       const T* __restrict__ V, int64_t ldv, RotaryArgs r, int steps) {
     constexpr int NV = write_nv<T>();
     constexpr bool PAIRS = TURN == PAIR_HALVES || TURN == PAIR_NEIGHBOURS;
     __shared__ float red[16];
@@ -136,38 +145,73 @@ __global__ __launch_bounds__(sizeof(T) == 4 ? 1024 : 512) void kv_write_kernel(C
         }
         if constexpr (TURN != NO_TURN) {
             // the turned keys of this call's slots; the others count for nothing
-            auto position = [&](int slot) { return r.positions ? r.positions[s.row0 + slot] : (int)(s.p0 + slot); };
-            if constexpr (PAIRS) {
+            extern __shared__ __attribute__((aligned(16))) float turns[];
+            constexpr int EACH = PAIRS ? 2 : 1;
+            const int span = a.bs / turn_steps<T>(TURN), width = turn_stride(r.n), sines = steps * span * width;
+            const int rows = (int)blockDim.x / r.n, left = (int)blockDim.x % r.n;
+            int base = 0;      // slot of the first row
 #pragma unroll
-                for (int i = 0; i < 2 * NV; i += 2) {
-                    const int c = chunk_of(i), slot = c / cpr, i0 = TURN == PAIR_HALVES ? 8 * (c % cpr) : 4 * (c % cpr);
-                    float (&p)[8] = *(float (*)[8])&v[8 * i], (&q)[8] = *(float (*)[8])&v[8 * i + 8];
-                    if (slot < s.lo || slot >= s.hi) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) p[k] = q[k] = 0.f;
-                    } else if (i0 < r.n) {
-                        turn_chunks<TURN>(r, position(slot), i0, p, q);
+            for (int i = 0; i < 2 * NV; i += EACH) {
+                if (i / EACH % steps == 0) {
+                    if (i > 0) __syncthreads();
+                    base = i / EACH * span;
+                    const int lo = std::max(s.lo, base), hi = std::min(s.hi, base + steps * span);
+                    for (int slot = lo + threadIdx.x / r.n, j = threadIdx.x % r.n; slot < hi;) {
+                        const int at = r.positions ? r.positions[s.row0 + slot] : (int)(s.p0 + slot);
+                        const float2 w = turn_of((double)at, r.freq[j], r.magnitude);
+                        turns[(slot - base) * width + j] = w.x;
+                        turns[sines + (slot - base) * width + j] = w.y;
+                        slot += rows;
+                        j += left;
+                        if (j >= r.n) {
+                            j -= r.n;
+                            ++slot;
+                        }
                     }
+                    __syncthreads();
                 }
-            } else {
+                const int c = chunk_of(i), slot = c / cpr, c0 = 8 * (c % cpr);
+                float (&p)[8] = *(float (*)[8])&v[8 * i], (&q)[8] = *(float (*)[8])&v[8 * (PAIRS ? i + 1 : i)];
+                if (slot < s.lo || slot >= s.hi) {
 #pragma unroll
-                for (int i = 0; i < 2 * NV; ++i) {
-                    const int c = chunk_of(i), slot = c / cpr, c0 = 8 * (c % cpr);
-                    float (&p)[8] = *(float (*)[8])&v[8 * i];
-                    if (slot < s.lo || slot >= s.hi) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) p[k] = 0.f;
-                        continue;
-                    }
-                    const int at = position(slot);
+                    for (int k = 0; k < 8; ++k) p[k] = q[k] = 0.f;
+                    continue;
+                }
+                const float* cs = turns + (slot - base) * width;
+                if constexpr (PAIRS) {
+                    const int i0 = TURN == PAIR_HALVES ? c0 : c0 / 2;
+                    if (i0 >= r.n) continue;
+                    float x[8], y[8];
+                    load8(cs + i0, x);
+                    load8(cs + sines + i0, y);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const int d = c0 + k;
+                        if (TURN == PAIR_HALVES) {
+                            turn_pair(p[k], q[k], x[k], y[k]);
+                        } else if (i0 + k < r.n) {
+                            float (&w)[8] = k < 4 ? p : q;
+                            turn_pair(w[2 * k & 7], w[(2 * k & 7) + 1], x[k], y[k]);
+                        }
+                    }
+                } else {
+                    if (c0 >= 2 * r.n) continue;
+                    float other[8];
+                    const T* x = X + slot * ld;
+                    if (c0 + 8 <= r.n || (c0 >= r.n && c0 + 8 <= 2 * r.n)) {
+                        load_some(x + (c0 < r.n ? c0 + r.n : c0 - r.n), 8, other);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int d = c0 + k;
+                            other[k] = d < 2 * r.n ? load_as_float(x, d < r.n ? d + r.n : d - r.n) : 0.f;
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int d = c0 + k, j = d < r.n ? d : d - r.n;
                         if (d >= 2 * r.n) break;
-                        float cs, sn;
-                        turn_of(at, r.freq[d < r.n ? d : d - r.n], r.magnitude, cs, sn);
-                        float u = load_as_float(X + slot * ld, d < r.n ? d : d - r.n), w = load_as_float(X + slot * ld, d < r.n ? d + r.n : d);
-                        turn_pair(u, w, cs, sn);
+                        float u = d < r.n ? p[k] : other[k], w = d < r.n ? other[k] : p[k];
+                        turn_pair(u, w, cs[j], cs[sines + j]);
                         p[k] = d < r.n ? u : w;
                     }
                 }
@@ -315,9 +359,9 @@ struct Launch {
     dim3 grid, block;
     int per;
 };
-int block_launch(const char* fn, const KVCacheInt8& c, const RaggedRows& r, int nv, Launch& l) {
+int block_launch(const char* fn, const KVCacheInt8& c, const RaggedRows& r, int nv, int most, Launch& l) {
     l.per = c.block * c.dim / (16 * nv);
-    const int nt = std::max(l.per, std::min(256, (int)cdiv((int64_t)l.per * c.heads, 64) * 64));
+    const int nt = std::max(l.per, std::min(most, (int)cdiv((int64_t)l.per * c.heads, 64) * 64));
     const int64_t units = r.rows / c.block + 2 * r.batch;
     // a launch of 2^32 threads or more wraps without an error: only some of its workgroups run
     if (units > (((int64_t)1 << 32) - 1) / nt) {
@@ -339,13 +383,30 @@ int launch_write(const char* fn, const KVCacheInt8& c, const RaggedRows& r, int 
                  const void* V, int64_t ldv, const RotaryArgs& rot, hipStream_t st) {
     const CacheArgs a = cache_args(c, r);
     Launch l;
-    PTQ_TRY(block_launch(fn, c, r, dtype == PTQ_F32 ? write_nv<float>() : write_nv<uint16_t>(), l));
+    // cosines and sines are shared by the heads of a workgroup
+    const int most = TURN == NO_TURN ? 256 : 512;
+    int steps = 0, lds = 0;
+    if (TURN != NO_TURN) {
+        const int all = dtype == PTQ_F32 ? turn_steps<float>(TURN) : turn_steps<uint16_t>(TURN);
+        steps = all;
+        while (steps > 1 && c.block / all * steps * turn_stride(rot.n) * 8 > TURN_LDS) steps /= 2;
+        lds = c.block / all * steps * turn_stride(rot.n) * 8;
+    }
+    PTQ_TRY(block_launch(fn, c, r, dtype == PTQ_F32 ? write_nv<float>() : write_nv<uint16_t>(), most, l));
+    if (lds == 65536) {      // fp32, blocks of 128 tokens, heads of 256: with the kernel's own LDS more than 64 KB
+        static bool ready = false;
+        if (!ready) {
+            PTQ_HIP(hipFuncSetAttribute((const void*)kv_write_kernel<float, TURN>,
+                                        hipFuncAttributeMaxDynamicSharedMemorySize, 65536));
+            ready = true;
+        }
+    }
     if (dtype == PTQ_F32)
-        hipLaunchKernelGGL((kv_write_kernel<float, TURN>), l.grid, l.block, 0, st, a, l.per, (const float*)K, ldk,
-                           (const float*)V, ldv, rot);
+        hipLaunchKernelGGL((kv_write_kernel<float, TURN>), l.grid, l.block, lds, st, a, l.per, (const float*)K, ldk,
+                           (const float*)V, ldv, rot, steps);
     else
-        hipLaunchKernelGGL((kv_write_kernel<uint16_t, TURN>), l.grid, l.block, 0, st, a, l.per, (const uint16_t*)K, ldk,
-                           (const uint16_t*)V, ldv, rot);
+        hipLaunchKernelGGL((kv_write_kernel<uint16_t, TURN>), l.grid, l.block, lds, st, a, l.per, (const uint16_t*)K, ldk,
+                           (const uint16_t*)V, ldv, rot, steps);
     PTQ_LAUNCH_CHECK();
     return PTQ_OK;
 }
@@ -375,7 +436,7 @@ int launch_kv_read(const KVCacheInt8& c, const RaggedRows& r, int dtype, void* K
     if (r.rows == 0 || r.batch == 0) return PTQ_OK;
     const CacheArgs a = cache_args(c, r);
     Launch l;
-    PTQ_TRY(block_launch("kv_cache_read_int8", c, r, READ_NV, l));
+    PTQ_TRY(block_launch("kv_cache_read_int8", c, r, READ_NV, 256, l));
     if (dtype == PTQ_F32)
         hipLaunchKernelGGL(kv_read_kernel<float>, l.grid, l.block, 0, st, a, l.per, (float*)K, ldk, (float*)V, ldv);
     else

@@ -1,11 +1,11 @@
 // Rotary positions, shared by rotary.hip and kv_cache.hip: the pairs of a head
 // turn by the angle position * frequency.
 //
-// The angle is formed in fp64, in turns, and reduced there: a position of 10^6
-// at frequency 1 keeps 2^-33 of a turn, where fp32 would keep 2^-4 of a radian.
-// What is left lies within an eighth of a turn of a multiple of a quarter, and
-// its sine and cosine are Taylor sums in fp32 (first omitted terms 7e-12 and
-// 1.2e-10): each is within 2^-23 of the true value.
+// The angle is formed in fp64, in quarters of a turn, and reduced there: a
+// position of 10^6 at frequency 1 keeps 2^-33 of a turn, where fp32 would keep
+// 2^-4 of a radian. What is left lies within half a quarter, and its sine and
+// cosine are Taylor sums in fp32 (first omitted terms 7e-12 and 1.2e-10): each is
+// within 2^-23 of the true value.
 #pragma once
 
 #include "int8.hpp"
@@ -30,11 +30,11 @@ inline PairLayout pair_layout(int n, int interleaved) {
     return interleaved ? PAIR_NEIGHBOURS : n % 8 == 0 ? PAIR_HALVES : PAIR_ANY_HALVES;
 }
 
-__device__ __forceinline__ void turn_of(int position, double freq, float magnitude, float& c, float& s) {
-    const double turns = (double)position * (freq * 0.15915494309189533577);
-    const double quarters = 4.0 * (turns - __builtin_rint(turns));      // in [-2, 2], exact
-    const double q = __builtin_rint(quarters);
-    const float x = (float)((quarters - q) * 1.57079632679489661923), y = x * x;
+// cosine and sine, times the magnitude, of position * freq
+__device__ __forceinline__ float2 turn_of(double position, double freq, float magnitude) {
+    const double t = position * (freq * 0.63661977236758134308);      // quarters
+    const double q = __builtin_rint(t);
+    const float x = (float)((t - q) * 1.57079632679489661923), y = x * x;
     float sn = fmaf(y, -2.50521084e-8f, 2.75573192e-6f);      // -1 / 11!, 1 / 9!
     sn = fmaf(y, sn, -1.98412698e-4f);
     sn = fmaf(y, sn, 8.33333333e-3f);
@@ -45,9 +45,11 @@ __device__ __forceinline__ void turn_of(int position, double freq, float magnitu
     cs = fmaf(y, cs, 4.16666667e-2f);
     cs = fmaf(y, cs, -0.5f);
     cs = fmaf(y, cs, 1.f);
-    const int k = (int)q & 3;
-    c = (k & 1 ? sn : cs) * ((k == 1 || k == 2) ? -magnitude : magnitude);
-    s = (k & 1 ? cs : sn) * (k >= 2 ? -magnitude : magnitude);
+    // q modulo 4: the low bits of q + 1.5 2^52 (an angle of 2^51 quarters has no place in a turn any more)
+    const uint32_t k = (uint32_t)__double2loint(q + 6755399441055744.0);
+    const float c = k & 1 ? sn : cs, s = k & 1 ? cs : sn;
+    const uint32_t neg_c = ((k + 1) << 30) & 0x80000000u, neg_s = (k << 30) & 0x80000000u;
+    return make_float2(__uint_as_float(__float_as_uint(c) ^ neg_c) * magnitude, __uint_as_float(__float_as_uint(s) ^ neg_s) * magnitude);
 }
 
 // the turned pair (a, b)
@@ -57,23 +59,28 @@ __device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) 
     b = fmaf(b, c, x * s);
 }
 
-// Two chunks of 8 channels of a head, a and b, that hold 8 pairs from pair i0
-// on: pair k is (a[k], b[k]), or neighbours within a, then within b. Pairs from
-// n on stay as they are, whatever they hold.
-template <int LAYOUT>
-__device__ __forceinline__ void turn_chunks(const RotaryArgs& r, int position, int i0, float (&a)[8], float (&b)[8]) {
-    static_assert(LAYOUT != PAIR_ANY_HALVES, "has no chunks");
+// Elements 0 .. n - 1 of 8 from anywhere; storing leaves the first ones out
+template <typename T>
+__device__ __forceinline__ void load_some(const T* p, int n, float (&v)[8]) {
+    if (n >= 8) {
+        struct { alignas(16) T x[8]; } w;
+        __builtin_memcpy(&w, p, sizeof(w));
+        load8(w.x, v);
+    } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        if (i0 + k >= r.n) break;
-        float c, s;
-        turn_of(position, r.freq[i0 + k], r.magnitude, c, s);
-        if constexpr (LAYOUT == PAIR_HALVES) {
-            turn_pair(a[k], b[k], c, s);
-        } else {
-            float (&x)[8] = k < 4 ? a : b;
-            turn_pair(x[2 * k & 7], x[(2 * k & 7) + 1], c, s);
-        }
+        for (int k = 0; k < 8; ++k) v[k] = k < n ? load_as_float(p, k) : 0.f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_some(T* p, int skip, int n, const float (&v)[8]) {
+    if (n >= 8 && skip == 0) {
+        struct { alignas(16) T x[8]; } w;
+        store8(w.x, v);
+        __builtin_memcpy(p, &w, sizeof(w));
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k >= skip && k < n) store1(p + k, v[k]);
     }
 }
 
