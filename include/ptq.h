@@ -526,11 +526,15 @@ int attention_int8_tree(const void* Q, int64_t ldq, void* O, int64_t ldo, float*
  * path[rows]: node 0 and the kept nodes in order, then -1; counts[batch]: how
  * many; next[batch]: the token, or -1 if the sum is not positive and finite. A
  * sequence without rows, or with more than 512, has counts 0 and next -1.
- * Rows of no sequence are left as they are. Asynchronous. Errors: EINVAL, EHIP.
+ * Rows of no sequence are left as they are. The workspace, of
+ * verify_drafts_workspace_bytes (0 for small vocabularies), need not be cleared.
+ * Asynchronous. Errors: EINVAL, EWORKSPACE, EHIP.
  * ---------------------------------------------------------------------- */
+size_t verify_drafts_workspace_bytes(int64_t batch, int64_t vocab);
 int verify_drafts(const void* target, int64_t ldt, const void* draft, int64_t ldd, int dtype, int64_t rows,
                   int64_t vocab, const int32_t* tokens, const int32_t* parents, const int32_t* offsets, int64_t batch,
-                  const float* u, const float* r, int32_t* path, int32_t* counts, int32_t* next, void* stream);
+                  const float* u, const float* r, int32_t* path, int32_t* counts, int32_t* next, void* workspace,
+                  size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

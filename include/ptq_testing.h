@@ -100,6 +100,14 @@ int ptq_test_attention_int8_tree(int tiles, int waves, int nsplit, const void* Q
                                  int head_dim, int block_size, float scale, int64_t window, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/* verify_drafts with the number of workgroups of a sequence given instead of
+ * chosen: 1 .. 4. Returns PTQ_OK, PTQ_EINVAL, PTQ_EWORKSPACE or PTQ_EHIP. */
+size_t ptq_test_verify_drafts_workspace_bytes(int shares, int64_t batch);
+int ptq_test_verify_drafts(int shares, const void* target, int64_t ldt, const void* draft, int64_t ldd, int dtype,
+                           int64_t rows, int64_t vocab, const int32_t* tokens, const int32_t* parents,
+                           const int32_t* offsets, int64_t batch, const float* u, const float* r, int32_t* path,
+                           int32_t* counts, int32_t* next, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,7 +13,7 @@ from .api import (PTQError, PTQ_BF16, PTQ_F32, library_path, hessian_workspace_b
                   matmul_int8_workspace_bytes, matmul_int8, linear_int8_workspace_bytes, linear_int8, KVCacheInt8,
                   kv_cache_write_int8, kv_cache_read_int8, attention_int8_cache_workspace_bytes,
                   attention_int8_cache, Rotary, rotary_apply, kv_cache_append_int8,
-                  attention_int8_tree_workspace_bytes, attention_int8_tree, verify_drafts)
+                  attention_int8_tree_workspace_bytes, attention_int8_tree, verify_drafts_workspace_bytes, verify_drafts)
 
 __all__ = [
     "PTQError", "PTQ_BF16", "PTQ_F32", "library_path", "hessian_workspace_bytes", "hessian_accumulate",
@@ -24,5 +24,5 @@ __all__ = [
     "matmul_int8_workspace_bytes", "matmul_int8", "linear_int8_workspace_bytes", "linear_int8", "KVCacheInt8",
     "kv_cache_write_int8", "kv_cache_read_int8", "attention_int8_cache_workspace_bytes", "attention_int8_cache",
     "Rotary", "rotary_apply", "kv_cache_append_int8", "attention_int8_tree_workspace_bytes", "attention_int8_tree",
-    "verify_drafts",
+    "verify_drafts_workspace_bytes", "verify_drafts",
 ]

@@ -98,7 +98,8 @@ def _load() -> ctypes.CDLL:
         "attention_int8_tree_workspace_bytes": (sz, [i64, i64, i32, i32, i32, i32, i32, i64, i64]),
         "attention_int8_tree": (i32, [vp, i64, vp, i64, vp, i32, i64, i32, vp, vp, vp, i64, vp, i64, vp, vp, vp, vp,
                                       i64, i32, i32, i32, ctypes.c_float, i64, vp, sz, vp]),
-        "verify_drafts": (i32, [vp, i64, vp, i64, i32, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp]),
+        "verify_drafts_workspace_bytes": (sz, [i64, i64]),
+        "verify_drafts": (i32, [vp, i64, vp, i64, i32, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, sz, vp]),
         "ptq_test_matmul_int8_plan": (i32, [i64, i64, i64, ctypes.POINTER(i32), ctypes.POINTER(i32)]),
         "ptq_test_matmul_int8_workspace_bytes": (sz, [i32, i32, i64, i64, i64]),
         "ptq_test_matmul_int8": (i32, [i32, i32, vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, i32, vp, i64, vp, sz,
@@ -115,6 +116,9 @@ def _load() -> ctypes.CDLL:
         "ptq_test_attention_int8_tree": (i32, [i32, i32, i32, vp, i64, vp, i64, vp, i32, i64, i32, vp, vp, vp, i64, vp,
                                                i64, vp, vp, vp, vp, i64, i32, i32, i32, ctypes.c_float, i64, vp, sz,
                                                vp]),
+        "ptq_test_verify_drafts_workspace_bytes": (sz, [i32, i64]),
+        "ptq_test_verify_drafts": (i32, [i32, vp, i64, vp, i64, i32, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, sz,
+                                         vp]),
         "layer_output_error": (i32, [vp, i32, i64, i64, vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, i32, dp, vp, sz,
                                      vp]),
     }
@@ -738,9 +742,17 @@ def _probabilities(t, rows, vocab, name):
     return max(_rows(t, name), vocab)
 
 
-def verify_drafts(target, tokens, parents, offsets, u, r, draft=None, path=None, counts=None, next=None):
+def verify_drafts_workspace_bytes(batch: int, vocab: int) -> int:
+    return int(_lib.verify_drafts_workspace_bytes(batch, vocab))
+
+
+def verify_drafts(target, tokens, parents, offsets, u, r, draft=None, path=None, counts=None, next=None, workspace=None):
     """verify_drafts (include/ptq.h): (path [rows], counts [batch], next [batch]) of each sequence's tree, from target
     and draft probabilities [rows, vocab] (draft None: drafts that were chosen) and random numbers u [rows], r [batch]."""
+    return _verify(None, target, tokens, parents, offsets, u, r, draft, path, counts, next, workspace)
+
+
+def _verify(shares, target, tokens, parents, offsets, u, r, draft, path, counts, next, workspace):
     if target.dim() != 2:
         raise ValueError("target must be [rows, vocab]")
     rows, vocab = target.shape
@@ -754,11 +766,16 @@ def verify_drafts(target, tokens, parents, offsets, u, r, draft=None, path=None,
     ints = lambda t, n: torch.empty(n, dtype=torch.int32, device=target.device) if t is None else t
     path, counts, next = ints(path, rows), ints(counts, batch), ints(next, batch)
     vec = lambda t, n, name, dtype=torch.int32: _vector(t, n, dtype, name)
-    _check(_lib.verify_drafts(_ptr(target), ldt, _ptr(draft), ldd, _dtype_code(target), rows, vocab,
-                              vec(tokens, rows, "tokens"), vec(parents, rows, "parents"),
-                              vec(offsets, batch + 1, "offsets"), batch, vec(u, rows, "u", torch.float32),
-                              vec(r, batch, "r", torch.float32), vec(path, rows, "path"), vec(counts, batch, "counts"),
-                              vec(next, batch, "next"), _stream()))
+    args = (_ptr(target), ldt, _ptr(draft), ldd, _dtype_code(target), rows, vocab, vec(tokens, rows, "tokens"),
+            vec(parents, rows, "parents"), vec(offsets, batch + 1, "offsets"), batch, vec(u, rows, "u", torch.float32),
+            vec(r, batch, "r", torch.float32), vec(path, rows, "path"), vec(counts, batch, "counts"),
+            vec(next, batch, "next"))
+    if shares is None:
+        ws, wsb = _scratch(verify_drafts_workspace_bytes(batch, vocab), target.device, workspace)
+        _check(_lib.verify_drafts(*args, _ptr(ws), wsb, _stream()))
+    else:
+        ws, wsb = _scratch(int(_lib.ptq_test_verify_drafts_workspace_bytes(shares, batch)), target.device, workspace)
+        _check(_lib.ptq_test_verify_drafts(shares, *args, _ptr(ws), wsb, _stream()))
     return path, counts, next
 
 
@@ -859,3 +876,8 @@ def _test_attention_int8_tree(tiles, waves, nsplit, Q, cache, offsets, seq_lens,
                                              _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scales), _ptr(cache.v_scales),
                                              nb, h, d, bs, float(scale or d ** -0.5), window, _ptr(ws), wsb, _stream()))
     return O, lse
+
+
+def _test_verify_drafts(shares, target, tokens, parents, offsets, u, r, draft=None):
+    """ptq_test_verify_drafts (include/ptq_testing.h): verify_drafts by this many workgroups a sequence."""
+    return _verify(shares, target, tokens, parents, offsets, u, r, draft, None, None, None, None)

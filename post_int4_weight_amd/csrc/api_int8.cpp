@@ -205,6 +205,36 @@ int check_probabilities(const char* fn, const char* name, const void* P, int dty
     return PTQ_OK;
 }
 
+constexpr int64_t MAX_BATCH_VERIFY = (int64_t)1 << 22;      // a workgroup of 1024 threads each, fewer than 2^32 threads
+
+// verify_drafts with the number of workgroups of a sequence given, or chosen (0)
+int verify(const char* fn, int shares, const void* target, int64_t ldt, const void* draft, int64_t ldd, int dtype,
+           int64_t vocab, const Drafts& d, int32_t* path, int32_t* counts, int32_t* next, void* workspace,
+           size_t workspace_bytes, void* stream) {
+    if (d.rows < 0 || d.rows > MAX_ROWS) REFUSE("%s: rows = %lld outside [0, 2^31)", fn, (long long)d.rows);
+    if (d.batch < 0 || d.batch >= MAX_BATCH_VERIFY / std::max(shares, 1))
+        REFUSE("%s: batch = %lld outside [0, 2^22)", fn, (long long)d.batch);
+    if (vocab < 1 || vocab > MAX_ROWS) REFUSE("%s: vocab = %lld outside [1, 2^31)", fn, (long long)vocab);
+    if (!dtype_ok(dtype)) REFUSE("%s: dtype = %d is neither PTQ_BF16 nor PTQ_F32", fn, dtype);
+    if (d.batch == 0) return PTQ_OK;
+    if (!d.offsets) REFUSE("%s: offsets is NULL", fn);
+    if (!counts || !next) REFUSE("%s: counts or next is NULL", fn);
+    if (d.rows > 0) {
+        PTQ_TRY(check_probabilities(fn, "target", target, dtype, vocab, ldt));
+        if (draft) PTQ_TRY(check_probabilities(fn, "draft", draft, dtype, vocab, ldd));
+        if (!d.tokens || !d.parents || !d.u || !d.r || !path) REFUSE("%s: tokens, parents, u, r or path is NULL", fn);
+    }
+    if (shares == 0) shares = verify_drafts_shares(d.batch, vocab);
+    const size_t need = verify_drafts_help_bytes(d.batch, shares);
+    if (need && (!workspace || workspace_bytes < need)) {
+        set_error("%s: workspace %zu bytes, need %zu", fn, workspace ? workspace_bytes : (size_t)0, need);
+        return PTQ_EWORKSPACE;
+    }
+    if (need && !aligned16(workspace)) REFUSE("%s: workspace is not 16-byte aligned", fn);
+    return launch_verify_drafts(target, ldt, draft, ldd, dtype, vocab, d, shares, path, counts, next, workspace,
+                                (hipStream_t)stream);
+}
+
 }  // namespace
 }  // namespace ptq
 
@@ -488,25 +518,33 @@ int ptq_test_attention_int8_tree(int tiles, int waves, int nsplit, const void* Q
                           workspace_bytes, stream);
 }
 
+size_t verify_drafts_workspace_bytes(int64_t batch, int64_t vocab) {
+    if (batch < 1 || batch >= MAX_BATCH_VERIFY || vocab < 1 || vocab > MAX_ROWS) return 0;
+    return verify_drafts_help_bytes(batch, verify_drafts_shares(batch, vocab));
+}
+
 int verify_drafts(const void* target, int64_t ldt, const void* draft, int64_t ldd, int dtype, int64_t rows,
                   int64_t vocab, const int32_t* tokens, const int32_t* parents, const int32_t* offsets, int64_t batch,
-                  const float* u, const float* r, int32_t* path, int32_t* counts, int32_t* next, void* stream) {
-    const char* fn = "verify_drafts";
-    if (rows < 0 || rows > MAX_ROWS) REFUSE("%s: rows = %lld outside [0, 2^31)", fn, (long long)rows);
-    // a workgroup of 1024 threads each, and fewer than 2^32 threads
-    if (batch < 0 || batch >= (int64_t)1 << 22) REFUSE("%s: batch = %lld outside [0, 2^22)", fn, (long long)batch);
-    if (vocab < 1 || vocab > MAX_ROWS) REFUSE("%s: vocab = %lld outside [1, 2^31)", fn, (long long)vocab);
-    if (!dtype_ok(dtype)) REFUSE("%s: dtype = %d is neither PTQ_BF16 nor PTQ_F32", fn, dtype);
-    if (batch == 0) return PTQ_OK;
-    if (!offsets) REFUSE("%s: offsets is NULL", fn);
-    if (!counts || !next) REFUSE("%s: counts or next is NULL", fn);
-    if (rows > 0) {
-        PTQ_TRY(check_probabilities(fn, "target", target, dtype, vocab, ldt));
-        if (draft) PTQ_TRY(check_probabilities(fn, "draft", draft, dtype, vocab, ldd));
-        if (!tokens || !parents || !u || !r || !path) REFUSE("%s: tokens, parents, u, r or path is NULL", fn);
-    }
+                  const float* u, const float* r, int32_t* path, int32_t* counts, int32_t* next, void* workspace,
+                  size_t workspace_bytes, void* stream) {
     const Drafts d{rows, batch, tokens, parents, offsets, u, r};
-    return launch_verify_drafts(target, ldt, draft, ldd, dtype, vocab, d, path, counts, next, (hipStream_t)stream);
+    return verify("verify_drafts", 0, target, ldt, draft, ldd, dtype, vocab, d, path, counts, next, workspace,
+                  workspace_bytes, stream);
+}
+
+size_t ptq_test_verify_drafts_workspace_bytes(int shares, int64_t batch) {
+    return shares < 1 || shares > VERIFY_SHARES || batch < 1 ? 0 : verify_drafts_help_bytes(batch, shares);
+}
+
+int ptq_test_verify_drafts(int shares, const void* target, int64_t ldt, const void* draft, int64_t ldd, int dtype,
+                           int64_t rows, int64_t vocab, const int32_t* tokens, const int32_t* parents,
+                           const int32_t* offsets, int64_t batch, const float* u, const float* r, int32_t* path,
+                           int32_t* counts, int32_t* next, void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "ptq_test_verify_drafts";
+    if (shares < 1 || shares > VERIFY_SHARES) REFUSE("%s: shares = %d outside [1, %d]", fn, shares, VERIFY_SHARES);
+    const Drafts d{rows, batch, tokens, parents, offsets, u, r};
+    return verify(fn, shares, target, ldt, draft, ldd, dtype, vocab, d, path, counts, next, workspace, workspace_bytes,
+                  stream);
 }
 
 }  // extern "C"

@@ -298,6 +298,10 @@ struct Drafts {
     const float* u; const float* r;
 };
 int launch_verify_drafts(const void* P, int64_t ldp, const void* Q, int64_t ldq, int dtype, int64_t vocab,
-                         const Drafts& d, int32_t* path, int32_t* counts, int32_t* next, hipStream_t st);
+                         const Drafts& d, int shares, int32_t* path, int32_t* counts, int32_t* next, void* workspace,
+                         hipStream_t st);
+int verify_drafts_shares(int64_t batch, int64_t vocab);
+constexpr int VERIFY_SHARES = 4;       // workgroups of a sequence at most
+size_t verify_drafts_help_bytes(int64_t batch, int shares);
 
 }  // namespace ptq

@@ -15,8 +15,13 @@
 // decided next to a border, and a token of probability 2^-17 among 10^5 others
 // would fall to the wrong side of fp32 sums.
 //
-// One workgroup a sequence. What every node's test needs of p and q is fetched
-// at once; the walk is then the same code on the same values in every wave.
+// One workgroup a sequence walks. What every node's test needs of p and q is
+// fetched at once; the walk is then the same code on the same values in every
+// wave. What bounds it: for small vocabularies the chain of loads (offsets, nodes,
+// their probabilities, the rows: 11 us for one sequence and 32000 tokens), for
+// large ones what one CU can load, 9 us for two rows of 128256 in fp32 (108 GB/s).
+// So there other workgroups help with the sums, see Help: 48 trees over 128256
+// tokens, fp32: 30 us, 46 without.
 #include "int8.hpp"
 
 namespace ptq {
@@ -24,6 +29,41 @@ namespace {
 
 constexpr int NT = 1024, NW = NT / 64;
 constexpr int NODES = TREE_NODES;
+constexpr int MAX_SHARES = VERIFY_SHARES;
+static_assert(MAX_SHARES * NW <= 64, "sums of a wave's segments: one a lane");
+
+// How the workgroups of a sequence share a sum. Its walker posts a job (the row,
+// and what is taken from it) under a new number and every workgroup, the walker
+// too, claims shares of it until none is left; the walker then waits for the
+// shares that were claimed. So it waits for workgroups alone that are running and
+// wait for nothing themselves, and needs no other: a helper that never runs, or
+// runs late, or has given up (POLLS looks without a new job) claims nothing.
+// Shares are summed in their order, whoever took them.
+//
+// Everything here is read and written by relaxed atomics of the device, which pass
+// the caches by. Acquiring and releasing would empty the L2 at every look: 207 us
+// where it takes 71 (48 sequences by four).
+struct Help {
+    unsigned long long ticket;     // number of the job << 32 | shares claimed
+    int node, without;             // the job: the row, whether tried tokens are left out, and c
+    double c;
+    double seg[MAX_SHARES * NW];   // sums, or NOT_YET
+};
+constexpr unsigned long long NOT_YET = 0x7ff4deadbeef0001ull;      // a NaN that no sum is: it signals
+constexpr unsigned OVER = 0xffffffffu;      // number after the last job
+constexpr int POLLS = 256;                  // at about 1 us each
+
+template <typename V>
+__device__ __forceinline__ V peek(const V* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+template <typename V>
+__device__ __forceinline__ void put(V* p, V x) { __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+// what this wave has put is there for all
+__device__ __forceinline__ void wait_put() {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+__device__ __forceinline__ unsigned long long claim_share(Help* h) {
+    return __hip_atomic_fetch_add(&h->ticket, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 
 struct VerifyArgs {
     const void* P; int64_t ldp;
@@ -31,6 +71,8 @@ struct VerifyArgs {
     int vocab;
     Drafts d;
     int32_t* path; int32_t* counts; int32_t* next;
+    int shares;          // workgroups of a sequence
+    Help* help;          // of each sequence, with more than one
 };
 
 // 16 bytes of a row that need not be aligned (vocabularies of odd sizes)
@@ -38,14 +80,11 @@ template <typename T>
 struct Chunk {
     static constexpr int N = 16 / sizeof(T);
     T x[N];
+    __device__ __forceinline__ void load(const T* p) { __builtin_memcpy(x, p, 16); }
     // the first `left` elements, zeros past them
     __device__ __forceinline__ void load(const T* p, int64_t left) {
-        if (left >= N) {
-            __builtin_memcpy(x, p, 16);
-        } else {
 #pragma unroll
-            for (int k = 0; k < N; ++k) x[k] = k < left ? p[k] : (T)0;
-        }
+        for (int k = 0; k < N; ++k) x[k] = k < left ? p[k] : (T)0;
     }
     __device__ __forceinline__ float at(int k) const { return load_as_float(x, k); }
 };
@@ -53,6 +92,17 @@ struct Chunk {
 __device__ __forceinline__ double sum_wave(double x) {
 #pragma unroll
     for (int o = 32; o > 0; o /= 2) x += __shfl_xor(x, o, 64);
+    return x;
+}
+
+// sums of the lanes up to each
+__device__ __forceinline__ double scan_wave(double x) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) {
+        const double y = __shfl_up(x, o, 64);
+        if (lane >= o) x += y;
+    }
     return x;
 }
 
@@ -64,89 +114,146 @@ struct Rest {
     const int* ex;
     int nex;
 
-    __device__ __forceinline__ double weight(float pv, float qv) const {
-        double w = (double)pv;
-        if constexpr (DRAWN) w -= c * (double)qv;
+    static __device__ __forceinline__ double weight(float pv, float qv, double c) {
+        const double w = (double)pv - c * (double)qv;
         return w < 0 ? 0. : w;      // a NaN stays one
     }
-    __device__ __forceinline__ double one(int64_t k) const {
+    // weights of the 8 tokens from k on; zeros from `end` on
+    __device__ __forceinline__ void eight(int64_t k, int64_t end, double (&w)[8]) const {
+        float pv[8], qv[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            pv[e] = k + e < end ? load_as_float(p, k + e) : 0.f;
+            qv[e] = DRAWN && c != 0. && k + e < end ? load_as_float(q, k + e) : 0.f;
+        }
         for (int j = 0; j < nex; ++j)
-            if (ex[j] == k) return 0.;
-        return weight(load_as_float(p, k), DRAWN ? load_as_float(q, k) : 0.f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (ex[j] == k + e) pv[e] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = weight(pv[e], qv[e], c);
     }
 };
 
-// Sums of the 16 shares of the vocabulary, one a wave, into seg; the whole sum comes back.
-template <typename T, bool DRAWN>
-__device__ double sum_rest(const Rest<T, DRAWN>& r, int vocab, int share, double (&seg)[NW]) {
+// This wave's sum of the weights of tokens lo .. hi; q counts where COVERED
+template <typename T, bool COVERED, typename R>
+__device__ __forceinline__ double sum_part(const R& r, int64_t lo, int64_t hi) {
     constexpr int N = Chunk<T>::N, STEP = 64 * N, U = 4;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t lo = (int64_t)wave * share, hi = std::min<int64_t>(lo + share, vocab);
+    const int lane = threadIdx.x & 63;
     double s[U] = {};
-    for (int64_t k0 = lo; k0 < hi; k0 += STEP * U) {
+    auto add = [&](Chunk<T> p, const Chunk<T>& q, int64_t at, double& to) __attribute__((always_inline)) {
+        for (int j = 0; j < r.nex; ++j)
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (r.ex[j] == at + k) p.x[k] = 0;
+#pragma unroll
+        for (int k = 0; k < N; ++k) to += R::weight(p.at(k), COVERED ? q.at(k) : 0.f, COVERED ? r.c : 0.);
+    };
+    int64_t k0 = lo + lane * N;
+    for (; k0 - lane * N + STEP * U <= hi; k0 += STEP * U) {
         Chunk<T> p[U], q[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t k = k0 + u * STEP + lane * N;
-            p[u].load(r.p + k, hi - k);
-            if constexpr (DRAWN) q[u].load(r.q + k, hi - k);
-        }
-        for (int j = 0; j < r.nex; ++j) {
-            const int64_t at = r.ex[j] - k0 - lane * N;
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int k = 0; k < N; ++k)
-                    if (at == u * STEP + k) p[u].x[k] = 0;
+            p[u].load(r.p + k0 + u * STEP);
+            if constexpr (COVERED) q[u].load(r.q + k0 + u * STEP);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int k = 0; k < N; ++k) s[u] += r.weight(p[u].at(k), DRAWN ? q[u].at(k) : 0.f);
+        for (int u = 0; u < U; ++u) add(p[u], q[u], k0 + u * STEP, s[u]);
     }
-    const double mine = sum_wave((s[0] + s[1]) + (s[2] + s[3]));
+    for (; k0 < hi; k0 += STEP) {
+        Chunk<T> p, q;
+        if (k0 + N <= hi) {
+            p.load(r.p + k0);
+            if constexpr (COVERED) q.load(r.q + k0);
+        } else {
+            p.load(r.p + k0, hi - k0);
+            if constexpr (COVERED) q.load(r.q + k0, hi - k0);
+        }
+        add(p, q, k0, s[0]);
+    }
+    return sum_wave((s[0] + s[1]) + (s[2] + s[3]));
+}
+
+// Segment `i` of the vocabulary: a wave's part of a share
+struct Segments {
+    int vocab, each, count;
+    __device__ __forceinline__ int64_t from(int i) const { return std::min<int64_t>((int64_t)i * each, vocab); }
+};
+
+// Sums a wave's segment of a share, for the walker to add up
+template <typename T, bool DRAWN>
+__device__ __forceinline__ void sum_share(const Rest<T, DRAWN>& r, const Segments& g, Help* h, int share, double* seg) {
+    const int lane = threadIdx.x & 63, i = share * NW + (threadIdx.x >> 6);
+    // a row that nothing is taken from yet is read alone
+    const double sum = DRAWN && r.c != 0. ? sum_part<T, DRAWN>(r, g.from(i), g.from(i + 1))
+                                          : sum_part<T, false>(r, g.from(i), g.from(i + 1));
+    if (lane != 0) return;
+    if (h) {
+        put(&h->seg[i], sum);
+    } else {
+        seg[i] = sum;
+    }
+}
+
+// Sums of all segments, into seg; the whole sum comes back.
+template <typename T, bool DRAWN>
+__device__ double sum_rest(const Rest<T, DRAWN>& r, const Segments& g, double (&seg)[MAX_SHARES * NW], Help* h,
+                           unsigned& job, int node, int& claim) {
+    const int t = threadIdx.x;
     __syncthreads();      // seg of the sum before has been read
-    if (lane == 0) seg[wave] = mine;
+    if (h) {
+        ++job;
+        if (t < g.count) put((unsigned long long*)&h->seg[t], NOT_YET);
+        if (t == 0) {
+            put(&h->node, node);
+            put(&h->c, r.c);
+            put(&h->without, (int)(r.nex > 0));
+        }
+        wait_put();
+        __syncthreads();
+        if (t == 0) put(&h->ticket, (unsigned long long)job << 32 | 1);
+    }
+    for (int share = 0; share < g.count / NW;) {
+        sum_share(r, g, h, share, seg);
+        if (!h) break;
+        __syncthreads();      // claim has been read
+        if (t == 0) claim = (int)(unsigned)claim_share(h);
+        __syncthreads();
+        share = claim;
+    }
+    if (h && t < g.count) {
+        unsigned long long x;
+        while ((x = peek((const unsigned long long*)&h->seg[t])) == NOT_YET) __builtin_amdgcn_s_sleep(1);
+        seg[t] = __longlong_as_double((long long)x);
+    }
     __syncthreads();
-    double total = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) total += seg[w];
-    return total;
+    const int lane = t & 63;
+    return sum_wave(lane < g.count ? seg[lane] : 0.);
 }
 
 // First token whose running sum exceeds goal; the last one with a weight where rounding leaves none.
 template <typename T, bool DRAWN>
-__device__ int draw_rest(const Rest<T, DRAWN>& r, int vocab, int share, const double (&seg)[NW], double goal,
+__device__ int draw_rest(const Rest<T, DRAWN>& r, const Segments& g, const double (&seg)[MAX_SHARES * NW], double goal,
                          double (&part)[NW], int& found) {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    double before = 0;
-    int at = -1, last = 0;
-    for (int w = 0; w < NW; ++w) {
-        if (seg[w] > 0) last = w;
-        if (at < 0) {
-            if (before + seg[w] > goal) at = w;
-            else before += seg[w];
-        }
-    }
-    if (at < 0) {
-        at = last;
-        before -= seg[last];
-    }
-    // the share again, each thread its own stretch
-    const int64_t lo = (int64_t)at * share, hi = std::min<int64_t>(lo + share, vocab);
+    const double mine = lane < g.count ? seg[lane] : 0., to = scan_wave(mine);
+    const uint64_t past = __ballot(mine > 0 && to > goal), any = __ballot(mine > 0);
+    const int at = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(any | 1);
+    double before = __shfl(to - mine, at, 64);
+    // the segment again, each thread its own stretch
+    const int64_t lo = g.from(at), hi = g.from(at + 1);
     const int64_t each = cdiv(hi - lo, NT), k0 = std::min(lo + t * each, hi), k1 = std::min(k0 + each, hi);
-    double sum = 0;
-    for (int64_t k = k0; k < k1; ++k) sum += r.one(k);
-    double upto = sum;
+    double sum = 0, w[8];
+    for (int64_t k = k0; k < k1; k += 8) {
+        r.eight(k, k1, w);
 #pragma unroll
-    for (int o = 1; o < 64; o *= 2) {
-        const double x = __shfl_up(upto, o, 64);
-        if (lane >= o) upto += x;
+        for (int e = 0; e < 8; ++e) sum += w[e];
     }
+    const double upto = scan_wave(sum);
     if (lane == 63) part[wave] = upto;
     if (t == 0) found = NT;
     __syncthreads();
-    for (int w = 0; w < wave; ++w) before += part[w];
+    before += sum_wave(lane < wave ? part[lane] : 0.);
     const uint64_t over = __ballot(before + upto > goal && sum > 0), some = __ballot(sum > 0);
     if (lane == 0 && over) atomicMin(&found, 64 * wave + __builtin_ctzll(over));
     __syncthreads();
@@ -162,11 +269,14 @@ __device__ int draw_rest(const Rest<T, DRAWN>& r, int vocab, int share, const do
     if (t == who) {
         double run = before + (upto - sum);
         int token = -1;
-        for (int64_t k = k0; k < k1; ++k) {
-            const double w = r.one(k);
-            run += w;
-            if (w > 0) token = (int)k;
-            if (w > 0 && run > goal) break;
+        for (int64_t k = k0; k < k1 && (token < 0 || run <= goal); k += 8) {
+            r.eight(k, k1, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (!(w[e] > 0) || (token >= 0 && run > goal)) continue;
+                run += w[e];
+                token = (int)k + e;
+            }
         }
         found = token;
     }
@@ -174,16 +284,40 @@ __device__ int draw_rest(const Rest<T, DRAWN>& r, int vocab, int share, const do
     return found;
 }
 
+// Tokens of the children of `node` (DRAWN = false: they have been tried)
+__device__ __forceinline__ int tried_tokens(const int* par, const int* tok, int n, int node, int* ex) {
+    const int lane = threadIdx.x & 63;
+    int count = 0;
+    for (int w = node / 64; w < (n + 63) / 64; ++w) {
+        const int i = 64 * w + lane;
+        const bool child = i < n && par[i] == node;
+        const uint64_t mask = __ballot(child);
+        if (child && threadIdx.x < 64) ex[count + __builtin_popcountll(mask & ((1ull << lane) - 1))] = tok[i];
+        count += __builtin_popcountll(mask);
+    }
+    __syncthreads();
+    return count;
+}
+
 template <typename T, bool DRAWN>
 __global__ __launch_bounds__(NT) void verify_kernel(VerifyArgs a) {
     __shared__ int par[NODES], tok[NODES], line[NODES], ex[NODES];
     __shared__ float pu[NODES], pp[NODES], qq[NODES];
-    __shared__ double seg[NW], part[NW];
-    __shared__ int found;
-    const int t = threadIdx.x, lane = t & 63, b = blockIdx.x;
+    __shared__ double seg[MAX_SHARES * NW], part[NW];
+    __shared__ int found, claim;
+    __shared__ unsigned number;
+    // walkers come first
+    const int t = threadIdx.x, lane = t & 63, batch = (int)a.d.batch, b = (int)(blockIdx.x % (unsigned)batch);
+    const bool walker = blockIdx.x < (unsigned)batch;
+    Help* const h = a.shares > 1 ? a.help + b : nullptr;
+    auto over = [&] {
+        if (h && t == 0) put(&h->ticket, (unsigned long long)OVER << 32);
+    };
     auto clamp = [&](int o) { return std::min<int64_t>(std::max(o, 0), a.d.rows); };
     const int64_t off = clamp(a.d.offsets[b]), rows = clamp(a.d.offsets[b + 1]) - off;
     if (rows <= 0 || rows > NODES) {
+        if (!walker) return;
+        over();
         for (int64_t i = t; i < rows; i += NT) a.path[off + i] = -1;
         if (t == 0) {
             a.counts[b] = 0;
@@ -199,18 +333,54 @@ __global__ __launch_bounds__(NT) void verify_kernel(VerifyArgs a) {
         const bool ok = i > 0 && p >= 0 && p < i && (unsigned)x < (unsigned)a.vocab;      // others are passed over
         par[i] = ok ? p : -1;
         tok[i] = x;
+        if (!walker) continue;
         pu[i] = a.d.u[off + i];
         pp[i] = ok ? load_as_float(P + p * a.ldp, x) : 0.f;
         if constexpr (DRAWN) qq[i] = ok ? load_as_float(Q + p * a.ldq, x) : 0.f;
     }
     __syncthreads();
 
-    // shares of whole chunks of a wave
-    const int step = 64 * Chunk<T>::N;
-    const int share = (int)std::min<int64_t>(cdiv(cdiv((int64_t)a.vocab, NW), step) * step, INT32_MAX);
+    // segments of whole steps of a wave
+    const int step = 64 * Chunk<T>::N, count_seg = a.shares * NW;
+    const Segments g{a.vocab, (int)std::min<int64_t>(cdiv(cdiv((int64_t)a.vocab, count_seg), step) * step, INT32_MAX), count_seg};
     Rest<T, DRAWN> r{P, Q, 0., ex, 0};
+    if (!walker) {
+        unsigned seen = 0;
+        for (bool look = true;;) {
+            if (t == 0) {
+                int polls = 0;
+                if (look)
+                    while (polls < POLLS && (unsigned)(peek(&h->ticket) >> 32) == seen) {
+                        ++polls;
+                        __builtin_amdgcn_s_sleep(8);
+                    }
+                number = OVER;
+                if (polls < POLLS) {
+                    const unsigned long long x = claim_share(h);
+                    number = (unsigned)(x >> 32);
+                    claim = (int)(unsigned)x;
+                }
+            }
+            __syncthreads();
+            if (number == OVER) return;
+            seen = number;
+            look = claim >= a.shares;
+            if (!look) {      // the job stays as it is while a share of it is being summed
+                const int node = std::min(std::max(peek(&h->node), 0), n - 1);
+                r.p = P + (int64_t)node * a.ldp;
+                if constexpr (DRAWN) r.q = Q + (int64_t)node * a.ldq;
+                r.c = peek(&h->c);
+                r.nex = 0;
+                if constexpr (!DRAWN)
+                    if (peek(&h->without)) r.nex = tried_tokens(par, tok, n, node, ex);
+                sum_share(r, g, h, claim, seg);
+            }
+            __syncthreads();      // number and claim have been read
+        }
+    }
     double z = 1., total = -1.;      // total: sum of what is left, -1 before it is known
     int cur = 0, count = 1;
+    unsigned job = 0;
     if (t == 0) line[0] = 0;
     for (bool moved = true; moved;) {
         moved = false;
@@ -223,9 +393,9 @@ __global__ __launch_bounds__(NT) void verify_kernel(VerifyArgs a) {
                 mask &= mask - 1;
                 double left;
                 if constexpr (DRAWN) {
-                    left = r.weight(pp[i], qq[i]);
+                    left = r.c != 0. ? r.weight(pp[i], qq[i], r.c) : r.weight(pp[i], 0.f, 0.);
                 } else {
-                    left = r.weight(pp[i], 0.f);
+                    left = r.weight(pp[i], 0.f, 0.);
                     for (int j = cur + 1; j < i; ++j)      // the same token has been tried
                         if (par[j] == cur && tok[j] == tok[i]) left = 0.;
                 }
@@ -242,31 +412,25 @@ __global__ __launch_bounds__(NT) void verify_kernel(VerifyArgs a) {
                     moved = true;
                 } else if constexpr (DRAWN) {
                     r.c += z;
-                    z = total = sum_rest(r, a.vocab, share, seg);
+                    z = total = sum_rest(r, g, seg, h, job, cur, claim);
                 } else {
                     z -= left;
                 }
             }
         }
     }
-    if constexpr (!DRAWN) {      // the children that were tried
-        for (int w = cur / 64; w < words; ++w) {
-            const int mine = 64 * w + lane;
-            const bool child = mine < n && par[mine] == cur;
-            const uint64_t mask = __ballot(child);
-            if (child && t < 64) ex[r.nex + __builtin_popcountll(mask & ((1ull << lane) - 1))] = tok[mine];
-            r.nex += __builtin_popcountll(mask);
+    if constexpr (!DRAWN) r.nex = tried_tokens(par, tok, n, cur, ex);
+    for (bool whole = false; total <= 0. && !whole;) {
+        if (total == 0.) {      // nothing is left: p itself
+            r.c = 0.;
+            r.nex = 0;
+            whole = true;
         }
-        __syncthreads();
+        total = sum_rest(r, g, seg, h, job, cur, claim);
     }
-    if (total == -1.) total = sum_rest(r, a.vocab, share, seg);
-    if (total == 0.) {      // nothing is left: p itself
-        r.c = 0.;
-        r.nex = 0;
-        total = sum_rest(r, a.vocab, share, seg);
-    }
+    over();
     int token = -1;
-    if (total > 0. && total < INFINITY) token = draw_rest(r, a.vocab, share, seg, (double)a.d.r[b] * total, part, found);
+    if (total > 0. && total < INFINITY) token = draw_rest(r, g, seg, (double)a.d.r[b] * total, part, found);
     __syncthreads();
     for (int i = t; i < n; i += NT) a.path[off + i] = i < count ? line[i] : -1;
     if (t == 0) {
@@ -275,9 +439,14 @@ __global__ __launch_bounds__(NT) void verify_kernel(VerifyArgs a) {
     }
 }
 
+__global__ void clear_help_kernel(Help* h, int batch) {
+    const int b = blockIdx.x * 64 + threadIdx.x;
+    if (b < batch) h[b].ticket = 0;
+}
+
 template <typename T>
 int launch(const VerifyArgs& a, hipStream_t st) {
-    const dim3 grid((unsigned)a.d.batch);
+    const dim3 grid((unsigned)(a.d.batch * a.shares));
     if (a.Q)
         hipLaunchKernelGGL((verify_kernel<T, true>), grid, dim3(NT), 0, st, a);
     else
@@ -288,10 +457,27 @@ int launch(const VerifyArgs& a, hipStream_t st) {
 
 }  // namespace
 
+// Workgroups of a sequence. Four, or as many as the CUs allow: 48 sequences of 6
+// nodes, 128256 tokens, fp32, 3 children not kept: 73 us by one, 59 by two, 51 by
+// four, 53 by five; 128 sequences 71 and 69 by two. Clearing what they share and
+// meeting cost more than that below about 10^5 tokens (65536, 32 sequences: 38 us
+// by one and 40 by four; with nothing to sum 15 and 20).
+int verify_drafts_shares(int64_t batch, int64_t vocab) {
+    if (vocab < 98304 || batch < 1) return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(MAX_SHARES, 256 / batch));
+}
+
+size_t verify_drafts_help_bytes(int64_t batch, int shares) { return shares > 1 ? (size_t)batch * sizeof(Help) : 0; }
+
 int launch_verify_drafts(const void* P, int64_t ldp, const void* Q, int64_t ldq, int dtype, int64_t vocab,
-                         const Drafts& d, int32_t* path, int32_t* counts, int32_t* next, hipStream_t st) {
+                         const Drafts& d, int shares, int32_t* path, int32_t* counts, int32_t* next, void* workspace,
+                         hipStream_t st) {
     if (d.batch == 0) return PTQ_OK;
-    const VerifyArgs a{P, ldp, Q, ldq, (int)vocab, d, path, counts, next};
+    const VerifyArgs a{P, ldp, Q, ldq, (int)vocab, d, path, counts, next, shares, (Help*)workspace};
+    if (shares > 1) {
+        hipLaunchKernelGGL(clear_help_kernel, dim3((unsigned)cdiv(d.batch, 64)), dim3(64), 0, st, a.help, (int)d.batch);
+        PTQ_LAUNCH_CHECK();
+    }
     return dtype == PTQ_F32 ? launch<float>(a, st) : launch<uint16_t>(a, st);
 }
 

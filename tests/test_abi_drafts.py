@@ -73,8 +73,9 @@ def test_tree():
 
 def test_verify():
     def call(t=P, ldt=100, d=P, ldd=100, dt=1, rows=5, vocab=100, tok=P, par=P, off=P, batch=2, u=P, r=P, path=P, counts=P,
-             next=P):
-        return lib.verify_drafts(t, ldt, d, ldd, dt, rows, vocab, tok, par, off, batch, u, r, path, counts, next, None)
+             next=P, ws=P, wsb=1 << 30):
+        return lib.verify_drafts(t, ldt, d, ldd, dt, rows, vocab, tok, par, off, batch, u, r, path, counts, next, ws, wsb,
+                                 None)
     for word, kw in (("rows", dict(rows=-1)), ("batch", dict(batch=-1)), ("batch", dict(batch=1 << 22)), ("vocab", dict(vocab=0)),
                      ("vocab", dict(vocab=1 << 31)), ("dtype", dict(dt=3)), ("offsets", dict(off=None)),
                      ("counts", dict(counts=None)), ("next", dict(next=None)), ("target is NULL", dict(t=None)),
@@ -84,6 +85,21 @@ def test_verify():
                      ("NULL", dict(path=None))):
         _refused(call(**kw), word)
     assert call(batch=0, off=None) == 0
+    assert lib.verify_drafts_workspace_bytes(2, 100) == 0 and lib.verify_drafts_workspace_bytes(0, 1 << 20) == 0
+    need = lib.verify_drafts_workspace_bytes(2, 1 << 20)
+    assert need > 0
+    big = dict(vocab=1 << 20, ldt=1 << 20, ldd=1 << 20)
+    assert call(**big, wsb=need - 1) == 4 and call(**big, ws=None) == 4
+    _refused(call(**big, ws=ctypes.c_void_p((1 << 20) + 8)), "workspace is not")
+
+
+def test_verify_hook():
+    def call(shares, batch=2, wsb=1 << 30):
+        return lib.ptq_test_verify_drafts(shares, P, 100, P, 100, 1, 5, 100, P, P, P, batch, P, P, P, P, P, P, wsb, None)
+    for shares in (0, 5, -1):
+        _refused(call(shares), "shares")
+    _refused(call(4, batch=1 << 20), "batch")
+    assert call(4, wsb=lib.ptq_test_verify_drafts_workspace_bytes(4, 2) - 1) == 4
 
 
 def test_tensors_on_the_host_are_refused():

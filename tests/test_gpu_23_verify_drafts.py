@@ -187,3 +187,32 @@ def test_strides_streams_and_graphs(gpu):
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(out, want[i])), i
+
+
+@pytest.mark.parametrize("drawn", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("vocab", [1, 700, 4099, 131073])
+@pytest.mark.parametrize("shares", [1, 2, 3, 4])
+def test_workgroups_of_a_sequence(gpu, shares, vocab, dtype, drawn):
+    """The same by any number of workgroups, calls that follow each other included (the state that they share starts anew)."""
+    from post_int4_weight_amd import api
+    announce(f"verify shares={shares} vocab={vocab} {dtype} drawn={drawn}")
+    far = _inputs([9, 0, 30, 1, 600, 7], vocab, dtype, drawn, 5, gpu, near=3.0, reach=30)      # many are not kept
+    far["u"].mul_(0.3).add_(0.7)
+    whole = _inputs([4, 4], vocab, dtype, drawn, 6, gpu)
+    if drawn:      # nothing is left
+        whole["draft"][:] = whole["target"] * 2
+        whole["u"][:] = 1.0
+    for d in (far, whole, far):
+        off = _offsets([len(t) for t in d["trees"]])
+        args = (d["target"], _ints(d["tokens"], gpu), _ints([p for t in d["trees"] for p in t], gpu), _ints(off, gpu),
+                d["u"].to(gpu), d["r"].to(gpu))
+        path, counts, token = (x.cpu().tolist() for x in api._test_verify_drafts(shares, *args, draft=d["draft"]))
+        target, draft = to64(d["target"]), to64(d["draft"]) if drawn else None
+        for b, t in enumerate(d["trees"]):
+            at = slice(off[b], off[b + 1])
+            kept, after = [], -1
+            if len(t) <= 512:
+                kept, after = ref.verify(target[at], draft[at] if drawn else None, d["tokens"][at], t,
+                                         d["u"][at].double().numpy(), float(d["r"][b]))
+            assert path[at] == kept + [-1] * (len(t) - len(kept)) and (counts[b], token[b]) == (len(kept), after), b
