@@ -88,7 +88,7 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t unit, int t
 // The same of a sequence whose last rows are the nodes of a tree: all see the keys before it (a window may hide the first),
 // and what a row sees from hi_min on is in its line.
 __device__ __forceinline__ bool find_tree_tile(const AttnArgs& a, int64_t unit, int tr, Tile& t) {
-    const RaggedUnit u = ragged_find(a.g, unit, a.group, tr, 1);
+    const RaggedUnit u = find_longest_first(a.g, (unsigned)unit, a.group, tr);
     t.b = u.b;
     t.off = u.off;
     const int64_t n = u.rows, rows = n * a.group, f0 = u.local * tr;
@@ -461,7 +461,7 @@ __global__ __launch_bounds__(64 * WAVES) void attention_tile_kernel(AttnArgs a) 
     const int h = (int)(tile % a.kv_heads);
     Tile tl;
     // later tiles of a sequence have more keys: they go first
-    const int64_t unit = gridDim.x / (unsigned)a.nsplit / a.kv_heads - 1 - tile / a.kv_heads;
+    const int64_t unit = TREE ? tile / a.kv_heads : gridDim.x / (unsigned)a.nsplit / a.kv_heads - 1 - tile / a.kv_heads;
     if (!(TREE ? find_tree_tile(a, unit, 32 * WAVES, tl) : find_tile(a, unit, 32 * WAVES, tl))) return;
     const int per = split_steps(tl, a.nsplit, 32 * WAVES);
     const int s0 = __builtin_amdgcn_readfirstlane(tl.it0 + split * per);

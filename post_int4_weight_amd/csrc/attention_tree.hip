@@ -36,8 +36,9 @@ struct TreeTile {
     bool bad;              // longer than its row of the table can hold, or more nodes than a line has: NaN
 };
 
+template <bool LONGEST_FIRST>
 __device__ __forceinline__ bool find_tile(const TreeArgs& a, unsigned unit, int tr, int tk, TreeTile& t) {
-    const RaggedUnit u = ragged_find(a.g, unit, a.group, tr, 1);
+    const RaggedUnit u = LONGEST_FIRST ? find_longest_first(a.g, unit, a.group, tr) : ragged_find(a.g, unit, a.group, tr, 1);
     t.b = u.b;
     t.off = u.off;
     const int64_t rows = u.rows * a.group, f0 = u.local * tr;      // below 2^25 (rows x heads)
@@ -189,7 +190,7 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
     const unsigned tile = blockIdx.x / (unsigned)a.nsplit;
     const int h = (int)(tile % (unsigned)a.kv_heads);
     TreeTile tl;
-    if (!find_tile(a, tile / (unsigned)a.kv_heads, ROWS, TK, tl)) return;
+    if (!find_tile<true>(a, tile / (unsigned)a.kv_heads, ROWS, TK, tl)) return;
     const int per = split_steps(tl, a.nsplit);
     const int s0 = tl.it0 + split * per, s1 = std::min(s0 + per, tl.it1);
     if (split > 0 && s0 >= s1) return;
@@ -506,7 +507,7 @@ __global__ __launch_bounds__(256) void attention_tree_join_kernel(TreeArgs a) {
     const unsigned part = blockIdx.x % (unsigned)(tr / 16), tile = blockIdx.x / (unsigned)(tr / 16);
     const int h = (int)(tile % (unsigned)a.kv_heads);
     TreeTile tl;
-    if (!find_tile(a, tile / (unsigned)a.kv_heads, tr, TK, tl)) return;
+    if (!find_tile<false>(a, tile / (unsigned)a.kv_heads, tr, TK, tl)) return;
     const int per = split_steps(tl, a.nsplit);
     const int n = std::max(1, (tl.it1 - tl.it0 + per - 1) / per);    // split 0 is always written
     const int r = threadIdx.x / 16, c = threadIdx.x % 16, f = tl.f0 + (int)part * 16 + r;

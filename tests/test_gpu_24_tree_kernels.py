@@ -1,5 +1,6 @@
 """GPU: every kernel of attention_int8_tree by name (the hook in include/ptq_testing.h), with and without splits, against the
 fp64 oracle within the bounds of test_gpu_22_attention_tree.py, which reaches the ones that the estimates choose."""
+import numpy as np
 import pytest
 import torch
 
@@ -78,3 +79,24 @@ def test_hook_refuses(gpu):
     for plan in ((2, 8, 1), (0, 2, 1), (1, 4, 1), (0, 8, 1), (1, 8, 1), (0, 4, 0), (0, 4, 65)):
         with pytest.raises(api.PTQError):
             api._test_attention_int8_tree(*plan, Q, cache, *args)
+
+
+@pytest.mark.parametrize("plan", [(0, 4, 1), (0, 8, 2), (1, 8, 1), (1, 8, 3)])
+@pytest.mark.parametrize("batch", [2, 63, 64, 65])
+def test_the_order_of_sequences(gpu, batch, plan):
+    """Ragged batches of more workgroups than start at once, whose longest sequences go first: equal lengths, sequences
+    without rows or keys, one longer than its row of the table."""
+    from post_int4_weight_amd import api
+    announce(f"tree kernels, order of {batch} sequences, plan {plan}")
+    rng = np.random.default_rng(batch)
+    prefix = [int(x) for x in rng.integers(0, 30, batch) * rng.integers(0, 30, batch)]
+    nodes = [int(x) for x in rng.integers(0, 9, batch)]
+    prefix[0], nodes[:2], heads, kv = 800, [5, 40], 32 if batch > 2 else 256, 8 if batch > 2 else 128
+    Q, cache, args, vals = _make(api, gpu, prefix, _trees(nodes, 3, batch), heads, kv, 64, 32, "bf16", seed=batch)
+    O, lse = api._test_attention_int8_tree(*plan, Q, cache, *args)
+    torch.cuda.synchronize()
+    _check(O, lse, Q, vals, _trees(nodes, 3, batch), heads, kv, 64 ** -0.5, 0)
+    args[1] = args[1].clone()
+    args[1][0] = args[2].shape[1] * 32 + 1
+    P, _ = api._test_attention_int8_tree(*plan, Q, cache, *args)
+    assert torch.isnan(P[:nodes[0]]).all() and torch.equal(P[nodes[0]:], O[nodes[0]:])
