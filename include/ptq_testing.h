@@ -85,9 +85,9 @@ int ptq_test_attention_int8_cache(int tiles, int waves, int nsplit, const void* 
                                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* attention_int8_tree with the kernel given instead of chosen: tiles of 256
- * query rows (1; head_dim up to 128, 8 waves) or of 32 (0; 4 waves, or 8 with
- * head_dim up to 128), and the splits of the keys (1 .. 64). _plan says what
- * attention_int8_tree chooses. Returns PTQ_OK, PTQ_EINVAL, PTQ_EWORKSPACE or
+ * query rows (1; head_dim up to 128, 8 waves), of 32 (0) or of 16 (2; 4 waves,
+ * or 8 with head_dim up to 128), and the splits of the keys (1 .. 64). _plan says
+ * what attention_int8_tree chooses. Returns PTQ_OK, PTQ_EINVAL, PTQ_EWORKSPACE or
  * PTQ_EHIP. */
 int ptq_test_attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim, int dtype,
                                  int block_size, int64_t table_width, int64_t window, int* tiles, int* waves, int* nsplit);

@@ -489,7 +489,7 @@ int ptq_test_attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_
         !tiles || !waves || !nsplit)
         REFUSE("%s: bad arguments", fn);
     const TreePlan p = attention_tree_plan(rows, batch, heads, kv_heads, head_dim, dtype, block_size, table_width, window);
-    *tiles = p.tr == ATTN_TILE;
+    *tiles = p.tr == ATTN_TILE ? 1 : p.tr == ATTN_ROWS ? 2 : 0;
     *waves = p.nw;
     *nsplit = p.nsplit;
     return PTQ_OK;
@@ -507,13 +507,13 @@ int ptq_test_attention_int8_tree(int tiles, int waves, int nsplit, const void* Q
                                  int head_dim, int block_size, float scale, int64_t window, void* workspace,
                                  size_t workspace_bytes, void* stream) {
     const char* fn = "ptq_test_attention_int8_tree";
-    if ((tiles != 0 && tiles != 1) || (waves != 8 && (waves != 4 || tiles)) || (waves == 8 && head_dim > 128) ||
+    if (tiles < 0 || tiles > 2 || (waves != 8 && (waves != 4 || tiles == 1)) || (waves == 8 && head_dim > 128) ||
         nsplit < 1 || nsplit > 64 || rows > 1 << 16 || batch > 1 << 10)
         REFUSE("%s: tiles = %d, waves = %d, nsplit = %d", fn, tiles, waves, nsplit);
     const KVCacheInt8 c{const_cast<int8_t*>(k_codes), const_cast<int8_t*>(v_codes), const_cast<float*>(k_scales),
                         const_cast<float*>(v_scales), num_blocks, kv_heads, head_dim, block_size};
     const RaggedRows r{rows, batch, offsets, seq_lens, block_table, table_width};
-    const TreePlan p{tiles ? ATTN_TILE : ATTN_TREE_ROWS, waves, nsplit};
+    const TreePlan p{tiles == 1 ? ATTN_TILE : tiles == 2 ? ATTN_ROWS : ATTN_TREE_ROWS, waves, nsplit};
     return attention_tree(fn, &p, c, r, parents, dtype, Q, ldq, heads, scale, window, O, ldo, lse, workspace,
                           workspace_bytes, stream);
 }

@@ -58,8 +58,9 @@ struct TreeArgs {
     int nsplit;
     float* part; float* part_lse;  // [nsplit][rows * heads][dim], [nsplit][rows * heads]
 };
-// The tiles of 256 rows of attention_int8.hip (head_dim up to 128): writes O and lse, or the splits' parts.
-int launch_attention_tree_tiles(const TreeArgs& a, int dtype, int dim, hipStream_t st);
+// The kernels of attention_int8.hip, by tiles of tr = ATTN_ROWS rows (nw waves: 4, or 8 up to 128 channels) or of
+// ATTN_TILE (up to 128 channels): write O and lse, or the splits' parts.
+int launch_attention_tree_rows(const TreeArgs& a, int dtype, int dim, int tr, int nw, hipStream_t st);
 
 // Unit w of the tiles of tr rows of each sequence, those of the longest sequence
 // first: workgroups start in their order, and the longest, started last, would be

@@ -167,7 +167,9 @@ struct StepCodes {
     float sk, sv;
 };
 
-template <typename T, int D, int NW>
+//
+// TREE: the queries are the nodes of trees of drafted tokens (attention_tree.hip).
+template <typename T, int D, int NW, bool TREE>
 __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
     constexpr int NT = sizeof(T) == 4 ? 2 : 1;    // fp16 terms of q and of the probabilities
     constexpr int NC = D / 32;                    // 32-deep steps of q.k
@@ -175,7 +177,7 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
     const int64_t tile = blockIdx.x / (unsigned)a.nsplit;
     const int h = (int)(tile % a.kv_heads);
     Tile tl;
-    if (!find_tile(a, tile / a.kv_heads, TR, tl)) return;
+    if (!(TREE ? find_tree_tile(a, tile / a.kv_heads, TR, tl) : find_tile(a, tile / a.kv_heads, TR, tl))) return;
     const int per = split_steps(tl, a.nsplit, TR);
     const int s0 = tl.it0 + split * per, s1 = std::min(s0 + per, tl.it1);
     if (split > 0 && s0 >= s1) return;
@@ -186,7 +188,19 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
     const int64_t token = tl.off + f / a.group;
     const int qh = h * a.group + f % a.group;
     const int64_t pos = tl.pos0 + f / a.group;
-    const int my_lo = (int)row_lo(a, pos), my_hi = (int)row_hi(a, pos, tl.len);
+    int my_lo = 0, my_hi = 0;
+    if constexpr (!TREE) my_lo = (int)row_lo(a, pos), my_hi = (int)row_hi(a, pos, tl.len);
+    // lines of the tile's nodes, where this split has keys of the tree or a window asks for depths
+    __shared__ TreeLines<TREE ? TR : 1> lines_of;
+    const int first_node = tl.f0 / a.group;
+    const bool lines = TREE && !tl.over && (a.window > 0 || (int64_t)s1 * TK > tl.pos0);
+    constexpr int PN = (NODES + 64 * NW - 1) / (64 * NW);
+    int up[PN];
+    if constexpr (TREE)
+        if (lines)
+#pragma unroll
+            for (int i = 0; i < PN; ++i)
+                up[i] = a.parents[tl.off + std::min((int)threadIdx.x + 64 * NW * i, tl.rows / a.group - 1)];
 
     const int32_t* table = a.table + (int64_t)tl.b * a.width;
     const int64_t pool = (int64_t)a.bs * D, stride = (int64_t)a.kv_heads * pool;      // codes of a (block, head), of a block
@@ -218,6 +232,7 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
         c.sk = a.ks[at];
         c.sv = a.vs[at];
         if (!ok(idv)) c.sk = c.sv = __builtin_nanf("");
+        if (TREE && !(c.sk < INFINITY)) c.sk = __builtin_nanf("");
         if (!(c.sv < INFINITY)) c.sv = __builtin_nanf("");     // times codes of one sign it would stay infinite
         if (tv >= end) c.sk = c.sv = 0.f;
     };
@@ -249,24 +264,28 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
         const int tv = it * TK + vgrp;
         const bool whole = it * TK >= tl.lo_max && (int64_t)it * TK + TK <= tl.hi_min;   // no row masks anything here
         const int r_lo = my_lo - tv, r_hi = my_hi - tv;
+        uint32_t seen = 0xffffu;
+        if constexpr (TREE)
+            if (!whole) seen = seen16(lines_of.line[f / a.group - first_node], tv, (int)tl.pos0, my_lo);
+        auto hidden = [&](int i) { return TREE ? !(seen >> i & 1) : !whole && (i < r_lo || i >= r_hi); };
         float top = -INFINITY;
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float x = s[t][i] * ck;
-                if (!whole && (4 * t + i < r_lo || 4 * t + i >= r_hi)) x = -INFINITY;
+                if (hidden(4 * t + i)) x = -INFINITY;
                 s[t][i] = x;
                 top = fmaxf(top, x);
             }
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
         // R: largest finite S_v of the row's blocks so far
-        float big = c.sv < INFINITY && (whole || (r_lo < 16 && r_hi > 0)) ? c.sv : 0.f;
+        float big = c.sv < INFINITY && (TREE ? seen != 0 : whole || (r_lo < 16 && r_hi > 0)) ? c.sv : 0.f;
         big = fmaxf(big, __shfl_xor(big, 16, 64));
         big = fmaxf(big, __shfl_xor(big, 32, 64));
         if (__any(top > m + LAZY || big > R)) {
-            const float m_new = fmaxf(m, top);
+            const float m_new = !TREE || top > m + LAZY ? fmaxf(m, top) : m;      // a tree's rows each by itself
             float fall = m_new == m ? 1.f : exp2_fast(m - m_new);
             m = m_new;
             l *= fall;
@@ -291,8 +310,8 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
                 l += p1;
                 f32x2 y = {p0 * rv, p1 * rv};
                 if (!whole) {      // S_v of a block that is not this row's may be NaN
-                    if (4 * t + i < r_lo || 4 * t + i >= r_hi) y[0] = 0.f;
-                    if (4 * t + i + 1 < r_lo || 4 * t + i + 1 >= r_hi) y[1] = 0.f;
+                    if (hidden(4 * t + i)) y[0] = 0.f;
+                    if (hidden(4 * t + i + 1)) y[1] = 0.f;
                 }
                 const f16x2 x = __builtin_convertvector(y, f16x2);
                 const int e = 4 * (t & 1) + i;
@@ -317,8 +336,26 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
 
     int it = s0 + wave;
     if (it < s1) ids(it);
+    constexpr bool EARLY = TREE && D <= 128;      // the first keys are on their way while lines are built
+    StepCodes<D> first;
+    if constexpr (EARLY)
+        if (it < s1) load(it, first);
     qs = load_query<T, NC, 16>((const T*)a.Q + token * a.ldq + (int64_t)qh * D, a.scale2, q,
                                [&](int c) { return 64 * (c / 2) + 16 * lg + 8 * (c % 2); });
+    if constexpr (TREE)
+        if (lines) {
+            const int count = std::min(tl.f0 + TR - 1, tl.rows - 1) / a.group - first_node + 1;
+            build_lines<64 * NW>(lines_of, up, tl.rows / a.group, first_node, count, a.window, (int)threadIdx.x);
+            const int depth = lines_of.level[f / a.group - first_node];
+            if (depth < 0) l = __builtin_nanf("");
+            my_lo = first_key((int)tl.pos0, depth, a.window);
+        }
+    if constexpr (EARLY)
+        if (it < s1) {
+            if (it + NW < s1) ids(it + NW);
+            work(it, first);
+            it += NW;
+        }
     for (; it < s1; it += NW) {
         StepCodes<D> c;
         load(it, c);
@@ -1073,12 +1110,12 @@ int launch(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
             hipLaunchKernelGGL((attention_tile_kernel<T, D, TILE_WAVES, false>), grid, dim3(64 * TILE_WAVES), TileLds<D>::BYTES, st,
                                a);
         } else if (p.nw == 8) {
-            hipLaunchKernelGGL((attention_rows_kernel<T, D, 8>), grid, dim3(512), 0, st, a);
+            hipLaunchKernelGGL((attention_rows_kernel<T, D, 8, false>), grid, dim3(512), 0, st, a);
         } else {
-            hipLaunchKernelGGL((attention_rows_kernel<T, D, 4>), grid, dim3(256), 0, st, a);
+            hipLaunchKernelGGL((attention_rows_kernel<T, D, 4, false>), grid, dim3(256), 0, st, a);
         }
     } else {
-        hipLaunchKernelGGL((attention_rows_kernel<T, D, 4>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((attention_rows_kernel<T, D, 4, false>), grid, dim3(256), 0, st, a);
     }
     PTQ_LAUNCH_CHECK();
     if (a.nsplit > 1) {
@@ -1149,23 +1186,44 @@ int run_attention_int8(const AttnPlan& p, const KVCacheInt8& c, const RaggedRows
 namespace {
 
 template <typename T, int D>
-int launch_tree(const AttnArgs& a, hipStream_t st) {
-    static bool ready = false;    // more than 64 KB of LDS
-    if (!ready) {
-        PTQ_HIP(hipFuncSetAttribute((const void*)attention_tile_kernel<T, D, TILE_WAVES, true>,
-                                    hipFuncAttributeMaxDynamicSharedMemorySize, TileLds<D>::BYTES));
-        ready = true;
+int launch_tree(const AttnArgs& a, int tr, int nw, hipStream_t st) {
+    const dim3 grid((unsigned)(tile_units(a.g.rows, a.g.batch, a.group, tr) * a.kv_heads * a.nsplit));
+    if constexpr (D <= 128) {
+        if (tr == ATTN_TILE) {
+            static bool ready = false;    // more than 64 KB of LDS
+            if (!ready) {
+                PTQ_HIP(hipFuncSetAttribute((const void*)attention_tile_kernel<T, D, TILE_WAVES, true>,
+                                            hipFuncAttributeMaxDynamicSharedMemorySize, TileLds<D>::BYTES));
+                ready = true;
+            }
+            hipLaunchKernelGGL((attention_tile_kernel<T, D, TILE_WAVES, true>), grid, dim3(64 * TILE_WAVES),
+                               TileLds<D>::BYTES, st, a);
+            PTQ_LAUNCH_CHECK();
+            return PTQ_OK;
+        }
+        if (nw == 8) {
+            hipLaunchKernelGGL((attention_rows_kernel<T, D, 8, true>), grid, dim3(512), 0, st, a);
+            PTQ_LAUNCH_CHECK();
+            return PTQ_OK;
+        }
     }
-    const int64_t units = tile_units(a.g.rows, a.g.batch, a.group, ATTN_TILE) * a.kv_heads;
-    hipLaunchKernelGGL((attention_tile_kernel<T, D, TILE_WAVES, true>), dim3((unsigned)(units * a.nsplit)),
-                       dim3(64 * TILE_WAVES), TileLds<D>::BYTES, st, a);
+    hipLaunchKernelGGL((attention_rows_kernel<T, D, 4, true>), grid, dim3(256), 0, st, a);
     PTQ_LAUNCH_CHECK();
     return PTQ_OK;
 }
 
+template <typename T>
+int launch_tree(const AttnArgs& a, int tr, int nw, hipStream_t st) {
+    switch (a.dim) {
+        case 64: return launch_tree<T, 64>(a, tr, nw, st);
+        case 128: return launch_tree<T, 128>(a, tr, nw, st);
+        default: return launch_tree<T, 256>(a, tr, nw, st);
+    }
+}
+
 }  // namespace
 
-int launch_attention_tree_tiles(const TreeArgs& t, int dtype, int dim, hipStream_t st) {
+int launch_attention_tree_rows(const TreeArgs& t, int dtype, int dim, int tr, int nw, hipStream_t st) {
     AttnArgs a{};
     a.g = t.g;
     a.table = t.table; a.width = t.width;
@@ -1176,8 +1234,7 @@ int launch_attention_tree_tiles(const TreeArgs& t, int dtype, int dim, hipStream
     a.scale2 = t.scale2;
     a.causal = 1; a.window = t.window; a.parents = t.parents;
     a.nsplit = t.nsplit; a.part = t.part; a.part_lse = t.part_lse;
-    if (dtype == PTQ_F32) return dim == 64 ? launch_tree<float, 64>(a, st) : launch_tree<float, 128>(a, st);
-    return dim == 64 ? launch_tree<uint16_t, 64>(a, st) : launch_tree<uint16_t, 128>(a, st);
+    return dtype == PTQ_F32 ? launch_tree<float>(a, tr, nw, st) : launch_tree<uint16_t>(a, tr, nw, st);
 }
 
 }  // namespace ptq

@@ -58,8 +58,8 @@ __device__ __forceinline__ bool find_tile(const TreeArgs& a, unsigned unit, int 
 
 // Steps of a split of a tile: an even share, but not so few that the start of a
 // workgroup and the join would outweigh them.
-__device__ __forceinline__ int split_steps(const TreeTile& t, int nsplit) {
-    return std::max(4, (t.it1 - t.it0 + nsplit - 1) / nsplit);
+__device__ __forceinline__ int split_steps(const TreeTile& t, int nsplit, int least = 4) {
+    return std::max(least, (t.it1 - t.it0 + nsplit - 1) / nsplit);
 }
 
 // |x| as bits, in the order of the values: a NaN's are the largest
@@ -150,7 +150,8 @@ struct QueryRow {
 // tiles on the same keys the vector instructions of the exponentials and of the
 // conversion of V. Tiles of 64 and 128 rows that share a step among waves were 1%
 // faster in the mean over 1700 shapes, and taken out; from about 300 rows a kv
-// head on, the tiles of 256 rows of attention_int8.hip win.
+// head on, the tiles of 256 rows of attention_int8.hip win, and for few rows and
+// keys its tiles of 16, whose keys go straight into registers.
 template <typename T>
 constexpr int blocks_of(int dim) { return dim <= (sizeof(T) == 4 ? 64 : 128) ? 2 : 1; }
 constexpr int waves_of(int dim) { return dim <= 128 ? 2 : 1; }
@@ -503,12 +504,12 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
 // time with all their loads at once; tr: rows of the tiles that were split.
 template <typename T, int D, int tr>
 __global__ __launch_bounds__(256) void attention_tree_join_kernel(TreeArgs a) {
-    constexpr int TK = tr == ATTN_TILE ? ptq::TK : 32 * blocks_of<T>(D);
+    constexpr int TK = tr == ROWS ? 32 * blocks_of<T>(D) : ptq::TK;
     const unsigned part = blockIdx.x % (unsigned)(tr / 16), tile = blockIdx.x / (unsigned)(tr / 16);
     const int h = (int)(tile % (unsigned)a.kv_heads);
     TreeTile tl;
     if (!find_tile<false>(a, tile / (unsigned)a.kv_heads, tr, TK, tl)) return;
-    const int per = split_steps(tl, a.nsplit);
+    const int per = split_steps(tl, a.nsplit, tr == ATTN_ROWS ? 8 : 4);
     const int n = std::max(1, (tl.it1 - tl.it0 + per - 1) / per);    // split 0 is always written
     const int r = threadIdx.x / 16, c = threadIdx.x % 16, f = tl.f0 + (int)part * 16 + r;
     if (f >= tl.rows) return;
@@ -560,13 +561,16 @@ template <typename T, int D>
 int launch(const TreeArgs& a, const TreePlan& p, hipStream_t st) {
     const int64_t units = tile_units(a.g.rows, a.g.batch, a.group, p.tr) * a.kv_heads;
     const dim3 grid((unsigned)(units * a.nsplit)), join((unsigned)(units * (p.tr / 16)));
-    if constexpr (D <= 128) {
-        if (p.tr == ATTN_TILE) {
-            PTQ_TRY(launch_attention_tree_tiles(a, sizeof(T) == 4 ? PTQ_F32 : PTQ_BF16, D, st));
-            if (a.nsplit > 1) hipLaunchKernelGGL((attention_tree_join_kernel<T, D, ATTN_TILE>), join, dim3(256), 0, st, a);
+    if (p.tr != ROWS) {
+        PTQ_TRY(launch_attention_tree_rows(a, sizeof(T) == 4 ? PTQ_F32 : PTQ_BF16, D, p.tr, p.nw, st));
+        if (a.nsplit > 1) {
+            if (p.tr == ATTN_ROWS)
+                hipLaunchKernelGGL((attention_tree_join_kernel<T, D, ATTN_ROWS>), join, dim3(256), 0, st, a);
+            else if constexpr (D <= 128)
+                hipLaunchKernelGGL((attention_tree_join_kernel<T, D, ATTN_TILE>), join, dim3(256), 0, st, a);
             PTQ_LAUNCH_CHECK();
-            return PTQ_OK;
         }
+        return PTQ_OK;
     }
     if (D <= 128 && p.nw == 8) {
         if constexpr (D <= 128) hipLaunchKernelGGL((attention_tree_kernel<T, D, 8>), grid, dim3(512), 0, st, a);
@@ -602,41 +606,49 @@ size_t attention_tree_part_bytes(int nsplit, int64_t rows, int heads, int dim) {
 
 // The choice of a TreePlan: the least of estimated times, in microseconds,
 //   start + rounds (first + steps each) + [join + bytes of the parts],
-// fitted to 1950 shapes with all their plans (1 .. 64 sequences of 1 .. 64 nodes, 1
-// .. 8 kv heads, groups of 1 .. 8, 64 .. 16000 keys); the choice is 3% slower than
-// the best plan in the mean, 10% at nine shapes of ten, 58% at worst. Lengths are
-// not known here: keys is the most there may be, and every sequence is taken to
-// have the mean number of rows. A round is as many workgroups as the card holds.
+// fitted to 750 shapes with all their plans (1 .. 64 sequences of 1 .. 64 nodes, 1
+// .. 8 kv heads, groups of 1 .. 8, 64 .. 16000 keys, half of them ragged). The
+// choice is 4% slower than the best plan in the mean, 15% at nine shapes of ten, 45%
+// at worst. Without one of the kernels the best plan would be slower in the mean by
+// 3.5% (tiles of 16 rows: 1 tree of 16 nodes over 1000 keys 15.3 us, of 32 rows 18.6),
+// 8.6% (of 32) and 5.9% (32 rows by four waves). Lengths are not known here: keys
+// is the most there may be, and every sequence is taken to have the mean number of
+// rows. A round is as many workgroups as the card holds.
 TreePlan attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int dtype, int block,
                              int64_t width, int64_t window) {
     const int64_t group = heads / kv_heads, most = width * block;
     const int64_t keys = window > 0 && window < most ? std::min(most, window + cdiv(rows, batch)) : most;
     const int64_t each = cdiv(rows * group, batch);
-    const bool f32 = dtype == PTQ_F32;
+    const bool f32 = dtype == PTQ_F32, wide = dim > 128;
     const int d = dim == 64 ? 0 : dim == 128 ? 1 : 2;
     struct Kind {
-        TreePlan plan;
+        int tr, nw;
         double start, first, step[2][3];      // step: bf16, fp32 at 64, 128, 256 channels
+        int slots[3], least;                  // workgroups at once, steps of a split at least
     };
-    const Kind kinds[] = {{{ROWS, 4, 1}, 7.8, dim <= 128 ? 4.1 : 6.9, {{1.3, 2.25, 2.1}, {1.7, 1.4, 2.75}}},
-                                 {{ROWS, 8, 1}, 6.7, 5.9, {{1.55, 2.85, 0}, {2.15, 2.1, 0}}},
-                                 {{ATTN_TILE, 8, 1}, 7.2, 3.5, {{1.3, 1.8, 0}, {1.9, 2.9, 0}}}};
+    const Kind kinds[] = {
+        {ATTN_ROWS, 4, 5.0, wide ? 6.1 : 6.7, {{1.55, 2.0, 3.8}, {1.8, 2.15, 4.0}}, {1024, 512, 256}, 8},
+        {ATTN_ROWS, 8, 6.1, 6.0, {{1.8, 2.6, 0}, {2.05, 3.15, 0}}, {512, 256, 0}, 8},
+        {ROWS, 4, 7.1, wide ? 8.0 : 4.8, {{1.5, 2.25, 2.1}, {1.8, 1.55, 2.6}}, {512, 512, 256}, 4},
+        {ROWS, 8, 6.2, 6.5, {{1.75, 2.8, 0}, {2.1, 2.1, 0}}, {256, 256, 0}, 4},
+        {ATTN_TILE, 8, 7.8, 3.8, {{1.35, 1.8, 0}, {1.8, 2.75, 0}}, {256, 256, 0}, 4},
+    };
     TreePlan best{};
     double least = 0;
     for (const Kind& k : kinds) {
-        if (k.plan.nw == 8 && dim > 128) continue;
-        const bool own_steps = k.plan.tr == ROWS;
-        const int tk = own_steps ? 32 * (f32 ? blocks_of<float>(dim) : blocks_of<uint16_t>(dim)) : TK;
-        const int64_t steps = std::max<int64_t>(1, cdiv(keys, tk)), tiles = batch * cdiv(each, k.plan.tr) * kv_heads;
-        const int64_t slots = k.plan.nw == 4 && dim <= 128 ? 512 : 256;
-        for (int ns = 1; ns <= 64 && (ns == 1 || ns * 4 <= steps); ++ns) {
-            const int64_t per = std::max<int64_t>(4, cdiv(steps, ns));
-            const double full = (double)(tiles * cdiv(steps, per)) / slots, rounds = std::max(1., (full + std::ceil(full)) / 2);
-            const double time = k.start + rounds * (k.first + k.step[f32][d] * cdiv(per, own_steps ? k.plan.nw : 1)) +
-                                (ns == 1 ? 0. : 3.5 + 0.35e-6 * ns * (double)rows * heads * dim * 8);
+        if (k.nw == 8 && wide) continue;
+        const int tk = k.tr == ROWS ? 32 * (f32 ? blocks_of<float>(dim) : blocks_of<uint16_t>(dim)) : TK;
+        const int steps = (int)std::max<int64_t>(1, cdiv(keys, tk)), waves = k.tr == ATTN_TILE ? 1 : k.nw;
+        const double tiles = (double)(batch * cdiv(each, k.tr) * kv_heads);
+        for (int ns = 1; ns <= 64 && (ns == 1 || ns * 4 <= steps); ns += std::max(1, ns / 4)) {
+            const int per = std::max(k.least, (steps + ns - 1) / ns), mine = (std::min(per, steps) + waves - 1) / waves;
+            const double full = tiles * ((steps + per - 1) / per) / k.slots[d];
+            const double rounds = std::max(1., (full + std::ceil(full)) / 2);
+            const double time = k.start + rounds * (k.first + k.step[f32][d] * mine) +
+                                (ns == 1 ? 0. : 3.1 + 0.37e-6 * ns * (double)rows * heads * dim * 8);
             if (best.nsplit == 0 || time < least) {
                 least = time;
-                best = TreePlan{k.plan.tr, k.plan.nw, ns};
+                best = TreePlan{k.tr, k.nw, ns};
             }
         }
     }

@@ -277,8 +277,8 @@ int run_attention_int8(const AttnPlan& p, const KVCacheInt8& c, const RaggedRows
                        float* lse, void* ws, size_t ws_bytes, hipStream_t st);
 
 // Attention of trees of drafted tokens over the cache (attention_tree.hip): tiles
-// of ATTN_TREE_ROWS query rows with nw = 4 waves, or 8 up to 128 channels, or of
-// ATTN_TILE (up to 128 channels, nw 8); nsplit splits of the keys.
+// of ATTN_ROWS or ATTN_TREE_ROWS query rows with nw = 4 waves, or 8 up to 128
+// channels, or of ATTN_TILE (up to 128 channels, nw 8); nsplit splits of the keys.
 constexpr int TREE_NODES = 512;     // of a sequence, at most
 constexpr int ATTN_TREE_ROWS = 32;
 struct TreePlan {

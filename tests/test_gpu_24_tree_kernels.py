@@ -9,7 +9,7 @@ from test_gpu_22_attention_tree import _check, _make, _trees
 
 pytestmark = pytest.mark.gpu
 
-PLANS = [(0, 4, 1), (0, 4, 5), (0, 8, 1), (0, 8, 3), (1, 8, 1), (1, 8, 3)]      # tiles, waves, splits
+PLANS = [(0, 4, 1), (0, 4, 5), (0, 8, 1), (0, 8, 3), (1, 8, 1), (1, 8, 3), (2, 4, 1), (2, 4, 3), (2, 8, 1), (2, 8, 2)]      # tiles, waves, splits
 SHAPES = [(64, 16), (64, 64), (128, 16), (128, 128), (256, 16), (256, 32)]
 
 
@@ -76,12 +76,12 @@ def test_rows_by_themselves(gpu, plan, dim, dtype):
 def test_hook_refuses(gpu):
     from post_int4_weight_amd import api
     Q, cache, args, _ = _make(api, gpu, [30], [[-1, 0]], 2, 1, 256, 16, "bf16", 3)
-    for plan in ((2, 8, 1), (0, 2, 1), (1, 4, 1), (0, 8, 1), (1, 8, 1), (0, 4, 0), (0, 4, 65)):
+    for plan in ((2, 8, 1), (3, 4, 1), (-1, 4, 1), (0, 2, 1), (1, 4, 1), (0, 8, 1), (1, 8, 1), (0, 4, 0), (0, 4, 65)):
         with pytest.raises(api.PTQError):
             api._test_attention_int8_tree(*plan, Q, cache, *args)
 
 
-@pytest.mark.parametrize("plan", [(0, 4, 1), (0, 8, 2), (1, 8, 1), (1, 8, 3)])
+@pytest.mark.parametrize("plan", [(0, 4, 1), (0, 8, 2), (1, 8, 1), (1, 8, 3), (2, 4, 1), (2, 8, 2)])
 @pytest.mark.parametrize("batch", [2, 63, 64, 65])
 def test_the_order_of_sequences(gpu, batch, plan):
     """Ragged batches of more workgroups than start at once, whose longest sequences go first: equal lengths, sequences
