@@ -488,10 +488,10 @@ int kv_cache_append_int8(int8_t* k_codes, int8_t* v_codes, float* k_scales, floa
  * block_table. NaN for a query: a parent on its way up that is not below its
  * node or less than -1, or a key in a block without a valid id.
  *
- * A row of Q is held in steps of 1 / 16256 of its largest element (bf16) or of
- * 1 / 2080768 (fp32), or in the fp16 terms of attention_int8_cache, whichever the
- * sizes choose; its products with the codes of K are exact. Probabilities, sums
- * and scales as for attention_int8_cache. Asynchronous.
+ * A row of Q is held in whole steps of at most 1 / 16384 of its largest element
+ * (bf16; elements of at least 1 / 64 of it are exact) or of 1 / 2080768 (fp32), or
+ * in the fp16 terms of attention_int8_cache, whichever the sizes choose.
+ * Probabilities, sums and scales as for attention_int8_cache. Asynchronous.
  * Errors: EINVAL, EWORKSPACE, EHIP.
  * ---------------------------------------------------------------------- */
 size_t attention_int8_tree_workspace_bytes(int64_t rows, int64_t batch, int heads, int kv_heads, int head_dim,

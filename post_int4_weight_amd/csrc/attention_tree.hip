@@ -6,10 +6,12 @@
 //   o_i = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q_i.k_j - m)
 //   k_j = S_k[block(j)] c_j,  v_j = S_v[block(j)] c'_j
 //
-// Arithmetic. Scores are int8 products: a row of q is whole numbers of steps of
-// its largest element, q = (max|q| / 16256) (128 hi + lo) for bf16 and three such
-// terms, max|q| / 2080768, for fp32 queries, so the codes of K go into the matrix cores as
-// they lie in memory and the sums are exact in int32. P V runs on the fp16
+// Arithmetic. Scores are int8 products, so the codes of K go into the matrix cores
+// as they lie in memory and the sums are exact in int32. A row of bf16 q is whole
+// numbers of steps, 256 hi + lo, a step the power of two in max|q| / (16384 ..
+// 32640): elements of at least max|q| / 64 are exact, others off by half a step at
+// most. (With steps of max|q| / 16256, which none divides, lse was off by 4e-6 of
+// itself; so it is 2e-7.) Rows of fp32 are three terms of max|q| / 2080768. P V runs on the fp16
 // matrix cores, where codes are exact: w_j = p_j S_v[block(j)] / R in fp16 (two
 // terms for fp32 queries), R the running maximum of S_v over the blocks that the
 // row attends to. Maxima, sums and the output accumulate in fp32.
@@ -92,9 +94,10 @@ struct QueryRow {
         load8((const T*)&raw[c][0], *(float (*)[8])&x[0]);
         load8((const T*)&raw[c][WORDS / 2], *(float (*)[8])&x[8]);
     }
-    // As whole numbers n of NT terms, n = sum_t q_t 2^(7 (NT - 1 - t)), the first signed and the others in [0, 128), and
-    // the factor with which they stand for the row times the softmax scale, whose sign goes into the numbers. A row with a
-    // NaN or an infinity gets the factor NaN. Adding 3 * 2^22 leaves n, half to even, in the low bits of the sum.
+    // As whole numbers n of NT terms, and the factor with which they stand for the row times the softmax scale, whose sign
+    // goes into the numbers. Two terms (bf16): n = 256 q_0 + q_1, |n| <= 32512, both signed. Three: n = sum_t q_t 2^(14 - 7 t),
+    // the first signed and the others in [0, 128). A row with a NaN or an infinity gets the factor NaN. Adding 3 * 2^22
+    // leaves n, half to even, in the low bits of the sum.
     template <int NT>
     __device__ __forceinline__ float terms(float scale2, i32x4 (&q)[NT][NC]) {
         uint32_t size = 0;
@@ -107,11 +110,20 @@ struct QueryRow {
         }
         size = std::max(size, (uint32_t)__shfl_xor((int)size, 32, 64));
         float m = __uint_as_float(size);
-        constexpr float LARGEST = NT == 2 ? 127 * 128 : 127 * 128 * 128, MAGIC = 12582912.f;
+        constexpr float LARGEST = 127 * 128 * 128, MAGIC = 12582912.f;
         const float up = m < 0x1p-100f ? 0x1p100f : 1.f, down = m < 0x1p-100f ? 0x1p-100f : 1.f;      // 1 / m is finite
         m *= up;
         const bool fine = m <= FLT_MAX;
-        const float inv = fine && m > 0.f ? __fdiv_rn(scale2 < 0.f ? -LARGEST : LARGEST, m) : 0.f;
+        float inv = 0.f, step;
+        if constexpr (NT == 2) {
+            // 2^14 / (m's power of two), or half of it where m has all 8 bits: 32640 has no hi
+            const uint32_t power = __float_as_uint(m * 1.004f) >> 23;      // 255 x 1.004 > 256 > 254 x 1.004
+            if (fine && m > 0.f) inv = __uint_as_float((268u - power) << 23 | (scale2 < 0.f ? 0x80000000u : 0u));
+            step = m > 0.f ? __uint_as_float((power - 14u) << 23) : 0.f;
+        } else {
+            if (fine && m > 0.f) inv = __fdiv_rn(scale2 < 0.f ? -LARGEST : LARGEST, m);
+            step = __fdiv_rn(m, LARGEST);
+        }
         const bool tiny = __any(up != 1.f);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -125,12 +137,19 @@ struct QueryRow {
                 uint32_t n[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) n[k] = __float_as_uint(fmaf(x[4 * w + k], inv, MAGIC));
-                q[NT - 1][c][w] = (int)(bytes_of<0>(n) & 0x7f7f7f7fu);
-                if constexpr (NT == 3) q[1][c][w] = (int)(bytes_of<7>(n) & 0x7f7f7f7fu);
-                q[0][c][w] = (int)bytes_of<7 * (NT - 1)>(n);
+                if constexpr (NT == 2) {
+                    q[1][c][w] = (int)bytes_of<0>(n);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) n[k] += 128;
+                    q[0][c][w] = (int)bytes_of<8>(n);
+                } else {
+                    q[2][c][w] = (int)(bytes_of<0>(n) & 0x7f7f7f7fu);
+                    q[1][c][w] = (int)(bytes_of<7>(n) & 0x7f7f7f7fu);
+                    q[0][c][w] = (int)bytes_of<14>(n);
+                }
             }
         }
-        return fine ? fabsf(scale2) * (__fdiv_rn(m, LARGEST) * down) : __builtin_nanf("");
+        return fine ? fabsf(scale2) * (step * down) : __builtin_nanf("");
     }
 };
 
@@ -324,7 +343,7 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
         float ck[U], top = -INFINITY, big = 0.f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            // the leading terms of q make one whole number below 2^30, a third one another
+            // the leading terms of q make one whole number below 2^31, a third one another
             i32x16 x[NQ];
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
@@ -338,7 +357,7 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                s[u][r] = (float)(x[0][r] * 128 + x[1][r]);
+                s[u][r] = (float)(x[0][r] * (NQ == 2 ? 256 : 128) + x[1][r]);
                 if constexpr (NQ == 3) s[u][r] = fmaf(s[u][r], 128.f, (float)x[NQ - 1][r]);
             }
             ck[u] = sk[u] * qs;

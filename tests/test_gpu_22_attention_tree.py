@@ -2,7 +2,7 @@
 that the cache's codes stand for.
 
 Bounds, per output element, u = 2^-24 and A = sum w |v| / sum w:
- * a logit: q is a whole number of steps of its row's largest element |q|_max, 1 / 16256 (bf16) or 1 / 2080768 (fp32) of it;
+ * a logit: q is a whole number of steps, at most 1 / 16256 (bf16) or 1 / 2080768 (fp32) of its row's largest element |q|_max;
    rounding to one is off by half a step, and by 2^-23 of the largest number before that: 0.502 or 0.75 of a step. The sum
    over channels is exact. Its conversion, the factors, the maximum's subtraction: 10 roundings of a logit C (and of the
    shift by 8): delta = step scale sum|k| + 10 u (C + 8).

@@ -4,7 +4,8 @@ import numpy as np
 import pytest
 import torch
 
-from gpu_util import announce
+from gpu_util import announce, to64
+from oracle import drafts as ref
 from test_gpu_22_attention_tree import _check, _make, _trees
 
 pytestmark = pytest.mark.gpu
@@ -100,3 +101,35 @@ def test_the_order_of_sequences(gpu, batch, plan):
     args[1][0] = args[2].shape[1] * 32 + 1
     P, _ = api._test_attention_int8_tree(*plan, Q, cache, *args)
     assert torch.isnan(P[:nodes[0]]).all() and torch.equal(P[nodes[0]:], O[nodes[0]:])
+
+
+@pytest.mark.parametrize("plan,dim", [(p, d) for p in PLANS for d in (64, 128, 256) if _fits(p, d)])
+def test_bf16_queries_are_exact(gpu, plan, dim):
+    """Rows whose elements are at least 1 / 64 of the largest are held exactly, whatever that one's bits (all 8 set among
+    them) and the sign of the softmax scale: lse is off by fp32's roundings alone. A logit C, u = 2^-24: the sums over
+    channels round D / 16 + 2 times where they are not exact, the factors and the maximum's subtraction 10 times: (D / 16 +
+    12) u (C + 8); the sum of N probabilities (N / 16 + 24) 2 u; and 2 u |lse| for its logarithm's scale, 2^-20 for the
+    logarithms."""
+    from post_int4_weight_amd import api
+    announce(f"tree kernels, exact queries, plan {plan} dim={dim}")
+    trees = [[-1, 0, 0, 2], [-1] + [i // 2 for i in range(30)]]
+    Q, cache, args, vals = _make(api, gpu, [300, 1000], trees, 4, 2, dim, 32, "bf16", 11)
+    gen = torch.Generator().manual_seed(12)
+    row = torch.exp2(torch.randint(-20, 4, (Q.shape[0], 4, 1), generator=gen).float())
+    size = torch.exp2(-5 * torch.rand(Q.shape, generator=gen)) * row
+    Q = (size * (2 * torch.randint(0, 2, Q.shape, generator=gen) - 1)).bfloat16()
+    Q[::3, :, 5] = Q[::3].abs().amax(2).float().log2().floor().exp2().mul(255 / 128).bfloat16()      # all bits set
+    Q = Q.to(gpu)
+    for scale in (dim ** -0.5, -0.05):
+        O, lse = api._test_attention_int8_tree(*plan, Q, cache, *args, scale=scale)
+        torch.cuda.synchronize()
+        q, got, first, u = to64(Q), to64(lse), 0, 2.0 ** -24
+        for (k, v), parents in zip(vals, trees):
+            base = k.shape[0] - len(parents)
+            for i in range(len(parents)):
+                keys = ref.keys_of(parents, i, base, 0)
+                for h in range(4):
+                    _, want, _, _, C = ref.attend(q[first + i, h], k[keys, h // 2], v[keys, h // 2], scale)
+                    tol = (dim / 16 + 12) * u * (C + 8) + (len(keys) / 16 + 24) * 2 * u + 2 * u * abs(want) + 2.0 ** -20
+                    assert abs(got[first + i, h] - want) <= tol, (i, h, got[first + i, h], want, tol)
+            first += len(parents)
