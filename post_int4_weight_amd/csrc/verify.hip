@@ -18,10 +18,10 @@
 // One workgroup a sequence walks. What every node's test needs of p and q is
 // fetched at once; the walk is then the same code on the same values in every
 // wave. What bounds it: for small vocabularies the chain of loads (offsets, nodes,
-// their probabilities, the rows: 11 us for one sequence and 32000 tokens), for
+// their probabilities, the rows: 9.6 us for one sequence and 32000 tokens), for
 // large ones what one CU can load, 9 us for two rows of 128256 in fp32 (108 GB/s).
 // So there other workgroups help with the sums, see Help: 48 trees over 128256
-// tokens, fp32: 30 us, 46 without.
+// tokens, fp32: 28 us, 43 without.
 #include "int8.hpp"
 
 namespace ptq {
@@ -89,22 +89,32 @@ struct Chunk {
     __device__ __forceinline__ float at(int k) const { return load_as_float(x, k); }
 };
 
-__device__ __forceinline__ double sum_wave(double x) {
-#pragma unroll
-    for (int o = 32; o > 0; o /= 2) x += __shfl_xor(x, o, 64);
-    return x;
+// x of the lane that a DPP control names, 0 where there is none or the row is not in ROWS
+template <int CONTROL, int ROWS>
+__device__ __forceinline__ double from_lane(double x) {
+    const long long v = __double_as_longlong(x);
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)v, CONTROL, ROWS, 0xf, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), CONTROL, ROWS, 0xf, false);
+    return __longlong_as_double((long long)hi << 32 | (unsigned)lo);
 }
-
-// sums of the lanes up to each
+// Sums of the lanes up to each: within rows of 16, then over the rows before. (By shuffles through LDS the kernel's five
+// sums and scans took 2 us of one sequence's 11.)
 __device__ __forceinline__ double scan_wave(double x) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) {
-        const double y = __shfl_up(x, o, 64);
-        if (lane >= o) x += y;
-    }
+    x += from_lane<0x111, 0xf>(x);      // row_shr 1, 2, 4, 8
+    x += from_lane<0x112, 0xf>(x);
+    x += from_lane<0x114, 0xf>(x);
+    x += from_lane<0x118, 0xf>(x);
+    x += from_lane<0x142, 0xa>(x);      // row_bcast 15: into the second and the fourth row
+    x += from_lane<0x143, 0xc>(x);      // row_bcast 31: into the upper two
     return x;
 }
+// x of one lane for all
+__device__ __forceinline__ double of_lane(double x, int lane) {
+    const long long v = __double_as_longlong(x);
+    const int lo = __builtin_amdgcn_readlane((int)v, lane), hi = __builtin_amdgcn_readlane((int)(v >> 32), lane);
+    return __longlong_as_double((long long)hi << 32 | (unsigned)lo);
+}
+__device__ __forceinline__ double sum_wave(double x) { return of_lane(scan_wave(x), 63); }
 
 // What is left of p: r = max(p - c q, 0), or p without the tokens ex[0 .. nex)
 template <typename T, bool DRAWN>
@@ -239,7 +249,7 @@ __device__ int draw_rest(const Rest<T, DRAWN>& r, const Segments& g, const doubl
     const double mine = lane < g.count ? seg[lane] : 0., to = scan_wave(mine);
     const uint64_t past = __ballot(mine > 0 && to > goal), any = __ballot(mine > 0);
     const int at = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(any | 1);
-    double before = __shfl(to - mine, at, 64);
+    double before = of_lane(to - mine, at);
     // the segment again, each thread its own stretch
     const int64_t lo = g.from(at), hi = g.from(at + 1);
     const int64_t each = cdiv(hi - lo, NT), k0 = std::min(lo + t * each, hi), k1 = std::min(k0 + each, hi);
