@@ -151,11 +151,24 @@ __device__ __forceinline__ double sum_part(const R& r, int64_t lo, int64_t hi) {
     constexpr int N = Chunk<T>::N, STEP = 64 * N, U = 4;
     const int lane = threadIdx.x & 63;
     double s[U] = {};
-    auto add = [&](Chunk<T> p, const Chunk<T>& q, int64_t at, double& to) __attribute__((always_inline)) {
-        for (int j = 0; j < r.nex; ++j)
+    // leaves out the tried tokens among the wave's `count` chunks
+    auto leave = [&](Chunk<T>* p, int count, int64_t at) __attribute__((always_inline)) {
+        const int64_t first = at - lane * N;
+        for (int j = 0; j < r.nex; j += 64) {
+            const int mine = r.ex[std::min(j + lane, r.nex - 1)];
+            uint64_t mask = __ballot(mine >= first && mine < first + count * STEP);
+            while (mask) {
+                const int64_t k = __builtin_amdgcn_readlane(mine, __builtin_ctzll(mask)) - at;
+                mask &= mask - 1;
 #pragma unroll
-            for (int k = 0; k < N; ++k)
-                if (r.ex[j] == at + k) p.x[k] = 0;
+                for (int u = 0; u < count; ++u)
+#pragma unroll
+                    for (int e = 0; e < N; ++e)
+                        if (k == u * STEP + e) p[u].x[e] = 0;
+            }
+        }
+    };
+    auto add = [&](const Chunk<T>& p, const Chunk<T>& q, double& to) __attribute__((always_inline)) {
 #pragma unroll
         for (int k = 0; k < N; ++k) to += R::weight(p.at(k), COVERED ? q.at(k) : 0.f, COVERED ? r.c : 0.);
     };
@@ -167,10 +180,11 @@ __device__ __forceinline__ double sum_part(const R& r, int64_t lo, int64_t hi) {
             p[u].load(r.p + k0 + u * STEP);
             if constexpr (COVERED) q[u].load(r.q + k0 + u * STEP);
         }
+        leave(p, U, k0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) add(p[u], q[u], k0 + u * STEP, s[u]);
+        for (int u = 0; u < U; ++u) add(p[u], q[u], s[u]);
     }
-    for (; k0 < hi; k0 += STEP) {
+    for (; k0 - lane * N < hi; k0 += STEP) {
         Chunk<T> p, q;
         if (k0 + N <= hi) {
             p.load(r.p + k0);
@@ -179,7 +193,8 @@ __device__ __forceinline__ double sum_part(const R& r, int64_t lo, int64_t hi) {
             p.load(r.p + k0, hi - k0);
             if constexpr (COVERED) q.load(r.q + k0, hi - k0);
         }
-        add(p, q, k0, s[0]);
+        leave(&p, 1, k0);
+        add(p, q, s[0]);
     }
     return sum_wave((s[0] + s[1]) + (s[2] + s[3]));
 }
@@ -406,8 +421,10 @@ __global__ __launch_bounds__(NT) void verify_kernel(VerifyArgs a) {
                     left = r.c != 0. ? r.weight(pp[i], qq[i], r.c) : r.weight(pp[i], 0.f, 0.);
                 } else {
                     left = r.weight(pp[i], 0.f, 0.);
-                    for (int j = cur + 1; j < i; ++j)      // the same token has been tried
-                        if (par[j] == cur && tok[j] == tok[i]) left = 0.;
+                    for (int v = cur / 64; v <= w; ++v) {      // the same token has been tried
+                        const int j = 64 * v + lane;
+                        if (__any(j < i && par[j] == cur && tok[j] == tok[i])) left = 0.;
+                    }
                 }
                 const double q = DRAWN ? (double)qq[i] : 1.;
                 if ((double)pu[i] * z * q < left) {

@@ -216,3 +216,25 @@ def test_workgroups_of_a_sequence(gpu, shares, vocab, dtype, drawn):
                 kept, after = ref.verify(target[at], draft[at] if drawn else None, d["tokens"][at], t,
                                          d["u"][at].double().numpy(), float(d["r"][b]))
             assert path[at] == kept + [-1] * (len(t) - len(kept)) and (counts[b], token[b]) == (len(kept), after), b
+
+
+def test_calls_at_once(gpu):
+    """Calls on several streams, more workgroups than the card holds: each walks on whether its helpers run or not."""
+    from post_int4_weight_amd import api
+    announce("verify, calls at once")
+    nodes, vocab, streams = [3] * 60, 100003, 6
+    d = _inputs(nodes, vocab, "f32", True, 9, gpu, near=3.0, reach=1)
+    d["u"].mul_(0.2).add_(0.8)
+    args = (d["target"], _ints(d["tokens"], gpu), _ints([p for t in d["trees"] for p in t], gpu), _ints(_offsets(nodes), gpu),
+            d["u"].to(gpu), d["r"].to(gpu))
+    want = api._test_verify_drafts(4, *args, draft=d["draft"])
+    assert all(torch.equal(x, y) for x, y in zip(want, _call(api, d, gpu)))
+    torch.cuda.synchronize()
+    side, got = [torch.cuda.Stream() for _ in range(streams)], []
+    for _ in range(5):
+        for s in side:
+            with torch.cuda.stream(s):
+                got.append(api._test_verify_drafts(4, *args, draft=d["draft"]))
+    torch.cuda.synchronize()
+    for out in got:
+        assert all(torch.equal(x, y) for x, y in zip(out, want))
