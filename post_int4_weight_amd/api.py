@@ -426,7 +426,8 @@ def _vector(t, n: int, dtype, name: str):
     """t as n dense values of dtype (any shape with that many), or None."""
     if t is None:
         return None
-    _on_gpu(t, name)
+    if not t.is_cuda:
+        _on_gpu(t, name)
     if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be {n} contiguous {dtype} values")
     return t.data_ptr()
@@ -537,8 +538,9 @@ class KVCacheInt8(NamedTuple):
                 or not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous())):
             raise ValueError("cache tensors must be contiguous: int8 k [blocks, heads, block_size, dim] and v "
                              "[blocks, heads, dim, block_size], fp32 scales [blocks, heads]")
-        for t, name in zip(self, ("cache.k", "cache.v", "cache.k_scales", "cache.v_scales")):
-            _on_gpu(t, name)
+        if not (k.is_cuda and v.is_cuda and ks.is_cuda and vs.is_cuda):
+            for t, name in zip(self, ("cache.k", "cache.v", "cache.k_scales", "cache.v_scales")):
+                _on_gpu(t, name)
         return nb, h, d, bs
 
 
@@ -549,7 +551,8 @@ def _heads3(t, rows, heads, dim, name):
     s0, s1, s2 = t.stride()
     if s2 != 1 or (heads > 1 and s1 != dim):
         raise ValueError(f"{name}: the heads of a row must follow each other")
-    _on_gpu(t, name)
+    if not t.is_cuda:
+        _on_gpu(t, name)
     return s0 if rows > 1 else heads * dim
 
 
@@ -677,11 +680,13 @@ def rotary_apply(X, rotary: Rotary, positions, Y=None):
     if X.dim() != 3:
         raise ValueError("X must be [rows, heads, head_dim]")
     rows, heads, dim = X.shape
-    if Y is None:
-        Y = torch.empty(rows, heads, dim, dtype=X.dtype, device=X.device)
-    if Y.dtype != X.dtype:
+    if Y is not None and Y.dtype != X.dtype:
         raise TypeError("Y must have X's dtype")
-    ldx, ldy = _heads3(X, rows, heads, dim, "X"), _heads3(Y, rows, heads, dim, "Y")
+    ldx = ldy = _heads3(X, rows, heads, dim, "X")
+    if Y is None:
+        Y, ldy = X.new_empty((rows, heads, dim)), heads * dim
+    elif Y is not X:
+        ldy = _heads3(Y, rows, heads, dim, "Y")
     _check(_lib.rotary_apply(_ptr(X), ldx, _ptr(Y), ldy, _dtype_code(X), rows, heads, dim,
                              _vector(positions, rows, torch.int32, "positions"), *rotary._args(), _stream()))
     return Y
@@ -718,13 +723,15 @@ def attention_int8_tree(Q, cache: KVCacheInt8, offsets, seq_lens, block_table, p
     rows, heads = Q.shape[0], Q.shape[1]
     if scale is None:
         scale = d ** -0.5
+    ldq = _heads3(Q, rows, heads, d, "Q")
     if O is None:
-        O = torch.empty(rows, heads, d, dtype=Q.dtype, device=Q.device)
+        O, ldo = Q.new_empty((rows, heads, d)), heads * d
+    else:
+        ldo = _heads3(O, rows, heads, d, "O")
+        if O.dtype != Q.dtype:
+            raise TypeError("O must have Q's dtype")
     if lse is None and return_lse:
         lse = torch.empty(rows, heads, dtype=torch.float32, device=Q.device)
-    ldq, ldo = _heads3(Q, rows, heads, d, "Q"), _heads3(O, rows, heads, d, "O")
-    if O.dtype != Q.dtype:
-        raise TypeError("O must have Q's dtype")
     off, lens, batch, table, width = _ragged(offsets, seq_lens, block_table, "seq_lens")
     ws, wsb = _scratch(attention_int8_tree_workspace_bytes(rows, batch, heads, h, d, _dtype_code(Q), bs, width, window),
                        Q.device, workspace)
@@ -737,7 +744,7 @@ def attention_int8_tree(Q, cache: KVCacheInt8, offsets, seq_lens, block_table, p
 
 
 def _probabilities(t, rows, vocab, name):
-    if t.dim() != 2 or tuple(t.shape) != (rows, vocab):
+    if t.shape != (rows, vocab):
         raise ValueError(f"{name} must be {(rows, vocab)}, got {tuple(t.shape)}")
     return max(_rows(t, name), vocab)
 
@@ -763,13 +770,18 @@ def _verify(shares, target, tokens, parents, offsets, u, r, draft, path, counts,
         ldd = _probabilities(draft, rows, vocab, "draft")
         if draft.dtype != target.dtype:
             raise TypeError("draft must have target's dtype")
-    ints = lambda t, n: torch.empty(n, dtype=torch.int32, device=target.device) if t is None else t
-    path, counts, next = ints(path, rows), ints(counts, batch), ints(next, batch)
-    vec = lambda t, n, name, dtype=torch.int32: _vector(t, n, dtype, name)
-    args = (_ptr(target), ldt, _ptr(draft), ldd, _dtype_code(target), rows, vocab, vec(tokens, rows, "tokens"),
-            vec(parents, rows, "parents"), vec(offsets, batch + 1, "offsets"), batch, vec(u, rows, "u", torch.float32),
-            vec(r, batch, "r", torch.float32), vec(path, rows, "path"), vec(counts, batch, "counts"),
-            vec(next, batch, "next"))
+    i32 = torch.int32
+    ins = (_vector(tokens, rows, i32, "tokens"), _vector(parents, rows, i32, "parents"),
+           _vector(offsets, batch + 1, i32, "offsets"), batch, _vector(u, rows, torch.float32, "u"),
+           _vector(r, batch, torch.float32, "r"))
+    if path is None and counts is None and next is None:      # one allocation for the three
+        outs = path, counts, next = torch.empty(rows + 2 * batch, dtype=i32, device=target.device).split((rows, batch, batch))
+        outs = [t.data_ptr() for t in outs]
+    else:
+        own = lambda t, n: torch.empty(n, dtype=i32, device=target.device) if t is None else t
+        path, counts, next = own(path, rows), own(counts, batch), own(next, batch)
+        outs = _vector(path, rows, i32, "path"), _vector(counts, batch, i32, "counts"), _vector(next, batch, i32, "next")
+    args = (_ptr(target), ldt, _ptr(draft), ldd, _dtype_code(target), rows, vocab, *ins, *outs)
     if shares is None:
         ws, wsb = _scratch(verify_drafts_workspace_bytes(batch, vocab), target.device, workspace)
         _check(_lib.verify_drafts(*args, _ptr(ws), wsb, _stream()))
