@@ -267,14 +267,13 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
         uint32_t seen = 0xffffu;
         if constexpr (TREE)
             if (!whole) seen = seen16(lines_of.line[f / a.group - first_node], tv, (int)tl.pos0, my_lo);
-        auto hidden = [&](int i) { return TREE ? !(seen >> i & 1) : !whole && (i < r_lo || i >= r_hi); };
         float top = -INFINITY;
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float x = s[t][i] * ck;
-                if (hidden(4 * t + i)) x = -INFINITY;
+                if (TREE ? !(seen >> (4 * t + i) & 1) : !whole && (4 * t + i < r_lo || 4 * t + i >= r_hi)) x = -INFINITY;
                 s[t][i] = x;
                 top = fmaxf(top, x);
             }
@@ -310,8 +309,8 @@ __global__ __launch_bounds__(64 * NW) void attention_rows_kernel(AttnArgs a) {
                 l += p1;
                 f32x2 y = {p0 * rv, p1 * rv};
                 if (!whole) {      // S_v of a block that is not this row's may be NaN
-                    if (hidden(4 * t + i)) y[0] = 0.f;
-                    if (hidden(4 * t + i + 1)) y[1] = 0.f;
+                    if (TREE ? !(seen >> (4 * t + i) & 1) : 4 * t + i < r_lo || 4 * t + i >= r_hi) y[0] = 0.f;
+                    if (TREE ? !(seen >> (4 * t + i + 1) & 1) : 4 * t + i + 1 < r_lo || 4 * t + i + 1 >= r_hi) y[1] = 0.f;
                 }
                 const f16x2 x = __builtin_convertvector(y, f16x2);
                 const int e = 4 * (t & 1) + i;
