@@ -35,7 +35,7 @@ def _check(Y, X, positions, rotary, dtype):
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("rows,heads,dim,rot", [(1, 1, 8, 2), (1, 5, 8, 8), (3, 2, 64, 64), (70, 3, 80, 32), (33, 9, 72, 48),
                                                 (5, 7, 96, 54), (130, 1, 128, 126), (600, 33, 128, 128), (9, 4, 256, 64),
-                                                (2, 2, 120, 112)])
+                                                (2, 2, 120, 112), (12000, 9, 128, 128), (12000, 9, 128, 90)])
 def test_rotary(gpu, rows, heads, dim, rot, interleaved, dtype):
     from post_int4_weight_amd import api
     announce(f"rotary rows={rows} heads={heads} dim={dim} rot={rot} interleaved={interleaved} {dtype}")
