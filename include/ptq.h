@@ -488,9 +488,8 @@ int kv_cache_append_int8(int8_t* k_codes, int8_t* v_codes, float* k_scales, floa
  * block_table. NaN for a query: a parent on its way up that is not below its
  * node or less than -1, or a key in a block without a valid id.
  *
- * A row of Q is held in whole steps of at most 1 / 16384 of its largest element
- * (bf16; elements of at least 1 / 64 of it are exact) or of 1 / 2080768 (fp32), or
- * in the fp16 terms of attention_int8_cache, whichever the sizes choose.
+ * Elements of a bf16 row of Q are exact down to 2^-20 of its largest, those of an
+ * fp32 row off by 2^-22 of themselves, or by 2^-28 of the largest, at most.
  * Probabilities, sums and scales as for attention_int8_cache. Asynchronous.
  * Errors: EINVAL, EWORKSPACE, EHIP.
  * ---------------------------------------------------------------------- */

@@ -6,15 +6,19 @@
 //   o_i = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q_i.k_j - m)
 //   k_j = S_k[block(j)] c_j,  v_j = S_v[block(j)] c'_j
 //
-// Arithmetic. Scores are int8 products, so the codes of K go into the matrix cores
-// as they lie in memory and the sums are exact in int32. A row of bf16 q is whole
-// numbers of steps, 256 hi + lo, a step the power of two in max|q| / (16384 ..
-// 32640): elements of at least max|q| / 64 are exact, others off by half a step at
-// most. (With steps of max|q| / 16256, which none divides, lse was off by 4e-6 of
-// itself; so it is 2e-7.) Rows of fp32 are three terms of max|q| / 2080768. P V runs on the fp16
-// matrix cores, where codes are exact: w_j = p_j S_v[block(j)] / R in fp16 (two
-// terms for fp32 queries), R the running maximum of S_v over the blocks that the
-// row attends to. Maxima, sums and the output accumulate in fp32.
+// Arithmetic, the same in all kernels of trees. Both products run on the fp16
+// matrix cores, where the codes of K and V are exact. A row of q is scaled by a
+// power of two and held in one fp16 term (bf16: elements of at least 2^-20 of the
+// largest are exact) or in two (fp32: off by 2^-22 of themselves or by 2^-28 of the
+// largest), w_j = p_j S_v[block(j)] / R in one (11 bits, which is below bf16's
+// rounding of the output) or in two, R the running maximum of S_v over the blocks
+// that the row attends to. Maxima, sums and the output accumulate in fp32. Scores
+// as int8 products of K's codes as they lie, with q in whole numbers of steps, need
+// no conversion of K, but one large channel then costs the others their bits (40
+// nodes over 2000 keys, D = 128, a channel 300 times larger: outputs off by 4.3e-3
+// instead of 1.7e-3, of fp32 by 4e-5 instead of 6e-7), and they were hardly faster:
+// 16 trees over 500 .. 8000 keys 97 us where these take 94, the chosen kernels of
+// 167 shapes 0.5% in the mean.
 #include "attention.hpp"
 
 #include <algorithm>
@@ -64,25 +68,13 @@ __device__ __forceinline__ int split_steps(const TreeTile& t, int nsplit, int le
     return std::max(least, (t.it1 - t.it0 + nsplit - 1) / nsplit);
 }
 
-// |x| as bits, in the order of the values: a NaN's are the largest
-__device__ __forceinline__ uint32_t size_of(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x16 __attribute__((ext_vector_type(16)));
-
-// Bytes SHIFT .. SHIFT + 7 of four numbers, as the bytes of one word
-template <int SHIFT>
-__device__ __forceinline__ uint32_t bytes_of(const uint32_t (&n)[4]) {
-    const uint32_t lo = __builtin_amdgcn_perm(n[1] >> SHIFT, n[0] >> SHIFT, 0x0c0c0400u);
-    return lo | __builtin_amdgcn_perm(n[3] >> SHIFT, n[2] >> SHIFT, 0x04000c0cu);
-}
-
-// One query row: 32 channels of it for each of the NC fragments, as they come from memory.
+// One query row: 32 channels of it for each of the NC pairs of fragments, as they come from memory.
 template <typename T, int NC>
 struct QueryRow {
     static constexpr int WORDS = 16 * sizeof(T) / 16;      // 16-byte words of 16 channels
     uint4 raw[NC][WORDS];
-    // lane half hf holds channels 32 c + 16 hf .. + 15 of fragment c; the lanes that differ in bit 5 share the row
+    // lane half hf holds channels 32 c + 16 hf .. + 15: 8 of fragment 2 c, 8 of 2 c + 1; the lanes that differ in bit 5
+    // share the row
     __device__ __forceinline__ void load(const T* p) {
         const int hf = (threadIdx.x >> 5) & 1;
 #pragma unroll
@@ -90,66 +82,36 @@ struct QueryRow {
 #pragma unroll
             for (int w = 0; w < WORDS; ++w) raw[c][w] = *(const uint4*)(p + 32 * c + 16 * hf + w * (16 / sizeof(T)));
     }
-    __device__ __forceinline__ void values(int c, float (&x)[16]) const {
-        load8((const T*)&raw[c][0], *(float (*)[8])&x[0]);
-        load8((const T*)&raw[c][WORDS / 2], *(float (*)[8])&x[8]);
-    }
-    // As whole numbers n of NT terms, and the factor with which they stand for the row times the softmax scale, whose sign
-    // goes into the numbers. Two terms (bf16): n = 256 q_0 + q_1, |n| <= 32512, both signed. Three: n = sum_t q_t 2^(14 - 7 t),
-    // the first signed and the others in [0, 128). A row with a NaN or an infinity gets the factor NaN. Adding 3 * 2^22
-    // leaves n, half to even, in the low bits of the sum.
+    __device__ __forceinline__ void values(int e, float (&x)[8]) const { load8((const T*)&raw[e / 2][e % 2 * (WORDS / 2)], x); }
+    // In NT fp16 terms, scaled by the power of two that brings the largest element to [8, 16), negated for a negative softmax
+    // scale; returns the factor with which they stand for the row times that scale, in units of log2. A row with a NaN or an
+    // infinity gets the factor NaN.
     template <int NT>
-    __device__ __forceinline__ float terms(float scale2, i32x4 (&q)[NT][NC]) {
-        uint32_t size = 0;
+    __device__ __forceinline__ float terms(float scale2, f16x8 (&q)[NT][2 * NC]) {
+        uint32_t size = 0;      // |x| as bits, in the order of the values: a NaN's are the largest
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            float x[16];
-            values(c, x);
+        for (int e = 0; e < 2 * NC; ++e) {
+            float x[8];
+            values(e, x);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) size = std::max(size, size_of(x[k]));
+            for (int k = 0; k < 8; ++k) size = std::max(size, __float_as_uint(x[k]) & 0x7fffffffu);
         }
         size = std::max(size, (uint32_t)__shfl_xor((int)size, 32, 64));
-        float m = __uint_as_float(size);
-        constexpr float LARGEST = 127 * 128 * 128, MAGIC = 12582912.f;
-        const float up = m < 0x1p-100f ? 0x1p100f : 1.f, down = m < 0x1p-100f ? 0x1p-100f : 1.f;      // 1 / m is finite
-        m *= up;
-        const bool fine = m <= FLT_MAX;
-        float inv = 0.f, step;
-        if constexpr (NT == 2) {
-            // 2^14 / (m's power of two), or half of it where m has all 8 bits: 32640 has no hi
-            const uint32_t power = __float_as_uint(m * 1.004f) >> 23;      // 255 x 1.004 > 256 > 254 x 1.004
-            if (fine && m > 0.f) inv = __uint_as_float((268u - power) << 23 | (scale2 < 0.f ? 0x80000000u : 0u));
-            step = m > 0.f ? __uint_as_float((power - 14u) << 23) : 0.f;
-        } else {
-            if (fine && m > 0.f) inv = __fdiv_rn(scale2 < 0.f ? -LARGEST : LARGEST, m);
-            step = __fdiv_rn(m, LARGEST);
-        }
-        const bool tiny = __any(up != 1.f);
+        const int field = std::min(257 - (int)(size >> 23), 253);
+        const float up = __uint_as_float((uint32_t)field << 23 | (scale2 < 0.f ? 0x80000000u : 0u));
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            float x[16];
-            values(c, x);
-            if (tiny)
+        for (int e = 0; e < 2 * NC; ++e) {
+            float x[8];
+            values(e, x);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) x[k] *= up;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                uint32_t n[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) n[k] = __float_as_uint(fmaf(x[4 * w + k], inv, MAGIC));
-                if constexpr (NT == 2) {
-                    q[1][c][w] = (int)bytes_of<0>(n);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) n[k] += 128;
-                    q[0][c][w] = (int)bytes_of<8>(n);
-                } else {
-                    q[2][c][w] = (int)(bytes_of<0>(n) & 0x7f7f7f7fu);
-                    q[1][c][w] = (int)(bytes_of<7>(n) & 0x7f7f7f7fu);
-                    q[0][c][w] = (int)bytes_of<14>(n);
-                }
+            for (int k = 0; k < 8; ++k) {
+                const float y = x[k] * up;
+                q[0][e][k] = (_Float16)y;
+                if constexpr (NT == 2) q[1][e][k] = (_Float16)(y - (float)q[0][e][k]);
             }
         }
-        return fine ? fabsf(scale2) * (step * down) : __builtin_nanf("");
+        const float back = __uint_as_float((uint32_t)(254 - field) << 23);
+        return size < 0x7f800000u ? fabsf(scale2) * back : __builtin_nanf("");
     }
 };
 
@@ -167,7 +129,7 @@ struct QueryRow {
 // the join. What bounds it: for few rows memory (16 trees of 8 nodes over 4000
 // keys, 32 heads on 8, D = 128: 37 us, the cache's 131 MB at 3.5 TB/s), with more
 // tiles on the same keys the vector instructions of the exponentials and of the
-// conversion of V. Tiles of 64 and 128 rows that share a step among waves were 1%
+// conversion of K and V. Tiles of 64 and 128 rows that share a step among waves were 1%
 // faster in the mean over 1700 shapes, and taken out; from about 300 rows a kv
 // head on, the tiles of 256 rows of attention_int8.hip win, and for few rows and
 // keys its tiles of 16, whose keys go straight into registers.
@@ -200,8 +162,7 @@ __device__ __forceinline__ void copy16(const void* from, void* to) {
 template <typename T, int D, int NW>
 __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(TreeArgs a) {
     constexpr int U = blocks_of<T>(D), TK = 32 * U;
-    constexpr int NQ = sizeof(T) == 4 ? 3 : 2;    // int8 terms of q
-    constexpr int NT = sizeof(T) == 4 ? 2 : 1;    // fp16 terms of the probabilities
+    constexpr int NT = sizeof(T) == 4 ? 2 : 1;    // fp16 terms of q and of the probabilities
     constexpr int NC = D / 32, NTH = 64 * NW;
     constexpr bool FOLD = NT == 1;       // S_v / R goes into the exponent
     __shared__ TreeLines<ROWS> lines_of;
@@ -318,7 +279,7 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
     const int whole = std::min(__builtin_amdgcn_readfirstlane((lo_max + TK - 1) / TK), s1);
     const int last = std::min(__builtin_amdgcn_readfirstlane(tl.base / TK), s1);
 
-    i32x4 q[NQ][NC];
+    f16x8 q[NT][2 * NC];
     f32x16 acc[NC];
 #pragma unroll
     for (int i = 0; i < NC; ++i)
@@ -326,7 +287,7 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
         for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
     // ref: what the scores' maximum m stands for in the exponents
     float m = -INFINITY, l = broken ? __builtin_nanf("") : 0.f, R = 0.f, rcp_R = 0.f, log2_R = 0.f, poison = 0.f;
-    const float qs = row.template terms<NQ>(a.scale2, q);
+    const float qs = row.template terms<NT>(a.scale2, q);
 
     auto work = [&](auto masked, int it) __attribute__((always_inline)) {
         constexpr bool MASK = decltype(masked)::value;
@@ -343,22 +304,17 @@ __global__ __launch_bounds__(64 * NW, waves_of(D)) void attention_tree_kernel(Tr
         float ck[U], top = -INFINITY, big = 0.f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            // the leading terms of q make one whole number below 2^31, a third one another
-            i32x16 x[NQ];
 #pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) x[n][r] = 0;
+            for (int r = 0; r < 16; ++r) s[u][r] = 0.f;
 #pragma unroll
             for (int e = 0; e < NC; ++e) {
-                const i32x4 k = *(const i32x4*)&codes.k[32 * u + li][(2 * e + hf) ^ swizzle<KC>(li)];
+                const uint4 k = codes.k[32 * u + li][(2 * e + hf) ^ swizzle<KC>(li)];
+                const f16x8 k0 = half8(k.x, k.y), k1 = half8(k.z, k.w);
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) x[n] = __builtin_amdgcn_mfma_i32_32x32x32_i8(k, q[n][e], x[n], 0, 0, 0);
-            }
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                s[u][r] = (float)(x[0][r] * (NQ == 2 ? 256 : 128) + x[1][r]);
-                if constexpr (NQ == 3) s[u][r] = fmaf(s[u][r], 128.f, (float)x[NQ - 1][r]);
+                for (int n = 0; n < NT; ++n) {
+                    s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k0, q[n][2 * e], s[u], 0, 0, 0);
+                    s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k1, q[n][2 * e + 1], s[u], 0, 0, 0);
+                }
             }
             ck[u] = sk[u] * qs;
             seen[u] = 0xffffu;
