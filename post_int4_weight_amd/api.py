@@ -746,7 +746,8 @@ def attention_int8_tree(Q, cache: KVCacheInt8, offsets, seq_lens, block_table, p
 def _probabilities(t, rows, vocab, name):
     if t.shape != (rows, vocab):
         raise ValueError(f"{name} must be {(rows, vocab)}, got {tuple(t.shape)}")
-    return max(_rows(t, name), vocab)
+    ld = _rows(t, name)
+    return ld if rows > 1 else vocab
 
 
 def verify_drafts_workspace_bytes(batch: int, vocab: int) -> int:
