@@ -1100,12 +1100,8 @@ int launch(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
     const dim3 grid((unsigned)(units * a.nsplit));
     if constexpr (D <= 128) {
         if (tr != TR) {
-            static bool ready = false;    // more than 64 KB of LDS
-            if (!ready) {
-                PTQ_HIP(hipFuncSetAttribute((const void*)attention_tile_kernel<T, D, TILE_WAVES, false>,
-                                            hipFuncAttributeMaxDynamicSharedMemorySize, TileLds<D>::BYTES));
-                ready = true;
-            }
+            static PerDevice ready;    // more than 64 KB of LDS
+            PTQ_TRY(allow_lds(ready, (const void*)attention_tile_kernel<T, D, TILE_WAVES, false>, TileLds<D>::BYTES));
             hipLaunchKernelGGL((attention_tile_kernel<T, D, TILE_WAVES, false>), grid, dim3(64 * TILE_WAVES), TileLds<D>::BYTES, st,
                                a);
         } else if (p.nw == 8) {
@@ -1189,12 +1185,8 @@ int launch_tree(const AttnArgs& a, int tr, int nw, hipStream_t st) {
     const dim3 grid((unsigned)(tile_units(a.g.rows, a.g.batch, a.group, tr) * a.kv_heads * a.nsplit));
     if constexpr (D <= 128) {
         if (tr == ATTN_TILE) {
-            static bool ready = false;    // more than 64 KB of LDS
-            if (!ready) {
-                PTQ_HIP(hipFuncSetAttribute((const void*)attention_tile_kernel<T, D, TILE_WAVES, true>,
-                                            hipFuncAttributeMaxDynamicSharedMemorySize, TileLds<D>::BYTES));
-                ready = true;
-            }
+            static PerDevice ready;    // more than 64 KB of LDS
+            PTQ_TRY(allow_lds(ready, (const void*)attention_tile_kernel<T, D, TILE_WAVES, true>, TileLds<D>::BYTES));
             hipLaunchKernelGGL((attention_tile_kernel<T, D, TILE_WAVES, true>), grid, dim3(64 * TILE_WAVES),
                                TileLds<D>::BYTES, st, a);
             PTQ_LAUNCH_CHECK();

@@ -5,6 +5,7 @@
 #include <stdint.h>
 #include <stddef.h>
 
+#include "per_device.hpp"
 #include "ptq.h"
 
 namespace ptq {
@@ -42,6 +43,17 @@ struct Status {
         int _s = (expr);              \
         if (_s != PTQ_OK) return _s;  \
     } while (0)
+
+// Lets launches of a kernel on the current device ask for up to `bytes` of dynamic LDS (more than 64 KB with what is the
+// kernel's own); `ready`: the kernel's.
+inline int allow_lds(PerDevice& ready, const void* kernel, int bytes) {
+    int device = 0;
+    PTQ_HIP(hipGetDevice(&device));
+    return ready.once(device, [&]() -> int {
+        PTQ_HIP(hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes));
+        return PTQ_OK;
+    });
+}
 
 // -------------------------------------------------------------- vectors --
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));

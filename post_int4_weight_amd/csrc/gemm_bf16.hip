@@ -765,21 +765,15 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_bf16_nt_direct_kernel(Bf16Gem
     store_tile<BMX, EPI, NW, MF>(g, acc, i0, j0, L, smem);
 }
 
-// Opt a kernel into more than 64 KB of dynamic LDS (once per instantiation).
+// Opt a kernel into more than 64 KB of dynamic LDS (once per instantiation and device).
 template <int BMX, int EPI, int DKT, int NW = 4, int MF = 32>
 int prepare_kernel() {
-    static bool done = false;
-    if (!done) {
-        if constexpr (DKT > 0)
-            PTQ_HIP(hipFuncSetAttribute((const void*)gemm_bf16_nt_direct_kernel<BMX, EPI, DKT, DNST<DKT>, NW, MF>,
-                                        hipFuncAttributeMaxDynamicSharedMemorySize,
-                                        dsmem_bytes<BMX, DKT, DNST<DKT>>()));
-        else
-            PTQ_HIP(hipFuncSetAttribute((const void*)gemm_bf16_nt_kernel<BMX, EPI>,
-                                        hipFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<BMX>()));
-        done = true;
-    }
-    return PTQ_OK;
+    static PerDevice ready;
+    if constexpr (DKT > 0)
+        return allow_lds(ready, (const void*)gemm_bf16_nt_direct_kernel<BMX, EPI, DKT, DNST<DKT>, NW, MF>,
+                         dsmem_bytes<BMX, DKT, DNST<DKT>>());
+    else
+        return allow_lds(ready, (const void*)gemm_bf16_nt_kernel<BMX, EPI>, smem_bytes<BMX>());
 }
 
 template <int BMX, int EPI, int DKT, int NW = 4, int MF = 32>

@@ -492,12 +492,8 @@ __global__ __launch_bounds__(NT, DWG) void gemm_f32_direct_pair_kernel(GemmArgs 
 
 template <bool B_KMAJOR, int DNST, int BT>
 int launch_direct_ring(const GemmArgs& a, hipStream_t st) {
-    static bool ready = false;
-    if (!ready) {
-        PTQ_HIP(hipFuncSetAttribute((const void*)gemm_f32_direct_kernel<B_KMAJOR, DNST, BT>,
-                                    hipFuncAttributeMaxDynamicSharedMemorySize, DNST * DSTAGE_BYTES<BT>));
-        ready = true;
-    }
+    static PerDevice ready;
+    PTQ_TRY(allow_lds(ready, (const void*)gemm_f32_direct_kernel<B_KMAJOR, DNST, BT>, DNST * DSTAGE_BYTES<BT>));
     const int64_t tm = cdiv(a.M, BT), tn = cdiv(a.N, BT);
     const unsigned grid = direct_grid(a, tm, tn);
     hipLaunchKernelGGL((gemm_f32_direct_kernel<B_KMAJOR, DNST, BT>), dim3(grid), dim3(NT), DNST * DSTAGE_BYTES<BT>,
@@ -539,12 +535,8 @@ int direct_shape(const GemmArgs& a) {
 
 template <int DNST, int BT>
 int launch_direct_pair(const GemmArgs& a0, const GemmArgs& a1, hipStream_t st) {
-    static bool ready = false;
-    if (!ready) {
-        PTQ_HIP(hipFuncSetAttribute((const void*)gemm_f32_direct_pair_kernel<DNST, BT>,
-                                    hipFuncAttributeMaxDynamicSharedMemorySize, DNST * DSTAGE_BYTES<BT>));
-        ready = true;
-    }
+    static PerDevice ready;
+    PTQ_TRY(allow_lds(ready, (const void*)gemm_f32_direct_pair_kernel<DNST, BT>, DNST * DSTAGE_BYTES<BT>));
     const int64_t tm0 = cdiv(a0.M, BT), tn0 = cdiv(a0.N, BT), tm1 = cdiv(a1.M, BT), tn1 = cdiv(a1.N, BT);
     const unsigned grid0 = (unsigned)cdiv(direct_grid(a0, tm0, tn0), XCDS) * XCDS, grid1 = direct_grid(a1, tm1, tn1);
     hipLaunchKernelGGL((gemm_f32_direct_pair_kernel<DNST, BT>), dim3(grid0 + grid1), dim3(NT),

@@ -394,12 +394,8 @@ int launch_write(const char* fn, const KVCacheInt8& c, const RaggedRows& r, int 
     }
     PTQ_TRY(block_launch(fn, c, r, dtype == PTQ_F32 ? write_nv<float>() : write_nv<uint16_t>(), most, l));
     if (lds == 65536) {      // fp32, blocks of 128 tokens, heads of 256: with the kernel's own LDS more than 64 KB
-        static bool ready = false;
-        if (!ready) {
-            PTQ_HIP(hipFuncSetAttribute((const void*)kv_write_kernel<float, TURN>,
-                                        hipFuncAttributeMaxDynamicSharedMemorySize, 65536));
-            ready = true;
-        }
+        static PerDevice ready;
+        PTQ_TRY(allow_lds(ready, (const void*)kv_write_kernel<float, TURN>, 65536));
     }
     if (dtype == PTQ_F32)
         hipLaunchKernelGGL((kv_write_kernel<float, TURN>), l.grid, l.block, lds, st, a, l.per, (const float*)K, ldk,

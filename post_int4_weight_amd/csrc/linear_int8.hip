@@ -564,12 +564,8 @@ int fused_rows_log2(int64_t rows, int64_t in) {
 
 template <typename T, bool SMOOTH>
 int launch_fused(const Int8GemmArgs& g, const T* X, int64_t ldx, const float* s, int rl, hipStream_t st) {
-    static bool ready = false;
-    if (!ready) {
-        PTQ_HIP(hipFuncSetAttribute((const void*)linear_int8_few_kernel<T, SMOOTH>,
-                                    hipFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024));
-        ready = true;
-    }
+    static PerDevice ready;
+    PTQ_TRY(allow_lds(ready, (const void*)linear_int8_few_kernel<T, SMOOTH>, 128 * 1024));
     for_parts(g, 16, 16, 64 * FW, [&](const Int8GemmArgs& part) {      // up to 16 tokens: parts of the outputs
         hipLaunchKernelGGL((linear_int8_few_kernel<T, SMOOTH>), dim3((unsigned)cdiv(part.out, 16)), dim3(64 * FW),
                            (unsigned)(part.rows * fused_pitch(part.in)), st, part, X, ldx, s, rl);
@@ -580,12 +576,8 @@ int launch_fused(const Int8GemmArgs& g, const T* X, int64_t ldx, const float* s,
 template <int TO, int TT, int WO, int WT, int NST>
 int launch_tile(const Int8GemmArgs& g, hipStream_t st) {
     constexpr int lds = NST * (TO + TT) * KT;
-    static bool ready = false;
-    if (!ready) {
-        PTQ_HIP(hipFuncSetAttribute((const void*)matmul_int8_tile_kernel<TO, TT, WO, WT, NST>,
-                                    hipFuncAttributeMaxDynamicSharedMemorySize, lds));
-        ready = true;
-    }
+    static PerDevice ready;
+    PTQ_TRY(allow_lds(ready, (const void*)matmul_int8_tile_kernel<TO, TT, WO, WT, NST>, lds));
     constexpr int joins = TT / WT / 16;             // workgroups of the join for each of the product's
     for_parts(g, TO, TT, 64 * WO * WT * (g.nsplit > 1 ? joins : 1), [&](const Int8GemmArgs& part) {
         const int64_t to = cdiv(part.out, TO), tt = cdiv(part.rows, TT);
