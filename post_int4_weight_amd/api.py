@@ -141,9 +141,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream():
+def _stream(t=None):
+    """The current stream, of the current device; t: an operand, which has to be there (a launch goes to no other device)."""
+    device = torch.cuda.current_device()
+    if t is not None and t.get_device() != device:
+        raise ValueError(f"tensors on {t.device}, but the current device is cuda:{device} (torch.cuda.device changes it)")
     # torch.cuda.current_stream().cuda_stream without the Stream object (0.3 us instead of 2.8)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -464,7 +468,7 @@ def quantize_tokens_int8(X: torch.Tensor, s=None, codes=None, scales=None):
         raise ValueError("codes must be [rows, in]")
     _check(_lib.quantize_tokens_int8(_ptr(X), _dtype_code(X), rows, n, ldx, _vector(s, n, torch.float32, "s"),
                                      _ptr(codes), _codes(codes, "codes"),
-                                     _vector(scales, rows, torch.float32, "scales"), _stream()))
+                                     _vector(scales, rows, torch.float32, "scales"), _stream(X)))
     return codes, scales
 
 
@@ -492,7 +496,7 @@ def matmul_int8(A, a_scales, codes, scales, bias=None, out_dtype=torch.bfloat16,
     _check(_lib.matmul_int8(_ptr(A), _codes(A, "A"), _vector(a_scales, rows, torch.float32, "a_scales"), rows,
                             _ptr(codes), _codes(codes, "codes"), _vector(scales, out, torch.float32, "scales"), out, n,
                             _vector(bias, out, torch.float32, "bias"), _dtype_code(Y), _ptr(Y), ldy, _ptr(ws), wsb,
-                            _stream()))
+                            _stream(A)))
     return Y
 
 
@@ -513,7 +517,7 @@ def linear_int8(X, codes, scales, bias=None, s=None, out_dtype=None, Y=None, wor
     _check(_lib.linear_int8(_ptr(X), _dtype_code(X), rows, _rows(X, "X"), _vector(s, n, torch.float32, "s"),
                             _ptr(codes), _codes(codes, "codes"), _vector(scales, out, torch.float32, "scales"), out, n,
                             _vector(bias, out, torch.float32, "bias"), _dtype_code(Y), _ptr(Y), ldy, _ptr(ws), wsb,
-                            _stream()))
+                            _stream(X)))
     return Y
 
 
@@ -574,7 +578,7 @@ def kv_cache_write_int8(cache: KVCacheInt8, K, V, offsets, starts, block_table):
         raise TypeError("K and V must have one dtype")
     _check(_lib.kv_cache_write_int8(_ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scales), _ptr(cache.v_scales), nb, h, d,
                                     bs, _ptr(K), ldk, _ptr(V), ldv, _dtype_code(K), rows,
-                                    *_ragged(offsets, starts, block_table, "starts"), _stream()))
+                                    *_ragged(offsets, starts, block_table, "starts"), _stream(K)))
 
 
 def kv_cache_read_int8(cache: KVCacheInt8, offsets, starts, block_table, rows: int, out_dtype=torch.bfloat16, K=None,
@@ -590,7 +594,7 @@ def kv_cache_read_int8(cache: KVCacheInt8, offsets, starts, block_table, rows: i
         raise TypeError("K and V must have one dtype")
     _check(_lib.kv_cache_read_int8(_ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scales), _ptr(cache.v_scales), nb, h, d,
                                    bs, _ptr(K), ldk, _ptr(V), ldv, _dtype_code(K), rows,
-                                   *_ragged(offsets, starts, block_table, "starts"), _stream()))
+                                   *_ragged(offsets, starts, block_table, "starts"), _stream(cache.k)))
     return K, V
 
 
@@ -620,7 +624,7 @@ def attention_int8_cache(Q, cache: KVCacheInt8, offsets, seq_lens, block_table, 
     _check(_lib.attention_int8_cache(_ptr(Q), ldq, _ptr(O), ldo, _vector(lse, rows * heads, torch.float32, "lse"),
                                      _dtype_code(Q), rows, heads, off, lens, batch, table, width, _ptr(cache.k),
                                      _ptr(cache.v), _ptr(cache.k_scales), _ptr(cache.v_scales), nb, h, d, bs,
-                                     float(scale), int(bool(causal)), window, _ptr(ws), wsb, _stream()))
+                                     float(scale), int(bool(causal)), window, _ptr(ws), wsb, _stream(Q)))
     return O if lse is None else (O, lse)
 
 
@@ -688,7 +692,7 @@ def rotary_apply(X, rotary: Rotary, positions, Y=None):
     elif Y is not X:
         ldy = _heads3(Y, rows, heads, dim, "Y")
     _check(_lib.rotary_apply(_ptr(X), ldx, _ptr(Y), ldy, _dtype_code(X), rows, heads, dim,
-                             _vector(positions, rows, torch.int32, "positions"), *rotary._args(), _stream()))
+                             _vector(positions, rows, torch.int32, "positions"), *rotary._args(), _stream(X)))
     return Y
 
 
@@ -703,7 +707,7 @@ def kv_cache_append_int8(cache: KVCacheInt8, K, V, offsets, starts, block_table,
     _check(_lib.kv_cache_append_int8(_ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scales), _ptr(cache.v_scales), nb, h, d,
                                      bs, _ptr(K), ldk, _ptr(V), ldv, _dtype_code(K), rows,
                                      *_ragged(offsets, starts, block_table, "starts"),
-                                     _vector(positions, rows, torch.int32, "positions"), *rotary._args(), _stream()))
+                                     _vector(positions, rows, torch.int32, "positions"), *rotary._args(), _stream(K)))
 
 
 def attention_int8_tree_workspace_bytes(rows: int, batch: int, heads: int, kv_heads: int, head_dim: int, dtype: int,
@@ -739,7 +743,7 @@ def attention_int8_tree(Q, cache: KVCacheInt8, offsets, seq_lens, block_table, p
                                     _dtype_code(Q), rows, heads, off, lens,
                                     _vector(parents, rows, torch.int32, "parents"), batch, table, width, _ptr(cache.k),
                                     _ptr(cache.v), _ptr(cache.k_scales), _ptr(cache.v_scales), nb, h, d, bs,
-                                    float(scale), window, _ptr(ws), wsb, _stream()))
+                                    float(scale), window, _ptr(ws), wsb, _stream(Q)))
     return O if lse is None else (O, lse)
 
 
@@ -785,10 +789,10 @@ def _verify(shares, target, tokens, parents, offsets, u, r, draft, path, counts,
     args = (_ptr(target), ldt, _ptr(draft), ldd, _dtype_code(target), rows, vocab, *ins, *outs)
     if shares is None:
         ws, wsb = _scratch(verify_drafts_workspace_bytes(batch, vocab), target.device, workspace)
-        _check(_lib.verify_drafts(*args, _ptr(ws), wsb, _stream()))
+        _check(_lib.verify_drafts(*args, _ptr(ws), wsb, _stream(target)))
     else:
         ws, wsb = _scratch(int(_lib.ptq_test_verify_drafts_workspace_bytes(shares, batch)), target.device, workspace)
-        _check(_lib.ptq_test_verify_drafts(shares, *args, _ptr(ws), wsb, _stream()))
+        _check(_lib.ptq_test_verify_drafts(shares, *args, _ptr(ws), wsb, _stream(target)))
     return path, counts, next
 
 

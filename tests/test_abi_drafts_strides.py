@@ -16,7 +16,7 @@ def _ints(*shape):
 @pytest.mark.parametrize("stride", [0, 1, VOCAB - 1])
 def test_rows_that_overlap(monkeypatch, name, stride):
     monkeypatch.setattr(api, "_on_gpu", lambda t, name: None)
-    monkeypatch.setattr(api, "_stream", lambda: None)
+    monkeypatch.setattr(api, "_stream", lambda t: None)
     rows = {n: torch.full((3, VOCAB), 0.1) for n in ("target", "draft")}
     rows[name] = torch.full((3 * VOCAB,), 0.1).as_strided((3, VOCAB), (stride, 1))
     with pytest.raises(api.PTQError, match=f"row stride {stride} of {name} < vocab = {VOCAB}"):
