@@ -457,8 +457,8 @@ int attention_int8_cache(const void* Q, int64_t ldq, void* O, int64_t ldo, float
  *
  * rotary_apply: Y = X turned, [rows, heads, head_dim] bf16 or fp32 (row strides
  * ldx and ldy, head_dim a multiple of 8), positions[rows]; channels from
- * rotary_dim on are copied. Y may be X (with its stride), and must not overlap
- * it otherwise.
+ * rotary_dim on are copied. Y may be X (with its stride), or other columns of its
+ * rows (with its stride), and must not overlap it otherwise.
  *
  * kv_cache_append_int8: kv_cache_write_int8 of turned keys, which are not
  * rounded before they are quantized. positions[rows], or NULL: each row's own

@@ -432,8 +432,11 @@ int rotary_apply(const void* X, int64_t ldx, void* Y, int64_t ldy, int dtype, in
     // rows of Y are written while others of X are still read
     const uintptr_t x0 = (uintptr_t)X, y0 = (uintptr_t)Y, es = dtype == PTQ_BF16 ? 2 : 4;
     const uintptr_t xn = ((uintptr_t)(rows - 1) * ldx + n) * es, yn = ((uintptr_t)(rows - 1) * ldy + n) * es;
-    if (x0 == y0 ? ldx != ldy && rows > 1 : x0 < y0 + yn && y0 < x0 + xn)
-        REFUSE("%s: Y overlaps X without being X", fn);
+    const bool cross = x0 == y0 ? ldx != ldy && rows > 1 : x0 < y0 + yn && y0 < x0 + xn;
+    // other columns of the same rows: Y's lie `after` bytes behind X's, modulo a row
+    const uintptr_t row = (uintptr_t)ldx * es, after = (y0 % row + row - x0 % row) % row, width = (uintptr_t)n * es;
+    const bool beside = ldx == ldy && after >= width && after + width <= row;
+    if (cross && !beside) REFUSE("%s: Y overlaps X without being X", fn);
     return launch_rotary(X, ldx, Y, ldy, dtype, rows, heads, head_dim, p, positions, (hipStream_t)stream);
 }
 
