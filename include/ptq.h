@@ -21,7 +21,7 @@
  *    marked "host". The library allocates nothing: scratch memory comes from
  *    the caller's workspace, whose size the matching *_workspace_bytes query
  *    returns (256-byte aligned; NULL with size 0 is allowed where the query
- *    returns 0).
+ *    returns 0). Calls that may run at the same time need one each.
  *  - Work is enqueued on `stream` (a hipStream_t; NULL = the default stream).
  *    Entry points that return host values (stats, alpha) synchronise that
  *    stream before returning; the others are asynchronous.
@@ -452,8 +452,9 @@ int attention_int8_cache(const void* Q, int64_t ldq, void* O, int64_t ldo, float
  *   y_a = m (x_a cos t - x_b sin t),  y_b = m (x_b cos t + x_a sin t),
  *   t = position * inv_freq[i], m = magnitude
  * inv_freq: fp64[n] (device; scaled for long contexts by the caller, or by the
- * Python binding's Rotary.make), the angle in fp64, the rest in fp32; a value
- * is rounded once, to its type. positions: int32, any value.
+ * Python binding's Rotary.make), the angle in fp64, the rest in fp32 (sines and
+ * cosines within 2^-23 + 2^-51 |t|); a value is rounded once, to its type.
+ * positions: int32, any value.
  *
  * rotary_apply: Y = X turned, [rows, heads, head_dim] bf16 or fp32 (row strides
  * ldx and ldy, head_dim a multiple of 8), positions[rows]; channels from
@@ -504,7 +505,11 @@ int attention_int8_tree(const void* Q, int64_t ldq, void* O, int64_t ldo, float*
 
 /* ------------------------------------------------------------------------
  * verify_drafts: which nodes of each sequence's tree are kept, so that the
- * tokens that come out are distributed as the target's. Node 0 of a sequence is
+ * tokens that come out are distributed as the target's where the children of a
+ * node were drawn independently of each other from its row of draft (the same
+ * token may come twice), or were chosen. Children drawn without replacement have
+ * other probabilities after each other, which one row cannot give: their tokens
+ * come out distributed otherwise. Node 0 of a sequence is
  * its last token, the others are drafted: tokens[rows] and parents[rows]
  * (int32, rows as in attention_int8_tree, at most 512 a sequence). Row i of
  * target [rows, vocab] (row stride ldt) holds the target's probabilities of the
@@ -526,8 +531,9 @@ int attention_int8_tree(const void* Q, int64_t ldq, void* O, int64_t ldo, float*
  * many; next[batch]: the token, or -1 if the sum is not positive and finite. A
  * sequence without rows, or with more than 512, has counts 0 and next -1.
  * Rows of no sequence are left as they are. The workspace, of
- * verify_drafts_workspace_bytes (0 for small vocabularies), need not be cleared.
- * Asynchronous. Errors: EINVAL, EWORKSPACE, EHIP.
+ * verify_drafts_workspace_bytes (0 for small vocabularies), need not be cleared,
+ * and must be one call's alone until that has ended: workgroups of the call wait
+ * for each other through it. Asynchronous. Errors: EINVAL, EWORKSPACE, EHIP.
  * ---------------------------------------------------------------------- */
 size_t verify_drafts_workspace_bytes(int64_t batch, int64_t vocab);
 int verify_drafts(const void* target, int64_t ldt, const void* draft, int64_t ldd, int dtype, int64_t rows,

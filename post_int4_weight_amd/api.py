@@ -760,7 +760,8 @@ def verify_drafts_workspace_bytes(batch: int, vocab: int) -> int:
 
 def verify_drafts(target, tokens, parents, offsets, u, r, draft=None, path=None, counts=None, next=None, workspace=None):
     """verify_drafts (include/ptq.h): (path [rows], counts [batch], next [batch]) of each sequence's tree, from target
-    and draft probabilities [rows, vocab] (draft None: drafts that were chosen) and random numbers u [rows], r [batch]."""
+    and draft probabilities [rows, vocab] (draft None: drafts that were chosen) and random numbers u [rows], r [batch]. The
+    children of a node are taken to be drawn independently of each other from its row of draft."""
     return _verify(None, target, tokens, parents, offsets, u, r, draft, path, counts, next, workspace)
 
 
