@@ -155,7 +155,7 @@ __device__ __forceinline__ double sum_part(const R& r, int64_t lo, int64_t hi) {
     auto leave = [&](Chunk<T>* p, int count, int64_t at) __attribute__((always_inline)) {
         const int64_t first = at - lane * N;
         for (int j = 0; j < r.nex; j += 64) {
-            const int mine = r.ex[std::min(j + lane, r.nex - 1)];
+            const int mine = j + lane < r.nex ? r.ex[j + lane] : -1;      // each once: one in 64 lanes takes 64 rounds below
             uint64_t mask = __ballot(mine >= first && mine < first + count * STEP);
             while (mask) {
                 const int64_t k = __builtin_amdgcn_readlane(mine, __builtin_ctzll(mask)) - at;
@@ -487,8 +487,11 @@ int launch(const VerifyArgs& a, hipStream_t st) {
 // Workgroups of a sequence. Four, or as many as the CUs allow: 48 sequences of 6
 // nodes, 128256 tokens, fp32, 3 children not kept: 73 us by one, 59 by two, 51 by
 // four, 53 by five; 128 sequences 71 and 69 by two. Clearing what they share and
-// meeting cost more than that below about 10^5 tokens (65536, 32 sequences: 38 us
-// by one and 40 by four; with nothing to sum 15 and 20).
+// meeting cost more than that below about 10^5 tokens. 48 sequences, one child not
+// kept, by one and by four: 65536 tokens 15 and 17 us, 80000 16 and 17, 100003 20
+// and 17, 128256 27 and 19, 152064 28 and 21; by two, 128 sequences: 25 and 27,
+// 33 and 31, 35 and 34 of the last three. Chosen drafts, which need one pass: 13
+// and 17 at 100003, 17 and 16 at 128256.
 int verify_drafts_shares(int64_t batch, int64_t vocab) {
     if (vocab < 98304 || batch < 1) return 1;
     return (int)std::max<int64_t>(1, std::min<int64_t>(MAX_SHARES, 256 / batch));
