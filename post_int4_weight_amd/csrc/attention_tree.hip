@@ -127,7 +127,7 @@ struct QueryRow {
 // whole rows at a time, and copies the next step over it when it has read it; the
 // other waves of the SIMD work meanwhile, and nothing waits for another wave until
 // the join. What bounds it: for few rows memory (16 trees of 8 nodes over 4000
-// keys, 32 heads on 8, D = 128: 37 us, the cache's 131 MB at 3.5 TB/s), with more
+// keys, 32 heads on 8, D = 128: 41 us, the cache's 131 MB at 3.2 TB/s), with more
 // tiles on the same keys the vector instructions of the exponentials and of the
 // conversion of K and V. Tiles of 64 and 128 rows that share a step among waves were 1%
 // faster in the mean over 1700 shapes, and taken out; from about 300 rows a kv
