@@ -489,8 +489,9 @@ int kv_cache_append_int8(int8_t* k_codes, int8_t* v_codes, float* k_scales, floa
  * block_table. NaN for a query: a parent on its way up that is not below its
  * node or less than -1, or a key in a block without a valid id.
  *
- * Elements of a bf16 row of Q are exact down to 2^-20 of its largest, those of an
- * fp32 row off by 2^-22 of themselves, or by 2^-28 of the largest, at most.
+ * Elements of a bf16 row of Q are held exactly down to 2^-20 of its largest and
+ * off by 2^-28 of that below, those of an fp32 row off by 2^-22 of themselves or by
+ * 2^-28 of the largest, at most.
  * Probabilities, sums and scales as for attention_int8_cache. Asynchronous.
  * Errors: EINVAL, EWORKSPACE, EHIP.
  * ---------------------------------------------------------------------- */
@@ -505,16 +506,14 @@ int attention_int8_tree(const void* Q, int64_t ldq, void* O, int64_t ldo, float*
 
 /* ------------------------------------------------------------------------
  * verify_drafts: which nodes of each sequence's tree are kept, so that the
- * tokens that come out are distributed as the target's where the children of a
- * node were drawn independently of each other from its row of draft (the same
- * token may come twice), or were chosen. Children drawn without replacement have
- * other probabilities after each other, which one row cannot give: their tokens
- * come out distributed otherwise. Node 0 of a sequence is
+ * tokens that come out are distributed as the target's. Node 0 of a sequence is
  * its last token, the others are drafted: tokens[rows] and parents[rows]
  * (int32, rows as in attention_int8_tree, at most 512 a sequence). Row i of
  * target [rows, vocab] (row stride ldt) holds the target's probabilities of the
  * token after node i, row i of draft (ldd) those that i's children were drawn
- * from; both bf16 or fp32. Random numbers u[rows] and r[batch], fp32 in [0, 1).
+ * from, independently of each other (the same token may come twice; after
+ * children drawn without replacement the output is not the target's); both bf16
+ * or fp32. Random numbers u[rows] and r[batch], fp32 in [0, 1).
  *
  * From node 0, with p its row of target, q of draft, w = max(p, 0) and z = 1:
  * its children x in index order,

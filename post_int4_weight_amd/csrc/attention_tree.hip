@@ -582,13 +582,15 @@ size_t attention_tree_part_bytes(int nsplit, int64_t rows, int heads, int dim) {
 // The choice of a TreePlan: the least of estimated times, in microseconds,
 //   start + rounds (first + steps each) + [join + bytes of the parts],
 // fitted to 750 shapes with all their plans (1 .. 64 sequences of 1 .. 64 nodes, 1
-// .. 8 kv heads, groups of 1 .. 8, 64 .. 16000 keys, half of them ragged). The
-// choice is 4% slower than the best plan in the mean, 15% at nine shapes of ten, 45%
-// at worst. Without one of the kernels the best plan would be slower in the mean by
-// 3.5% (tiles of 16 rows: 1 tree of 16 nodes over 1000 keys 15.3 us, of 32 rows 18.6),
-// 8.6% (of 32) and 5.9% (32 rows by four waves). Lengths are not known here: keys
-// is the most there may be, and every sequence is taken to have the mean number of
-// rows. A round is as many workgroups as the card holds.
+// .. 8 kv heads, groups of 1 .. 8, 64 .. 16000 keys, half of them ragged). Over 670
+// others like them the choice is 3.6% slower than the best plan in the mean, 12% at
+// nine shapes of ten, 44% at worst. Without one of the kernels the best plan would
+// be slower in the mean by 5.7% (tiles of 16 rows: 1 tree of 16 nodes over 1000 keys
+// 15.3 us, of 32 rows 18.6), 3.8% (of 32), 2.4% (32 rows by four waves) and 0.4% (of
+// 256, which more rows a sequence need: 8 trees of 200 .. 512 nodes, 4 heads a
+// group, over 500 .. 8000 keys: 295 us). Lengths are not known here: keys is the
+// most there may be, and every sequence is taken to have the mean number of rows. A
+// round is as many workgroups as the card holds.
 TreePlan attention_tree_plan(int64_t rows, int64_t batch, int heads, int kv_heads, int dim, int dtype, int block,
                              int64_t width, int64_t window) {
     const int64_t group = heads / kv_heads, most = width * block;
